@@ -1297,4 +1297,152 @@ gift_status gift_select_fragile(int L, const unsigned long long *counts, int k, 
   return GIFT_OK;
 }
 
+// -----------------------------------------------------------------------------------------
+// norm, 8-bit activation checkpoints, weight gradient
+// -----------------------------------------------------------------------------------------
+namespace {
+
+constexpr int kMaxExtent = 1 << 30;   // tokens and row lengths: index arithmetic per axis stays in 32 bits
+
+bool valid_dt(gift_dtype t) { return t == GIFT_DT_F32 || t == GIFT_DT_BF16; }
+bool valid_act_fmt(gift_format f) { return f == GIFT_FMT_E4M3 || f == GIFT_FMT_E5M2; }
+int fmt8(gift_format f) { return f == GIFT_FMT_E4M3 ? FMT_E4M3 : FMT_E5M2; }
+bool valid_extent(int n) { return n >= 1 && n <= kMaxExtent; }
+
+// The workspace of one call, carved from the first 256-byte boundary (the size has room for it).
+struct ActWs {
+  float *part = nullptr;    // slice partials of the sums over tokens
+  float *db = nullptr;      // weight gradient: db when only the call itself needs it
+  size_t bytes = 0;
+};
+
+ActWs act_layout(void *base, const gift_ctx *ctx, gift_op op, gift_dtype dt, int T, int d_out, int d_in) {
+  ActWs w;
+  Carve c(base ? reinterpret_cast<void *>(((uintptr_t)base + kAlign - 1) / kAlign * kAlign) : nullptr);
+  if (op == GIFT_OP_LAYERNORM_BACKWARD) {
+    w.part = c.take<float>(norm_part_floats(T, d_in));
+  } else {
+    Launch L{};
+    L.sms = ctx->sms;
+    const WeightGradWs g = weight_grad_layout(L, dt == GIFT_DT_BF16, T, d_out, d_in);
+    w.part = c.take<float>(g.part_floats);
+    w.db = c.take<float>(d_out);
+  }
+  w.bytes = c.off + kAlign;
+  return w;
+}
+
+}  // namespace
+
+gift_status gift_act_sizes(gift_format fmt, int T, int d, size_t *code_bytes, size_t *scale_bytes) {
+  if (!code_bytes || !scale_bytes || !valid_extent(T) || !valid_extent(d) || !valid_act_fmt(fmt))
+    return GIFT_ERR_INVALID_ARG;
+  *code_bytes = (size_t)T * d;
+  *scale_bytes = (size_t)T * (((size_t)d + 127) / 128);
+  return GIFT_OK;
+}
+
+size_t gift_act_workspace_bytes(const gift_ctx *ctx, gift_op op, gift_dtype dt, int T, int d_out, int d_in) {
+  if (!ctx || !valid_dt(dt) || !valid_extent(T) || !valid_extent(d_in)) return (size_t)-1;
+  if (op != GIFT_OP_LAYERNORM_BACKWARD && (op != GIFT_OP_WEIGHT_GRAD || !valid_extent(d_out))) return (size_t)-1;
+  return act_layout(nullptr, ctx, op, dt, T, d_out, d_in).bytes;
+}
+
+gift_status gift_act_encode(gift_ctx *ctx, const void *x, gift_dtype x_dt, int T, int d, gift_format fmt,
+                            void *codes, void *scales, int *d_status, cudaStream_t stream) {
+  if (!ctx || !x || !codes || !scales || !valid_extent(T) || !valid_extent(d) || !valid_dt(x_dt) ||
+      !valid_act_fmt(fmt))
+    return GIFT_ERR_INVALID_ARG;
+  CK(launch_act_encode(mk(ctx, d_status, stream), fmt8(fmt), x, x_dt == GIFT_DT_BF16, T, d,
+                       static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales)));
+  return GIFT_OK;
+}
+
+gift_status gift_act_decode(gift_ctx *ctx, const void *codes, const void *scales, gift_format fmt, int T, int d,
+                            void *x_out, gift_dtype out_dt, int *d_status, cudaStream_t stream) {
+  if (!ctx || !x_out || !codes || !scales || !valid_extent(T) || !valid_extent(d) || !valid_dt(out_dt) ||
+      !valid_act_fmt(fmt))
+    return GIFT_ERR_INVALID_ARG;
+  CK(launch_act_decode(mk(ctx, d_status, stream), fmt8(fmt), static_cast<const uint8_t *>(codes),
+                       static_cast<const uint8_t *>(scales), T, d, x_out, out_dt == GIFT_DT_BF16));
+  return GIFT_OK;
+}
+
+gift_status gift_layernorm_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d, const float *gamma,
+                                   const float *beta, float eps, void *y, float *mean, float *rstd, gift_format fmt,
+                                   void *codes, void *scales, int *d_status, cudaStream_t stream) {
+  if (!ctx || !x || !y || !valid_extent(T) || !valid_extent(d) || !valid_dt(dt)) return GIFT_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || eps > kF32Max) return GIFT_ERR_INVALID_ARG;
+  if (!codes != !scales || (codes && !valid_act_fmt(fmt))) return GIFT_ERR_INVALID_ARG;
+  NormForward a{};
+  a.x = x;
+  a.T = T;
+  a.d = d;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.eps = eps;
+  a.y = y;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.codes = static_cast<uint8_t *>(codes);
+  a.scales = static_cast<uint8_t *>(scales);
+  CK(launch_norm_forward(mk(ctx, d_status, stream), fmt8(fmt), dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
+gift_status gift_layernorm_backward(gift_ctx *ctx, const void *dy, gift_dtype dt, int T, int d, const void *saved,
+                                    int saved_is_codes, const void *scales, gift_format fmt, const float *mean,
+                                    const float *rstd, const float *gamma, void *dx, float *dgamma, float *dbeta,
+                                    void *ws, size_t ws_bytes, int *d_status, cudaStream_t stream) {
+  if (!ctx || !dy || !saved || !rstd || !dx || !valid_extent(T) || !valid_extent(d) || !valid_dt(dt))
+    return GIFT_ERR_INVALID_ARG;
+  if (saved_is_codes ? (!scales || !valid_act_fmt(fmt)) : !mean) return GIFT_ERR_INVALID_ARG;
+  const bool sums = dgamma || dbeta;
+  if (sums && (!ws || ws_bytes < act_layout(nullptr, ctx, GIFT_OP_LAYERNORM_BACKWARD, dt, T, d, d).bytes))
+    return GIFT_ERR_INVALID_ARG;
+  NormBackward a{};
+  a.dy = dy;
+  a.T = T;
+  a.d = d;
+  a.x = saved_is_codes ? nullptr : saved;
+  a.codes = saved_is_codes ? static_cast<const uint8_t *>(saved) : nullptr;
+  a.scales = saved_is_codes ? static_cast<const uint8_t *>(scales) : nullptr;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.gamma = gamma;
+  a.dx = dx;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.part = sums ? act_layout(ws, ctx, GIFT_OP_LAYERNORM_BACKWARD, dt, T, d, d).part : nullptr;
+  CK(launch_norm_backward(mk(ctx, d_status, stream), fmt8(fmt), dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
+gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_dt, const void *codes,
+                             const void *scales, gift_format fmt, int T, int d_out, int d_in, const float *gamma,
+                             const float *beta, float *dW, float *db, void *ws, size_t ws_bytes, int *d_status,
+                             cudaStream_t stream) {
+  if (!ctx || !delta || !codes || !scales || !dW || !ws || !valid_extent(T) || !valid_extent(d_out) ||
+      !valid_extent(d_in) || !valid_dt(delta_dt) || !valid_act_fmt(fmt))
+    return GIFT_ERR_INVALID_ARG;
+  if (ws_bytes < act_layout(nullptr, ctx, GIFT_OP_WEIGHT_GRAD, delta_dt, T, d_out, d_in).bytes)
+    return GIFT_ERR_INVALID_ARG;
+  const ActWs w = act_layout(ws, ctx, GIFT_OP_WEIGHT_GRAD, delta_dt, T, d_out, d_in);
+  WeightGrad a{};
+  a.delta = delta;
+  a.codes = static_cast<const uint8_t *>(codes);
+  a.scales = static_cast<const uint8_t *>(scales);
+  a.T = T;
+  a.d_out = d_out;
+  a.d_in = d_in;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.dW = dW;
+  a.db = db;
+  a.part = w.part;
+  a.db_ws = w.db;
+  CK(launch_weight_grad(mk(ctx, d_status, stream), fmt8(fmt), delta_dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
 }  // extern "C"

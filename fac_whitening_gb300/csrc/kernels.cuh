@@ -324,4 +324,50 @@ cudaError_t launch_lowrank_outputs(const Launch &L, const float *Q, int d_in, in
                                    float *sigma);
 cudaError_t launch_eye(const Launch &L, float *Q, int n);
 
+// ---- act.cu: the 8-bit activation checkpoint ---------------------------------------------
+cudaError_t launch_act_encode(const Launch &L, int fmt, const void *x, bool bf16, int T, int d, uint8_t *codes,
+                              uint8_t *scales);
+cudaError_t launch_act_decode(const Launch &L, int fmt, const uint8_t *codes, const uint8_t *scales, int T, int d,
+                              void *out, bool bf16);
+// ---- norm.cu: layer norm ------------------------------------------------------------------
+struct NormForward {
+  const void *x;
+  int T, d;
+  const float *gamma, *beta;   // nullable
+  float eps;
+  void *y;
+  float *mean, *rstd;          // nullable
+  uint8_t *codes, *scales;     // both or neither
+};
+struct NormBackward {
+  const void *dy;
+  int T, d;
+  const void *x;               // the forward pass's input, or (codes set) its checkpoint
+  const uint8_t *codes, *scales;
+  const float *mean, *rstd, *gamma;
+  void *dx;
+  float *dgamma, *dbeta;       // nullable
+  float *part;                 // norm_part_floats
+};
+size_t norm_part_floats(int T, int d);
+cudaError_t launch_norm_forward(const Launch &L, int fmt, bool bf16, const NormForward &a);
+cudaError_t launch_norm_backward(const Launch &L, int fmt, bool bf16, const NormBackward &a);
+// out[c] = sum_t x[t][c], slices of tokens added in order; part: col_part_floats
+size_t col_part_floats(int T, int d);
+cudaError_t launch_col_sums(const Launch &L, const void *x, bool bf16, int T, int d, float *part, float *out);
+// ---- weight_grad.cu -------------------------------------------------------------------------
+struct WeightGradWs {
+  size_t part_floats = 0;      // column-sum partials of db
+};
+struct WeightGrad {
+  const void *delta;
+  const uint8_t *codes, *scales;
+  int T, d_out, d_in;
+  const float *gamma, *beta;   // nullable
+  float *dW, *db;              // db nullable
+  float *part, *db_ws;         // workspace: column-sum partials, db when the caller wants none
+};
+WeightGradWs weight_grad_layout(const Launch &L, bool bf16, int T, int d_out, int d_in);
+cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const WeightGrad &a);
+
 }  // namespace gift

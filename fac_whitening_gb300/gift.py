@@ -25,7 +25,8 @@ SCALING = {"tensor": 0, "block128": 1, "block512": 2}
 XFORM = {"identity": 0, "lowrank": 1, "chol_input": 2, "chol_two_sided": 3}
 PREC = {"fp32": 0, "tc": 1}
 DTYPE = {"f32": 0, "bf16": 1}
-OP = {"factor_update": 0, "encode": 1, "decode": 2, "amax": 3, "kfac_factor": 4, "reduce_decode": 5}
+OP = {"factor_update": 0, "encode": 1, "decode": 2, "amax": 3, "kfac_factor": 4, "reduce_decode": 5,
+      "layernorm_backward": 6, "weight_grad": 7}
 OPT_SUBSPACE_ITERS = 0
 OPT_BARRIER_WAIT = 1
 OPT_SKETCH = 2
@@ -94,6 +95,15 @@ def _declare(lib):
         "gift_boundary_hit_rate": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp, _vp]),
         "gift_encode_lowrank_noalloc": (_i, [_vp, ctypes.POINTER(GiftFactor), _vp, _i, _i, _i, _vp, _vp, _vp, _vp,
                                              _vp, _vp]),
+        "gift_act_sizes": (_i, [_i, _i, _i, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
+        "gift_act_workspace_bytes": (_sz, [_vp, _i, _i, _i, _i, _i]),
+        "gift_act_encode": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
+        "gift_act_decode": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp]),
+        "gift_layernorm_forward": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _i, _vp, _vp,
+                                        _vp, _vp]),
+        "gift_layernorm_backward": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                         _sz, _vp, _vp]),
+        "gift_weight_grad": (_i, [_vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -405,3 +415,107 @@ def gift_encode_lowrank_noalloc(ctx: Context, f: Factor, W, fmt: str, codes, sca
     _check(lib().gift_encode_lowrank_noalloc(ctx.handle, _fptr(f), _p(W), d_out, d_in, FMT[fmt], _p(amax_in),
                                              _p(codes), _p(scales), _p(amax_out), _p(status), _stream(stream)),
            "gift_encode_lowrank_noalloc")
+
+
+# ---- norm, 8-bit activation checkpoints, weight gradient ------------------------------------
+def _dt(t) -> int:
+    """The gift_dtype of a tensor, or of a torch dtype."""
+    import torch
+    dt = getattr(t, "dtype", t)
+    if dt == torch.bfloat16:
+        return DTYPE["bf16"]
+    if dt == torch.float32:
+        return DTYPE["f32"]
+    raise ValueError(f"libgift takes float32 or bfloat16 activations and gradients, not {dt}")
+
+
+def _need(t, shape, what: str, dtype=None):
+    """Refuse a buffer whose shape or type is not what the call passes on to the library."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: expected {tuple(shape)}{'' if dtype is None else ' ' + str(dtype)}, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+
+
+def _need_saved(codes, scales, T: int, d: int):
+    """Refuse checkpoint buffers that are not bytes or are smaller than a T x d checkpoint."""
+    for t, n, what in ((codes, T * d, "codes"), (scales, T * ((d + 127) // 128), "scales")):
+        if t.element_size() != 1 or t.numel() < n:
+            raise ValueError(f"{what}: expected at least {n} bytes, got {t.numel()} of {t.dtype}")
+
+
+def gift_act_sizes(fmt: str, T: int, d: int):
+    """(code bytes, scale bytes) of an 8-bit checkpoint of T x d activations."""
+    cb, sb = _sz(), _sz()
+    _check(lib().gift_act_sizes(FMT[fmt], T, d, ctypes.byref(cb), ctypes.byref(sb)), "gift_act_sizes")
+    return cb.value, sb.value
+
+
+def gift_act_workspace_bytes(ctx: Context, op: str, dtype, T: int, d_out: int, d_in: int) -> int:
+    n = lib().gift_act_workspace_bytes(ctx.handle, OP[op], _dt(dtype), T, d_out, d_in)
+    if n == ctypes.c_size_t(-1).value:
+        raise GiftError(ERR_INVALID_ARG, "gift_act_workspace_bytes")
+    return n
+
+
+def gift_act_encode(ctx: Context, x, fmt: str, codes, scales, status=None, stream=None):
+    T, d = x.shape
+    _need_saved(codes, scales, T, d)
+    _check(lib().gift_act_encode(ctx.handle, _p(x), _dt(x), T, d, FMT[fmt], _p(codes), _p(scales), _p(status),
+                                 _stream(stream)), "gift_act_encode")
+
+
+def gift_act_decode(ctx: Context, codes, scales, fmt: str, x_out, status=None, stream=None):
+    T, d = x_out.shape
+    _need_saved(codes, scales, T, d)
+    _check(lib().gift_act_decode(ctx.handle, _p(codes), _p(scales), FMT[fmt], T, d, _p(x_out), _dt(x_out),
+                                 _p(status), _stream(stream)), "gift_act_decode")
+
+
+def gift_layernorm_forward(ctx: Context, x, gamma, beta, eps: float, y, mean=None, rstd=None, fmt: str = "e4m3",
+                           codes=None, scales=None, status=None, stream=None):
+    import torch
+    T, d = x.shape
+    _need(y, (T, d), "y", x.dtype)
+    for t, n, what in ((gamma, d, "gamma"), (beta, d, "beta"), (mean, T, "mean"), (rstd, T, "rstd")):
+        _need(t, (n,), what, torch.float32)
+    if codes is not None and scales is not None:
+        _need_saved(codes, scales, T, d)
+    _check(lib().gift_layernorm_forward(ctx.handle, _p(x), _dt(x), T, d, _p(gamma), _p(beta), eps, _p(y), _p(mean),
+                                        _p(rstd), FMT[fmt], _p(codes), _p(scales), _p(status), _stream(stream)),
+           "gift_layernorm_forward")
+
+
+def gift_layernorm_backward(ctx: Context, dy, saved, gamma, rstd, dx, dgamma=None, dbeta=None, mean=None,
+                            scales=None, fmt: str = "e4m3", ws=None, status=None, stream=None):
+    """saved: the forward pass's x (with mean), or its checkpoint's codes (with scales)."""
+    import torch
+    T, d = dy.shape
+    _need(dx, (T, d), "dx", dy.dtype)
+    for t, n, what in ((gamma, d, "gamma"), (dgamma, d, "dgamma"), (dbeta, d, "dbeta"), (mean, T, "mean"),
+                       (rstd, T, "rstd")):
+        _need(t, (n,), what, torch.float32)
+    if scales is None:
+        _need(saved, (T, d), "saved", dy.dtype)
+    else:
+        _need_saved(saved, scales, T, d)
+    _check(lib().gift_layernorm_backward(ctx.handle, _p(dy), _dt(dy), T, d, _p(saved), int(scales is not None),
+                                         _p(scales), FMT[fmt], _p(mean), _p(rstd), _p(gamma), _p(dx), _p(dgamma),
+                                         _p(dbeta), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                         _p(status), _stream(stream)), "gift_layernorm_backward")
+
+
+def gift_weight_grad(ctx: Context, delta, codes, scales, fmt: str, dW, db=None, gamma=None, beta=None, ws=None,
+                     status=None, stream=None):
+    import torch
+    T, d_out = delta.shape
+    d_in = dW.shape[1]
+    _need(dW, (d_out, d_in), "dW", torch.float32)
+    _need_saved(codes, scales, T, d_in)
+    for t, n, what in ((db, d_out, "db"), (gamma, d_in, "gamma"), (beta, d_in, "beta")):
+        _need(t, (n,), what, torch.float32)
+    _check(lib().gift_weight_grad(ctx.handle, _p(delta), _dt(delta), _p(codes), _p(scales), FMT[fmt], T, d_out, d_in,
+                                  _p(gamma), _p(beta), _p(dW), _p(db), _p(ws),
+                                  0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream(stream)),
+           "gift_weight_grad")

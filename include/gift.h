@@ -138,14 +138,16 @@ typedef struct {
  * per-call state, so calls on different streams may run concurrently. */
 typedef struct gift_ctx gift_ctx;
 
-/* Operations for gift_workspace_bytes. */
+/* Operations for gift_workspace_bytes (the last two for gift_act_workspace_bytes). */
 typedef enum {
   GIFT_OP_FACTOR_UPDATE = 0,
   GIFT_OP_ENCODE = 1,
   GIFT_OP_DECODE = 2,
   GIFT_OP_AMAX = 3,
   GIFT_OP_KFAC_FACTOR = 4,
-  GIFT_OP_REDUCE_DECODE = 5
+  GIFT_OP_REDUCE_DECODE = 5,
+  GIFT_OP_LAYERNORM_BACKWARD = 6, /* sized by gift_act_workspace_bytes */
+  GIFT_OP_WEIGHT_GRAD = 7         /* sized by gift_act_workspace_bytes */
 } gift_op;
 
 /* Tunables for gift_set_option. */
@@ -473,6 +475,102 @@ gift_status gift_select_fragile(int L, const unsigned long long *counts, int k, 
 gift_status gift_encode_lowrank_noalloc(gift_ctx *ctx, const gift_factor *f, const float *W, int d_out, int d_in,
                                         gift_format fmt, const float *amax_in, void *codes, float *scales,
                                         float *amax_out, int *d_status, cudaStream_t stream);
+
+/* ---- The step that makes the codec's inputs: norm, kept activations, weight gradient -------
+ * [notes] eq. (4) and Algorithm 1 start from a layer's activations a and its gradient W_g; the
+ * pages do not say how a training step keeps a for its backward pass.  These entry points keep
+ * it in 8 bits and form W_g (and a norm's gradients) from what was kept.
+ *
+ * An 8-bit checkpoint of a T x d tensor x (row t is one token):
+ *   codes  : T x d bytes, E4M3 or E5M2, row-major;
+ *   scales : T x ceil(d / 128) bytes, one per token and 128 consecutive columns (the last group
+ *            of a row is shorter): the byte k + 127 of a scale 2^k;
+ *   k      : the smallest exponent with max|x| <= FMAX 2^k over the group, held within
+ *            [-110, 127 - EMAX] (EMAX = 8 or 15, the exponent of FMAX = 448 or 57344);
+ *   code   : x 2^-k rounded to nearest even, saturating; the value it stands for is code 2^k.
+ * The scale is a power of two, so no element loses mantissa bits to it and every value is exact
+ * in BF16 (the tensor cores multiply it as it is) and in FP32.  A group that holds NaN or Inf has
+ * the scale byte 255 and stands for NaN.
+ * In all of them T, d, d_out and d_in are at most 2^30 (INVALID_ARG above); their products may
+ * pass 2^32. */
+
+/* Sizes of one 8-bit checkpoint in bytes.  Host-only.  INVALID_ARG: null outputs, T or d < 1, a
+ * format other than E4M3 or E5M2. */
+gift_status gift_act_sizes(gift_format fmt, int T, int d, size_t *code_bytes, size_t *scale_bytes);
+
+/* Bytes of device workspace of GIFT_OP_LAYERNORM_BACKWARD (d_out is ignored, d_in = d) or
+ * GIFT_OP_WEIGHT_GRAD with gradients (dy, delta) of type dt.  Host-only; (size_t)-1 for invalid
+ * arguments or another op. */
+size_t gift_act_workspace_bytes(const gift_ctx *ctx, gift_op op, gift_dtype dt, int T, int d_out, int d_in);
+
+/* Keep x (device, T x d of type x_dt) as an 8-bit checkpoint: codes and scales (device,
+ * gift_act_sizes bytes).  INVALID_ARG: null pointers, T or d < 1, a bad type or format.
+ * d_status: NONFINITE when x holds NaN or Inf (their groups stand for NaN, the others are
+ * valid). */
+gift_status gift_act_encode(gift_ctx *ctx, const void *x, gift_dtype x_dt, int T, int d, gift_format fmt,
+                            void *codes, void *scales, int *d_status, cudaStream_t stream);
+
+/* The values of an 8-bit checkpoint (exact, NaN for a group marked so) into x_out (device, T x d
+ * of type out_dt), for callers that take plain activations (gift_factor_update,
+ * gift_kfac_factor).  INVALID_ARG as gift_act_encode.  d_status: NONFINITE when a group is marked. */
+gift_status gift_act_decode(gift_ctx *ctx, const void *codes, const void *scales, gift_format fmt, int T, int d,
+                            void *x_out, gift_dtype out_dt, int *d_status, cudaStream_t stream);
+
+/* Layer norm over the last dimension: for each row, mean = sum(x) / d, rstd =
+ * (sum((x - mean)^2) / d + eps)^-1/2, n = (x - mean) rstd, y = gamma n + beta.  Statistics are
+ * FP32, from the deviations (two passes over a row held on chip); y is rounded once.
+ *  x, y   : device, T x d of type dt (y in x's type).
+ *  gamma, beta : device, d FP32, nullable (1 and 0).
+ *  mean, rstd  : device, T FP32, nullable: kept for the backward pass.
+ *  codes, scales : device, both or neither: the 8-bit checkpoint of n in `fmt` (ignored when
+ *           NULL), made from n in FP32.  It serves gift_layernorm_backward and, with gamma and
+ *           beta, gift_weight_grad of the linear layer that reads y.
+ *  eps    : finite, >= 0.
+ * INVALID_ARG: null x or y, one of codes and scales without the other, T or d < 1, a bad type,
+ * format or eps.  d_status: NONFINITE when a row's mean or rstd is not finite. */
+gift_status gift_layernorm_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d, const float *gamma,
+                                   const float *beta, float eps, void *y, float *mean, float *rstd, gift_format fmt,
+                                   void *codes, void *scales, int *d_status, cudaStream_t stream);
+
+/* Layer norm's gradients: with h = dy gamma (per row),
+ *   dx = rstd (h - sum(h) / d - n sum(h n) / d),  dgamma = sum_t dy n,  dbeta = sum_t dy,
+ * n taken from the forward pass's input ((x - mean) rstd) or from its 8-bit checkpoint.
+ *  dy, dx : device, T x d of type dt.
+ *  saved  : device; x (T x d of type dt) when saved_is_codes == 0, else the checkpoint's codes of
+ *           format `fmt` with their scales.
+ *  scales : device, the checkpoint's scales (NULL for x).
+ *  mean   : device, T FP32, the forward pass's (NULL for a checkpoint, which needs none).
+ *  rstd   : device, T FP32, the forward pass's.
+ *  gamma  : device, d FP32, nullable (1).
+ *  dgamma, dbeta : device, d FP32, each nullable.  Sums over tokens are FP32, in an order fixed
+ *           by the shape and the context: equal calls give equal bits.
+ *  ws     : gift_act_workspace_bytes(GIFT_OP_LAYERNORM_BACKWARD, dt, T, d, d) bytes (may be NULL
+ *           when dgamma and dbeta both are).
+ * INVALID_ARG: a null dy, saved, rstd or dx, a missing mean or scales, T or d < 1, a bad type or
+ * format, a workspace too small.  d_status: NONFINITE when a row's sums are not finite. */
+gift_status gift_layernorm_backward(gift_ctx *ctx, const void *dy, gift_dtype dt, int T, int d, const void *saved,
+                                    int saved_is_codes, const void *scales, gift_format fmt, const float *mean,
+                                    const float *rstd, const float *gamma, void *dx, float *dgamma, float *dbeta,
+                                    void *ws, size_t ws_bytes, int *d_status, cudaStream_t stream);
+
+/* A linear layer's weight gradient from its input's 8-bit checkpoint: dW = delta^T v (not divided
+ * by T), v the checkpoint's values, and the bias gradient db = sum_t delta.  For a checkpoint of a
+ * norm's n the layer's input was gamma n + beta: with gamma (and beta)
+ *   dW[o][i] = gamma[i] sum_t delta[t][o] n[t][i] + beta[i] db[o].
+ * Products are exact (an FP32 delta enters as three BF16 terms); sums are FP32, rounded to
+ * nearest at least every 256 tokens, in an order fixed by the shape and the context.
+ *  delta  : device, T x d_out of type delta_dt.
+ *  codes, scales : the checkpoint (T x d_in, format fmt).
+ *  gamma, beta   : device, d_in FP32, each nullable (1 and 0).
+ *  dW     : device, d_out x d_in FP32: gift_encode's W.
+ *  db     : device, d_out FP32, nullable.
+ *  ws     : gift_act_workspace_bytes(GIFT_OP_WEIGHT_GRAD, delta_dt, T, d_out, d_in) bytes.
+ * INVALID_ARG: a null delta, codes, scales, dW or ws, T, d_out or d_in < 1, a bad type or format,
+ * a workspace too small.  d_status: TIMEOUT. */
+gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_dt, const void *codes,
+                             const void *scales, gift_format fmt, int T, int d_out, int d_in, const float *gamma,
+                             const float *beta, float *dW, float *db, void *ws, size_t ws_bytes, int *d_status,
+                             cudaStream_t stream);
 
 #ifdef __cplusplus
 }
