@@ -1313,6 +1313,8 @@ bool valid_extent(int n) { return n >= 1 && n <= kMaxExtent; }
 struct ActWs {
   float *part = nullptr;    // slice partials of the sums over tokens
   float *db = nullptr;      // weight gradient: db when only the call itself needs it
+  float *slices = nullptr;  // sums of token slices
+  uint8_t *delta = nullptr, *codes = nullptr;   // operands with aligned rows
   size_t bytes = 0;
 };
 
@@ -1322,11 +1324,12 @@ ActWs act_layout(void *base, const gift_ctx *ctx, gift_op op, gift_dtype dt, int
   if (op == GIFT_OP_LAYERNORM_BACKWARD) {
     w.part = c.take<float>(norm_part_floats(T, d_in));
   } else {
-    Launch L{};
-    L.sms = ctx->sms;
-    const WeightGradWs g = weight_grad_layout(L, dt == GIFT_DT_BF16, T, d_out, d_in);
+    const WeightGradWs g = weight_grad_layout(ctx->sms, dt == GIFT_DT_BF16, T, d_out, d_in);
     w.part = c.take<float>(g.part_floats);
     w.db = c.take<float>(d_out);
+    w.slices = c.take<float>(g.slice_floats);
+    w.delta = c.take<uint8_t>(g.delta_bytes);
+    w.codes = c.take<uint8_t>(g.code_bytes);
   }
   w.bytes = c.off + kAlign;
   return w;
@@ -1441,6 +1444,9 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
   a.db = db;
   a.part = w.part;
   a.db_ws = w.db;
+  a.slices = w.slices;
+  a.delta_ws = w.delta;
+  a.code_ws = w.codes;
   CK(launch_weight_grad(mk(ctx, d_status, stream), fmt8(fmt), delta_dt == GIFT_DT_BF16, a));
   return GIFT_OK;
 }

@@ -358,6 +358,9 @@ cudaError_t launch_col_sums(const Launch &L, const void *x, bool bf16, int T, in
 // ---- weight_grad.cu -------------------------------------------------------------------------
 struct WeightGradWs {
   size_t part_floats = 0;      // column-sum partials of db
+  size_t slice_floats = 0;     // sums of the token slices
+  size_t delta_bytes = 0;      // delta's BF16 terms, or its copy with aligned rows
+  size_t code_bytes = 0;       // the codes' copy with aligned rows
 };
 struct WeightGrad {
   const void *delta;
@@ -366,8 +369,11 @@ struct WeightGrad {
   const float *gamma, *beta;   // nullable
   float *dW, *db;              // db nullable
   float *part, *db_ws;         // workspace: column-sum partials, db when the caller wants none
+  float *slices;
+  void *delta_ws;
+  uint8_t *code_ws;
 };
-WeightGradWs weight_grad_layout(const Launch &L, bool bf16, int T, int d_out, int d_in);
+WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in);
 cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const WeightGrad &a);
 
 }  // namespace gift

@@ -1,98 +1,706 @@
-// Weight gradient from an 8-bit checkpoint, dW = delta^T v: FP32 SIMT.
+// Weight gradient from an 8-bit checkpoint, dW = delta^T v, on the 5th-generation tensor cores.
 //
-// 64 x 64 tiles of dW, 16 tokens per step through shared memory, 4 x 4 outputs per thread; the
-// running sums are folded into the totals every 256 tokens, so that rounding grows with the
-// number of folds and not with T.
+// dW[o][i] = sum_t delta[t][o] v[t][i] contracts over tokens, the slow axis of both operands.  The
+// kernel forms D[i][o] with the checkpoint as the A operand in tensor memory (M = i) and delta as
+// the B operand in shared memory (N = o, read MN-major as TMA wrote it: no transposed copy of
+// either).  A value code * 2^k is exact in BF16, so the products are exact and the only roundings
+// are the sums'.
+//
+// A pair of CTAs (a cluster of two SMs, cta_group::2) owns a 256 (i) x 128 NH (o) tile and walks
+// its tokens 64 at a time; each CTA holds 128 of the i and half of the o columns:
+//   warp 12      TMA: the 64 x 128 code tile and 64 x 64 delta boxes of a stage;
+//   warp 14      the 64 scale bytes of the stage's tokens (one group of 128 columns: the CTA's)
+//                as BF16 powers of two;
+//   warps 8-11   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
+//                tokens of one column, which is tcgen05.st's 16x256b layout; the code's bits placed
+//                in the BF16 fields times 2^120 (2^112 for E5M2) and times 2^k, both exact;
+//   warp 13      the pair's first CTA issues 256 x 128 x 16 MMAs;
+//   warps 0-7    fold: the tensor core truncates its sums, so a segment of at most 256 tokens goes
+//                into one of three 128-column accumulators and is added to FP32 registers to
+//                nearest; the two halves of a tile change accumulators half a segment apart, so
+//                that one is always being drained while two are being filled.
+// What bounds it: the MMA rate; the operand bytes a pair needs from L2 are 48 per clock and SM.
+// Few tiles: the tokens are cut into slices whose sums a second kernel adds in order.
+// Every mbarrier wait is clock-bounded and reports GIFT_ERR_TIMEOUT.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "act.cuh"
 #include "kernels.cuh"
+#include "tc.cuh"
 
 namespace gift {
 
 namespace {
 
-constexpr int kWTile = 64, kWStep = 16, kWThreads = 256, kWFold = 256;
+constexpr int kK = 64;                       // tokens of a stage
+constexpr int kBox = kK * 128;               // bytes of one 128-byte-wide box: codes, or 64 BF16 columns
+constexpr int kAStages = 4;                  // A operand slots in tensor memory, 32 columns each
+constexpr int kACol = 384;                   // after three 128-column accumulators
+constexpr int kFoldWarps = 8, kDeqWarps = 4;
+constexpr int kThreads = 512;
+constexpr int kSmemBudget = 200 * 1024;
+constexpr long long kWait = 4000000000LL;
 
-template <int F, typename E>
-__global__ void __launch_bounds__(kWThreads) k_weight_grad_simt(const E *__restrict__ delta,
-                                                                const uint8_t *__restrict__ codes,
-                                                                const uint8_t *__restrict__ scales, int T, int d_out,
-                                                                int d_in, const float *__restrict__ gamma,
-                                                                const float *__restrict__ beta,
-                                                                const float *__restrict__ db, float *__restrict__ dW) {
-  __shared__ float sa[kWStep][kWTile], sb[kWStep][kWTile];
-  const int i0 = blockIdx.x * kWTile, o0 = blockIdx.y * kWTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int groups = (d_in + kActGroup - 1) / kActGroup;
-  float acc[4][4] = {}, tot[4][4] = {};
-  for (int t0 = 0; t0 < T; t0 += kWStep) {
-#pragma unroll
-    for (int j = 0; j < kWStep * kWTile / kWThreads; ++j) {
-      const int q = threadIdx.x + j * kWThreads, r = q / kWTile, c = q % kWTile, t = t0 + r;
-      sa[r][c] = (t < T && o0 + c < d_out) ? ld1(delta + (size_t)t * d_out + o0 + c) : 0.0f;
-      sb[r][c] = (t < T && i0 + c < d_in)
-                     ? dec_fp8<F>(codes[(size_t)t * d_in + i0 + c]) *
-                           act_scale(scales[(size_t)t * groups + (i0 + c) / kActGroup])
-                     : 0.0f;
+template <int NH, int TERMS>
+struct Cfg {
+  static constexpr int stage_bytes = kBox * (1 + NH * TERMS);
+  static constexpr int stages = kSmemBudget / stage_bytes > 8 ? 8 : kSmemBudget / stage_bytes;
+  static constexpr int period = TERMS == 1 ? 4 : 2;   // stages of a segment: at most 256 tokens
+  static constexpr int smem = stages * stage_bytes + 1024;
+};
+
+struct Params {
+  int T, d_out, d_in, groups;
+  int nk;                      // stages over all tokens
+  int mt, nt, slices, items;
+  const uint8_t *scales;
+  const float *gamma, *beta, *db;   // nullable; only with one slice
+  float *out;                  // dW, or the slices' sums (slice s at s d_out d_in)
+};
+
+// One work item: an output tile and a range of stages.
+struct Item {
+  int i0, o0, slice, k0, nk;
+  __device__ __forceinline__ Item(const Params &P, int item, int on) {
+    const int tiles = P.mt * P.nt, tile = item % tiles;
+    slice = item / tiles;
+    i0 = tile % P.mt * 256;
+    o0 = tile / P.mt * on;
+    k0 = (int)((long long)P.nk * slice / P.slices);
+    nk = (int)((long long)P.nk * (slice + 1) / P.slices) - k0;
+  }
+};
+
+// The accumulators free to start a segment, first freed first.  The MMA warp and the fold warps
+// each keep one and see the same sequence.
+struct FreeList {
+  uint32_t q = 0x210;   // 4 bits per entry
+  int n = 3;
+  __device__ __forceinline__ int pop() {
+    const int b = (int)(q & 15u);
+    q >>= 4;
+    --n;
+    return b;
+  }
+  __device__ __forceinline__ void push(int b) { q |= (uint32_t)b << (4 * n++); }
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// arrive on the pair's first CTA's copy of `bar`
+__device__ __forceinline__ void arrive_first(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(tc::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          tc::smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void alloc_pair(uint32_t *dst) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n"
+               "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::"r"(tc::smem_u32(dst))
+               : "memory");
+}
+__device__ __forceinline__ void dealloc_pair(uint32_t taddr) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(taddr) : "memory");
+}
+// D (+)= A[tmem] B[smem], one 256 x 128 x 16 step over both CTAs
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on both CTAs' `bar` once the MMAs issued so far have completed
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+          tc::smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// MN-major, 128-byte swizzle, one atom (64 BF16) wide: 8-token groups 1024 bytes apart
+__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t kIdesc = tc::idesc_bf16(256, 128) | (1u << 16);   // B is MN-major
+
+__device__ __forceinline__ void ldmatrix_t8(uint32_t addr, uint32_t *r) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  __nv_bfloat162 x, y;
+  *reinterpret_cast<uint32_t *>(&x) = a;
+  *reinterpret_cast<uint32_t *>(&y) = b;
+  x = __hmul2(x, y);
+  return *reinterpret_cast<uint32_t *>(&x);
+}
+// Two codes, in the upper byte of each half of x, times 2^k (s: BF16 pair).  The code's exponent
+// and mantissa bits moved to the BF16 fields stand for its value over 2^120 (2^112 for E5M2;
+// BF16 subnormals cover the code's); both products are exact.
+template <int F>
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x, uint32_t s) {
+  constexpr uint32_t mask = F == FMT_E4M3 ? 0x07F007F0u : 0x0FE00FE0u;
+  constexpr uint32_t up = F == FMT_E4M3 ? 0x7B807B80u : 0x77807780u;
+  const uint32_t bits = ((x >> (F == FMT_E4M3 ? 4 : 3)) & mask) | (x & 0x80008000u);
+  return mul_bf16x2(mul_bf16x2(bits, up), s);
+}
+
+template <int F, int NH, int TERMS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_weight_grad(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap tm_codes,
+                  const __grid_constant__ CUtensorMap tm_delta, int *status) {
+  using C = Cfg<NH, TERMS>;
+  constexpr int kStages = C::stages, kPeriod = C::period;
+  extern __shared__ uint8_t dsm[];
+  uint8_t *sm = reinterpret_cast<uint8_t *>(((uintptr_t)dsm + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t full[kStages], empty[kStages], ready[kAStages], aempty[kAStages], dfull[3], dempty[3];
+  __shared__ __align__(16) uint16_t scale_sh[kStages][kK];
+  __shared__ uint32_t tmem_sh;
+  __shared__ volatile int failed;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp == 0) alloc_pair(&tmem_sh);
+  if (tid == 32) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full[s], 2);
+      tc::mbar_init(&empty[s], 1);
     }
-    __syncthreads();
+    for (int s = 0; s < kAStages; ++s) {
+      tc::mbar_init(&ready[s], 2 * kDeqWarps);
+      tc::mbar_init(&aempty[s], 1);
+    }
+    for (int b = 0; b < 3; ++b) {
+      tc::mbar_init(&dfull[b], 1);
+      tc::mbar_init(&dempty[b], 2 * kFoldWarps);
+    }
+    tc::fence_mbar_init();
+    failed = 0;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_sh;
+
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (failed) return false;
+    const long long t0 = clock64();
+    while (!try_wait_cluster(bar, parity)) {
+      if (clock64() - t0 > kWait) {
+        failed = 1;
+        set_status(status, GIFT_ERR_TIMEOUT);
+        return false;
+      }
+    }
+    return true;
+  };
+
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    if (warp == 12 && lane == 0) {
+      // ---------------- TMA ----------------
+      int issued[kStages] = {};
+      uint32_t g = 0;
+      bool ok = true;
+      for (int it = pair; it < P.items && ok; it += pairs) {
+        const Item w(P, it, 128 * NH);
+        for (int j = 0; j < w.nk; ++j, ++g) {
+          const uint32_t s = g % kStages;
+          if (!(ok = wait(&empty[s], ((g / kStages) & 1) ^ 1))) break;
+          uint8_t *st = sm + s * C::stage_bytes;
+          const int t = (w.k0 + j) * kK;
+          tc::mbar_arrive_expect_tx(&full[s], C::stage_bytes);
+          tc::tma_load_2d(st, &tm_codes, w.i0 + 128 * rank, t, &full[s]);
 #pragma unroll
-    for (int r = 0; r < kWStep; ++r)
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(sa[r][ty + 16 * u], sb[r][tx + 16 * v], acc[u][v]);
-    __syncthreads();
-    if ((t0 + kWStep) % kWFold == 0 || t0 + kWStep >= T) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          tot[u][v] += acc[u][v];
-          acc[u][v] = 0.0f;
+          for (int b = 0; b < NH * TERMS; ++b)   // box b: half b / TERMS, term b % TERMS
+            tma_load_3d(st + (1 + b) * kBox, &tm_delta, w.o0 + 128 * (b / TERMS) + 64 * rank, t, b % TERMS, &full[s]);
+          ++issued[s];
         }
+      }
+      if (failed) {   // leave no copy in flight
+        for (int s = 0; s < kStages; ++s)
+          if (issued[s]) tc::mbar_wait_bounded(&full[s], (uint32_t)((issued[s] - 1) & 1), kWait);
+      } else {        // nor an arrival of the MMA's commits
+        for (uint32_t s = 0; s < kStages; ++s)
+          if (issued[s]) wait(&empty[s], (uint32_t)((issued[s] - 1) & 1));
+        for (uint32_t a = 0; a < kAStages; ++a)
+          if (g > a) wait(&aempty[a], ((g - 1 - a) / kAStages) & 1);
+      }
+    } else if (warp == 13 && lane == 0 && rank == 0) {
+      // ---------------- MMA ----------------
+      FreeList fl;
+      uint32_t g = 0, used[3] = {0, 0, 0};
+      int cur[2] = {0, 0};
+      bool ok = true;
+      for (int it = pair; it < P.items && ok; it += pairs) {
+        const Item w(P, it, 128 * NH);
+        for (int j = 0; j < w.nk && ok; ++j, ++g) {
+          const uint32_t s = g % kStages, a = g % kAStages;
+          const int at = j % kPeriod;
+          if (!(ok = wait(&ready[a], (g / kAStages) & 1))) break;
+          tc::fence_after_sync();
+          const uint32_t b0 = tc::smem_u32(sm + s * C::stage_bytes) + kBox, a0 = tmem + kACol + 32 * a;
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const bool fresh = j == 0 || at == h * (kPeriod / 2);
+            if (fresh) {
+              if (j) fl.push(cur[h]);
+              const int b = fl.pop();
+              cur[h] = b;
+              const uint32_t n = b == 0 ? used[0]++ : b == 1 ? used[1]++ : used[2]++;
+              if (!(ok = wait(&dempty[b], (n & 1) ^ 1))) break;
+              tc::fence_after_sync();
+            }
+            const uint32_t d = tmem + 128 * cur[h];
+#pragma unroll
+            for (int k = 0; k < kK / 16; ++k)
+#pragma unroll
+              for (int p = 0; p < TERMS; ++p)
+                mma_pair(d, a0 + 8 * k, sdesc_mnmajor(b0 + (h * TERMS + p) * kBox + 2048 * k), kIdesc,
+                         fresh && k == 0 && p == 0 ? 0u : 1u);
+          }
+          if (!ok) break;
+          commit_pair(&empty[s]);
+          commit_pair(&aempty[a]);
+          if (j + 1 == w.nk) {
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+              commit_pair(&dfull[cur[h]]);
+              fl.push(cur[h]);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < NH; ++h)
+              if ((j + 1) % kPeriod == h * (kPeriod / 2)) commit_pair(&dfull[cur[h]]);
+          }
+        }
+      }
+    } else if (warp == 14) {
+      // ---------------- scales: loads run four stages ahead ----------------
+      constexpr int kAhead = 4;
+      uint32_t ring[kAhead];
+      int ia = pair, ja = 0;   // the stage whose scales are loaded next
+      Item w(P, min(ia, P.items - 1), 128 * NH);
+      auto load = [&]() -> uint32_t {
+        uint32_t v = 0x3F803F80u;
+        if (ia < P.items) {
+          const int c0 = w.i0 + 128 * rank, t = (w.k0 + ja) * kK + 2 * lane;
+          if (c0 < P.d_in) {
+            const uint8_t *p = P.scales + (size_t)t * P.groups + c0 / kActGroup;
+            const uint32_t x = t < P.T ? p[0] : 127u, y = t + 1 < P.T ? p[P.groups] : 127u;
+            v = (x == kActBad ? 0x7FC0u : x << 7) | (y == kActBad ? 0x7FC0u : y << 7) << 16;
+          }
+          if (++ja == w.nk) {
+            ja = 0;
+            ia += pairs;
+            w = Item(P, min(ia, P.items - 1), 128 * NH);
+          }
+        }
+        return v;
+      };
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) ring[u] = load();
+      int total = 0;
+      for (int it = pair; it < P.items; it += pairs) total += Item(P, it, 128 * NH).nk;
+      bool ok = true;
+      for (int g0 = 0; g0 < total && ok; g0 += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const uint32_t g = (uint32_t)(g0 + u), s = g % kStages;
+          if ((int)g >= total || !ok) break;
+          if (!(ok = wait(&empty[s], ((g / kStages) & 1) ^ 1))) break;
+          reinterpret_cast<uint32_t *>(scale_sh[s])[lane] = ring[u];
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&full[s]);
+          ring[u] = load();
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;\n");
+    // ---------------- codes -> BF16 in tensor memory ----------------
+    const int q = warp & 3;
+    uint32_t g = 0;
+    bool ok = true;
+    for (int it = pair; it < P.items && ok; it += pairs) {
+      const Item w(P, it, 128 * NH);
+      for (int j = 0; j < w.nk; ++j, ++g) {
+        const uint32_t s = g % kStages, a = g % kAStages;
+        if (!(ok = wait(&full[s], (g / kStages) & 1))) break;
+        __syncwarp();
+        const uint32_t base = tc::smem_u32(sm + s * C::stage_bytes);
+        const int r = lane & 15;
+        uint32_t v[2][16];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int m = 0; m < 4; m += 2) {
+            const int row = 16 * (m + (lane >> 4)) + r;
+            ldmatrix_t8(base + row * 128 + (((2 * q + hh) ^ (row & 7)) << 4), &v[hh][2 * m]);
+          }
+        uint2 sc[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) sc[m] = *reinterpret_cast<const uint2 *>(&scale_sh[s][16 * m + 4 * (lane & 3)]);
+        if (!(ok = wait(&aempty[a], ((g / kAStages) & 1) ^ 1))) break;
+        __syncwarp();
+        tc::fence_after_sync();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t x[16];
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t c = v[hh][2 * m + u];
+              x[4 * m + 2 * u] = codes_to_bf16<F>(__byte_perm(c, 0, 0x1404), sc[m].x);
+              x[4 * m + 2 * u + 1] = codes_to_bf16<F>(__byte_perm(c, 0, 0x3424), sc[m].y);
+            }
+          tmem_st_16x256b_x4(tmem + kACol + 32 * a + ((uint32_t)(32 * q + 16 * hh) << 16), x);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_first(&ready[a]);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
+    // ---------------- fold and store (this warp: 32 rows i, 64 of each half's columns) ----------------
+    const int q = warp & 3, c = warp >> 2;
+    const uint32_t off = ((uint32_t)(32 * q) << 16) + 64 * c;
+    FreeList fl;
+    uint32_t used[3] = {0, 0, 0};
+    int cur[2] = {0, 0};
+    bool ok = true;
+    for (int it = pair; it < P.items && ok; it += pairs) {
+      const Item w(P, it, 128 * NH);
+      float acc[NH][64];
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int e = 0; e < 64; ++e) acc[h][e] = 0.0f;
+      // add half h's finished segment and hand its accumulator back
+      auto fold = [&](int h, float(&sum)[64]) {
+        const int b = cur[h];
+        const uint32_t n = b == 0 ? used[0]++ : b == 1 ? used[1]++ : used[2]++;
+        if (!(ok = wait(&dfull[b], n & 1))) return;
+        __syncwarp();
+        tc::fence_after_sync();
+#pragma unroll
+        for (int e = 0; e < 64; e += 16) {
+          uint32_t raw[16];
+          tc::tmem_ld16_nowait(tmem + off + 128 * b + e, raw);
+          tc::tmem_wait_ld16(raw);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) sum[e + x] += __uint_as_float(raw[x]);
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_first(&dempty[b]);
+      };
+#pragma unroll
+      for (int h = 0; h < NH; ++h) cur[h] = fl.pop();
+      for (int j = 1; j <= w.nk && ok; ++j) {
+        const bool last = j == w.nk;
+        const int at = j % kPeriod;
+        if (last || at == 0) {
+          fold(0, acc[0]);
+          fl.push(cur[0]);
+          if (!last) cur[0] = fl.pop();
+        }
+        if (NH == 2 && (last || at == kPeriod / 2)) {
+          fold(1, acc[NH - 1]);
+          fl.push(cur[1]);
+          if (!last) cur[1] = fl.pop();
+        }
+      }
+      if (!ok) break;
+      const int i = w.i0 + 128 * rank + 32 * q + lane;
+      if (i < P.d_in) {
+        const float ga = P.gamma ? P.gamma[i] : 1.0f, be = P.beta ? P.beta[i] : 0.0f;
+        float *out = P.out + (size_t)w.slice * P.d_out * P.d_in + i;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const int o = w.o0 + 128 * h + 64 * c;
+          float *p = out + (size_t)o * P.d_in;
+#pragma unroll
+          for (int e = 0; e < 64; ++e, p += P.d_in) {
+            if (o + e >= P.d_out) break;
+            float v = acc[h][e] * ga;
+            if (P.beta) v = fmaf(be, P.db[o + e], v);
+            *p = v;
+          }
+        }
+      }
     }
   }
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int o = o0 + ty + 16 * u;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int i = i0 + tx + 16 * v;
-      if (o >= d_out || i >= d_in) continue;
-      float w = gamma ? tot[u][v] * gamma[i] : tot[u][v];
-      if (beta) w = fmaf(beta[i], db[o], w);
-      dW[(size_t)o * d_in + i] = w;
-    }
+
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  cluster_sync();   // the peer no longer arrives on this CTA's barriers, and its MMAs are done
+  if (warp == 0) {
+    tc::fence_after_sync();
+    dealloc_pair(tmem);
   }
 }
 
-template <int F, typename E>
-cudaError_t simt(const Launch &L, const WeightGrad &a, const float *db) {
-  const dim3 grid((a.d_in + kWTile - 1) / kWTile, (a.d_out + kWTile - 1) / kWTile);
-  k_weight_grad_simt<F, E><<<grid, kWThreads, 0, L.stream>>>(static_cast<const E *>(a.delta), a.codes, a.scales, a.T,
-                                                             a.d_out, a.d_in, a.gamma, a.beta, db, a.dW);
+// dW = gamma * (the slices' sums in order) + beta db
+__global__ void __launch_bounds__(256) k_join_slices(const float *__restrict__ part, int slices, int d_out, int d_in,
+                                                     const float *__restrict__ gamma, const float *__restrict__ beta,
+                                                     const float *__restrict__ db, float *__restrict__ dW) {
+  const size_t n = (size_t)d_out * d_in, step = (size_t)gridDim.x * 256;
+  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < n; e += step) {
+    float v = part[e];
+    for (int s = 1; s < slices; ++s) v += part[s * n + e];
+    if (gamma || beta) {
+      const size_t o = e / d_in;
+      const int i = (int)(e - o * d_in);
+      if (gamma) v *= gamma[i];
+      if (beta) v = fmaf(beta[i], db[o], v);
+    }
+    dW[e] = v;
+  }
+}
+
+// FP32 delta as three BF16 terms (exact), planes of T rows of ld columns
+__global__ void __launch_bounds__(256) k_delta_terms(const float *__restrict__ x, int T, int d, int ld,
+                                                     uint16_t *__restrict__ out) {
+  const size_t n = (size_t)T * d, plane = (size_t)T * ld, step = (size_t)gridDim.x * 256;
+  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < n; e += step) {
+    const size_t t = e / d, at = t * ld + (e - t * d);
+    tc::bf16_split3(x[e], out[at], out[plane + at], out[2 * plane + at]);
+  }
+}
+
+// Rows of `bytes` bytes at any alignment -> rows of ld (a multiple of 16) bytes, 16 at a time
+__global__ void __launch_bounds__(256) k_repitch(const uint8_t *__restrict__ src, int T, size_t bytes, size_t ld,
+                                                 uint8_t *__restrict__ dst) {
+  const size_t per = (bytes + 15) / 16, n = (size_t)T * per, step = (size_t)gridDim.x * 256;
+  const uintptr_t lo = (uintptr_t)src, hi = lo + (size_t)T * bytes;
+  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < n; e += step) {
+    const size_t t = e / per, c = (e - t * per) * 16;
+    const uintptr_t a = lo + t * bytes + c, w0 = a & ~(uintptr_t)3;
+    const int sh = (int)(a & 3) * 8;
+    uint32_t w[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      const uintptr_t p = w0 + 4 * k;
+      w[k] = 0;
+      if (p >= lo && p + 4 <= hi) {
+        w[k] = *reinterpret_cast<const uint32_t *>(p);
+      } else {
+        for (int b = 0; b < 4; ++b)
+          if (p + b >= lo && p + b < hi) w[k] |= (uint32_t)*reinterpret_cast<const uint8_t *>(p + b) << (8 * b);
+      }
+    }
+    uint4 v;
+    v.x = __funnelshift_r(w[0], w[1], sh);
+    v.y = __funnelshift_r(w[1], w[2], sh);
+    v.z = __funnelshift_r(w[2], w[3], sh);
+    v.w = __funnelshift_r(w[3], w[4], sh);
+    *reinterpret_cast<uint4 *>(dst + t * ld + c) = v;   // past the row's end: never read (the tensor map's width)
+  }
+}
+
+// ---- host ---------------------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// `planes` matrices of rows x cols elements, rows `pitch` bytes apart, read in 128-byte x 64-row boxes
+bool boxes(CUtensorMap *m, bool bf16, const void *base, int rows, int cols, size_t pitch, int planes) {
+  const auto enc = encoder();
+  if (!enc) return false;
+  const int rank = bf16 ? 3 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {pitch, pitch * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {bf16 ? 64u : 128u, (cuuint32_t)kK, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
+             const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t pad16(size_t bytes) { return (bytes + 15) / 16 * 16; }
+
+struct Plan {
+  int nh, mt, nt, nk, slices, pairs;
+};
+
+// Tiles of 256 x 256, or 256 x 128 where one half covers d_out.  Tokens are cut into slices where
+// the tiles alone leave pairs of SMs idle: the count with the least waves x (stages of an item +
+// its start and end, about 4 stages) + the slices' own traffic (written and read once, about
+// 4 MB per stage time of 0.27 us at 256 columns; the join kernel's launch about 8 stages).
+Plan plan_of(int sms, int T, int d_out, int d_in) {
+  Plan p;
+  p.nh = d_out <= 128 ? 1 : 2;
+  p.mt = (d_in + 255) / 256;
+  p.nt = (d_out + 128 * p.nh - 1) / (128 * p.nh);
+  p.nk = (T + kK - 1) / kK;
+  p.pairs = sms / 2 > 1 ? sms / 2 : 1;
+  const long long tiles = (long long)p.mt * p.nt;
+  const double traffic = 8.0 * d_out * d_in / 1.0e6;
+  p.slices = 1;
+  double best = 1e300;
+  for (int s = 1; s <= 64 && s <= p.nk; ++s) {
+    const long long waves = (tiles * s + p.pairs - 1) / p.pairs;
+    const double cost = (double)waves * ((p.nk + s - 1) / s + 4) + (s > 1 ? 8.0 + s * traffic : 0.0);
+    if (cost < best) {
+      best = cost;
+      p.slices = s;
+    }
+  }
+  return p;
+}
+
+template <int F, int NH, int TERMS>
+cudaError_t launch(const Launch &L, const Params &P, const CUtensorMap &tc_, const CUtensorMap &td, int pairs) {
+  using C = Cfg<NH, TERMS>;
+  const cudaError_t e = ensure_dynamic_smem<k_weight_grad<F, NH, TERMS>>(C::smem);
+  if (e != cudaSuccess) return e;
+  k_weight_grad<F, NH, TERMS><<<2 * (P.items < pairs ? P.items : pairs), kThreads, C::smem, L.stream>>>(P, tc_, td,
+                                                                                                       L.status);
   return cudaGetLastError();
+}
+
+template <int F>
+cudaError_t launch_fmt(const Launch &L, const Params &P, const CUtensorMap &tc_, const CUtensorMap &td, const Plan &p,
+                       bool bf16) {
+  if (bf16) return p.nh == 1 ? launch<F, 1, 1>(L, P, tc_, td, p.pairs) : launch<F, 2, 1>(L, P, tc_, td, p.pairs);
+  return p.nh == 1 ? launch<F, 1, 3>(L, P, tc_, td, p.pairs) : launch<F, 2, 3>(L, P, tc_, td, p.pairs);
+}
+
+int stream_grid(const Launch &L, size_t n) {
+  const size_t c = (n + 255) / 256, most = (size_t)L.sms * 8;
+  return (int)(c < most ? c : most);
 }
 
 }  // namespace
 
-WeightGradWs weight_grad_layout(const Launch &L, bool bf16, int T, int d_out, int d_in) {
-  (void)L; (void)bf16; (void)d_in;
+WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) {
   WeightGradWs w;
+  const Plan p = plan_of(sms, T, d_out, d_in);
   w.part_floats = col_part_floats(T, d_out);
+  w.slice_floats = p.slices > 1 ? (size_t)p.slices * d_out * d_in : 0;
+  // a BF16 delta and the codes are copied only when their rows are not 16-byte aligned, which the
+  // caller's pointers decide: room for both
+  w.delta_bytes = (size_t)T * pad16((size_t)d_out * 2) * (bf16 ? 1 : 3);
+  w.code_bytes = (size_t)T * pad16(d_in);
   return w;
 }
 
 cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const WeightGrad &a) {
+  const Plan p = plan_of(L.sms, a.T, a.d_out, a.d_in);
   const float *db = nullptr;
+  cudaError_t e;
   if (a.db || a.beta) {
     float *out = a.db ? a.db : a.db_ws;
-    const cudaError_t e = launch_col_sums(L, a.delta, bf16, a.T, a.d_out, a.part, out);
-    if (e != cudaSuccess) return e;
+    if ((e = launch_col_sums(L, a.delta, bf16, a.T, a.d_out, a.part, out)) != cudaSuccess) return e;
     db = out;
   }
-  if (fmt == FMT_E4M3) return bf16 ? simt<FMT_E4M3, __nv_bfloat16>(L, a, db) : simt<FMT_E4M3, float>(L, a, db);
-  return bf16 ? simt<FMT_E5M2, __nv_bfloat16>(L, a, db) : simt<FMT_E5M2, float>(L, a, db);
+  // operands with 16-byte aligned rows
+  const void *delta = a.delta;
+  size_t dpitch = (size_t)a.d_out * 2;
+  if (!bf16) {
+    dpitch = pad16(dpitch);
+    k_delta_terms<<<stream_grid(L, (size_t)a.T * a.d_out), 256, 0, L.stream>>>(
+        static_cast<const float *>(a.delta), a.T, a.d_out, (int)(dpitch / 2), static_cast<uint16_t *>(a.delta_ws));
+    delta = a.delta_ws;
+  } else if (dpitch % 16 || !aligned16(delta)) {
+    const size_t ld = pad16(dpitch);
+    k_repitch<<<stream_grid(L, (size_t)a.T * ld / 16), 256, 0, L.stream>>>(static_cast<const uint8_t *>(delta), a.T,
+                                                                           dpitch, ld,
+                                                                           static_cast<uint8_t *>(a.delta_ws));
+    delta = a.delta_ws;
+    dpitch = ld;
+  }
+  const uint8_t *codes = a.codes;
+  size_t cpitch = a.d_in;
+  if (cpitch % 16 || !aligned16(codes)) {
+    const size_t ld = pad16(cpitch);
+    k_repitch<<<stream_grid(L, (size_t)a.T * ld / 16), 256, 0, L.stream>>>(codes, a.T, cpitch, ld, a.code_ws);
+    codes = a.code_ws;
+    cpitch = ld;
+  }
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+  CUtensorMap tm_codes, tm_delta;
+  if (!boxes(&tm_codes, false, codes, a.T, a.d_in, cpitch, 1) ||
+      !boxes(&tm_delta, true, delta, a.T, a.d_out, dpitch, bf16 ? 1 : 3))
+    return cudaErrorInvalidValue;
+  Params P;
+  P.T = a.T;
+  P.d_out = a.d_out;
+  P.d_in = a.d_in;
+  P.groups = (a.d_in + kActGroup - 1) / kActGroup;
+  P.nk = p.nk;
+  P.mt = p.mt;
+  P.nt = p.nt;
+  P.slices = p.slices;
+  P.items = p.mt * p.nt * p.slices;
+  P.scales = a.scales;
+  const bool one = p.slices == 1;
+  P.gamma = one ? a.gamma : nullptr;
+  P.beta = one ? a.beta : nullptr;
+  P.db = one ? db : nullptr;
+  P.out = one ? a.dW : a.slices;
+  e = fmt == FMT_E4M3 ? launch_fmt<FMT_E4M3>(L, P, tm_codes, tm_delta, p, bf16)
+                      : launch_fmt<FMT_E5M2>(L, P, tm_codes, tm_delta, p, bf16);
+  if (e != cudaSuccess || one) return e;
+  k_join_slices<<<stream_grid(L, (size_t)a.d_out * a.d_in), 256, 0, L.stream>>>(a.slices, p.slices, a.d_out, a.d_in,
+                                                                               a.gamma, a.beta, db, a.dW);
+  return cudaGetLastError();
 }
 
 }  // namespace gift
