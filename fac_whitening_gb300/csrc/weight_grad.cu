@@ -8,13 +8,13 @@
 //
 // A pair of CTAs (a cluster of two SMs, cta_group::2) owns a 256 (i) x 128 NH (o) tile and walks
 // its tokens 64 at a time; each CTA holds 128 of the i and half of the o columns:
-//   warp 12      TMA: the 64 x 128 code tile and 64 x 64 delta boxes of a stage;
-//   warp 14      the 64 scale bytes of the stage's tokens (one group of 128 columns: the CTA's)
+//   warp 16      TMA: the 64 x 128 code tile and 64 x 64 delta boxes of a stage;
+//   warp 18      the 64 scale bytes of the stage's tokens (one group of 128 columns: the CTA's)
 //                as BF16 powers of two;
-//   warps 8-11   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
+//   warps 8-15   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
 //                tokens of one column, which is tcgen05.st's 16x256b layout; the code's bits placed
 //                in the BF16 fields times 2^120 (2^112 for E5M2) and times 2^k, both exact;
-//   warp 13      the pair's first CTA issues 256 x 128 x 16 MMAs;
+//   warp 17      the pair's first CTA issues 256 x 128 x 16 MMAs;
 //   warps 0-7    fold: the tensor core truncates its sums, so a segment of at most 256 tokens goes
 //                into one of three 128-column accumulators and is added to FP32 registers to
 //                nearest; the two halves of a tile change accumulators half a segment apart, so
@@ -37,8 +37,10 @@ constexpr int kK = 64;                       // tokens of a stage
 constexpr int kBox = kK * 128;               // bytes of one 128-byte-wide box: codes, or 64 BF16 columns
 constexpr int kAStages = 4;                  // A operand slots in tensor memory, 32 columns each
 constexpr int kACol = 384;                   // after three 128-column accumulators
-constexpr int kFoldWarps = 8, kDeqWarps = 4;
-constexpr int kThreads = 512;
+constexpr int kFoldWarps = 8;                // warps 0-7
+constexpr int kDeqWarp = 8;                  // warps 8-15: two groups of four, alternate stages
+constexpr int kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;
+constexpr int kThreads = 640;
 constexpr int kSmemBudget = 200 * 1024;
 constexpr long long kWait = 4000000000LL;
 
@@ -72,18 +74,55 @@ struct Item {
   }
 };
 
-// The accumulators free to start a segment, first freed first.  The MMA warp and the fold warps
-// each keep one and see the same sequence.
-struct FreeList {
-  uint32_t q = 0x210;   // 4 bits per entry
-  int n = 3;
-  __device__ __forceinline__ int pop() {
-    const int b = (int)(q & 15u);
-    q >>= 4;
-    --n;
-    return b;
+// Which of the three 128-column accumulators each half of the tile is summed in.  A half that
+// starts a segment takes the one that has been free longest; the MMA warp and the fold warps each
+// keep one of these and see the same sequence.
+template <int NH>
+struct Accumulators {
+  int cur0 = NH == 2 ? 1 : 2, cur1 = 2, spare = 0;
+  uint32_t phase = 0;   // bit b: uses of accumulator b so far, mod 2
+  __device__ __forceinline__ void start_tile() {
+    if (NH == 2) {
+      const int t = spare;
+      spare = cur1;
+      cur1 = cur0;
+      cur0 = t;
+    } else {
+      next(0);
+    }
   }
-  __device__ __forceinline__ void push(int b) { q |= (uint32_t)b << (4 * n++); }
+  __device__ __forceinline__ void next(int h) {
+    if (NH == 1) {
+      cur0 = cur0 == 2 ? 0 : cur0 + 1;
+    } else if (h == 0) {
+      const int t = cur0;
+      cur0 = spare;
+      spare = t;
+    } else {
+      const int t = cur1;
+      cur1 = spare;
+      spare = t;
+    }
+  }
+  __device__ __forceinline__ int cur(int h) const { return h == 0 ? cur0 : cur1; }
+  // the parity of accumulator b's current use, counted
+  __device__ __forceinline__ uint32_t use(int b) {
+    const uint32_t par = (phase >> b) & 1u;
+    phase ^= 1u << b;
+    return par;
+  }
+};
+
+// A slot of a ring and the parity of its current use.
+template <int N>
+struct Ring {
+  uint32_t at = 0, parity = 0;
+  __device__ __forceinline__ void advance() {
+    if (++at == N) {
+      at = 0;
+      parity ^= 1u;
+    }
+  }
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -94,24 +133,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
-// arrive on the pair's first CTA's copy of `bar`
+// Arrive on the pair's first CTA's copy of `bar`.  What the barrier orders is tensor memory (its
+// own fences) and TMA's writes, no thread's stores, so no cluster-wide release is asked for: one
+// (.release.cluster) held every arriving warp for hundreds of cycles, 531 -> 457 us for
+// 16384 x 1536 x 6144 without it.
 __device__ __forceinline__ void arrive_first(uint64_t *bar) {
   asm volatile(
       "{\n\t.reg .b32 ra;\n\t"
       "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(tc::smem_u32(bar))
+      "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(tc::smem_u32(bar))
       : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(tc::smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
   asm volatile(
@@ -128,13 +159,19 @@ __device__ __forceinline__ void alloc_pair(uint32_t *dst) {
 __device__ __forceinline__ void dealloc_pair(uint32_t taddr) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(taddr) : "memory");
 }
+// B: MN-major, 128-byte swizzle, one atom (64 BF16) wide, 8-token groups 1024 bytes apart.  The
+// descriptor's lower half holds the start address, the upper half is constant.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return (addr >> 4) | ((uint32_t)(kBox >> 4) << 16); }
+constexpr uint32_t kIdesc = tc::idesc_bf16(256, 128) | (1u << 16);   // B is MN-major
 // D (+)= A[tmem] B[smem], one 256 x 128 x 16 step over both CTAs
-__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t bdesc_lo, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], bd, %4, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(bdesc_lo), "n"(kDescHi), "n"(kIdesc), "r"(accumulate)
       : "memory");
 }
 // arrive on both CTAs' `bar` once the MMAs issued so far have completed
@@ -145,12 +182,16 @@ __device__ __forceinline__ void commit_pair(uint64_t *bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// MN-major, 128-byte swizzle, one atom (64 BF16) wide: 8-token groups 1024 bytes apart
-__device__ __forceinline__ uint64_t sdesc_mnmajor(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(kBox >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// one thread of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok));
+  return ok != 0;
 }
-constexpr uint32_t kIdesc = tc::idesc_bf16(256, 128) | (1u << 16);   // B is MN-major
 
 __device__ __forceinline__ void ldmatrix_t8(uint32_t addr, uint32_t *r) {
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
@@ -207,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kAStages; ++s) {
-      tc::mbar_init(&ready[s], 2 * kDeqWarps);
+      tc::mbar_init(&ready[s], 2 * 4);
       tc::mbar_init(&aempty[s], 1);
     }
     for (int b = 0; b < 3; ++b) {
@@ -224,10 +265,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_sh;
 
   auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (failed) return false;
+    if (tc::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!try_wait_cluster(bar, parity)) {
-      if (clock64() - t0 > kWait) {
+    while (!tc::mbar_try_wait(bar, parity)) {
+      if (failed || clock64() - t0 > kWait) {
         failed = 1;
         set_status(status, GIFT_ERR_TIMEOUT);
         return false;
@@ -236,100 +277,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-    if (warp == 12 && lane == 0) {
+  // registers: 96 per thread at launch (480 over the five groups of four warps), redistributed as
+  // 152 + 152 + 64 + 64 + 48
+  if (warp >= kTmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
+    if (warp == kTmaWarp && lane == 0) {
       // ---------------- TMA ----------------
-      int issued[kStages] = {};
-      uint32_t g = 0;
+      Ring<kStages> r;
+      uint32_t g = 0;   // stages so far
       bool ok = true;
       for (int it = pair; it < P.items && ok; it += pairs) {
         const Item w(P, it, 128 * NH);
-        for (int j = 0; j < w.nk; ++j, ++g) {
-          const uint32_t s = g % kStages;
-          if (!(ok = wait(&empty[s], ((g / kStages) & 1) ^ 1))) break;
-          uint8_t *st = sm + s * C::stage_bytes;
+        for (int j = 0; j < w.nk; ++j, ++g, r.advance()) {
+          if (!(ok = wait(&empty[r.at], r.parity ^ 1u))) break;
+          uint8_t *st = sm + r.at * C::stage_bytes;
+          uint64_t *bar = &full[r.at];
           const int t = (w.k0 + j) * kK;
-          tc::mbar_arrive_expect_tx(&full[s], C::stage_bytes);
-          tc::tma_load_2d(st, &tm_codes, w.i0 + 128 * rank, t, &full[s]);
+          tc::mbar_arrive_expect_tx(bar, C::stage_bytes);
+          tc::tma_load_2d(st, &tm_codes, w.i0 + 128 * rank, t, bar);
 #pragma unroll
           for (int b = 0; b < NH * TERMS; ++b)   // box b: half b / TERMS, term b % TERMS
-            tma_load_3d(st + (1 + b) * kBox, &tm_delta, w.o0 + 128 * (b / TERMS) + 64 * rank, t, b % TERMS, &full[s]);
-          ++issued[s];
+            tma_load_3d(st + (1 + b) * kBox, &tm_delta, w.o0 + 128 * (b / TERMS) + 64 * rank, t, b % TERMS, bar);
         }
       }
-      if (failed) {   // leave no copy in flight
-        for (int s = 0; s < kStages; ++s)
-          if (issued[s]) tc::mbar_wait_bounded(&full[s], (uint32_t)((issued[s] - 1) & 1), kWait);
-      } else {        // nor an arrival of the MMA's commits
-        for (uint32_t s = 0; s < kStages; ++s)
-          if (issued[s]) wait(&empty[s], (uint32_t)((issued[s] - 1) & 1));
-        for (uint32_t a = 0; a < kAStages; ++a)
-          if (g > a) wait(&aempty[a], ((g - 1 - a) / kAStages) & 1);
-      }
-    } else if (warp == 13 && lane == 0 && rank == 0) {
-      // ---------------- MMA ----------------
-      FreeList fl;
-      uint32_t g = 0, used[3] = {0, 0, 0};
-      int cur[2] = {0, 0};
+      // leave no copy in flight, nor an arrival of the MMAs' commits
+      for (uint32_t s = 0; s < kStages; ++s)
+        if (g > s) {
+          const uint32_t par = ((g - 1 - s) / kStages) & 1u;
+          if (failed) tc::mbar_wait_bounded(&full[s], par, kWait);
+          else wait(&empty[s], par);
+        }
+      for (uint32_t a = 0; a < kAStages; ++a)
+        if (g > a && !failed) wait(&aempty[a], ((g - 1 - a) / kAStages) & 1u);
+    } else if (warp == kMmaWarp && rank == 0) {
+      // ---------------- MMA: the whole warp walks the loop (its values stay in uniform registers,
+      // which the MMAs take), one elected thread issues ----------------
+      const bool one = elect_one();
+      const uint32_t b_first = desc_lo(tc::smem_u32(sm) + kBox);
+      Accumulators<NH> acc;
+      Ring<kStages> st;
+      Ring<kAStages> as;
       bool ok = true;
       for (int it = pair; it < P.items && ok; it += pairs) {
-        const Item w(P, it, 128 * NH);
-        for (int j = 0; j < w.nk && ok; ++j, ++g) {
-          const uint32_t s = g % kStages, a = g % kAStages;
-          const int at = j % kPeriod;
-          if (!(ok = wait(&ready[a], (g / kAStages) & 1))) break;
-          tc::fence_after_sync();
-          const uint32_t b0 = tc::smem_u32(sm + s * C::stage_bytes) + kBox, a0 = tmem + kACol + 32 * a;
+        const int nk = Item(P, it, 128 * NH).nk;
+        acc.start_tile();
+        for (int j = 0; j < nk; ++j) {
+          const int at = j & (kPeriod - 1);
+          if (!(ok = wait(&ready[as.at], as.parity))) break;
+          const uint32_t b0 = b_first + st.at * (C::stage_bytes >> 4), a0 = tmem + kACol + 32 * as.at;
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
             const bool fresh = j == 0 || at == h * (kPeriod / 2);
             if (fresh) {
-              if (j) fl.push(cur[h]);
-              const int b = fl.pop();
-              cur[h] = b;
-              const uint32_t n = b == 0 ? used[0]++ : b == 1 ? used[1]++ : used[2]++;
-              if (!(ok = wait(&dempty[b], (n & 1) ^ 1))) break;
-              tc::fence_after_sync();
+              if (j) acc.next(h);
+              const int b = acc.cur(h);
+              if (!(ok = wait(&dempty[b], acc.use(b) ^ 1u))) break;
             }
-            const uint32_t d = tmem + 128 * cur[h];
+            __syncwarp();
+            tc::fence_after_sync();
+            const uint32_t d = tmem + 128 * acc.cur(h);
+            if (one) {
 #pragma unroll
-            for (int k = 0; k < kK / 16; ++k)
+              for (int k = 0; k < kK / 16; ++k)
 #pragma unroll
-              for (int p = 0; p < TERMS; ++p)
-                mma_pair(d, a0 + 8 * k, sdesc_mnmajor(b0 + (h * TERMS + p) * kBox + 2048 * k), kIdesc,
-                         fresh && k == 0 && p == 0 ? 0u : 1u);
+                for (int p = 0; p < TERMS; ++p)
+                  mma_pair(d, a0 + 8 * k, b0 + (h * TERMS + p) * (kBox >> 4) + 128 * k,
+                           k == 0 && p == 0 ? (fresh ? 0u : 1u) : 1u);
+            }
           }
           if (!ok) break;
-          commit_pair(&empty[s]);
-          commit_pair(&aempty[a]);
-          if (j + 1 == w.nk) {
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-              commit_pair(&dfull[cur[h]]);
-              fl.push(cur[h]);
-            }
-          } else {
-#pragma unroll
-            for (int h = 0; h < NH; ++h)
-              if ((j + 1) % kPeriod == h * (kPeriod / 2)) commit_pair(&dfull[cur[h]]);
+          const bool last = j + 1 == nk;
+          const int nat = (j + 1) & (kPeriod - 1);
+          if (one) {
+            commit_pair(&empty[st.at]);
+            commit_pair(&aempty[as.at]);
+            if (last || nat == 0) commit_pair(&dfull[acc.cur(0)]);
+            if (NH == 2 && (last || nat == kPeriod / 2)) commit_pair(&dfull[acc.cur(1)]);
           }
+          st.advance();
+          as.advance();
         }
       }
-    } else if (warp == 14) {
+    } else if (warp == kScaleWarp) {
       // ---------------- scales: loads run four stages ahead ----------------
       constexpr int kAhead = 4;
-      uint32_t ring[kAhead];
+      uint32_t rx[kAhead], ry[kAhead];   // the bytes of tokens 2 lane and 2 lane + 1, as loaded
       int ia = pair, ja = 0;   // the stage whose scales are loaded next
       Item w(P, min(ia, P.items - 1), 128 * NH);
-      auto load = [&]() -> uint32_t {
-        uint32_t v = 0x3F803F80u;
+      auto load = [&](uint32_t &x, uint32_t &y) {
+        x = y = 127u;   // past the tokens: 1, so that zero codes stay zero
         if (ia < P.items) {
           const int c0 = w.i0 + 128 * rank, t = (w.k0 + ja) * kK + 2 * lane;
           if (c0 < P.d_in) {
             const uint8_t *p = P.scales + (size_t)t * P.groups + c0 / kActGroup;
-            const uint32_t x = t < P.T ? p[0] : 127u, y = t + 1 < P.T ? p[P.groups] : 127u;
-            v = (x == kActBad ? 0x7FC0u : x << 7) | (y == kActBad ? 0x7FC0u : y << 7) << 16;
+            if (t < P.T) x = p[0];
+            if (t + 1 < P.T) y = p[P.groups];
           }
           if (++ja == w.nk) {
             ja = 0;
@@ -337,62 +379,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             w = Item(P, min(ia, P.items - 1), 128 * NH);
           }
         }
-        return v;
       };
+      auto bf16 = [](uint32_t b) { return b == kActBad ? 0x7FC0u : b << 7; };   // 2^(b - 127), or NaN
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) ring[u] = load();
+      for (int u = 0; u < kAhead; ++u) load(rx[u], ry[u]);
       int total = 0;
       for (int it = pair; it < P.items; it += pairs) total += Item(P, it, 128 * NH).nk;
       bool ok = true;
+      Ring<kStages> r;
       for (int g0 = 0; g0 < total && ok; g0 += kAhead) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const uint32_t g = (uint32_t)(g0 + u), s = g % kStages;
-          if ((int)g >= total || !ok) break;
-          if (!(ok = wait(&empty[s], ((g / kStages) & 1) ^ 1))) break;
-          reinterpret_cast<uint32_t *>(scale_sh[s])[lane] = ring[u];
+        for (int u = 0; u < kAhead; ++u, r.advance()) {
+          if (g0 + u >= total || !ok) break;
+          if (!(ok = wait(&empty[r.at], r.parity ^ 1u))) break;
+          reinterpret_cast<uint32_t *>(scale_sh[r.at])[lane] = bf16(rx[u]) | bf16(ry[u]) << 16;
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&full[s]);
-          ring[u] = load();
+          if (lane == 0) tc::mbar_arrive(&full[r.at]);
+          load(rx[u], ry[u]);
         }
       }
     }
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;\n");
+  } else if (warp >= kDeqWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
     // ---------------- codes -> BF16 in tensor memory ----------------
-    const int q = warp & 3;
-    uint32_t g = 0;
-    bool ok = true;
-    for (int it = pair; it < P.items && ok; it += pairs) {
-      const Item w(P, it, 128 * NH);
-      for (int j = 0; j < w.nk; ++j, ++g) {
-        const uint32_t s = g % kStages, a = g % kAStages;
-        if (!(ok = wait(&full[s], (g / kStages) & 1))) break;
+    const int q = warp & 3, group = (warp - kDeqWarp) >> 2;
+    int total = 0;
+    for (int it = pair; it < P.items; it += pairs) total += Item(P, it, 128 * NH).nk;
+    Ring<kStages> st;
+    Ring<kAStages> as;
+    for (int g = 0; g < total; ++g, st.advance(), as.advance()) {
+      if ((g & 1) == group) {
+        const uint32_t s = st.at, a = as.at;
+        if (!wait(&full[s], st.parity) || !wait(&aempty[a], as.parity ^ 1u)) break;
         __syncwarp();
+        tc::fence_after_sync();
         const uint32_t base = tc::smem_u32(sm + s * C::stage_bytes);
-        const int r = lane & 15;
-        uint32_t v[2][16];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-          for (int m = 0; m < 4; m += 2) {
-            const int row = 16 * (m + (lane >> 4)) + r;
-            ldmatrix_t8(base + row * 128 + (((2 * q + hh) ^ (row & 7)) << 4), &v[hh][2 * m]);
-          }
         uint2 sc[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) sc[m] = *reinterpret_cast<const uint2 *>(&scale_sh[s][16 * m + 4 * (lane & 3)]);
-        if (!(ok = wait(&aempty[a], ((g / kAStages) & 1) ^ 1))) break;
-        __syncwarp();
-        tc::fence_after_sync();
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          uint32_t x[16];
+          uint32_t v[8], x[16];
+#pragma unroll
+          for (int m = 0; m < 4; m += 2) {
+            const int row = 16 * m + lane;
+            ldmatrix_t8(base + row * 128 + (((2 * q + hh) ^ (row & 7)) << 4), &v[2 * m]);
+          }
 #pragma unroll
           for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const uint32_t c = v[hh][2 * m + u];
+              const uint32_t c = v[2 * m + u];
               x[4 * m + 2 * u] = codes_to_bf16<F>(__byte_perm(c, 0, 0x1404), sc[m].x);
               x[4 * m + 2 * u + 1] = codes_to_bf16<F>(__byte_perm(c, 0, 0x3424), sc[m].y);
             }
@@ -405,26 +442,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
     // ---------------- fold and store (this warp: 32 rows i, 64 of each half's columns) ----------------
     const int q = warp & 3, c = warp >> 2;
     const uint32_t off = ((uint32_t)(32 * q) << 16) + 64 * c;
-    FreeList fl;
-    uint32_t used[3] = {0, 0, 0};
-    int cur[2] = {0, 0};
+    Accumulators<NH> acc;
     bool ok = true;
     for (int it = pair; it < P.items && ok; it += pairs) {
       const Item w(P, it, 128 * NH);
-      float acc[NH][64];
+      float sum[NH][64];
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int e = 0; e < 64; ++e) acc[h][e] = 0.0f;
+        for (int e = 0; e < 64; ++e) sum[h][e] = 0.0f;
       // add half h's finished segment and hand its accumulator back
-      auto fold = [&](int h, float(&sum)[64]) {
-        const int b = cur[h];
-        const uint32_t n = b == 0 ? used[0]++ : b == 1 ? used[1]++ : used[2]++;
-        if (!(ok = wait(&dfull[b], n & 1))) return;
+      auto fold = [&](int h, float(&to)[64]) {
+        const int b = acc.cur(h);
+        if (!(ok = wait(&dfull[b], acc.use(b)))) return;
         __syncwarp();
         tc::fence_after_sync();
 #pragma unroll
@@ -433,26 +467,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc::tmem_ld16_nowait(tmem + off + 128 * b + e, raw);
           tc::tmem_wait_ld16(raw);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) sum[e + x] += __uint_as_float(raw[x]);
+          for (int x = 0; x < 16; ++x) to[e + x] += __uint_as_float(raw[x]);
         }
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive_first(&dempty[b]);
       };
-#pragma unroll
-      for (int h = 0; h < NH; ++h) cur[h] = fl.pop();
+      acc.start_tile();
       for (int j = 1; j <= w.nk && ok; ++j) {
         const bool last = j == w.nk;
-        const int at = j % kPeriod;
+        const int at = j & (kPeriod - 1);
         if (last || at == 0) {
-          fold(0, acc[0]);
-          fl.push(cur[0]);
-          if (!last) cur[0] = fl.pop();
+          fold(0, sum[0]);
+          if (!last) acc.next(0);
         }
-        if (NH == 2 && (last || at == kPeriod / 2)) {
-          fold(1, acc[NH - 1]);
-          fl.push(cur[1]);
-          if (!last) cur[1] = fl.pop();
+        if (NH == 2 && ok && (last || at == kPeriod / 2)) {
+          fold(1, sum[NH - 1]);
+          if (!last) acc.next(1);
         }
       }
       if (!ok) break;
@@ -467,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 64; ++e, p += P.d_in) {
             if (o + e >= P.d_out) break;
-            float v = acc[h][e] * ga;
+            float v = sum[h][e] * ga;
             if (P.beta) v = fmaf(be, P.db[o + e], v);
             *p = v;
           }
