@@ -14,7 +14,7 @@
 //   warps 8-15   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
 //                tokens of one column, which is tcgen05.st's 16x256b layout; the code's bits placed
 //                in the BF16 fields times 2^120 (2^112 for E5M2) and times 2^k, both exact;
-//   warp 17      the pair's first CTA issues 256 x 128 x 16 MMAs;
+//   warps 17, 19 the pair's first CTA issues 256 x 128 x 16 MMAs, a warp for each half of the tile;
 //   warps 0-7    fold: the tensor core truncates its sums, so a segment of at most 256 tokens goes
 //                into one of three 128-column accumulators and is added to FP32 registers to
 //                nearest; the two halves of a tile change accumulators half a segment apart, so
@@ -39,7 +39,7 @@ constexpr int kAStages = 4;                  // A operand slots in tensor memory
 constexpr int kACol = 384;                   // after three 128-column accumulators
 constexpr int kFoldWarps = 8;                // warps 0-7
 constexpr int kDeqWarp = 8;                  // warps 8-15: two groups of four, alternate stages
-constexpr int kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;
+constexpr int kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;   // and the second half's MMA warp, 19
 constexpr int kThreads = 640;
 constexpr int kSmemBudget = 200 * 1024;
 constexpr long long kWait = 4000000000LL;
@@ -214,15 +214,22 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   x = __hmul2(x, y);
   return *reinterpret_cast<uint32_t *>(&x);
 }
-// Two codes, in the upper byte of each half of x, times 2^k (s: BF16 pair).  The code's exponent
-// and mantissa bits moved to the BF16 fields stand for its value over 2^120 (2^112 for E5M2;
-// BF16 subnormals cover the code's); both products are exact.
+// Four codes c -> two BF16 pairs of code * 2^-120 (2^-112 for E5M2): the sign stays the top bit, the
+// exponent and mantissa bits move to the BF16 fields, a code's subnormals become BF16's.  Done on
+// all four at once (upper bytes, lower bytes), then interleaved.
 template <int F>
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x, uint32_t s) {
-  constexpr uint32_t mask = F == FMT_E4M3 ? 0x07F007F0u : 0x0FE00FE0u;
+__device__ __forceinline__ void spread_codes(uint32_t c, uint32_t &w0, uint32_t &w1) {
+  constexpr int down = F == FMT_E4M3 ? 4 : 3;
+  constexpr uint32_t top = F == FMT_E4M3 ? 0x07070707u : 0x0F0F0F0Fu, low = F == FMT_E4M3 ? 0xF0F0F0F0u : 0xE0E0E0E0u;
+  const uint32_t hi = ((c >> down) & top) | (c & 0x80808080u), lo = (c << (8 - down)) & low;
+  w0 = __byte_perm(lo, hi, 0x5140);
+  w1 = __byte_perm(lo, hi, 0x7362);
+}
+// times 2^120 (2^112), then times the tokens' scales: both exact
+template <int F>
+__device__ __forceinline__ uint32_t scale_codes(uint32_t w, uint32_t s) {
   constexpr uint32_t up = F == FMT_E4M3 ? 0x7B807B80u : 0x77807780u;
-  const uint32_t bits = ((x >> (F == FMT_E4M3 ? 4 : 3)) & mask) | (x & 0x80008000u);
-  return mul_bf16x2(mul_bf16x2(bits, up), s);
+  return mul_bf16x2(mul_bf16x2(w, up), s);
 }
 
 template <int F, int NH, int TERMS>
@@ -233,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   constexpr int kStages = C::stages, kPeriod = C::period;
   extern __shared__ uint8_t dsm[];
   uint8_t *sm = reinterpret_cast<uint8_t *>(((uintptr_t)dsm + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[kStages], empty[kStages], ready[kAStages], aempty[kAStages], dfull[3], dempty[3];
+  __shared__ uint64_t full[kStages], empty[kStages], ready[kAStages], dfull[3], dempty[3];
   __shared__ __align__(16) uint16_t scale_sh[kStages][kK];
   __shared__ uint32_t tmem_sh;
   __shared__ volatile int failed;
@@ -245,12 +252,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 32) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&full[s], 2);
-      tc::mbar_init(&empty[s], 1);
+      tc::mbar_init(&empty[s], NH);
     }
-    for (int s = 0; s < kAStages; ++s) {
-      tc::mbar_init(&ready[s], 2 * 4);
-      tc::mbar_init(&aempty[s], 1);
-    }
+    for (int s = 0; s < kAStages; ++s) tc::mbar_init(&ready[s], 2 * 4);
     for (int b = 0; b < 3; ++b) {
       tc::mbar_init(&dfull[b], 1);
       tc::mbar_init(&dempty[b], 2 * kFoldWarps);
@@ -307,13 +311,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (failed) tc::mbar_wait_bounded(&full[s], par, kWait);
           else wait(&empty[s], par);
         }
-      for (uint32_t a = 0; a < kAStages; ++a)
-        if (g > a && !failed) wait(&aempty[a], ((g - 1 - a) / kAStages) & 1u);
-    } else if (warp == kMmaWarp && rank == 0) {
-      // ---------------- MMA: the whole warp walks the loop (its values stay in uniform registers,
-      // which the MMAs take), one elected thread issues ----------------
+    } else if ((warp == kMmaWarp || (NH == 2 && warp == kMmaWarp + 2)) && rank == 0) {
+      // ---------------- MMA, a warp per half of the tile: the whole warp walks the loop (its values
+      // stay in uniform registers, which the MMAs take), one elected thread issues.  A warp's waits
+      // and commits cost about as much as its half's MMAs, so two warps keep the queue full ----------------
       const bool one = elect_one();
-      const uint32_t b_first = desc_lo(tc::smem_u32(sm) + kBox);
+      const int half = (warp - kMmaWarp) >> 1;
+      const uint32_t b_first = desc_lo(tc::smem_u32(sm) + kBox) + half * TERMS * (kBox >> 4);
       Accumulators<NH> acc;
       Ring<kStages> st;
       Ring<kAStages> as;
@@ -324,35 +328,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = 0; j < nk; ++j) {
           const int at = j & (kPeriod - 1);
           if (!(ok = wait(&ready[as.at], as.parity))) break;
-          const uint32_t b0 = b_first + st.at * (C::stage_bytes >> 4), a0 = tmem + kACol + 32 * as.at;
+          // both halves' changes of accumulator are followed and waited for: each phase is seen once
 #pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const bool fresh = j == 0 || at == h * (kPeriod / 2);
-            if (fresh) {
+          for (int h = 0; h < NH; ++h)
+            if (j == 0 || at == h * (kPeriod / 2)) {
               if (j) acc.next(h);
               const int b = acc.cur(h);
-              if (!(ok = wait(&dempty[b], acc.use(b) ^ 1u))) break;
+              ok = ok && wait(&dempty[b], acc.use(b) ^ 1u);
             }
-            __syncwarp();
-            tc::fence_after_sync();
-            const uint32_t d = tmem + 128 * acc.cur(h);
-            if (one) {
-#pragma unroll
-              for (int k = 0; k < kK / 16; ++k)
-#pragma unroll
-                for (int p = 0; p < TERMS; ++p)
-                  mma_pair(d, a0 + 8 * k, b0 + (h * TERMS + p) * (kBox >> 4) + 128 * k,
-                           k == 0 && p == 0 ? (fresh ? 0u : 1u) : 1u);
-            }
-          }
           if (!ok) break;
-          const bool last = j + 1 == nk;
-          const int nat = (j + 1) & (kPeriod - 1);
+          __syncwarp();
+          tc::fence_after_sync();
+          const bool fresh = j == 0 || at == half * (kPeriod / 2);
+          const bool done = j + 1 == nk || ((j + 1) & (kPeriod - 1)) == half * (kPeriod / 2);
+          const uint32_t b0 = b_first + st.at * (C::stage_bytes >> 4), a0 = tmem + kACol + 32 * as.at;
+          const int mine = acc.cur(half);
+          const uint32_t d = tmem + 128 * mine;
           if (one) {
+#pragma unroll
+            for (int k = 0; k < kK / 16; ++k)
+#pragma unroll
+              for (int p = 0; p < TERMS; ++p)
+                mma_pair(d, a0 + 8 * k, b0 + p * (kBox >> 4) + 128 * k, k == 0 && p == 0 ? (fresh ? 0u : 1u) : 1u);
             commit_pair(&empty[st.at]);
-            commit_pair(&aempty[as.at]);
-            if (last || nat == 0) commit_pair(&dfull[acc.cur(0)]);
-            if (NH == 2 && (last || nat == kPeriod / 2)) commit_pair(&dfull[acc.cur(1)]);
+            if (done) commit_pair(&dfull[mine]);
           }
           st.advance();
           as.advance();
@@ -405,33 +404,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3, group = (warp - kDeqWarp) >> 2;
     int total = 0;
     for (int it = pair; it < P.items; it += pairs) total += Item(P, it, 128 * NH).nk;
-    Ring<kStages> st;
-    Ring<kAStages> as;
-    for (int g = 0; g < total; ++g, st.advance(), as.advance()) {
-      if ((g & 1) == group) {
-        const uint32_t s = st.at, a = as.at;
-        if (!wait(&full[s], st.parity) || !wait(&aempty[a], as.parity ^ 1u)) break;
+    Ring<kStages> st, freed;   // freed: the stage kAStages ago, whose MMAs read the same slot
+    for (int g = 0; g < total; ++g, st.advance()) {
+      const bool mine = (g & 1) == group;
+      const uint32_t s = st.at, a = (uint32_t)g & (kAStages - 1);
+      if (mine && !wait(&full[s], st.parity)) break;
+      // With kStages <= kAStages the stage just filled was freed by those MMAs or later ones.  (Its
+      // barrier may then be a phase further, which a parity cannot tell: it is not asked.)
+      if (kStages > kAStages && g >= kAStages) {
+        if (mine && !wait(&empty[freed.at], freed.parity)) break;
+        freed.advance();
+      }
+      if (mine) {
         __syncwarp();
         tc::fence_after_sync();
         const uint32_t base = tc::smem_u32(sm + s * C::stage_bytes);
+        uint32_t v[2][8];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int m = 0; m < 4; m += 2) {
+            const int row = 16 * m + lane;
+            ldmatrix_t8(base + row * 128 + (((2 * q + hh) ^ (row & 7)) << 4), &v[hh][2 * m]);
+          }
         uint2 sc[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) sc[m] = *reinterpret_cast<const uint2 *>(&scale_sh[s][16 * m + 4 * (lane & 3)]);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          uint32_t v[8], x[16];
-#pragma unroll
-          for (int m = 0; m < 4; m += 2) {
-            const int row = 16 * m + lane;
-            ldmatrix_t8(base + row * 128 + (((2 * q + hh) ^ (row & 7)) << 4), &v[2 * m]);
-          }
+          uint32_t x[16];
 #pragma unroll
           for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const uint32_t c = v[2 * m + u];
-              x[4 * m + 2 * u] = codes_to_bf16<F>(__byte_perm(c, 0, 0x1404), sc[m].x);
-              x[4 * m + 2 * u + 1] = codes_to_bf16<F>(__byte_perm(c, 0, 0x3424), sc[m].y);
+              uint32_t w0, w1;
+              spread_codes<F>(v[hh][2 * m + u], w0, w1);
+              x[4 * m + 2 * u] = scale_codes<F>(w0, sc[m].x);
+              x[4 * m + 2 * u + 1] = scale_codes<F>(w1, sc[m].y);
             }
           tmem_st_16x256b_x4(tmem + kACol + 32 * a + ((uint32_t)(32 * q + 16 * hh) << 16), x);
         }
