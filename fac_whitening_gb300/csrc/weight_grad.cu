@@ -8,13 +8,13 @@
 //
 // A pair of CTAs (a cluster of two SMs, cta_group::2) owns a 256 (i) x 128 NH (o) tile and walks
 // its tokens 64 at a time; each CTA holds 128 of the i and half of the o columns:
-//   warp 16      TMA: the 64 x 128 code tile and 64 x 64 delta boxes of a stage;
-//   warp 18      the 64 scale bytes of the stage's tokens (one group of 128 columns: the CTA's)
+//   warp 24      TMA: the 64 x 128 code tile and 64 x 64 delta boxes of a stage;
+//   warp 26      the 64 scale bytes of the stage's tokens (one group of 128 columns: the CTA's)
 //                as BF16 powers of two;
-//   warps 8-15   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
+//   warps 8-23   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
 //                tokens of one column, which is tcgen05.st's 16x256b layout; the code's bits placed
 //                in the BF16 fields times 2^120 (2^112 for E5M2) and times 2^k, both exact;
-//   warps 17, 19 the pair's first CTA issues 256 x 128 x 16 MMAs, a warp for each half of the tile;
+//   warps 25, 27 the pair's first CTA issues 256 x 128 x 16 MMAs, a warp for each half of the tile;
 //   warps 0-7    fold: the tensor core truncates its sums, so a segment of at most 256 tokens goes
 //                into one of three 128-column accumulators and is added to FP32 registers to
 //                nearest; the two halves of a tile change accumulators half a segment apart, so
@@ -38,9 +38,9 @@ constexpr int kBox = kK * 128;               // bytes of one 128-byte-wide box: 
 constexpr int kAStages = 4;                  // A operand slots in tensor memory, 32 columns each
 constexpr int kACol = 384;                   // after three 128-column accumulators
 constexpr int kFoldWarps = 8;                // warps 0-7
-constexpr int kDeqWarp = 8;                  // warps 8-15: two groups of four, alternate stages
-constexpr int kTmaWarp = 16, kMmaWarp = 17, kScaleWarp = 18;   // and the second half's MMA warp, 19
-constexpr int kThreads = 640;
+constexpr int kDeqWarp = 8, kDeqWarps = 16;  // warps 8-23: eight per stage, alternate stages
+constexpr int kTmaWarp = 24, kMmaWarp = 25, kScaleWarp = 26;   // and the second half's MMA warp, 27
+constexpr int kThreads = 896;
 constexpr int kSmemBudget = 200 * 1024;
 constexpr long long kWait = 4000000000LL;
 
@@ -254,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(&full[s], 2);
       tc::mbar_init(&empty[s], NH);
     }
-    for (int s = 0; s < kAStages; ++s) tc::mbar_init(&ready[s], 2 * 4);
+    for (int s = 0; s < kAStages; ++s) tc::mbar_init(&ready[s], kDeqWarps);   // half of them, of both CTAs
     for (int b = 0; b < 3; ++b) {
       tc::mbar_init(&dfull[b], 1);
       tc::mbar_init(&dempty[b], 2 * kFoldWarps);
@@ -281,10 +281,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return true;
   };
 
-  // registers: 96 per thread at launch (480 over the five groups of four warps), redistributed as
-  // 152 + 152 + 64 + 64 + 48
+  // registers: 72 per thread at launch (504 over the seven groups of four warps), redistributed as
+  // 2 x 152 + 5 x 40
   if (warp >= kTmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
     if (warp == kTmaWarp && lane == 0) {
       // ---------------- TMA ----------------
       Ring<kStages> r;
@@ -399,56 +399,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= kDeqWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-    // ---------------- codes -> BF16 in tensor memory ----------------
-    const int q = warp & 3, group = (warp - kDeqWarp) >> 2;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    // ---------------- codes -> BF16 in tensor memory: 16 of the CTA's rows i of every other stage ----------------
+    const int dw = warp - kDeqWarp, r0 = 32 * (dw & 3) + 16 * ((dw >> 2) & 1), turn = dw >> 3;
     int total = 0;
     for (int it = pair; it < P.items; it += pairs) total += Item(P, it, 128 * NH).nk;
+    const uint32_t mine = tc::smem_u32(sm) + lane * 128 + (((r0 >> 4) ^ (lane & 7)) << 4);
     Ring<kStages> st, freed;   // freed: the stage kAStages ago, whose MMAs read the same slot
     for (int g = 0; g < total; ++g, st.advance()) {
-      const bool mine = (g & 1) == group;
-      const uint32_t s = st.at, a = (uint32_t)g & (kAStages - 1);
-      if (mine && !wait(&full[s], st.parity)) break;
-      // With kStages <= kAStages the stage just filled was freed by those MMAs or later ones.  (Its
-      // barrier may then be a phase further, which a parity cannot tell: it is not asked.)
-      if (kStages > kAStages && g >= kAStages) {
-        if (mine && !wait(&empty[freed.at], freed.parity)) break;
-        freed.advance();
-      }
-      if (mine) {
+      const bool my_turn = (g & 1) == turn;
+      if (my_turn) {
+        const uint32_t s = st.at;
+        if (!wait(&full[s], st.parity)) break;
         __syncwarp();
-        tc::fence_after_sync();
-        const uint32_t base = tc::smem_u32(sm + s * C::stage_bytes);
-        uint32_t v[2][8];
+        uint32_t v[8];
+        ldmatrix_t8(mine + s * C::stage_bytes, v);
+        ldmatrix_t8(mine + s * C::stage_bytes + 32 * 128, v + 4);
+        uint32_t x[16];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
+        for (int m = 0; m < 4; ++m) {
+          const uint2 sc = *reinterpret_cast<const uint2 *>(&scale_sh[s][16 * m + 4 * (lane & 3)]);
 #pragma unroll
-          for (int m = 0; m < 4; m += 2) {
-            const int row = 16 * m + lane;
-            ldmatrix_t8(base + row * 128 + (((2 * q + hh) ^ (row & 7)) << 4), &v[hh][2 * m]);
+          for (int u = 0; u < 2; ++u) {
+            uint32_t w0, w1;
+            spread_codes<F>(v[2 * m + u], w0, w1);
+            x[4 * m + 2 * u] = scale_codes<F>(w0, sc.x);
+            x[4 * m + 2 * u + 1] = scale_codes<F>(w1, sc.y);
           }
-        uint2 sc[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) sc[m] = *reinterpret_cast<const uint2 *>(&scale_sh[s][16 * m + 4 * (lane & 3)]);
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t x[16];
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t w0, w1;
-              spread_codes<F>(v[hh][2 * m + u], w0, w1);
-              x[4 * m + 2 * u] = scale_codes<F>(w0, sc[m].x);
-              x[4 * m + 2 * u + 1] = scale_codes<F>(w1, sc[m].y);
-            }
-          tmem_st_16x256b_x4(tmem + kACol + 32 * a + ((uint32_t)(32 * q + 16 * hh) << 16), x);
         }
+        // With kStages <= kAStages the stage just filled was freed by those MMAs or later ones.  (Its
+        // barrier may then be a phase further, which a parity cannot tell: it is not asked.)
+        if (kStages > kAStages && g >= kAStages) {
+          if (!wait(&empty[freed.at], freed.parity)) break;
+          __syncwarp();
+        }
+        const uint32_t a = (uint32_t)g & (kAStages - 1);
+        tc::fence_after_sync();
+        tmem_st_16x256b_x4(tmem + kACol + 32 * a + ((uint32_t)r0 << 16), x);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive_first(&ready[a]);
       }
+      if (kStages > kAStages && g >= kAStages) freed.advance();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
