@@ -8,14 +8,14 @@
 //
 // A pair of CTAs (a cluster of two SMs, cta_group::2) owns a 256 (i) x 128 NH (o) tile and walks
 // its tokens 64 at a time; each CTA holds 128 of the i and half of the o columns:
-//   warp 24      TMA: the 64 x 128 code tile and 64 x 64 delta boxes of a stage;
-//   warp 26      the 64 scale bytes of the stage's tokens (one group of 128 columns: the CTA's)
+//   warp 0       TMA: the 64 x 128 code tile and 64 x 64 delta boxes of a stage;
+//   warp 2       the 64 scale bytes of the stage's tokens (one group of 128 columns: the CTA's)
 //                as BF16 powers of two;
-//   warps 8-23   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
+//   warps 4-19   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
 //                tokens of one column, which is tcgen05.st's 16x256b layout; the code's bits placed
 //                in the BF16 fields times 2^120 (2^112 for E5M2) and times 2^k, both exact;
-//   warps 25, 27 the pair's first CTA issues 256 x 128 x 16 MMAs, a warp for each half of the tile;
-//   warps 0-7    fold: the tensor core truncates its sums, so a segment of at most 256 tokens goes
+//   warps 1, 3   the pair's first CTA issues 256 x 128 x 16 MMAs, a warp for each half of the tile;
+//   warps 20-27  fold: the tensor core truncates its sums, so a segment of at most 256 tokens goes
 //                into one of three 128-column accumulators and is added to FP32 registers to
 //                nearest; the two halves of a tile change accumulators half a segment apart, so
 //                that one is always being drained while two are being filled.
@@ -24,6 +24,8 @@
 // Every mbarrier wait is clock-bounded and reports GIFT_ERR_TIMEOUT.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "act.cuh"
 #include "kernels.cuh"
@@ -35,42 +37,45 @@ namespace {
 
 constexpr int kK = 64;                       // tokens of a stage
 constexpr int kBox = kK * 128;               // bytes of one 128-byte-wide box: codes, or 64 BF16 columns
-constexpr int kAStages = 4;                  // A operand slots in tensor memory, 32 columns each
+constexpr int kGroup = 4;                    // stages of a group, and A operand slots in tensor memory
+                                             // (32 columns each): stage j of a group uses slot j
 constexpr int kACol = 384;                   // after three 128-column accumulators
-constexpr int kFoldWarps = 8;                // warps 0-7
-constexpr int kDeqWarp = 8, kDeqWarps = 16;  // warps 8-23: eight per stage, alternate stages
-constexpr int kTmaWarp = 24, kMmaWarp = 25, kScaleWarp = 26;   // and the second half's MMA warp, 27
+constexpr int kFoldWarps = 8;                // warps 20-27
+constexpr int kDeqWarp = 4, kDeqWarps = 16;  // warps 4-19: eight per stage, alternate stages
+constexpr int kFoldWarp = 20;
+constexpr int kTmaWarp = 0, kMmaWarp = 1, kScaleWarp = 2;   // and the second half's MMA warp, 3
 constexpr int kThreads = 896;
-constexpr int kSmemBudget = 200 * 1024;
 constexpr long long kWait = 4000000000LL;
 
 template <int NH, int TERMS>
 struct Cfg {
   static constexpr int stage_bytes = kBox * (1 + NH * TERMS);
-  static constexpr int stages = kSmemBudget / stage_bytes > 8 ? 8 : kSmemBudget / stage_bytes;
-  static constexpr int period = TERMS == 1 ? 4 : 2;   // stages of a segment: at most 256 tokens
-  static constexpr int smem = stages * stage_bytes + 1024;
+  static constexpr int rounds = TERMS == 1 ? 2 : 1;           // groups of stages in shared memory
+  static constexpr int stages = kGroup * rounds;
+  static constexpr int period = TERMS == 1 ? 4 : 2;           // stages of a segment: at most 256 tokens
+  static constexpr int smem = stages * stage_bytes + 1024;    // at most 225 KB
 };
 
 struct Params {
   int T, d_out, d_in, groups;
-  int nk;                      // stages over all tokens
+  int ng;                      // groups of stages (256 tokens) over all tokens; tokens past T are zeros
   int mt, nt, slices, items;
   const uint8_t *scales;
   const float *gamma, *beta, *db;   // nullable; only with one slice
   float *out;                  // dW, or the slices' sums (slice s at s d_out d_in)
 };
 
-// One work item: an output tile and a range of stages.
+// One work item: an output tile and a range of groups.
 struct Item {
-  int i0, o0, slice, k0, nk;
+  int i0, o0, slice, t0, ng;
   __device__ __forceinline__ Item(const Params &P, int item, int on) {
     const int tiles = P.mt * P.nt, tile = item % tiles;
     slice = item / tiles;
     i0 = tile % P.mt * 256;
     o0 = tile / P.mt * on;
-    k0 = (int)((long long)P.nk * slice / P.slices);
-    nk = (int)((long long)P.nk * (slice + 1) / P.slices) - k0;
+    const int g0 = (int)((long long)P.ng * slice / P.slices);
+    t0 = g0 * (kGroup * kK);
+    ng = (int)((long long)P.ng * (slice + 1) / P.slices) - g0;
   }
 };
 
@@ -105,6 +110,8 @@ struct Accumulators {
     }
   }
   __device__ __forceinline__ int cur(int h) const { return h == 0 ? cur0 : cur1; }
+  // what the next change takes
+  __device__ __forceinline__ int upcoming() const { return NH == 2 ? spare : cur0 == 2 ? 0 : cur0 + 1; }
   // the parity of accumulator b's current use, counted
   __device__ __forceinline__ uint32_t use(int b) {
     const uint32_t par = (phase >> b) & 1u;
@@ -113,16 +120,11 @@ struct Accumulators {
   }
 };
 
-// A slot of a ring and the parity of its current use.
-template <int N>
-struct Ring {
-  uint32_t at = 0, parity = 0;
-  __device__ __forceinline__ void advance() {
-    if (++at == N) {
-      at = 0;
-      parity ^= 1u;
-    }
-  }
+// Where the CTA's n-th group of stages lies in shared memory, and the parity of its barriers.
+template <int ROUNDS>
+struct Place {
+  uint32_t first, parity;
+  __device__ __forceinline__ explicit Place(uint32_t n) : first(n % ROUNDS * kGroup), parity(n / ROUNDS & 1u) {}
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -237,10 +239,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_weight_grad(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap tm_codes,
                   const __grid_constant__ CUtensorMap tm_delta, int *status) {
   using C = Cfg<NH, TERMS>;
-  constexpr int kStages = C::stages, kPeriod = C::period;
+  constexpr int kStages = C::stages, kPeriod = C::period, kRounds = C::rounds;
   extern __shared__ uint8_t dsm[];
   uint8_t *sm = reinterpret_cast<uint8_t *>(((uintptr_t)dsm + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[kStages], empty[kStages], ready[kAStages], dfull[3], dempty[3];
+  __shared__ uint64_t full[kStages], empty[kStages], ready[kGroup], dfull[3], dempty[3];
   __shared__ __align__(16) uint16_t scale_sh[kStages][kK];
   __shared__ uint32_t tmem_sh;
   __shared__ volatile int failed;
@@ -254,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(&full[s], 2);
       tc::mbar_init(&empty[s], NH);
     }
-    for (int s = 0; s < kAStages; ++s) tc::mbar_init(&ready[s], kDeqWarps);   // half of them, of both CTAs
+    for (int s = 0; s < kGroup; ++s) tc::mbar_init(&ready[s], kDeqWarps);   // half of them, of both CTAs
     for (int b = 0; b < 3; ++b) {
       tc::mbar_init(&dfull[b], 1);
       tc::mbar_init(&dempty[b], 2 * kFoldWarps);
@@ -283,134 +285,150 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   // registers: 72 per thread at launch (504 over the seven groups of four warps), redistributed as
   // 2 x 152 + 5 x 40
-  if (warp >= kTmaWarp) {
+  if (warp < kDeqWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
     if (warp == kTmaWarp && lane == 0) {
       // ---------------- TMA ----------------
-      Ring<kStages> r;
-      uint32_t g = 0;   // stages so far
+      uint32_t n = 0;   // groups so far
       bool ok = true;
       for (int it = pair; it < P.items && ok; it += pairs) {
         const Item w(P, it, 128 * NH);
-        for (int j = 0; j < w.nk; ++j, ++g, r.advance()) {
-          if (!(ok = wait(&empty[r.at], r.parity ^ 1u))) break;
-          uint8_t *st = sm + r.at * C::stage_bytes;
-          uint64_t *bar = &full[r.at];
-          const int t = (w.k0 + j) * kK;
-          tc::mbar_arrive_expect_tx(bar, C::stage_bytes);
-          tc::tma_load_2d(st, &tm_codes, w.i0 + 128 * rank, t, bar);
+        for (int gi = 0; gi < w.ng && ok; ++gi, ++n) {
+          const Place<kRounds> at(n);
+#pragma unroll 1
+          for (int j = 0; j < kGroup; ++j) {
+            uint64_t *bar = &full[at.first + j];
+            if (!(ok = wait(&empty[at.first + j], at.parity ^ 1u))) break;
+            uint8_t *st = sm + (at.first + j) * C::stage_bytes;
+            const int t = w.t0 + (gi * kGroup + j) * kK;
+            tc::mbar_arrive_expect_tx(bar, C::stage_bytes);
+            tc::tma_load_2d(st, &tm_codes, w.i0 + 128 * rank, t, bar);
 #pragma unroll
-          for (int b = 0; b < NH * TERMS; ++b)   // box b: half b / TERMS, term b % TERMS
-            tma_load_3d(st + (1 + b) * kBox, &tm_delta, w.o0 + 128 * (b / TERMS) + 64 * rank, t, b % TERMS, bar);
+            for (int b = 0; b < NH * TERMS; ++b)   // box b: half b / TERMS, term b % TERMS
+              tma_load_3d(st + (1 + b) * kBox, &tm_delta, w.o0 + 128 * (b / TERMS) + 64 * rank, t, b % TERMS, bar);
+          }
         }
       }
-      // leave no copy in flight, nor an arrival of the MMAs' commits
-      for (uint32_t s = 0; s < kStages; ++s)
-        if (g > s) {
-          const uint32_t par = ((g - 1 - s) / kStages) & 1u;
-          if (failed) tc::mbar_wait_bounded(&full[s], par, kWait);
-          else wait(&empty[s], par);
+      // leave no copy in flight, nor an arrival of the MMAs' commits: the last groups' stages
+      if (ok) {
+        for (uint32_t r = 0; r < kRounds && r < n; ++r) {
+          const Place<kRounds> at(n - 1 - r);
+          for (int j = 0; j < kGroup; ++j) wait(&empty[at.first + j], at.parity);
         }
+      } else {
+        for (int s = 0; s < kStages; ++s) {   // a phase that a copy is still to complete is the current one
+          tc::mbar_wait_bounded(&full[s], 0, kWait / 8);
+          tc::mbar_wait_bounded(&full[s], 1, kWait / 8);
+        }
+      }
     } else if ((warp == kMmaWarp || (NH == 2 && warp == kMmaWarp + 2)) && rank == 0) {
       // ---------------- MMA, a warp per half of the tile: the whole warp walks the loop (its values
       // stay in uniform registers, which the MMAs take), one elected thread issues.  A warp's waits
       // and commits cost about as much as its half's MMAs, so two warps keep the queue full ----------------
       const bool one = elect_one();
-      const int half = (warp - kMmaWarp) >> 1;
-      const uint32_t b_first = desc_lo(tc::smem_u32(sm) + kBox) + half * TERMS * (kBox >> 4);
+      const uint32_t b_first = desc_lo(tc::smem_u32(sm) + kBox), a0 = tmem + kACol;
       Accumulators<NH> acc;
-      Ring<kStages> st;
-      Ring<kAStages> as;
-      bool ok = true;
-      for (int it = pair; it < P.items && ok; it += pairs) {
-        const int nk = Item(P, it, 128 * NH).nk;
-        acc.start_tile();
-        for (int j = 0; j < nk; ++j) {
-          const int at = j & (kPeriod - 1);
-          if (!(ok = wait(&ready[as.at], as.parity))) break;
+      auto walk = [&](auto half_c) {
+        constexpr int half = decltype(half_c)::value;
+        uint32_t n = 0;
+        for (int it = pair; it < P.items; it += pairs) {
+          const int ng = Item(P, it, 128 * NH).ng;
+          acc.start_tile();
           // both halves' changes of accumulator are followed and waited for: each phase is seen once
 #pragma unroll
           for (int h = 0; h < NH; ++h)
-            if (j == 0 || at == h * (kPeriod / 2)) {
-              if (j) acc.next(h);
-              const int b = acc.cur(h);
-              ok = ok && wait(&dempty[b], acc.use(b) ^ 1u);
+            if (!wait(&dempty[acc.cur(h)], acc.use(acc.cur(h)) ^ 1u)) return;
+          for (int gi = 0; gi < ng; ++gi, ++n) {
+            const Place<kRounds> at(n);
+            const uint32_t b_group = b_first + at.first * (C::stage_bytes >> 4) + half * TERMS * (kBox >> 4);
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+              constexpr int kHalf = kPeriod / 2;
+              if (j % kPeriod == 0 && (j || gi)) {
+                acc.next(0);
+                if (!wait(&dempty[acc.cur(0)], acc.use(acc.cur(0)) ^ 1u)) return;
+              }
+              if (NH == 2 && j % kPeriod == kHalf) {
+                acc.next(1);
+                if (!wait(&dempty[acc.cur(1)], acc.use(acc.cur(1)) ^ 1u)) return;
+              }
+              const int mine = acc.cur(half);
+              const bool fresh = j % kPeriod == half * kHalf || (half == 1 && j == 0 && gi == 0);
+              if (!wait(&ready[j], n & 1u)) return;
+              __syncwarp();
+              tc::fence_after_sync();
+              if (one) {
+#pragma unroll
+                for (int k = 0; k < kK / 16; ++k)
+#pragma unroll
+                  for (int p = 0; p < TERMS; ++p)
+                    mma_pair(tmem + 128 * mine, a0 + 32 * j + 8 * k,
+                             b_group + j * (C::stage_bytes >> 4) + p * (kBox >> 4) + 128 * k,
+                             k == 0 && p == 0 ? (fresh ? 0u : 1u) : 1u);
+                commit_pair(&empty[at.first + j]);
+                if ((j + 1) % kPeriod == half * kHalf || (half == 1 && j + 1 == kGroup && gi + 1 == ng))
+                  commit_pair(&dfull[mine]);
+              }
             }
-          if (!ok) break;
-          __syncwarp();
-          tc::fence_after_sync();
-          const bool fresh = j == 0 || at == half * (kPeriod / 2);
-          const bool done = j + 1 == nk || ((j + 1) & (kPeriod - 1)) == half * (kPeriod / 2);
-          const uint32_t b0 = b_first + st.at * (C::stage_bytes >> 4), a0 = tmem + kACol + 32 * as.at;
-          const int mine = acc.cur(half);
-          const uint32_t d = tmem + 128 * mine;
-          if (one) {
-#pragma unroll
-            for (int k = 0; k < kK / 16; ++k)
-#pragma unroll
-              for (int p = 0; p < TERMS; ++p)
-                mma_pair(d, a0 + 8 * k, b0 + p * (kBox >> 4) + 128 * k, k == 0 && p == 0 ? (fresh ? 0u : 1u) : 1u);
-            commit_pair(&empty[st.at]);
-            if (done) commit_pair(&dfull[mine]);
-          }
-          st.advance();
-          as.advance();
-        }
-      }
-    } else if (warp == kScaleWarp) {
-      // ---------------- scales: loads run four stages ahead ----------------
-      constexpr int kAhead = 4;
-      uint32_t rx[kAhead], ry[kAhead];   // the bytes of tokens 2 lane and 2 lane + 1, as loaded
-      int ia = pair, ja = 0;   // the stage whose scales are loaded next
-      Item w(P, min(ia, P.items - 1), 128 * NH);
-      auto load = [&](uint32_t &x, uint32_t &y) {
-        x = y = 127u;   // past the tokens: 1, so that zero codes stay zero
-        if (ia < P.items) {
-          const int c0 = w.i0 + 128 * rank, t = (w.k0 + ja) * kK + 2 * lane;
-          if (c0 < P.d_in) {
-            const uint8_t *p = P.scales + (size_t)t * P.groups + c0 / kActGroup;
-            if (t < P.T) x = p[0];
-            if (t + 1 < P.T) y = p[P.groups];
-          }
-          if (++ja == w.nk) {
-            ja = 0;
-            ia += pairs;
-            w = Item(P, min(ia, P.items - 1), 128 * NH);
           }
         }
       };
+      if (warp == kMmaWarp) walk(std::integral_constant<int, 0>());
+      else walk(std::integral_constant<int, 1>());
+    } else if (warp == kScaleWarp) {
+      // ---------------- scales: a group's bytes are loaded while the group before it is handed out ----------------
+      uint32_t rx[kGroup], ry[kGroup];   // the bytes of tokens 2 lane and 2 lane + 1, as loaded
+      int ia = pair, ga = 0;             // the group that is loaded next
+      Item w(P, min(ia, P.items - 1), 128 * NH);
+      auto load = [&](int j) {
+        rx[j] = ry[j] = 127u;   // past the tokens: 1, so that zero codes stay zero
+        const int c0 = w.i0 + 128 * rank, t = w.t0 + (ga * kGroup + j) * kK + 2 * lane;
+        if (ia < P.items && c0 < P.d_in) {
+          const uint8_t *p = P.scales + (size_t)t * P.groups + c0 / kActGroup;
+          if (t < P.T) rx[j] = p[0];
+          if (t + 1 < P.T) ry[j] = p[P.groups];
+        }
+      };
       auto bf16 = [](uint32_t b) { return b == kActBad ? 0x7FC0u : b << 7; };   // 2^(b - 127), or NaN
+      auto next_group = [&]() {
+        if (++ga == w.ng) {
+          ga = 0;
+          ia += pairs;
+          w = Item(P, min(ia, P.items - 1), 128 * NH);
+        }
+      };
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) load(rx[u], ry[u]);
-      int total = 0;
-      for (int it = pair; it < P.items; it += pairs) total += Item(P, it, 128 * NH).nk;
+      for (int j = 0; j < kGroup; ++j) load(j);
       bool ok = true;
-      Ring<kStages> r;
-      for (int g0 = 0; g0 < total && ok; g0 += kAhead) {
+      for (uint32_t n = 0; ia < P.items && ok; ++n) {
+        const Place<kRounds> at(n);
+        next_group();
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u, r.advance()) {
-          if (g0 + u >= total || !ok) break;
-          if (!(ok = wait(&empty[r.at], r.parity ^ 1u))) break;
-          reinterpret_cast<uint32_t *>(scale_sh[r.at])[lane] = bf16(rx[u]) | bf16(ry[u]) << 16;
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&full[r.at]);
-          load(rx[u], ry[u]);
+        for (int j = 0; j < kGroup; ++j) {
+          ok = ok && wait(&empty[at.first + j], at.parity ^ 1u);
+          if (ok) {
+            reinterpret_cast<uint32_t *>(scale_sh[at.first + j])[lane] = bf16(rx[j]) | bf16(ry[j]) << 16;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&full[at.first + j]);
+            load(j);
+          }
         }
       }
     }
-  } else if (warp >= kDeqWarp) {
+  } else if (warp < kFoldWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
     // ---------------- codes -> BF16 in tensor memory: 16 of the CTA's rows i of every other stage ----------------
     const int dw = warp - kDeqWarp, r0 = 32 * (dw & 3) + 16 * ((dw >> 2) & 1), turn = dw >> 3;
-    int total = 0;
-    for (int it = pair; it < P.items; it += pairs) total += Item(P, it, 128 * NH).nk;
+    uint32_t total = 0;
+    for (int it = pair; it < P.items; it += pairs) total += (uint32_t)Item(P, it, 128 * NH).ng;
     const uint32_t mine = tc::smem_u32(sm) + lane * 128 + (((r0 >> 4) ^ (lane & 7)) << 4);
-    Ring<kStages> st, freed;   // freed: the stage kAStages ago, whose MMAs read the same slot
-    for (int g = 0; g < total; ++g, st.advance()) {
-      const bool my_turn = (g & 1) == turn;
-      if (my_turn) {
-        const uint32_t s = st.at;
-        if (!wait(&full[s], st.parity)) break;
+    bool ok = true;
+    for (uint32_t n = 0; n < total && ok; ++n) {
+      const Place<kRounds> at(n), before(n - 1);
+#pragma unroll
+      for (int jj = 0; jj < kGroup; jj += 2) {
+        const uint32_t j = jj + turn, s = at.first + j;
+        if (!(ok = wait(&full[s], at.parity))) break;
         __syncwarp();
         uint32_t v[8];
         ldmatrix_t8(mine + s * C::stage_bytes, v);
@@ -427,26 +445,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             x[4 * m + 2 * u + 1] = scale_codes<F>(w1, sc.y);
           }
         }
-        // With kStages <= kAStages the stage just filled was freed by those MMAs or later ones.  (Its
-        // barrier may then be a phase further, which a parity cannot tell: it is not asked.)
-        if (kStages > kAStages && g >= kAStages) {
-          if (!wait(&empty[freed.at], freed.parity)) break;
+        // the slot's last MMAs, a group ago, are done: with one group of stages, the stage just filled
+        // was freed by them (and its barrier may be a phase further by now: it is not asked)
+        if (kRounds > 1 && n > 0) {
+          if (!(ok = wait(&empty[before.first + j], before.parity))) break;
           __syncwarp();
         }
-        const uint32_t a = (uint32_t)g & (kAStages - 1);
         tc::fence_after_sync();
-        tmem_st_16x256b_x4(tmem + kACol + 32 * a + ((uint32_t)r0 << 16), x);
+        tmem_st_16x256b_x4(tmem + kACol + 32 * j + ((uint32_t)r0 << 16), x);
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) arrive_first(&ready[a]);
+        if (lane == 0) arrive_first(&ready[j]);
       }
-      if (kStages > kAStages && g >= kAStages) freed.advance();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
     // ---------------- fold and store (this warp: 32 rows i, 64 of each half's columns) ----------------
-    const int q = warp & 3, c = warp >> 2;
+    const int q = warp & 3, c = (warp - kFoldWarp) >> 2;
     const uint32_t off = ((uint32_t)(32 * q) << 16) + 64 * c;
     Accumulators<NH> acc;
     bool ok = true;
@@ -460,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // add half h's finished segment and hand its accumulator back
       auto fold = [&](int h, float(&to)[64]) {
         const int b = acc.cur(h);
-        if (!(ok = wait(&dfull[b], acc.use(b)))) return;
+        if (!(ok = ok && wait(&dfull[b], acc.use(b)))) return;
         __syncwarp();
         tc::fence_after_sync();
 #pragma unroll
@@ -476,18 +492,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive_first(&dempty[b]);
       };
       acc.start_tile();
-      for (int j = 1; j <= w.nk && ok; ++j) {
-        const bool last = j == w.nk;
-        const int at = j & (kPeriod - 1);
-        if (last || at == 0) {
-          fold(0, sum[0]);
-          if (!last) acc.next(0);
-        }
-        if (NH == 2 && ok && (last || at == kPeriod / 2)) {
+#pragma unroll 1
+      for (int seg = 1; seg <= w.ng * (kGroup / kPeriod) && ok; ++seg) {
+        if (NH == 2) {   // half 1 changes in the middle of half 0's segment, and at the end
           fold(1, sum[NH - 1]);
-          if (!last) acc.next(1);
+          acc.next(1);
         }
+        fold(0, sum[0]);
+        if (seg < w.ng * (kGroup / kPeriod)) acc.next(0);
       }
+      if (NH == 2) fold(1, sum[NH - 1]);
       if (!ok) break;
       const int i = w.i0 + 128 * rank + 32 * q + lane;
       if (i < P.d_in) {
@@ -608,27 +622,27 @@ bool boxes(CUtensorMap *m, bool bf16, const void *base, int rows, int cols, size
 size_t pad16(size_t bytes) { return (bytes + 15) / 16 * 16; }
 
 struct Plan {
-  int nh, mt, nt, nk, slices, pairs;
+  int nh, mt, nt, ng, slices, pairs;
 };
 
 // Tiles of 256 x 256, or 256 x 128 where one half covers d_out.  Tokens are cut into slices where
-// the tiles alone leave pairs of SMs idle: the count with the least waves x (stages of an item +
-// its start and end, about 4 stages) + the slices' own traffic (written and read once, about
-// 4 MB per stage time of 0.27 us at 256 columns; the join kernel's launch about 8 stages).
+// the tiles alone leave pairs of SMs idle: the count with the least waves x (groups of an item +
+// its start and end, about 1 group) + the slices' own traffic (written and read once, about 4 MB in
+// the time of a group, 1.1 us at 256 columns; the join kernel's launch about 2 groups).
 Plan plan_of(int sms, int T, int d_out, int d_in) {
   Plan p;
   p.nh = d_out <= 128 ? 1 : 2;
   p.mt = (d_in + 255) / 256;
   p.nt = (d_out + 128 * p.nh - 1) / (128 * p.nh);
-  p.nk = (T + kK - 1) / kK;
+  p.ng = (T + kGroup * kK - 1) / (kGroup * kK);
   p.pairs = sms / 2 > 1 ? sms / 2 : 1;
   const long long tiles = (long long)p.mt * p.nt;
-  const double traffic = 8.0 * d_out * d_in / 1.0e6;
+  const double traffic = 8.0 * d_out * d_in / 4.0e6;
   p.slices = 1;
   double best = 1e300;
-  for (int s = 1; s <= 64 && s <= p.nk; ++s) {
+  for (int s = 1; s <= 64 && s <= p.ng; ++s) {
     const long long waves = (tiles * s + p.pairs - 1) / p.pairs;
-    const double cost = (double)waves * ((p.nk + s - 1) / s + 4) + (s > 1 ? 8.0 + s * traffic : 0.0);
+    const double cost = (double)waves * ((p.ng + s - 1) / s + 1) + (s > 1 ? 2.0 + s * traffic : 0.0);
     if (cost < best) {
       best = cost;
       p.slices = s;
@@ -717,7 +731,7 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   P.d_out = a.d_out;
   P.d_in = a.d_in;
   P.groups = (a.d_in + kActGroup - 1) / kActGroup;
-  P.nk = p.nk;
+  P.ng = p.ng;
   P.mt = p.mt;
   P.nt = p.nt;
   P.slices = p.slices;
