@@ -1315,6 +1315,7 @@ struct ActWs {
   float *db = nullptr;      // weight gradient: db when only the call itself needs it
   float *slices = nullptr;  // sums of token slices
   uint8_t *delta = nullptr, *codes = nullptr;   // operands with aligned rows
+  uint16_t *scales = nullptr;                   // scales by group
   size_t bytes = 0;
 };
 
@@ -1330,6 +1331,7 @@ ActWs act_layout(void *base, const gift_ctx *ctx, gift_op op, gift_dtype dt, int
     w.slices = c.take<float>(g.slice_floats);
     w.delta = c.take<uint8_t>(g.delta_bytes);
     w.codes = c.take<uint8_t>(g.code_bytes);
+    w.scales = c.take<uint16_t>(g.scale_words);
   }
   w.bytes = c.off + kAlign;
   return w;
@@ -1447,6 +1449,7 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
   a.slices = w.slices;
   a.delta_ws = w.delta;
   a.code_ws = w.codes;
+  a.scale_ws = w.scales;
   CK(launch_weight_grad(mk(ctx, d_status, stream), fmt8(fmt), delta_dt == GIFT_DT_BF16, a));
   return GIFT_OK;
 }

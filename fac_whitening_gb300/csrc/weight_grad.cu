@@ -8,9 +8,8 @@
 //
 // A pair of CTAs (a cluster of two SMs, cta_group::2) owns a 256 (i) x 128 NH (o) tile and walks
 // its tokens 64 at a time; each CTA holds 128 of the i and half of the o columns:
-//   warp 0       TMA: the 64 x 128 code tile and 64 x 64 delta boxes of a stage;
-//   warp 2       the 64 scale bytes of the stage's tokens (one group of 128 columns: the CTA's)
-//                as BF16 powers of two;
+//   warps 0, 2   TMA: a stage's 64 x 128 code tile and its tokens' scales (one group of 128 columns:
+//                the CTA's; transposed and made BF16 by a kernel before); its 64 x 64 delta boxes;
 //   warps 4-19   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
 //                tokens of one column, which is tcgen05.st's 16x256b layout; the code's bits placed
 //                in the BF16 fields times 2^120 (2^112 for E5M2) and times 2^k, both exact;
@@ -43,24 +42,29 @@ constexpr int kACol = 384;                   // after three 128-column accumulat
 constexpr int kFoldWarps = 8;                // warps 20-27
 constexpr int kDeqWarp = 4, kDeqWarps = 16;  // warps 4-19: eight per stage, alternate stages
 constexpr int kFoldWarp = 20;
-constexpr int kTmaWarp = 0, kMmaWarp = 1, kScaleWarp = 2;   // and the second half's MMA warp, 3
+constexpr int kCodesWarp = 0, kMmaWarp = 1, kDeltaWarp = 2;   // and the second half's MMA warp, 3
 constexpr int kThreads = 896;
 constexpr long long kWait = 4000000000LL;
 
+// Two rings in shared memory.  A code box is free as soon as it is converted; delta's boxes are held
+// until their MMAs are done, up to four stages later.  So delta gets the deeper part of the 224 KB:
+// with one ring of eight stages for both, four were left for loads in flight, which the L2's
+// latency under load outlasted (65536 tokens: 818 us; with both rings as below ...).
 template <int NH, int TERMS>
 struct Cfg {
-  static constexpr int stage_bytes = kBox * (1 + NH * TERMS);
-  static constexpr int rounds = TERMS == 1 ? 2 : 1;           // groups of stages in shared memory
-  static constexpr int stages = kGroup * rounds;
+  static constexpr int delta_bytes = kBox * NH * TERMS;       // of a stage
+  static constexpr int codes = TERMS == 1 ? (NH == 2 ? 8 : 12) : (NH == 2 ? 4 : 8);   // a multiple of kGroup
+  static constexpr int deltas = TERMS == 1 ? (NH == 2 ? 10 : 14) : (NH == 2 ? 4 : 6);
   static constexpr int period = TERMS == 1 ? 4 : 2;           // stages of a segment: at most 256 tokens
-  static constexpr int smem = stages * stage_bytes + 1024;    // at most 225 KB
+  static constexpr int smem = codes * kBox + deltas * delta_bytes + 1024;
 };
 
 struct Params {
   int T, d_out, d_in, groups;
   int ng;                      // groups of stages (256 tokens) over all tokens; tokens past T are zeros
   int mt, nt, slices, items;
-  const uint8_t *scales;
+  const uint16_t *scales;      // BF16 powers of two, groups rows of tp tokens
+  int tp;
   const float *gamma, *beta, *db;   // nullable; only with one slice
   float *out;                  // dW, or the slices' sums (slice s at s d_out d_in)
 };
@@ -120,11 +124,11 @@ struct Accumulators {
   }
 };
 
-// Where the CTA's n-th group of stages lies in shared memory, and the parity of its barriers.
-template <int ROUNDS>
-struct Place {
-  uint32_t first, parity;
-  __device__ __forceinline__ explicit Place(uint32_t n) : first(n % ROUNDS * kGroup), parity(n / ROUNDS & 1u) {}
+// The slot of a ring of N that its g-th use takes, and the parity of that use.
+template <int N>
+struct Slot {
+  uint32_t at, parity;
+  __device__ __forceinline__ explicit Slot(uint32_t g) : at(g % N), parity(g / N & 1u) {}
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -152,6 +156,13 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, 
           tc::smem_u32(dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
       : "memory");
+}
+// untiled copy; both addresses and the size are multiples of 16 bytes
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                   tc::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void alloc_pair(uint32_t *dst) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n"
@@ -239,11 +250,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_weight_grad(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap tm_codes,
                   const __grid_constant__ CUtensorMap tm_delta, int *status) {
   using C = Cfg<NH, TERMS>;
-  constexpr int kStages = C::stages, kPeriod = C::period, kRounds = C::rounds;
+  constexpr int kCodes = C::codes, kDeltas = C::deltas, kPeriod = C::period;
   extern __shared__ uint8_t dsm[];
   uint8_t *sm = reinterpret_cast<uint8_t *>(((uintptr_t)dsm + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[kStages], empty[kStages], ready[kGroup], dfull[3], dempty[3];
-  __shared__ __align__(16) uint16_t scale_sh[kStages][kK];
+  uint8_t *const sm_delta = sm + kCodes * kBox;
+  // codes (with their scales): loaded, converted; delta: loaded, multiplied; A slot: converted in both
+  // CTAs; accumulators: summed, folded
+  __shared__ uint64_t cfull[kCodes], cempty[kCodes], bfull[kDeltas], bempty[kDeltas], ready[kGroup], dfull[3], dempty[3];
+  __shared__ __align__(128) uint16_t scale_sh[kCodes][kK];
   __shared__ uint32_t tmem_sh;
   __shared__ volatile int failed;
 
@@ -252,9 +266,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) alloc_pair(&tmem_sh);
   if (tid == 32) {
-    for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&full[s], 2);
-      tc::mbar_init(&empty[s], NH);
+    for (int s = 0; s < kCodes; ++s) {
+      tc::mbar_init(&cfull[s], 1);
+      tc::mbar_init(&cempty[s], kDeqWarps / 2);
+    }
+    for (int s = 0; s < kDeltas; ++s) {
+      tc::mbar_init(&bfull[s], 1);
+      tc::mbar_init(&bempty[s], NH);
     }
     for (int s = 0; s < kGroup; ++s) tc::mbar_init(&ready[s], kDeqWarps);   // half of them, of both CTAs
     for (int b = 0; b < 3; ++b) {
@@ -287,46 +305,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // 2 x 152 + 5 x 40
   if (warp < kDeqWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
-    if (warp == kTmaWarp && lane == 0) {
+    // Each of these warps walks its loop whole, so that addresses and coordinates stay in uniform
+    // registers, which TMA and the MMAs take; one elected thread issues.
+    const bool one = elect_one();
+    if (warp == kCodesWarp || warp == kDeltaWarp) {
       // ---------------- TMA ----------------
-      uint32_t n = 0;   // groups so far
+      uint32_t g = 0;   // stages so far
       bool ok = true;
-      for (int it = pair; it < P.items && ok; it += pairs) {
-        const Item w(P, it, 128 * NH);
-        for (int gi = 0; gi < w.ng && ok; ++gi, ++n) {
-          const Place<kRounds> at(n);
-#pragma unroll 1
-          for (int j = 0; j < kGroup; ++j) {
-            uint64_t *bar = &full[at.first + j];
-            if (!(ok = wait(&empty[at.first + j], at.parity ^ 1u))) break;
-            uint8_t *st = sm + (at.first + j) * C::stage_bytes;
-            const int t = w.t0 + (gi * kGroup + j) * kK;
-            tc::mbar_arrive_expect_tx(bar, C::stage_bytes);
-            tc::tma_load_2d(st, &tm_codes, w.i0 + 128 * rank, t, bar);
-#pragma unroll
-            for (int b = 0; b < NH * TERMS; ++b)   // box b: half b / TERMS, term b % TERMS
-              tma_load_3d(st + (1 + b) * kBox, &tm_delta, w.o0 + 128 * (b / TERMS) + 64 * rank, t, b % TERMS, bar);
+      if (warp == kCodesWarp) {
+        for (int it = pair; it < P.items && ok; it += pairs) {
+          const Item w(P, it, 128 * NH);
+          // the CTA's columns are one group; past d_in there are only zero codes, of any scale
+          const int i = w.i0 + 128 * rank;
+          const uint16_t *scales = P.scales + (size_t)min(i / kActGroup, P.groups - 1) * P.tp;
+          for (int t = w.t0; t < w.t0 + kGroup * kK * w.ng; t += kK, ++g) {
+            const Slot<kCodes> c(g);
+            if (!(ok = wait(&cempty[c.at], c.parity ^ 1u))) break;
+            __syncwarp();
+            if (one) {
+              tc::mbar_arrive_expect_tx(&cfull[c.at], kBox + kK * 2);
+              tc::tma_load_2d(sm + c.at * kBox, &tm_codes, i, t, &cfull[c.at]);
+              bulk_load(scale_sh[c.at], scales + t, kK * 2, &cfull[c.at]);
+            }
           }
         }
-      }
-      // leave no copy in flight, nor an arrival of the MMAs' commits: the last groups' stages
-      if (ok) {
-        for (uint32_t r = 0; r < kRounds && r < n; ++r) {
-          const Place<kRounds> at(n - 1 - r);
-          for (int j = 0; j < kGroup; ++j) wait(&empty[at.first + j], at.parity);
-        }
       } else {
-        for (int s = 0; s < kStages; ++s) {   // a phase that a copy is still to complete is the current one
-          tc::mbar_wait_bounded(&full[s], 0, kWait / 8);
-          tc::mbar_wait_bounded(&full[s], 1, kWait / 8);
+        for (int it = pair; it < P.items && ok; it += pairs) {
+          const Item w(P, it, 128 * NH);
+          for (int t = w.t0; t < w.t0 + kGroup * kK * w.ng; t += kK, ++g) {
+            const Slot<kDeltas> d(g);
+            if (!(ok = wait(&bempty[d.at], d.parity ^ 1u))) break;
+            __syncwarp();
+            if (one) {
+              uint64_t *bar = &bfull[d.at];
+              uint8_t *st = sm_delta + d.at * C::delta_bytes;
+              tc::mbar_arrive_expect_tx(bar, C::delta_bytes);
+#pragma unroll
+              for (int b = 0; b < NH * TERMS; ++b)   // box b: half b / TERMS, term b % TERMS
+                tma_load_3d(st + b * kBox, &tm_delta, w.o0 + 128 * (b / TERMS) + 64 * rank, t, b % TERMS, bar);
+            }
+          }
         }
+        // leave no arrival of the MMAs' commits behind: the last stages'
+        for (uint32_t r = 1; ok && r <= kDeltas && r <= g; ++r) {
+          const Slot<kDeltas> d(g - r);
+          wait(&bempty[d.at], d.parity);
+        }
+      }
+      if (!ok) {   // leave no copy in flight: whichever parity a barrier is in, one of the two waits is for it
+        for (int s = 0; s < kCodes + kDeltas; ++s)
+          for (uint32_t par = 0; par < 2; ++par)
+            tc::mbar_wait_bounded(s < kCodes ? &cfull[s] : &bfull[s - kCodes], par, kWait / 16);
       }
     } else if ((warp == kMmaWarp || (NH == 2 && warp == kMmaWarp + 2)) && rank == 0) {
-      // ---------------- MMA, a warp per half of the tile: the whole warp walks the loop (its values
-      // stay in uniform registers, which the MMAs take), one elected thread issues.  A warp's waits
-      // and commits cost about as much as its half's MMAs, so two warps keep the queue full ----------------
-      const bool one = elect_one();
-      const uint32_t b_first = desc_lo(tc::smem_u32(sm) + kBox), a0 = tmem + kACol;
+      // ---------------- MMA, a warp per half of the tile: a warp's waits and commits cost about as
+      // much as its half's MMAs, so two warps keep the queue full ----------------
+      const uint32_t b_first = desc_lo(tc::smem_u32(sm_delta)), a0 = tmem + kACol;
       Accumulators<NH> acc;
       auto walk = [&](auto half_c) {
         constexpr int half = decltype(half_c)::value;
@@ -339,8 +373,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int h = 0; h < NH; ++h)
             if (!wait(&dempty[acc.cur(h)], acc.use(acc.cur(h)) ^ 1u)) return;
           for (int gi = 0; gi < ng; ++gi, ++n) {
-            const Place<kRounds> at(n);
-            const uint32_t b_group = b_first + at.first * (C::stage_bytes >> 4) + half * TERMS * (kBox >> 4);
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
               constexpr int kHalf = kPeriod / 2;
@@ -354,6 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
               const int mine = acc.cur(half);
               const bool fresh = j % kPeriod == half * kHalf || (half == 1 && j == 0 && gi == 0);
+              const uint32_t db = (kGroup * n + j) % kDeltas;
+              const uint32_t b0 = b_first + (db * NH + half) * TERMS * (kBox >> 4);
               if (!wait(&ready[j], n & 1u)) return;
               __syncwarp();
               tc::fence_after_sync();
@@ -363,9 +397,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                   for (int p = 0; p < TERMS; ++p)
                     mma_pair(tmem + 128 * mine, a0 + 32 * j + 8 * k,
-                             b_group + j * (C::stage_bytes >> 4) + p * (kBox >> 4) + 128 * k,
+                             b0 + p * (kBox >> 4) + 128 * k,
                              k == 0 && p == 0 ? (fresh ? 0u : 1u) : 1u);
-                commit_pair(&empty[at.first + j]);
+                commit_pair(&bempty[db]);
                 if ((j + 1) % kPeriod == half * kHalf || (half == 1 && j + 1 == kGroup && gi + 1 == ng))
                   commit_pair(&dfull[mine]);
               }
@@ -375,45 +409,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       if (warp == kMmaWarp) walk(std::integral_constant<int, 0>());
       else walk(std::integral_constant<int, 1>());
-    } else if (warp == kScaleWarp) {
-      // ---------------- scales: a group's bytes are loaded while the group before it is handed out ----------------
-      uint32_t rx[kGroup], ry[kGroup];   // the bytes of tokens 2 lane and 2 lane + 1, as loaded
-      int ia = pair, ga = 0;             // the group that is loaded next
-      Item w(P, min(ia, P.items - 1), 128 * NH);
-      auto load = [&](int j) {
-        rx[j] = ry[j] = 127u;   // past the tokens: 1, so that zero codes stay zero
-        const int c0 = w.i0 + 128 * rank, t = w.t0 + (ga * kGroup + j) * kK + 2 * lane;
-        if (ia < P.items && c0 < P.d_in) {
-          const uint8_t *p = P.scales + (size_t)t * P.groups + c0 / kActGroup;
-          if (t < P.T) rx[j] = p[0];
-          if (t + 1 < P.T) ry[j] = p[P.groups];
-        }
-      };
-      auto bf16 = [](uint32_t b) { return b == kActBad ? 0x7FC0u : b << 7; };   // 2^(b - 127), or NaN
-      auto next_group = [&]() {
-        if (++ga == w.ng) {
-          ga = 0;
-          ia += pairs;
-          w = Item(P, min(ia, P.items - 1), 128 * NH);
-        }
-      };
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) load(j);
-      bool ok = true;
-      for (uint32_t n = 0; ia < P.items && ok; ++n) {
-        const Place<kRounds> at(n);
-        next_group();
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          ok = ok && wait(&empty[at.first + j], at.parity ^ 1u);
-          if (ok) {
-            reinterpret_cast<uint32_t *>(scale_sh[at.first + j])[lane] = bf16(rx[j]) | bf16(ry[j]) << 16;
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&full[at.first + j]);
-            load(j);
-          }
-        }
-      }
     }
   } else if (warp < kFoldWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
@@ -424,19 +419,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t mine = tc::smem_u32(sm) + lane * 128 + (((r0 >> 4) ^ (lane & 7)) << 4);
     bool ok = true;
     for (uint32_t n = 0; n < total && ok; ++n) {
-      const Place<kRounds> at(n), before(n - 1);
 #pragma unroll
       for (int jj = 0; jj < kGroup; jj += 2) {
-        const uint32_t j = jj + turn, s = at.first + j;
-        if (!(ok = wait(&full[s], at.parity))) break;
+        const uint32_t j = jj + turn, g = kGroup * n + j;
+        const Slot<kCodes> c(g);
+        if (!(ok = wait(&cfull[c.at], c.parity))) break;
         __syncwarp();
         uint32_t v[8];
-        ldmatrix_t8(mine + s * C::stage_bytes, v);
-        ldmatrix_t8(mine + s * C::stage_bytes + 32 * 128, v + 4);
+        ldmatrix_t8(mine + c.at * kBox, v);
+        ldmatrix_t8(mine + c.at * kBox + 32 * 128, v + 4);
         uint32_t x[16];
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const uint2 sc = *reinterpret_cast<const uint2 *>(&scale_sh[s][16 * m + 4 * (lane & 3)]);
+          const uint2 sc = *reinterpret_cast<const uint2 *>(&scale_sh[c.at][16 * m + 4 * (lane & 3)]);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t w0, w1;
@@ -445,16 +440,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             x[4 * m + 2 * u + 1] = scale_codes<F>(w1, sc.y);
           }
         }
-        // the slot's last MMAs, a group ago, are done: with one group of stages, the stage just filled
-        // was freed by them (and its barrier may be a phase further by now: it is not asked)
-        if (kRounds > 1 && n > 0) {
-          if (!(ok = wait(&empty[before.first + j], before.parity))) break;
-          __syncwarp();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&cempty[c.at]);
+        // The slot's last MMAs, a group ago, are done: their delta is free (its barrier cannot be a phase
+        // further yet), or, with one group of stages, this one's delta has been loaded in its place.
+        const Slot<kDeltas> d(g);
+        if (kDeltas > kGroup) {
+          if (n > 0) {
+            const Slot<kDeltas> before(g - kGroup);
+            if (!(ok = wait(&bempty[before.at], before.parity))) break;
+          }
+        } else if (!(ok = wait(&bfull[d.at], d.parity))) {
+          break;
         }
+        __syncwarp();
         tc::fence_after_sync();
         tmem_st_16x256b_x4(tmem + kACol + 32 * j + ((uint32_t)r0 << 16), x);
         tc::tmem_wait_st();
         tc::fence_before_sync();
+        // one of the stage's warps answers for this CTA's half of delta
+        if (kDeltas > kGroup && (dw & 7) == 0 && !(ok = wait(&bfull[d.at], d.parity))) break;
         __syncwarp();
         if (lane == 0) arrive_first(&ready[j]);
       }
@@ -548,6 +553,23 @@ __global__ void __launch_bounds__(256) k_join_slices(const float *__restrict__ p
       if (beta) v = fmaf(beta[i], db[o], v);
     }
     dW[e] = v;
+  }
+}
+
+// Scale bytes [T][groups] -> BF16 powers of two [groups][tp] (NaN for a marked group, 1 past T): 256
+// tokens x 64 groups per CTA through shared memory.
+__global__ void __launch_bounds__(256) k_scales_bf16(const uint8_t *__restrict__ scales, int T, int groups, int tp,
+                                                     uint16_t *__restrict__ out) {
+  __shared__ uint8_t tile[256][65];
+  const int t0 = blockIdx.x * 256, g0 = blockIdx.y * 64, ng = min(64, groups - g0);
+  for (int e = threadIdx.x; e < 256 * ng; e += 256) {
+    const int r = e / ng, c = e - r * ng;
+    tile[r][c] = t0 + r < T ? scales[(size_t)(t0 + r) * groups + g0 + c] : 127;
+  }
+  __syncthreads();
+  for (int c = 0; c < ng; ++c) {
+    const uint32_t b = tile[threadIdx.x][c];
+    out[(size_t)(g0 + c) * tp + t0 + threadIdx.x] = (uint16_t)(b == kActBad ? 0x7FC0u : b << 7);
   }
 }
 
@@ -684,6 +706,7 @@ WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) 
   // caller's pointers decide: room for both
   w.delta_bytes = (size_t)T * pad16((size_t)d_out * 2) * (bf16 ? 1 : 3);
   w.code_bytes = (size_t)T * pad16(d_in);
+  w.scale_words = (size_t)p.ng * kGroup * kK * ((d_in + kActGroup - 1) / kActGroup);
   return w;
 }
 
@@ -736,7 +759,9 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   P.nt = p.nt;
   P.slices = p.slices;
   P.items = p.mt * p.nt * p.slices;
-  P.scales = a.scales;
+  P.scales = a.scale_ws;
+  P.tp = p.ng * kGroup * kK;
+  k_scales_bf16<<<dim3(p.ng, (P.groups + 63) / 64), 256, 0, L.stream>>>(a.scales, a.T, P.groups, P.tp, a.scale_ws);
   const bool one = p.slices == 1;
   P.gamma = one ? a.gamma : nullptr;
   P.beta = one ? a.beta : nullptr;
