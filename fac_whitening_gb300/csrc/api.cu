@@ -1315,7 +1315,7 @@ struct ActWs {
   float *db = nullptr;      // weight gradient: db when only the call itself needs it
   float *slices = nullptr;  // sums of token slices
   uint8_t *delta = nullptr, *codes = nullptr;   // operands with aligned rows
-  uint16_t *scales = nullptr;                   // scales by group
+  uint8_t *scales = nullptr;                    // scales by group
   size_t bytes = 0;
 };
 
@@ -1331,7 +1331,7 @@ ActWs act_layout(void *base, const gift_ctx *ctx, gift_op op, gift_dtype dt, int
     w.slices = c.take<float>(g.slice_floats);
     w.delta = c.take<uint8_t>(g.delta_bytes);
     w.codes = c.take<uint8_t>(g.code_bytes);
-    w.scales = c.take<uint16_t>(g.scale_words);
+    w.scales = c.take<uint8_t>(g.scale_bytes);
   }
   w.bytes = c.off + kAlign;
   return w;

@@ -361,7 +361,7 @@ struct WeightGradWs {
   size_t slice_floats = 0;     // sums of the token slices
   size_t delta_bytes = 0;      // delta's BF16 terms, or its copy with aligned rows
   size_t code_bytes = 0;       // the codes' copy with aligned rows
-  size_t scale_words = 0;      // the scales as BF16, a row of tokens per group
+  size_t scale_bytes = 0;      // the scales as the kernel reads them, by group and stage
 };
 struct WeightGrad {
   const void *delta;
@@ -373,7 +373,7 @@ struct WeightGrad {
   float *slices;
   void *delta_ws;
   uint8_t *code_ws;
-  uint16_t *scale_ws;
+  void *scale_ws;
 };
 WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in);
 cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const WeightGrad &a);

@@ -40,8 +40,8 @@ constexpr int kGroup = 4;                    // stages of a group, and A operand
                                              // (32 columns each): stage j of a group uses slot j
 constexpr int kACol = 384;                   // after three 128-column accumulators
 constexpr int kFoldWarps = 8;                // warps 20-27
-constexpr int kDeqWarp = 4, kDeqWarps = 16;  // warps 4-19: eight per stage, alternate stages
-constexpr int kFoldWarp = 20;
+constexpr int kDeqWarp = 4, kDeqWarps = 16;  // warps 4-19: four per stage, by turns
+constexpr int kFoldWarp = kDeqWarp + kDeqWarps;
 constexpr int kCodesWarp = 0, kMmaWarp = 1, kDeltaWarp = 2;   // and the second half's MMA warp, 3
 constexpr int kThreads = 896;
 constexpr long long kWait = 4000000000LL;
@@ -59,12 +59,22 @@ struct Cfg {
   static constexpr int smem = codes * kBox + deltas * delta_bytes + 1024;
 };
 
+// What a stage's conversion reads: for each token t of the group, its scale 2^k times 2^120 (2^112)
+// as BF16, cut off at 2^127; the exponent that was cut off (0 for activations below 448 * 2^7 or
+// 57344 * 2^15), and whether any was.
+struct StageScales {
+  uint16_t first[kK];
+  uint8_t over[kK];
+  uint32_t any_over, pad[3];
+};
+constexpr int kScaleBytes = sizeof(StageScales);
+
 struct Params {
   int T, d_out, d_in, groups;
   int ng;                      // groups of stages (256 tokens) over all tokens; tokens past T are zeros
   int mt, nt, slices, items;
-  const uint16_t *scales;      // BF16 powers of two, groups rows of tp tokens
-  int tp;
+  const StageScales *scales;   // groups rows of `stages`
+  int stages;
   const float *gamma, *beta, *db;   // nullable; only with one slice
   float *out;                  // dW, or the slices' sums (slice s at s d_out d_in)
 };
@@ -220,6 +230,16 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// two FP32 sums at once, each to nearest
+__device__ __forceinline__ void add_f32x2(float2 &to, uint32_t x, uint32_t y) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "add.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}\n"
+      : "+f"(to.x), "+f"(to.y)
+      : "f"(__uint_as_float(x)), "f"(__uint_as_float(y)));
+}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   __nv_bfloat162 x, y;
   *reinterpret_cast<uint32_t *>(&x) = a;
@@ -238,13 +258,6 @@ __device__ __forceinline__ void spread_codes(uint32_t c, uint32_t &w0, uint32_t 
   w0 = __byte_perm(lo, hi, 0x5140);
   w1 = __byte_perm(lo, hi, 0x7362);
 }
-// times 2^120 (2^112), then times the tokens' scales: both exact
-template <int F>
-__device__ __forceinline__ uint32_t scale_codes(uint32_t w, uint32_t s) {
-  constexpr uint32_t up = F == FMT_E4M3 ? 0x7B807B80u : 0x77807780u;
-  return mul_bf16x2(mul_bf16x2(w, up), s);
-}
-
 template <int F, int NH, int TERMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_weight_grad(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap tm_codes,
@@ -257,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // codes (with their scales): loaded, converted; delta: loaded, multiplied; A slot: converted in both
   // CTAs; accumulators: summed, folded
   __shared__ uint64_t cfull[kCodes], cempty[kCodes], bfull[kDeltas], bempty[kDeltas], ready[kGroup], dfull[3], dempty[3];
-  __shared__ __align__(128) uint16_t scale_sh[kCodes][kK];
+  __shared__ __align__(16) StageScales scale_sh[kCodes];
   __shared__ uint32_t tmem_sh;
   __shared__ volatile int failed;
 
@@ -268,13 +281,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (tid == 32) {
     for (int s = 0; s < kCodes; ++s) {
       tc::mbar_init(&cfull[s], 1);
-      tc::mbar_init(&cempty[s], kDeqWarps / 2);
+      tc::mbar_init(&cempty[s], 4);
     }
     for (int s = 0; s < kDeltas; ++s) {
       tc::mbar_init(&bfull[s], 1);
       tc::mbar_init(&bempty[s], NH);
     }
-    for (int s = 0; s < kGroup; ++s) tc::mbar_init(&ready[s], kDeqWarps);   // half of them, of both CTAs
+    for (int s = 0; s < kGroup; ++s) tc::mbar_init(&ready[s], 2 * 4);
     for (int b = 0; b < 3; ++b) {
       tc::mbar_init(&dfull[b], 1);
       tc::mbar_init(&dempty[b], 2 * kFoldWarps);
@@ -317,15 +330,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const Item w(P, it, 128 * NH);
           // the CTA's columns are one group; past d_in there are only zero codes, of any scale
           const int i = w.i0 + 128 * rank;
-          const uint16_t *scales = P.scales + (size_t)min(i / kActGroup, P.groups - 1) * P.tp;
-          for (int t = w.t0; t < w.t0 + kGroup * kK * w.ng; t += kK, ++g) {
+          const StageScales *scales = P.scales + (size_t)min(i / kActGroup, P.groups - 1) * P.stages + w.t0 / kK;
+          for (int t = w.t0; t < w.t0 + kGroup * kK * w.ng; t += kK, ++g, ++scales) {
             const Slot<kCodes> c(g);
             if (!(ok = wait(&cempty[c.at], c.parity ^ 1u))) break;
             __syncwarp();
             if (one) {
-              tc::mbar_arrive_expect_tx(&cfull[c.at], kBox + kK * 2);
+              tc::mbar_arrive_expect_tx(&cfull[c.at], kBox + kScaleBytes);
               tc::tma_load_2d(sm + c.at * kBox, &tm_codes, i, t, &cfull[c.at]);
-              bulk_load(scale_sh[c.at], scales + t, kK * 2, &cfull[c.at]);
+              bulk_load(&scale_sh[c.at], scales, kScaleBytes, &cfull[c.at]);
             }
           }
         }
@@ -412,57 +425,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kFoldWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
-    // ---------------- codes -> BF16 in tensor memory: 16 of the CTA's rows i of every other stage ----------------
-    const int dw = warp - kDeqWarp, r0 = 32 * (dw & 3) + 16 * ((dw >> 2) & 1), turn = dw >> 3;
+    // ---------------- codes -> BF16 in tensor memory: 32 of the CTA's rows i of every fourth stage ----------------
+    const int dw = warp - kDeqWarp, q = dw & 3, turn = dw >> 2;
     uint32_t total = 0;
     for (int it = pair; it < P.items; it += pairs) total += (uint32_t)Item(P, it, 128 * NH).ng;
-    const uint32_t mine = tc::smem_u32(sm) + lane * 128 + (((r0 >> 4) ^ (lane & 7)) << 4);
-    bool ok = true;
-    for (uint32_t n = 0; n < total && ok; ++n) {
+    const uint32_t mine = tc::smem_u32(sm) + lane * 128, slot = tmem + kACol + 32 * turn + ((uint32_t)(32 * q) << 16);
+    for (uint32_t n = 0; n < total; ++n) {
+      const uint32_t g = kGroup * n + turn;
+      const Slot<kCodes> c(g);
+      const Slot<kDeltas> d(g);
+      if (!wait(&cfull[c.at], c.parity)) break;
+      __syncwarp();
+      const StageScales &sc = scale_sh[c.at];
+      bool ok = true;
 #pragma unroll
-      for (int jj = 0; jj < kGroup; jj += 2) {
-        const uint32_t j = jj + turn, g = kGroup * n + j;
-        const Slot<kCodes> c(g);
-        if (!(ok = wait(&cfull[c.at], c.parity))) break;
-        __syncwarp();
-        uint32_t v[8];
-        ldmatrix_t8(mine + c.at * kBox, v);
-        ldmatrix_t8(mine + c.at * kBox + 32 * 128, v + 4);
-        uint32_t x[16];
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t v[8], x[16];
+        const uint32_t from = mine + c.at * kBox + (((2 * q + hh) ^ (lane & 7)) << 4);
+        ldmatrix_t8(from, v);
+        ldmatrix_t8(from + 32 * 128, v + 4);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const uint2 sc = *reinterpret_cast<const uint2 *>(&scale_sh[c.at][16 * m + 4 * (lane & 3)]);
+          const uint2 s = *reinterpret_cast<const uint2 *>(&sc.first[16 * m + 4 * (lane & 3)]);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t w0, w1;
             spread_codes<F>(v[2 * m + u], w0, w1);
-            x[4 * m + 2 * u] = scale_codes<F>(w0, sc.x);
-            x[4 * m + 2 * u + 1] = scale_codes<F>(w1, sc.y);
+            x[4 * m + 2 * u] = mul_bf16x2(w0, s.x);
+            x[4 * m + 2 * u + 1] = mul_bf16x2(w1, s.y);
           }
         }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&cempty[c.at]);
-        // The slot's last MMAs, a group ago, are done: their delta is free (its barrier cannot be a phase
-        // further yet), or, with one group of stages, this one's delta has been loaded in its place.
-        const Slot<kDeltas> d(g);
-        if (kDeltas > kGroup) {
-          if (n > 0) {
-            const Slot<kDeltas> before(g - kGroup);
-            if (!(ok = wait(&bempty[before.at], before.parity))) break;
+        if (sc.any_over) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t o = *reinterpret_cast<const uint32_t *>(&sc.over[16 * m + 4 * (lane & 3)]);
+            const uint32_t sx = 0x3F803F80u + ((o & 0xFFu) << 7) + ((o & 0xFF00u) << 15),
+                           sy = 0x3F803F80u + ((o >> 9) & 0x7F80u) + ((o >> 24) << 23);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[4 * m + u] = mul_bf16x2(x[4 * m + u], u & 1 ? sy : sx);
           }
-        } else if (!(ok = wait(&bfull[d.at], d.parity))) {
-          break;
         }
-        __syncwarp();
-        tc::fence_after_sync();
-        tmem_st_16x256b_x4(tmem + kACol + 32 * j + ((uint32_t)r0 << 16), x);
-        tc::tmem_wait_st();
-        tc::fence_before_sync();
-        // one of the stage's warps answers for this CTA's half of delta
-        if (kDeltas > kGroup && (dw & 7) == 0 && !(ok = wait(&bfull[d.at], d.parity))) break;
-        __syncwarp();
-        if (lane == 0) arrive_first(&ready[j]);
+        if (hh == 0) {
+          // The slot's last MMAs, a group ago, are done: their delta is free (its barrier cannot be a phase
+          // further yet), or, with one group of stages, this one's delta has been loaded in its place.
+          if (kDeltas > kGroup) {
+            if (n > 0) {
+              const Slot<kDeltas> before(g - kGroup);
+              ok = wait(&bempty[before.at], before.parity);
+            }
+          } else {
+            ok = wait(&bfull[d.at], d.parity);
+          }
+          if (!ok) break;
+          __syncwarp();
+          tc::fence_after_sync();
+        }
+        tmem_st_16x256b_x4(slot + ((uint32_t)(16 * hh) << 16), x);
       }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&cempty[c.at]);
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      // one of the stage's warps answers for this CTA's half of delta
+      if (kDeltas > kGroup && q == 0 && !wait(&bfull[d.at], d.parity)) break;
+      __syncwarp();
+      if (lane == 0) arrive_first(&ready[turn]);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
@@ -473,13 +501,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int it = pair; it < P.items && ok; it += pairs) {
       const Item w(P, it, 128 * NH);
-      float sum[NH][64];
+      float2 sum[NH][32];
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
-        for (int e = 0; e < 64; ++e) sum[h][e] = 0.0f;
+        for (int e = 0; e < 32; ++e) sum[h][e] = make_float2(0.0f, 0.0f);
       // add half h's finished segment and hand its accumulator back
-      auto fold = [&](int h, float(&to)[64]) {
+      auto fold = [&](int h, float2(&to)[32]) {
         const int b = acc.cur(h);
         if (!(ok = ok && wait(&dfull[b], acc.use(b)))) return;
         __syncwarp();
@@ -490,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc::tmem_ld16_nowait(tmem + off + 128 * b + e, raw);
           tc::tmem_wait_ld16(raw);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) to[e + x] += __uint_as_float(raw[x]);
+          for (int x = 0; x < 16; x += 2) add_f32x2(to[(e + x) / 2], raw[x], raw[x + 1]);
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -519,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 64; ++e, p += P.d_in) {
             if (o + e >= P.d_out) break;
-            float v = sum[h][e] * ga;
+            float v = (e & 1 ? sum[h][e / 2].y : sum[h][e / 2].x) * ga;
             if (P.beta) v = fmaf(be, P.db[o + e], v);
             *p = v;
           }
@@ -556,20 +584,34 @@ __global__ void __launch_bounds__(256) k_join_slices(const float *__restrict__ p
   }
 }
 
-// Scale bytes [T][groups] -> BF16 powers of two [groups][tp] (NaN for a marked group, 1 past T): 256
-// tokens x 64 groups per CTA through shared memory.
-__global__ void __launch_bounds__(256) k_scales_bf16(const uint8_t *__restrict__ scales, int T, int groups, int tp,
-                                                     uint16_t *__restrict__ out) {
+// Scale bytes [T][groups] -> StageScales [groups][stages] (NaN for a marked group, 1 past T): 256
+// tokens x 64 groups per CTA through shared memory, a warp writes a stage.
+template <int F>
+__global__ void __launch_bounds__(256) k_stage_scales(const uint8_t *__restrict__ scales, int T, int groups,
+                                                      int stages, StageScales *__restrict__ out) {
   __shared__ uint8_t tile[256][65];
+  constexpr int up = F == FMT_E4M3 ? 120 : 112;
   const int t0 = blockIdx.x * 256, g0 = blockIdx.y * 64, ng = min(64, groups - g0);
   for (int e = threadIdx.x; e < 256 * ng; e += 256) {
     const int r = e / ng, c = e - r * ng;
     tile[r][c] = t0 + r < T ? scales[(size_t)(t0 + r) * groups + g0 + c] : 127;
   }
   __syncthreads();
-  for (int c = 0; c < ng; ++c) {
-    const uint32_t b = tile[threadIdx.x][c];
-    out[(size_t)(g0 + c) * tp + t0 + threadIdx.x] = (uint16_t)(b == kActBad ? 0x7FC0u : b << 7);
+  const int lane = threadIdx.x & 31;
+  for (int e = threadIdx.x >> 5; e < 4 * ng; e += 8) {
+    const int st = e & 3, c = e >> 2;
+    uint32_t first[2], over[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int b = tile[64 * st + 2 * lane + u][c];
+      over[u] = b == (int)kActBad ? 0u : (uint32_t)max(0, b + up - 254);
+      first[u] = b == (int)kActBad ? 0x7FC0u : (uint32_t)(b + up - (int)over[u]) << 7;
+    }
+    StageScales &o = out[(size_t)(g0 + c) * stages + t0 / kK + st];
+    reinterpret_cast<uint32_t *>(o.first)[lane] = first[0] | first[1] << 16;
+    reinterpret_cast<uint16_t *>(o.over)[lane] = (uint16_t)(over[0] | over[1] << 8);
+    const bool any = __any_sync(0xFFFFFFFFu, (over[0] | over[1]) != 0);
+    if (lane == 0) o.any_over = any;
   }
 }
 
@@ -706,7 +748,7 @@ WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) 
   // caller's pointers decide: room for both
   w.delta_bytes = (size_t)T * pad16((size_t)d_out * 2) * (bf16 ? 1 : 3);
   w.code_bytes = (size_t)T * pad16(d_in);
-  w.scale_words = (size_t)p.ng * kGroup * kK * ((d_in + kActGroup - 1) / kActGroup);
+  w.scale_bytes = (size_t)p.ng * kGroup * kScaleBytes * ((d_in + kActGroup - 1) / kActGroup);
   return w;
 }
 
@@ -759,9 +801,12 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   P.nt = p.nt;
   P.slices = p.slices;
   P.items = p.mt * p.nt * p.slices;
-  P.scales = a.scale_ws;
-  P.tp = p.ng * kGroup * kK;
-  k_scales_bf16<<<dim3(p.ng, (P.groups + 63) / 64), 256, 0, L.stream>>>(a.scales, a.T, P.groups, P.tp, a.scale_ws);
+  StageScales *scales = static_cast<StageScales *>(a.scale_ws);
+  P.scales = scales;
+  P.stages = p.ng * kGroup;
+  const dim3 sgrid(p.ng, (P.groups + 63) / 64);
+  if (fmt == FMT_E4M3) k_stage_scales<FMT_E4M3><<<sgrid, 256, 0, L.stream>>>(a.scales, a.T, P.groups, P.stages, scales);
+  else k_stage_scales<FMT_E5M2><<<sgrid, 256, 0, L.stream>>>(a.scales, a.T, P.groups, P.stages, scales);
   const bool one = p.slices == 1;
   P.gamma = one ? a.gamma : nullptr;
   P.beta = one ? a.beta : nullptr;
