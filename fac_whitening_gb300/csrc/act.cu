@@ -1,8 +1,11 @@
 // The 8-bit activation checkpoint: encode and decode.
 //
-// One warp takes a group of 128 consecutive columns of one token: its amax, the scale exponent
-// from the amax's bit pattern, the codes x 2^-k by the hardware's round-to-nearest-even,
-// saturating conversion.  Both directions stream each byte once; HBM bounds them.
+// A warp takes a piece of 512 consecutive columns of one token (four scale groups) at a time: the
+// groups' amax by shuffles, the scale exponent from the amax's bit pattern, the codes x 2^-k by the
+// hardware's round-to-nearest-even, saturating conversion.  Both directions move each byte once
+// (2 + 1 + 1/128 bytes an element for BF16) and HBM bounds them: 32-byte accesses, and enough warps
+// that the next pieces' loads are in flight while one is converted.  Rows that do not allow 32-byte
+// accesses go element by element, consecutive over the warp.
 #include "act.cuh"
 #include "kernels.cuh"
 
@@ -12,73 +15,74 @@ namespace {
 
 constexpr int kActThreads = 256;
 
-template <int F, typename E>
+template <int F, typename E, bool VEC>
 __global__ void __launch_bounds__(kActThreads) k_act_encode(const E *__restrict__ x, int T, int d, int groups,
                                                             uint8_t *__restrict__ codes, uint8_t *__restrict__ scales,
                                                             int *status) {
   const int lane = threadIdx.x & 31;
-  const size_t warps = (size_t)gridDim.x * (kActThreads / 32), n = (size_t)T * groups;
-  for (size_t w = (size_t)blockIdx.x * (kActThreads / 32) + (threadIdx.x >> 5); w < n; w += warps) {
-    const size_t t = w / groups;
-    const int c0 = (int)(w - t * groups) * kActGroup, len = min(kActGroup, d - c0);
-    const size_t base = t * d + c0;
-    float v[4];
-    uint32_t m = 0;
+  bool bad = false;
+  for (PieceWalk w((size_t)blockIdx.x * (kActThreads / 32) + (threadIdx.x >> 5), (size_t)gridDim.x * (kActThreads / 32),
+                   (d + kPiece - 1) / kPiece);
+       w.t < T; w.next()) {
+    const int c0 = w.p * kPiece, n = d - c0;
+    const size_t at = (size_t)w.t * d + c0;
+    Raw<E> r;
+    load_piece<VEC>(x + at, n, lane, r);
+    float v[16];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = lane + 32 * i;
-      v[i] = c < len ? ld1(x + base + c) : 0.0f;
-      m = max(m, abs_bits(v[i]));
-    }
-    const uint32_t sb = act_scale_byte<F>(warp_max_u32(m));
-    const float inv = act_inv_scale(sb == kActBad ? 127u : sb);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = lane + 32 * i;
-      if (c < len) codes[base + c] = pack1_fp8<F>(__fmul_rn(v[i], inv));
-    }
-    if (lane == 0) {
-      scales[w] = (uint8_t)sb;
-      if (sb == kActBad) set_status(status, GIFT_ERR_NONFINITE);
-    }
+    for (int e = 0; e < 16; ++e) v[e] = r.get(e);
+    bad |= encode_piece<F, VEC>(v, n, lane, codes + at, scales + (size_t)w.t * groups + w.p * 4);
   }
+  if (bad) set_status(status, GIFT_ERR_NONFINITE);
 }
 
-template <int F, typename E>
+template <int F, typename E, bool VEC>
 __global__ void __launch_bounds__(kActThreads) k_act_decode(const uint8_t *__restrict__ codes,
                                                             const uint8_t *__restrict__ scales, int T, int d,
                                                             int groups, E *__restrict__ out, int *status) {
   const int lane = threadIdx.x & 31;
-  const size_t warps = (size_t)gridDim.x * (kActThreads / 32), n = (size_t)T * groups;
-  for (size_t w = (size_t)blockIdx.x * (kActThreads / 32) + (threadIdx.x >> 5); w < n; w += warps) {
-    const size_t t = w / groups;
-    const int c0 = (int)(w - t * groups) * kActGroup, len = min(kActGroup, d - c0);
-    const size_t base = t * d + c0;
-    const uint32_t sb = scales[w];
-    const float s = act_scale(sb);
-    for (int c = lane; c < len; c += 32) st1(out + base + c, __fmul_rn(dec_fp8<F>(codes[base + c]), s));
-    if (lane == 0 && sb == kActBad) set_status(status, GIFT_ERR_NONFINITE);
+  bool bad = false;
+  for (PieceWalk w((size_t)blockIdx.x * (kActThreads / 32) + (threadIdx.x >> 5), (size_t)gridDim.x * (kActThreads / 32),
+                   (d + kPiece - 1) / kPiece);
+       w.t < T; w.next()) {
+    const int c0 = w.p * kPiece, n = d - c0;
+    const size_t at = (size_t)w.t * d + c0;
+    RawCodes r;
+    load_codes<VEC>(codes + at, scales + (size_t)w.t * groups + w.p * 4, n, lane, r);
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = code_value<F, VEC>(r, e);
+    store_piece<VEC>(out + at, n, lane, v);
+    // a marked group's first value is NaN whatever its code
+    bad |= VEC ? r.s == kActBad
+               : (r.s & 0xFFu) == kActBad || ((r.s >> 8) & 0xFFu) == kActBad || ((r.s >> 16) & 0xFFu) == kActBad ||
+                     (r.s >> 24) == kActBad;
   }
+  if (bad) set_status(status, GIFT_ERR_NONFINITE);
 }
 
-int act_grid(const Launch &L, size_t groups) {
-  const size_t ctas = (groups + kActThreads / 32 - 1) / (kActThreads / 32);
-  return (int)(ctas < (size_t)L.sms * 8 ? ctas : (size_t)L.sms * 8);
+// a warp per piece, up to the resident CTAs of the context's SMs
+int act_grid(const Launch &L, int T, int d) {
+  const size_t pieces = (size_t)T * ((d + kPiece - 1) / kPiece), ctas = (pieces + kActThreads / 32 - 1) / (kActThreads / 32);
+  const size_t most = (size_t)L.sms * 8;
+  return (int)(ctas < most ? ctas : most);
 }
 
 template <int F, typename E>
 cudaError_t encode(const Launch &L, const void *x, int T, int d, uint8_t *codes, uint8_t *scales) {
-  const int groups = (d + kActGroup - 1) / kActGroup;
-  k_act_encode<F, E><<<act_grid(L, (size_t)T * groups), kActThreads, 0, L.stream>>>(
-      static_cast<const E *>(x), T, d, groups, codes, scales, L.status);
+  const int groups = (d + kActGroup - 1) / kActGroup, grid = act_grid(L, T, d);
+  const E *p = static_cast<const E *>(x);
+  if (rows_vec(d, x, codes)) k_act_encode<F, E, true><<<grid, kActThreads, 0, L.stream>>>(p, T, d, groups, codes, scales, L.status);
+  else k_act_encode<F, E, false><<<grid, kActThreads, 0, L.stream>>>(p, T, d, groups, codes, scales, L.status);
   return cudaGetLastError();
 }
 
 template <int F, typename E>
 cudaError_t decode(const Launch &L, const uint8_t *codes, const uint8_t *scales, int T, int d, void *out) {
-  const int groups = (d + kActGroup - 1) / kActGroup;
-  k_act_decode<F, E><<<act_grid(L, (size_t)T * groups), kActThreads, 0, L.stream>>>(codes, scales, T, d, groups,
-                                                                                    static_cast<E *>(out), L.status);
+  const int groups = (d + kActGroup - 1) / kActGroup, grid = act_grid(L, T, d);
+  E *p = static_cast<E *>(out);
+  if (rows_vec(d, out, codes)) k_act_decode<F, E, true><<<grid, kActThreads, 0, L.stream>>>(codes, scales, T, d, groups, p, L.status);
+  else k_act_decode<F, E, false><<<grid, kActThreads, 0, L.stream>>>(codes, scales, T, d, groups, p, L.status);
   return cudaGetLastError();
 }
 

@@ -23,8 +23,11 @@ __device__ __forceinline__ uint32_t act_scale_byte(uint32_t amax_bits) {
   k = min(max(k, kActKMin), 127 - act_emax<F>());
   return (uint32_t)(k + 127);
 }
-// 2^-k, what an element is multiplied with before it is rounded (k in [-110, 119]: normal)
-__device__ __forceinline__ float act_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^-k, what an element is multiplied with before it is rounded (k in [-110, 119]: normal); 1 for a
+// marked group, whose codes mean nothing
+__device__ __forceinline__ float act_inv_scale(uint32_t byte) {
+  return byte == kActBad ? 1.0f : __uint_as_float((254u - byte) << 23);
+}
 // 2^k; NaN for a marked group
 __device__ __forceinline__ float act_scale(uint32_t byte) {
   return byte == kActBad ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
@@ -34,5 +37,224 @@ __device__ __forceinline__ float ld1(const float *p) { return *p; }
 __device__ __forceinline__ float ld1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void st1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void st1(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// ------------------------------------------------------------------------------------------------
+// Row pieces.  A warp handles a row in pieces of 512 columns, 16 per lane, so that a piece holds
+// four whole scale groups.  Two layouts: VEC, for rows whose pitch and base allow 32-byte accesses
+// (d a multiple of 16), lane l holds columns 16 l .. 16 l + 15 (a group is eight lanes); otherwise
+// lane l holds columns l, l + 32, ... (a group is four consecutive registers of the warp), each
+// access one element wide and consecutive over the warp.
+// ------------------------------------------------------------------------------------------------
+constexpr int kPiece = 512;
+
+__device__ __forceinline__ void ld256(const void *p, uint32_t *r) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st256(void *p, const uint32_t *r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// The element type's registers for a lane's 16 columns of a piece, as loaded.
+template <typename E>
+struct Raw;
+template <>
+struct Raw<float> {
+  uint32_t r[16];
+  __device__ __forceinline__ float get(int e) const { return __uint_as_float(r[e]); }
+  __device__ __forceinline__ void put(int e, float v) { r[e] = __float_as_uint(v); }
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint32_t r[8];
+  __device__ __forceinline__ float get(int e) const {
+    return __uint_as_float(e & 1 ? r[e / 2] & 0xFFFF0000u : r[e / 2] << 16);
+  }
+};
+
+// column of a lane's e-th value within its piece
+template <bool VEC>
+__device__ __forceinline__ int piece_col(int lane, int e) { return VEC ? 16 * lane + e : 32 * e + lane; }
+
+// Load a lane's values of the piece at p (n columns of the row are left, zeros past them).
+template <bool VEC>
+__device__ __forceinline__ void load_piece(const float *p, int n, int lane, Raw<float> &x) {
+  if (VEC) {
+    if (16 * lane < n) {
+      ld256(p + 16 * lane, x.r);
+      ld256(p + 16 * lane + 8, x.r + 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x.r[e] = 0u;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x.r[e] = 32 * e + lane < n ? __float_as_uint(p[32 * e + lane]) : 0u;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load_piece(const __nv_bfloat16 *p, int n, int lane, Raw<__nv_bfloat16> &x) {
+  if (VEC) {
+    if (16 * lane < n) {
+      ld256(p + 16 * lane, x.r);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.r[e] = 0u;
+    }
+  } else {
+    const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+    uint32_t v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 32 * e + lane < n ? (uint32_t)q[32 * e + lane] : 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x.r[e] = v[2 * e] | v[2 * e + 1] << 16;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store_piece(float *p, int n, int lane, const float *v) {
+  if (VEC) {
+    if (16 * lane < n) {
+      uint32_t r[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e]);
+      st256(p + 16 * lane, r);
+      st256(p + 16 * lane + 8, r + 8);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (32 * e + lane < n) p[32 * e + lane] = v[e];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_piece(__nv_bfloat16 *p, int n, int lane, const float *v) {
+  if (VEC) {
+    if (16 * lane < n) {
+      uint32_t r[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+      st256(p + 16 * lane, r);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (32 * e + lane < n) p[32 * e + lane] = __float2bfloat16_rn(v[e]);
+  }
+}
+
+// Encode a lane's 16 values: codes to cp, the piece's scale bytes to sp.  Returns whether a group was
+// marked.  All lanes of the warp call it.
+template <int F, bool VEC>
+__device__ __forceinline__ bool encode_piece(const float *v, int n, int lane, uint8_t *cp, uint8_t *sp) {
+  if (VEC) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = max(m, abs_bits(v[e]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const uint32_t sb = act_scale_byte<F>(m);
+    const float inv = act_inv_scale(sb);
+    if (16 * lane < n) {
+      uint4 c;
+      uint32_t *w = &c.x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = pack4_fp8<F>(__fmul_rn(v[4 * k], inv), __fmul_rn(v[4 * k + 1], inv), __fmul_rn(v[4 * k + 2], inv),
+                            __fmul_rn(v[4 * k + 3], inv));
+      *reinterpret_cast<uint4 *>(cp + 16 * lane) = c;
+      if ((lane & 7) == 0) sp[lane >> 3] = (uint8_t)sb;
+    }
+    return sb == kActBad;
+  }
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 4 * k; e < 4 * k + 4; ++e) m = max(m, abs_bits(v[e]));
+    const uint32_t sb = act_scale_byte<F>(warp_max_u32(m));
+    const float inv = act_inv_scale(sb);
+    bad |= sb == kActBad;
+#pragma unroll
+    for (int e = 4 * k; e < 4 * k + 4; ++e)
+      if (32 * e + lane < n) cp[32 * e + lane] = pack1_fp8<F>(__fmul_rn(v[e], inv));
+    if (lane == 0 && kActGroup * k < n) sp[k] = (uint8_t)sb;
+  }
+  return bad;
+}
+
+// A lane's 16 codes of a piece and their scales, as loaded.
+struct RawCodes {
+  uint32_t c[4];   // VEC: 16 bytes in order; otherwise byte k of c[g] is element 4 g + k
+  uint32_t s;      // VEC: the lane's scale byte; otherwise the four groups' bytes
+};
+template <bool VEC>
+__device__ __forceinline__ void load_codes(const uint8_t *cp, const uint8_t *sp, int n, int lane, RawCodes &x) {
+  if (VEC) {
+    x.c[0] = x.c[1] = x.c[2] = x.c[3] = 0u;
+    x.s = 127u;
+    if (16 * lane < n) {
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(x.c[0]), "=r"(x.c[1]), "=r"(x.c[2]), "=r"(x.c[3])
+                   : "l"(cp + 16 * lane));
+      x.s = sp[lane >> 3];
+    }
+  } else {
+    x.s = 0x7F7F7F7Fu;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      x.c[g] = 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (32 * (4 * g + k) + lane < n) x.c[g] |= (uint32_t)cp[32 * (4 * g + k) + lane] << (8 * k);
+    }
+    if (lane < 4 && kActGroup * lane < n) x.s = sp[lane];   // gathered below
+    uint32_t s = 0;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) s |= (__shfl_sync(0xFFFFFFFFu, x.s, g) & 0xFFu) << (8 * g);
+    x.s = s;
+  }
+}
+// the value of element e
+template <int F, bool VEC>
+__device__ __forceinline__ float code_value(const RawCodes &x, int e) {
+  const uint32_t sb = VEC ? x.s : (x.s >> (8 * (e >> 2))) & 0xFFu;
+  return __fmul_rn(dec_fp8<F>((x.c[e >> 2] >> (8 * (e & 3))) & 0xFFu), act_scale(sb));
+}
+
+// Walks the row pieces of a T x (pieces per row) grid in steps of a fixed number of warps, without a
+// division per step.
+struct PieceWalk {
+  int t, p;
+  int dt, dp, per;
+  __device__ __forceinline__ PieceWalk(size_t first, size_t step, int per_row) : per(per_row) {
+    t = (int)(first / per_row);
+    p = (int)(first - (size_t)t * per_row);
+    dt = (int)(step / per_row);
+    dp = (int)(step - (size_t)dt * per_row);
+  }
+  __device__ __forceinline__ void next() {
+    t += dt;
+    p += dp;
+    if (p >= per) {
+      p -= per;
+      ++t;
+    }
+  }
+};
+
+// Whether rows of d elements at x (32-byte accesses) and of d codes (16-byte) take the VEC layout.
+inline bool rows_vec(int d, const void *x, const void *codes) {
+  return d % 16 == 0 && ((uintptr_t)x & 31u) == 0 && ((uintptr_t)codes & 15u) == 0;
+}
 
 }  // namespace gift
