@@ -1323,7 +1323,7 @@ ActWs act_layout(void *base, const gift_ctx *ctx, gift_op op, gift_dtype dt, int
   ActWs w;
   Carve c(base ? reinterpret_cast<void *>(((uintptr_t)base + kAlign - 1) / kAlign * kAlign) : nullptr);
   if (op == GIFT_OP_LAYERNORM_BACKWARD) {
-    w.part = c.take<float>(norm_part_floats(T, d_in));
+    w.part = c.take<float>(norm_part_floats(ctx->sms, T, d_in));
   } else {
     const WeightGradWs g = weight_grad_layout(ctx->sms, dt == GIFT_DT_BF16, T, d_out, d_in);
     w.part = c.take<float>(g.part_floats);

@@ -349,7 +349,8 @@ struct NormBackward {
   float *dgamma, *dbeta;       // nullable
   float *part;                 // norm_part_floats
 };
-size_t norm_part_floats(int T, int d);
+size_t norm_part_floats(int sms, int T, int d);
+int norm_partials(int sms, int T);
 cudaError_t launch_norm_forward(const Launch &L, int fmt, bool bf16, const NormForward &a);
 cudaError_t launch_norm_backward(const Launch &L, int fmt, bool bf16, const NormBackward &a);
 // out[c] = sum_t x[t][c], slices of tokens added in order; part: col_part_floats

@@ -1,9 +1,17 @@
 // Layer norm forward and backward.
 //
-// Forward, one CTA per row: the mean, the sum of squared deviations, then y and (optionally) the
-// 8-bit checkpoint of the normalised row, a warp per group of 128 columns.
-// Backward: dx row by row (two sums over the row), and the sums over tokens of dy n and dy in
-// slices of consecutive tokens, the slices added in order.
+// Both hold a row's share in registers, 16 columns per lane and piece of 512 (act.cuh), and move each
+// byte once; HBM bounds them (forward 4 bytes an element for BF16, 5 with the checkpoint; backward 6,
+// or 5 from the checkpoint).
+//
+// Forward: a row belongs to one warp up to 2048 columns (no barrier at all), to 4, 8 or 16 warps
+// above.  The mean, then the squared deviations from it, are reduced from registers; y and the
+// checkpoint are written from them.
+//
+// Backward: sums over a row (h and h n) for dx, and sums over tokens (dy n and dy) for the gain's and
+// offset's gradients.  The latter stay in the registers of the thread that owns the column: a CTA
+// takes every gridDim-th row, adds its row groups' sums through shared memory at the end and writes
+// one partial; k_norm_sums adds the partials.  The order is fixed by the shape and the grid.
 #include "act.cuh"
 #include "kernels.cuh"
 
@@ -13,9 +21,319 @@ namespace {
 
 constexpr int kNormThreads = 256;
 
-__device__ __forceinline__ float block_sum(float v, float *sh /* kNormThreads / 32 */) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// wait for the programmatic predecessor's results / let the successor launch
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Row groups of `nw` warps within a CTA, and their sums: every warp of the group gets the total.  Two
+// buffers in turn, so that one barrier per sum is enough.
+struct RowGroup {
+  int nw, id, w;
+  float2 *sh;   // 2 x 16
+  int turn = 0;
+  __device__ __forceinline__ RowGroup(int nw_, float2 (*shared)[2][16]) : nw(nw_) {
+    const int warp = threadIdx.x >> 5;
+    id = warp / nw;
+    w = warp - id * nw;
+    sh = &shared[id][0][0];
+  }
+  __device__ __forceinline__ float2 sum(float2 v) {
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (nw == 1) return v;
+    const int lane = threadIdx.x & 31;
+    float2 *b = sh + 16 * turn;
+    turn ^= 1;
+    if (lane == 0) b[w] = v;
+    asm volatile("bar.sync %0, %1;\n" ::"r"(1 + id), "r"(32 * nw) : "memory");
+    v = lane < nw ? b[lane] : make_float2(0.0f, 0.0f);
+    return make_float2(warp_sum(v.x), warp_sum(v.y));
+  }
+};
+
+template <bool VEC>
+__device__ __forceinline__ bool in_row(int n, int lane, int e) { return (VEC ? 16 * lane : 32 * e + lane) < n; }
+
+// 16 per-column factors of a lane (c0: the piece's first column)
+template <bool VEC>
+__device__ __forceinline__ void load_cols(const float *p, int c0, int n, int lane, float fill, float *v) {
+  if (p == nullptr) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = fill;
+  } else if (VEC) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const float4 f = 16 * lane < n ? __ldg(reinterpret_cast<const float4 *>(p + c0 + 16 * lane + e))
+                                     : make_float4(fill, fill, fill, fill);
+      v[e] = f.x;
+      v[e + 1] = f.y;
+      v[e + 2] = f.z;
+      v[e + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 32 * e + lane < n ? __ldg(p + c0 + 32 * e + lane) : fill;
+  }
+}
+
+template <typename E, bool VEC, int U>
+__global__ void __launch_bounds__(512) k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt,
+                                                      int *status) {
+  __shared__ float2 red[16][2][16];
+  const int lane = threadIdx.x & 31, T = a.T, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
+  RowGroup G(nw, red);
+  const int per_cta = (int)(blockDim.x >> 5) / nw;
+  const float inv_d = __frcp_rn((float)d);
+  for (int t = blockIdx.x * per_cta + G.id; t < T; t += gridDim.x * per_cta) {
+    const size_t row = (size_t)t * d;
+    Raw<E> r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c0 = (G.w * U + u) * kPiece;
+      load_piece<VEC>(static_cast<const E *>(a.x) + row + c0, d - c0, lane, r[u]);
+    }
+    float x[U][16], s = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[u][e] = r[u].get(e);
+        s += x[u][e];
+      }
+    const float mean = G.sum(make_float2(s, 0.0f)).x * inv_d;
+    float q = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = d - (G.w * U + u) * kPiece;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[u][e] = in_row<VEC>(n, lane, e) ? x[u][e] - mean : 0.0f;
+        q = fmaf(x[u][e], x[u][e], q);
+      }
+    }
+    const float rstd = __frcp_rn(__fsqrt_rn(fmaf(G.sum(make_float2(q, 0.0f)).x, inv_d, a.eps)));
+    if (G.w == 0 && lane == 0) {
+      if (a.mean) a.mean[t] = mean;
+      if (a.rstd) a.rstd[t] = rstd;
+      if (!isfinite(mean) || !isfinite(rstd)) set_status(status, GIFT_ERR_NONFINITE);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c0 = (G.w * U + u) * kPiece, n = d - c0;
+      if (n > 0) {
+        float g[16], b[16], y[16];
+        load_cols<VEC>(a.gamma, c0, n, lane, 1.0f, g);
+        load_cols<VEC>(a.beta, c0, n, lane, 0.0f, b);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          x[u][e] *= rstd;
+          y[e] = fmaf(x[u][e], g[e], b[e]);
+        }
+        store_piece<VEC>(static_cast<E *>(a.y) + row + c0, n, lane, y);
+        if (a.codes) {
+          uint8_t *cp = a.codes + row + c0, *sp = a.scales + (size_t)t * groups + c0 / kActGroup;
+          if (fmt == FMT_E4M3) encode_piece<FMT_E4M3, VEC>(x[u], n, lane, cp, sp);
+          else encode_piece<FMT_E5M2, VEC>(x[u], n, lane, cp, sp);
+        }
+      }
+    }
+  }
+}
+
+// What the backward pass needs of a lane's 16 columns of a row, as loaded.
+template <typename E, bool SAVED>
+struct RowPiece {
+  Raw<E> dy;
+  Raw<E> x;
+};
+template <typename E>
+struct RowPiece<E, true> {
+  Raw<E> dy;
+  RawCodes x;
+};
+
+// U = 1: dx and the column sums.  U > 1 (rows over 8192 columns): dx alone, the column sums take
+// a pass of their own (k_norm_cols), since their 32 registers a piece do not fit beside the row's.
+template <typename E, bool VEC, bool SAVED, int U>
+__global__ void __launch_bounds__(512) k_norm_backward(const __grid_constant__ NormBackward a, int nw, int fmt,
+                                                       int *status) {
+  extern __shared__ float acc_sh[];
+  __shared__ float2 red[16][2][16];
+  grid_release();
+  const int lane = threadIdx.x & 31, T = a.T, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
+  RowGroup G(nw, red);
+  const int per_cta = (int)(blockDim.x >> 5) / nw, step = gridDim.x * per_cta;
+  const float inv_d = __frcp_rn((float)d);
+  float g[16], dg[16], db[16];   // U = 1: held for the CTA's rows
+  if (U == 1) load_cols<VEC>(a.gamma, G.w * kPiece, d - G.w * kPiece, lane, 1.0f, g);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) dg[e] = db[e] = 0.0f;
+  RowPiece<E, SAVED> now[U], next[1];
+  auto load = [&](int t, RowPiece<E, SAVED> *p) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c0 = (G.w * U + u) * kPiece, n = t < T ? d - c0 : 0;
+      const size_t at = (size_t)t * d + c0;
+      load_piece<VEC>(static_cast<const E *>(a.dy) + at, n, lane, p[u].dy);
+      if constexpr (SAVED) load_codes<VEC>(a.codes + at, a.scales + (size_t)t * groups + c0 / kActGroup, n, lane, p[u].x);
+      else load_piece<VEC>(static_cast<const E *>(a.x) + at, n, lane, p[u].x);
+    }
+  };
+  int t = blockIdx.x * per_cta + G.id;
+  if (U == 1) load(t, next);
+  for (; t < T; t += step) {
+    const float rstd = a.rstd[t], mean = SAVED ? 0.0f : a.mean[t];
+    if (U == 1) {
+      now[0] = next[0];
+      load(t + step, next);
+    } else {
+      load(t, now);
+    }
+    auto n_of = [&](int u, int e) -> float {
+      if constexpr (SAVED)
+        return fmt == FMT_E4M3 ? code_value<FMT_E4M3, VEC>(now[u].x, e) : code_value<FMT_E5M2, VEC>(now[u].x, e);
+      else
+        return (now[u].x.get(e) - mean) * rstd;
+    };
+    float2 s = make_float2(0.0f, 0.0f);
+    float keep[16];   // U = 1: n
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (U > 1) load_cols<VEC>(a.gamma, (G.w * U + u) * kPiece, d - (G.w * U + u) * kPiece, lane, 1.0f, g);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float dy = now[u].dy.get(e), h = dy * g[e], n = n_of(u, e);
+        if (U == 1) {
+          keep[e] = n;
+          dg[e] = fmaf(dy, n, dg[e]);
+          db[e] += dy;
+        }
+        s.x += h;
+        s.y = fmaf(h, n, s.y);
+      }
+    }
+    s = G.sum(s);
+    if (G.w == 0 && lane == 0 && !(isfinite(s.x) && isfinite(s.y) && isfinite(rstd)))
+      set_status(status, GIFT_ERR_NONFINITE);
+    const float ma = s.x * inv_d, mb = s.y * inv_d;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c0 = (G.w * U + u) * kPiece;
+      if (U > 1) load_cols<VEC>(a.gamma, c0, d - c0, lane, 1.0f, g);
+      float dx[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        dx[e] = rstd * (fmaf(now[u].dy.get(e), g[e], -ma) - (U == 1 ? keep[e] : n_of(u, e)) * mb);
+      store_piece<VEC>(static_cast<E *>(a.dx) + (size_t)t * d + c0, d - c0, lane, dx);
+    }
+  }
+  if (U > 1 || !a.part) return;
+  // the CTA's partial: the row groups' sums in order, through shared memory where there are several
+  float *out = a.part + (size_t)2 * blockIdx.x * d;
+  for (int k = 0; k < per_cta; ++k) {
+    if (k > 0) __syncthreads();
+    if (G.id == k) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int c = G.w * kPiece + piece_col<VEC>(lane, e);
+        float *sg = acc_sh + c, *sb = acc_sh + nw * kPiece + c;
+        if (k > 0) {
+          dg[e] = *sg + dg[e];
+          db[e] = *sb + db[e];
+        }
+        if (k + 1 < per_cta) {
+          *sg = dg[e];
+          *sb = db[e];
+        } else if (c < d) {
+          out[c] = dg[e];
+          out[d + c] = db[e];
+        }
+      }
+    }
+  }
+}
+
+// The column sums alone: a warp takes one piece of the columns over a slice of consecutive tokens;
+// part[2 slice] = sum dy n, part[2 slice + 1] = sum dy.
+template <typename E, bool VEC, bool SAVED>
+__global__ void __launch_bounds__(kNormThreads) k_norm_cols(const __grid_constant__ NormBackward a, int fmt, int rows) {
+  const int lane = threadIdx.x & 31, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
+  const int c0 = (blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5)) * kPiece, n = d - c0;
+  grid_release();
+  if (n <= 0) return;
+  float dg[16], db[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) dg[e] = db[e] = 0.0f;
+  const int t1 = min(a.T, (int)(blockIdx.y + 1) * rows);
+#pragma unroll 2
+  for (int t = blockIdx.y * rows; t < t1; ++t) {
+    const size_t at = (size_t)t * d + c0;
+    RowPiece<E, SAVED> p;
+    load_piece<VEC>(static_cast<const E *>(a.dy) + at, n, lane, p.dy);
+    float rstd = 1.0f, mean = 0.0f;
+    if constexpr (SAVED) {
+      load_codes<VEC>(a.codes + at, a.scales + (size_t)t * groups + c0 / kActGroup, n, lane, p.x);
+    } else {
+      load_piece<VEC>(static_cast<const E *>(a.x) + at, n, lane, p.x);
+      rstd = a.rstd[t];
+      mean = a.mean[t];
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float dy = p.dy.get(e);
+      float v;
+      if constexpr (SAVED)
+        v = fmt == FMT_E4M3 ? code_value<FMT_E4M3, VEC>(p.x, e) : code_value<FMT_E5M2, VEC>(p.x, e);
+      else
+        v = (p.x.get(e) - mean) * rstd;
+      dg[e] = fmaf(dy, v, dg[e]);
+      db[e] += dy;
+    }
+  }
+  float *out = a.part + (size_t)2 * blockIdx.y * d;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int c = c0 + piece_col<VEC>(lane, e);
+    if (c < d) {
+      out[c] = dg[e];
+      out[d + c] = db[e];
+    }
+  }
+}
+
+// out[c] = sum over partials of part[k stride + c]: 32 columns per CTA, eight warps take every eighth
+// partial, their sums are added in order.  blockIdx.y: the first or the second output.
+__global__ void __launch_bounds__(kNormThreads) k_norm_sums(const float *__restrict__ part, int parts, size_t stride,
+                                                            size_t second, int d, float *out0, float *out1) {
+  __shared__ float sh[8][32];
+  grid_wait();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float *out = blockIdx.y ? out1 : out0;
+  if (!out) return;
+  const float *p = part + blockIdx.y * second + c;
+  float s = 0.0f;
+  if (c < d) {
+#pragma unroll 8
+    for (int k = w; k < parts; k += 8) s += p[k * stride];
+  }
+  sh[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < d) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += sh[k][lane];
+    out[c] = s;
+  }
+}
+
+// ---- rows too long for registers: column by column, the row read once per sum --------------------------
+__device__ __forceinline__ float cta_sum(float v, float *sh /* kNormThreads / 32 */) {
+  v = warp_sum(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
   __syncthreads();
@@ -25,109 +343,84 @@ __device__ __forceinline__ float block_sum(float v, float *sh /* kNormThreads / 
   return r;
 }
 
-template <int F, typename E>
-__global__ void __launch_bounds__(kNormThreads) k_norm_forward(const E *__restrict__ x, int T, int d,
-                                                               const float *__restrict__ gamma,
-                                                               const float *__restrict__ beta, float eps,
-                                                               E *__restrict__ y, float *__restrict__ mean_out,
-                                                               float *__restrict__ rstd_out,
-                                                               uint8_t *__restrict__ codes,
-                                                               uint8_t *__restrict__ scales, int *status) {
+template <typename E>
+__global__ void __launch_bounds__(kNormThreads) k_norm_forward_long(const __grid_constant__ NormForward a, int fmt,
+                                                                    int *status) {
   __shared__ float sh[kNormThreads / 32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.d;
   const int groups = (d + kActGroup - 1) / kActGroup;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    const E *xr = x + (size_t)t * d;
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const size_t row = (size_t)t * d;
+    const E *xr = static_cast<const E *>(a.x) + row;
     float s = 0.0f;
     for (int c = threadIdx.x; c < d; c += kNormThreads) s += ld1(xr + c);
-    const float mean = __fdiv_rn(block_sum(s, sh), (float)d);
+    const float mean = __fdiv_rn(cta_sum(s, sh), (float)d);
     float q = 0.0f;
     for (int c = threadIdx.x; c < d; c += kNormThreads) {
       const float u = ld1(xr + c) - mean;
       q = fmaf(u, u, q);
     }
-    const float rstd = __frcp_rn(__fsqrt_rn(__fdiv_rn(block_sum(q, sh), (float)d) + eps));
+    const float rstd = __frcp_rn(__fsqrt_rn(__fdiv_rn(cta_sum(q, sh), (float)d) + a.eps));
     if (threadIdx.x == 0) {
-      if (mean_out) mean_out[t] = mean;
-      if (rstd_out) rstd_out[t] = rstd;
+      if (a.mean) a.mean[t] = mean;
+      if (a.rstd) a.rstd[t] = rstd;
       if (!isfinite(mean) || !isfinite(rstd)) set_status(status, GIFT_ERR_NONFINITE);
     }
-    for (int g = warp; g < groups; g += kNormThreads / 32) {
-      float n[4];
-      uint32_t m = 0;
+    for (int c0 = warp * kPiece; c0 < d; c0 += kNormThreads / 32 * kPiece) {
+      const int n = d - c0;
+      Raw<E> r;
+      load_piece<false>(xr + c0, n, lane, r);
+      float x[16], g[16], b[16], y[16];
+      load_cols<false>(a.gamma, c0, n, lane, 1.0f, g);
+      load_cols<false>(a.beta, c0, n, lane, 0.0f, b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = g * kActGroup + lane + 32 * i;
-        n[i] = c < d ? (ld1(xr + c) - mean) * rstd : 0.0f;
-        m = max(m, abs_bits(n[i]));
-        if (c < d) st1(y + (size_t)t * d + c, fmaf(n[i], gamma ? gamma[c] : 1.0f, beta ? beta[c] : 0.0f));
+      for (int e = 0; e < 16; ++e) {
+        x[e] = in_row<false>(n, lane, e) ? (r.get(e) - mean) * rstd : 0.0f;
+        y[e] = fmaf(x[e], g[e], b[e]);
       }
-      if (codes) {
-        const uint32_t sb = act_scale_byte<F>(warp_max_u32(m));
-        const float inv = act_inv_scale(sb == kActBad ? 127u : sb);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = g * kActGroup + lane + 32 * i;
-          if (c < d) codes[(size_t)t * d + c] = pack1_fp8<F>(__fmul_rn(n[i], inv));
-        }
-        if (lane == 0) scales[(size_t)t * groups + g] = (uint8_t)sb;
+      store_piece<false>(static_cast<E *>(a.y) + row + c0, n, lane, y);
+      if (a.codes) {
+        uint8_t *cp = a.codes + row + c0, *sp = a.scales + (size_t)t * groups + c0 / kActGroup;
+        if (fmt == FMT_E4M3) encode_piece<FMT_E4M3, false>(x, n, lane, cp, sp);
+        else encode_piece<FMT_E5M2, false>(x, n, lane, cp, sp);
       }
     }
   }
 }
 
 // The normalised element (t, c) from what the forward pass kept.
-template <int F, typename E>
-struct Saved {
-  const E *x;             // or the checkpoint
-  const uint8_t *codes, *scales;
-  const float *mean, *rstd;
-  int d, groups;
-  __device__ __forceinline__ float at(int t, int c) const {
-    const size_t i = (size_t)t * d + c;
-    if (codes) return dec_fp8<F>(codes[i]) * act_scale(scales[(size_t)t * groups + c / kActGroup]);
-    return (ld1(x + i) - mean[t]) * rstd[t];
+template <typename E>
+__device__ __forceinline__ float saved_at(const NormBackward &a, int fmt, int groups, int t, int c) {
+  const size_t i = (size_t)t * a.d + c;
+  if (a.codes) {
+    const float s = act_scale(a.scales[(size_t)t * groups + c / kActGroup]);
+    return (fmt == FMT_E4M3 ? dec_e4m3(a.codes[i]) : dec_e5m2(a.codes[i])) * s;
   }
-};
-
-template <int F, typename E>
-__global__ void __launch_bounds__(kNormThreads) k_norm_dx(const E *__restrict__ dy, const Saved<F, E> S, int T, int d,
-                                                          const float *__restrict__ gamma, E *__restrict__ dx,
-                                                          int *status) {
-  __shared__ float sh[kNormThreads / 32];
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    float a = 0.0f, b = 0.0f;
-    for (int c = threadIdx.x; c < d; c += kNormThreads) {
-      const float h = ld1(dy + (size_t)t * d + c) * (gamma ? gamma[c] : 1.0f);
-      a += h;
-      b = fmaf(h, S.at(t, c), b);
-    }
-    a = __fdiv_rn(block_sum(a, sh), (float)d);
-    b = __fdiv_rn(block_sum(b, sh), (float)d);
-    const float rstd = S.rstd[t];
-    if (threadIdx.x == 0 && !(isfinite(a) && isfinite(b) && isfinite(rstd))) set_status(status, GIFT_ERR_NONFINITE);
-    for (int c = threadIdx.x; c < d; c += kNormThreads) {
-      const float h = ld1(dy + (size_t)t * d + c) * (gamma ? gamma[c] : 1.0f);
-      st1(dx + (size_t)t * d + c, rstd * (h - a - S.at(t, c) * b));
-    }
-  }
+  return (ld1(static_cast<const E *>(a.x) + i) - a.mean[t]) * a.rstd[t];
 }
 
-// partials of one slice of consecutive tokens: part[2 slice] = sum dy n, part[2 slice + 1] = sum dy
-template <int F, typename E>
-__global__ void __launch_bounds__(kNormThreads) k_norm_cols(const E *__restrict__ dy, const Saved<F, E> S, int T,
-                                                            int d, int rows, float *__restrict__ part) {
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
-  if (c >= d) return;
-  const int t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
-  float g = 0.0f, b = 0.0f;
-  for (int t = t0; t < t1; ++t) {
-    const float v = ld1(dy + (size_t)t * d + c);
-    g = fmaf(v, S.at(t, c), g);
-    b += v;
+template <typename E>
+__global__ void __launch_bounds__(kNormThreads) k_norm_dx_long(const __grid_constant__ NormBackward A, int fmt,
+                                                               int *status) {
+  __shared__ float sh[kNormThreads / 32];
+  const int d = A.d, groups = (d + kActGroup - 1) / kActGroup;
+  for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
+    const E *dy = static_cast<const E *>(A.dy) + (size_t)t * d;
+    float a = 0.0f, b = 0.0f;
+    for (int c = threadIdx.x; c < d; c += kNormThreads) {
+      const float h = ld1(dy + c) * (A.gamma ? A.gamma[c] : 1.0f);
+      a += h;
+      b = fmaf(h, saved_at<E>(A, fmt, groups, t, c), b);
+    }
+    a = __fdiv_rn(cta_sum(a, sh), (float)d);
+    b = __fdiv_rn(cta_sum(b, sh), (float)d);
+    const float rstd = A.rstd[t];
+    if (threadIdx.x == 0 && !(isfinite(a) && isfinite(b) && isfinite(rstd))) set_status(status, GIFT_ERR_NONFINITE);
+    for (int c = threadIdx.x; c < d; c += kNormThreads) {
+      const float h = ld1(dy + c) * (A.gamma ? A.gamma[c] : 1.0f);
+      st1(static_cast<E *>(A.dx) + (size_t)t * d + c, rstd * (h - a - saved_at<E>(A, fmt, groups, t, c) * b));
+    }
   }
-  part[(size_t)(2 * blockIdx.y) * d + c] = g;
-  part[(size_t)(2 * blockIdx.y + 1) * d + c] = b;
 }
 
 // sums over tokens of one matrix, in slices
@@ -135,6 +428,7 @@ template <typename E>
 __global__ void __launch_bounds__(kNormThreads) k_col_sums(const E *__restrict__ x, int T, int d, int rows,
                                                            float *__restrict__ part) {
   const int c = blockIdx.x * kNormThreads + threadIdx.x;
+  grid_release();
   if (c >= d) return;
   const int t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
   float s = 0.0f;
@@ -142,64 +436,169 @@ __global__ void __launch_bounds__(kNormThreads) k_col_sums(const E *__restrict__
   part[(size_t)blockIdx.y * d + c] = s;
 }
 
-// out[c] = sum over slices of part[slice stride + c]
-__global__ void __launch_bounds__(kNormThreads) k_sum_parts(const float *__restrict__ part, int slices, size_t stride,
-                                                            int d, float *__restrict__ out) {
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
-  if (c >= d) return;
-  float s = 0.0f;
-  for (int i = 0; i < slices; ++i) s += part[(size_t)i * stride + c];
-  out[c] = s;
-}
-
-constexpr int kColRows = 128;   // tokens of a slice, at least
+// ---- host ---------------------------------------------------------------------------------------------
+constexpr int kColRows = 128;      // tokens of a slice, at least
 
 int col_rows(int T) {   // at most 256 slices
   const int r = (T + 255) / 256;
   return r < kColRows ? kColRows : r;
 }
 
-template <int F, typename E>
-cudaError_t backward(const Launch &L, const NormBackward &a) {
-  Saved<F, E> S;
-  S.x = a.codes ? nullptr : static_cast<const E *>(a.x);
-  S.codes = a.codes;
-  S.scales = a.scales;
-  S.mean = a.mean;
-  S.rstd = a.rstd;
-  S.d = a.d;
-  S.groups = (a.d + kActGroup - 1) / kActGroup;
-  const E *dy = static_cast<const E *>(a.dy);
-  const int grid = a.T < L.sms * 8 ? a.T : L.sms * 8;
-  k_norm_dx<F, E><<<grid, kNormThreads, 0, L.stream>>>(dy, S, a.T, a.d, a.gamma, static_cast<E *>(a.dx), L.status);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || (!a.dgamma && !a.dbeta)) return e;
-  const int rows = col_rows(a.T), slices = (a.T + rows - 1) / rows, cb = (a.d + kNormThreads - 1) / kNormThreads;
-  k_norm_cols<F, E><<<dim3(cb, slices), kNormThreads, 0, L.stream>>>(dy, S, a.T, a.d, rows, a.part);
-  if (a.dgamma)
-    k_sum_parts<<<cb, kNormThreads, 0, L.stream>>>(a.part, slices, (size_t)2 * a.d, a.d, a.dgamma);
-  if (a.dbeta)
-    k_sum_parts<<<cb, kNormThreads, 0, L.stream>>>(a.part + a.d, slices, (size_t)2 * a.d, a.d, a.dbeta);
+bool cols_aligned(const float *p) { return !p || aligned16(p); }
+
+// CTAs of a persistent launch: what is resident on the context's SMs, at most one per `per_cta` rows
+template <typename K>
+int resident(K kernel, const Launch &L, int threads, int smem, int T, int per_cta) {
+  int per_sm = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+    per_sm = 1;
+  const long long most = (long long)L.sms * per_sm, need = ((long long)T + per_cta - 1) / per_cta;
+  return (int)(need < most ? need : most);
+}
+
+// launch with the programmatic dependency that grid_wait() ends
+template <typename... P, typename... Q>
+cudaError_t launch_after(cudaStream_t s, void (*kernel)(P...), dim3 grid, int threads, Q... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// Rows by registers: pieces per lane and warps per row.
+struct RowPlan {
+  int u, nw, threads;
+};
+
+// Forward: up to 4 pieces in one warp (2048 columns); then 2 or 4 pieces in 4, 8 or 16 warps.
+bool forward_plan(int d, RowPlan *p) {
+  const int pieces = (d + kPiece - 1) / kPiece;
+  if (pieces > 64) return false;
+  if (pieces <= 4) *p = {pieces, 1, 256};
+  else if (pieces <= 8) *p = {2, 4, 256};
+  else if (pieces <= 16) *p = {2, 8, 256};
+  else if (pieces <= 32) *p = {4, 8, 256};
+  else *p = {4, 16, 512};
+  return true;
+}
+
+// Backward: up to 8192 columns one piece per lane and as many warps per row as pieces (CTAs of 8 to
+// 16 warps), with the column sums; up to 32768 two or four pieces per lane, without them.
+bool backward_plan(int d, RowPlan *p) {
+  const int pieces = (d + kPiece - 1) / kPiece;
+  if (pieces > 64) return false;
+  p->u = pieces <= 16 ? 1 : pieces <= 32 ? 2 : 4;
+  p->nw = (pieces + p->u - 1) / p->u;
+  p->threads = 32 * p->nw * (p->nw >= 8 ? 1 : 8 / p->nw);
+  return true;
+}
+
+template <typename E, bool VEC, int U>
+cudaError_t forward(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
+  const int per_cta = p.threads / 32 / p.nw;
+  const int grid = resident(k_norm_forward<E, VEC, U>, L, p.threads, 0, a.T, per_cta);
+  k_norm_forward<E, VEC, U><<<grid, p.threads, 0, L.stream>>>(a, p.nw, fmt, L.status);
   return cudaGetLastError();
 }
 
-template <int F, typename E>
-cudaError_t forward(const Launch &L, const NormForward &a) {
+template <typename E, bool VEC>
+cudaError_t forward_u(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
+  switch (p.u) {
+    case 1: return forward<E, VEC, 1>(L, fmt, a, p);
+    case 2: return forward<E, VEC, 2>(L, fmt, a, p);
+    case 3: return forward<E, VEC, 3>(L, fmt, a, p);
+    default: return forward<E, VEC, 4>(L, fmt, a, p);
+  }
+}
+
+template <typename E>
+cudaError_t forward_e(const Launch &L, int fmt, const NormForward &a) {
+  RowPlan p;
+  if (!forward_plan(a.d, &p)) {
+    const int grid = a.T < L.sms * 8 ? a.T : L.sms * 8;
+    k_norm_forward_long<E><<<grid, kNormThreads, 0, L.stream>>>(a, fmt, L.status);
+    return cudaGetLastError();
+  }
+  const bool vec = rows_vec(a.d, a.x, a.codes) && rows_vec(a.d, a.y, nullptr) && cols_aligned(a.gamma) &&
+                   cols_aligned(a.beta);
+  return vec ? forward_u<E, true>(L, fmt, a, p) : forward_u<E, false>(L, fmt, a, p);
+}
+
+cudaError_t sums_after(const Launch &L, const NormBackward &a, int parts) {
+  return launch_after(L.stream, k_norm_sums, dim3((a.d + 31) / 32, 2), kNormThreads, a.part, parts, (size_t)2 * a.d,
+                      (size_t)a.d, a.d, a.dgamma, a.dbeta);
+}
+
+template <typename E, bool VEC, bool SAVED>
+cudaError_t column_pass(const Launch &L, int fmt, const NormBackward &a) {
+  if (!a.part) return cudaSuccess;
+  const int rows = col_rows(a.T), slices = (a.T + rows - 1) / rows, per = kNormThreads / 32 * kPiece;
+  k_norm_cols<E, VEC, SAVED><<<dim3((a.d + per - 1) / per, slices), kNormThreads, 0, L.stream>>>(a, fmt, rows);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : sums_after(L, a, slices);
+}
+
+template <typename E, bool VEC, bool SAVED, int U>
+cudaError_t backward(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
+  const int per_cta = p.threads / 32 / p.nw, smem = U == 1 && per_cta > 1 ? 2 * p.nw * kPiece * 4 : 0;
+  int grid = resident(k_norm_backward<E, VEC, SAVED, U>, L, p.threads, smem, a.T, per_cta);
+  if (grid > norm_partials(L.sms, a.T)) grid = norm_partials(L.sms, a.T);
+  k_norm_backward<E, VEC, SAVED, U><<<grid, p.threads, smem, L.stream>>>(a, p.nw, fmt, L.status);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (U > 1) return column_pass<E, VEC, SAVED>(L, fmt, a);
+  return a.part ? sums_after(L, a, grid) : cudaSuccess;
+}
+
+template <typename E, bool VEC, bool SAVED>
+cudaError_t backward_s(const Launch &L, int fmt, const NormBackward &a) {
+  RowPlan p;
+  if (backward_plan(a.d, &p)) {
+    switch (p.u) {
+      case 1: return backward<E, VEC, SAVED, 1>(L, fmt, a, p);
+      case 2: return backward<E, VEC, SAVED, 2>(L, fmt, a, p);
+      default: return backward<E, VEC, SAVED, 4>(L, fmt, a, p);
+    }
+  }
   const int grid = a.T < L.sms * 8 ? a.T : L.sms * 8;
-  k_norm_forward<F, E><<<grid, kNormThreads, 0, L.stream>>>(static_cast<const E *>(a.x), a.T, a.d, a.gamma, a.beta,
-                                                            a.eps, static_cast<E *>(a.y), a.mean, a.rstd, a.codes,
-                                                            a.scales, L.status);
-  return cudaGetLastError();
+  k_norm_dx_long<E><<<grid, kNormThreads, 0, L.stream>>>(a, fmt, L.status);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : column_pass<E, VEC, SAVED>(L, fmt, a);
+}
+
+template <typename E>
+cudaError_t backward_e(const Launch &L, int fmt, const NormBackward &a) {
+  const bool vec = rows_vec(a.d, a.dy, a.codes) && rows_vec(a.d, a.dx, nullptr) && rows_vec(a.d, a.x, nullptr) &&
+                   cols_aligned(a.gamma);
+  if (a.codes) return vec ? backward_s<E, true, true>(L, fmt, a) : backward_s<E, false, true>(L, fmt, a);
+  return vec ? backward_s<E, true, false>(L, fmt, a) : backward_s<E, false, false>(L, fmt, a);
 }
 
 }  // namespace
 
-size_t norm_part_floats(int T, int d) {
+// partials of the backward pass: a CTA each, at most four per SM
+int norm_partials(int sms, int T) {
+  const long long most = (long long)sms * 4;
+  return (int)(T < most ? T : most);
+}
+
+size_t norm_part_floats(int sms, int T, int d) {
+  RowPlan p;
+  if (backward_plan(d, &p) && p.u == 1) return (size_t)2 * norm_partials(sms, T) * d;
   const int rows = col_rows(T);
   return (size_t)2 * ((T + rows - 1) / rows) * d;
 }
 
-size_t col_part_floats(int T, int d) { return norm_part_floats(T, d) / 2; }
+size_t col_part_floats(int T, int d) {
+  const int rows = col_rows(T);
+  return (size_t)((T + rows - 1) / rows) * d;
+}
 
 cudaError_t launch_col_sums(const Launch &L, const void *x, bool bf16, int T, int d, float *part, float *out) {
   const int rows = col_rows(T), slices = (T + rows - 1) / rows, cb = (d + kNormThreads - 1) / kNormThreads;
@@ -207,20 +606,16 @@ cudaError_t launch_col_sums(const Launch &L, const void *x, bool bf16, int T, in
     k_col_sums<<<dim3(cb, slices), kNormThreads, 0, L.stream>>>(static_cast<const __nv_bfloat16 *>(x), T, d, rows, part);
   else
     k_col_sums<<<dim3(cb, slices), kNormThreads, 0, L.stream>>>(static_cast<const float *>(x), T, d, rows, part);
-  k_sum_parts<<<cb, kNormThreads, 0, L.stream>>>(part, slices, (size_t)d, d, out);
-  return cudaGetLastError();
+  return launch_after(L.stream, k_norm_sums, dim3((d + 31) / 32, 1), kNormThreads, part, slices, (size_t)d, (size_t)0,
+                      d, out, static_cast<float *>(nullptr));
 }
 
 cudaError_t launch_norm_forward(const Launch &L, int fmt, bool bf16, const NormForward &a) {
-  if (fmt == FMT_E4M3)
-    return bf16 ? forward<FMT_E4M3, __nv_bfloat16>(L, a) : forward<FMT_E4M3, float>(L, a);
-  return bf16 ? forward<FMT_E5M2, __nv_bfloat16>(L, a) : forward<FMT_E5M2, float>(L, a);
+  return bf16 ? forward_e<__nv_bfloat16>(L, fmt, a) : forward_e<float>(L, fmt, a);
 }
 
 cudaError_t launch_norm_backward(const Launch &L, int fmt, bool bf16, const NormBackward &a) {
-  if (fmt == FMT_E4M3)
-    return bf16 ? backward<FMT_E4M3, __nv_bfloat16>(L, a) : backward<FMT_E4M3, float>(L, a);
-  return bf16 ? backward<FMT_E5M2, __nv_bfloat16>(L, a) : backward<FMT_E5M2, float>(L, a);
+  return bf16 ? backward_e<__nv_bfloat16>(L, fmt, a) : backward_e<float>(L, fmt, a);
 }
 
 }  // namespace gift
