@@ -28,9 +28,9 @@ __global__ void __launch_bounds__(kActThreads) k_act_encode(const E *__restrict_
     const size_t at = (size_t)w.t * d + c0;
     Raw<E> r;
     load_piece<VEC>(x + at, n, lane, r);
-    float v[16];
+    float2 v[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = r.get(e);
+    for (int k = 0; k < 8; ++k) v[k] = r.pair(k);
     bad |= encode_piece<F, VEC>(v, n, lane, codes + at, scales + (size_t)w.t * groups + w.p * 4);
   }
   if (bad) set_status(status, GIFT_ERR_NONFINITE);
@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(kActThreads) k_act_decode(const uint8_t *__res
     const size_t at = (size_t)w.t * d + c0;
     RawCodes r;
     load_codes<VEC>(codes + at, scales + (size_t)w.t * groups + w.p * 4, n, lane, r);
-    float v[16];
+    float2 v[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = code_value<F, VEC>(r, e);
+    for (int k = 0; k < 8; ++k) v[k] = code_pair<F, VEC>(r, k);
     store_piece<VEC>(out + at, n, lane, v);
     // a marked group's first value is NaN whatever its code
     bad |= VEC ? r.s == kActBad

@@ -63,20 +63,49 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
+// Two FP32 operations at once, each rounded to nearest.
+__device__ __forceinline__ uint64_t as_b64(float2 v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 as_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_b64(a)), "l"(as_b64(b)));
+  return as_f32x2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_b64(a)), "l"(as_b64(b)));
+  return as_f32x2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_b64(a)), "l"(as_b64(b)), "l"(as_b64(c)));
+  return as_f32x2(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // The element type's registers for a lane's 16 columns of a piece, as loaded.
 template <typename E>
 struct Raw;
 template <>
 struct Raw<float> {
   uint32_t r[16];
-  __device__ __forceinline__ float get(int e) const { return __uint_as_float(r[e]); }
-  __device__ __forceinline__ void put(int e, float v) { r[e] = __float_as_uint(v); }
+  __device__ __forceinline__ float2 pair(int k) const {   // elements 2 k and 2 k + 1
+    return make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+  }
 };
 template <>
 struct Raw<__nv_bfloat16> {
   uint32_t r[8];
-  __device__ __forceinline__ float get(int e) const {
-    return __uint_as_float(e & 1 ? r[e / 2] & 0xFFFF0000u : r[e / 2] << 16);
+  __device__ __forceinline__ float2 pair(int k) const {
+    return make_float2(__uint_as_float(r[k] << 16), __uint_as_float(r[k] & 0xFFFF0000u));
   }
 };
 
@@ -120,57 +149,60 @@ __device__ __forceinline__ void load_piece(const __nv_bfloat16 *p, int n, int la
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store_piece(float *p, int n, int lane, const float *v) {
+__device__ __forceinline__ void store_piece(float *p, int n, int lane, const float2 *v) {
   if (VEC) {
     if (16 * lane < n) {
       uint32_t r[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(v[e]);
+      for (int k = 0; k < 8; ++k) {
+        r[2 * k] = __float_as_uint(v[k].x);
+        r[2 * k + 1] = __float_as_uint(v[k].y);
+      }
       st256(p + 16 * lane, r);
       st256(p + 16 * lane + 8, r + 8);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      if (32 * e + lane < n) p[32 * e + lane] = v[e];
+      if (32 * e + lane < n) p[32 * e + lane] = e & 1 ? v[e / 2].y : v[e / 2].x;
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void store_piece(__nv_bfloat16 *p, int n, int lane, const float *v) {
+__device__ __forceinline__ void store_piece(__nv_bfloat16 *p, int n, int lane, const float2 *v) {
   if (VEC) {
     if (16 * lane < n) {
       uint32_t r[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+      for (int k = 0; k < 8; ++k) r[k] = pack_bf16(v[k].x, v[k].y);
       st256(p + 16 * lane, r);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      if (32 * e + lane < n) p[32 * e + lane] = __float2bfloat16_rn(v[e]);
+      if (32 * e + lane < n) p[32 * e + lane] = __float2bfloat16_rn(e & 1 ? v[e / 2].y : v[e / 2].x);
   }
 }
 
 // Encode a lane's 16 values: codes to cp, the piece's scale bytes to sp.  Returns whether a group was
 // marked.  All lanes of the warp call it.
 template <int F, bool VEC>
-__device__ __forceinline__ bool encode_piece(const float *v, int n, int lane, uint8_t *cp, uint8_t *sp) {
+__device__ __forceinline__ bool encode_piece(const float2 *v, int n, int lane, uint8_t *cp, uint8_t *sp) {
   if (VEC) {
     uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) m = max(m, abs_bits(v[e]));
+    for (int k = 0; k < 8; ++k) m = max(m, max(abs_bits(v[k].x), abs_bits(v[k].y)));
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const uint32_t sb = act_scale_byte<F>(m);
-    const float inv = act_inv_scale(sb);
+    const float2 inv = both(act_inv_scale(sb));
     if (16 * lane < n) {
-      uint4 c;
-      uint32_t *w = &c.x;
+      uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = pack4_fp8<F>(__fmul_rn(v[4 * k], inv), __fmul_rn(v[4 * k + 1], inv), __fmul_rn(v[4 * k + 2], inv),
-                            __fmul_rn(v[4 * k + 3], inv));
-      *reinterpret_cast<uint4 *>(cp + 16 * lane) = c;
+      for (int k = 0; k < 4; ++k) {
+        const float2 a = mul2(v[2 * k], inv), b = mul2(v[2 * k + 1], inv);
+        w[k] = pack4_fp8<F>(a.x, a.y, b.x, b.y);
+      }
+      *reinterpret_cast<uint4 *>(cp + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
       if ((lane & 7) == 0) sp[lane >> 3] = (uint8_t)sb;
     }
     return sb == kActBad;
@@ -178,15 +210,15 @@ __device__ __forceinline__ bool encode_piece(const float *v, int n, int lane, ui
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 4 * k; e < 4 * k + 4; ++e) m = max(m, abs_bits(v[e]));
-    const uint32_t sb = act_scale_byte<F>(warp_max_u32(m));
+    const float2 a = v[2 * k], b = v[2 * k + 1];
+    const uint32_t sb = act_scale_byte<F>(
+        warp_max_u32(max(max(abs_bits(a.x), abs_bits(a.y)), max(abs_bits(b.x), abs_bits(b.y)))));
     const float inv = act_inv_scale(sb);
     bad |= sb == kActBad;
+    const uint32_t w = pack4_fp8<F>(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv), __fmul_rn(b.x, inv), __fmul_rn(b.y, inv));
 #pragma unroll
-    for (int e = 4 * k; e < 4 * k + 4; ++e)
-      if (32 * e + lane < n) cp[32 * e + lane] = pack1_fp8<F>(__fmul_rn(v[e], inv));
+    for (int e = 0; e < 4; ++e)
+      if (32 * (4 * k + e) + lane < n) cp[32 * (4 * k + e) + lane] = (uint8_t)(w >> (8 * e));
     if (lane == 0 && kActGroup * k < n) sp[k] = (uint8_t)sb;
   }
   return bad;
@@ -224,11 +256,19 @@ __device__ __forceinline__ void load_codes(const uint8_t *cp, const uint8_t *sp,
     x.s = s;
   }
 }
-// the value of element e
+// The values of elements 2 k and 2 k + 1 (of one group in either layout): the hardware's conversion to
+// FP16 holds every code exactly, and so does FP32.
 template <int F, bool VEC>
-__device__ __forceinline__ float code_value(const RawCodes &x, int e) {
-  const uint32_t sb = VEC ? x.s : (x.s >> (8 * (e >> 2))) & 0xFFu;
-  return __fmul_rn(dec_fp8<F>((x.c[e >> 2] >> (8 * (e & 3))) & 0xFFu), act_scale(sb));
+__device__ __forceinline__ float2 code_pair(const RawCodes &x, int k) {
+  const uint16_t c = (uint16_t)(k & 1 ? x.c[k >> 1] >> 16 : x.c[k >> 1] & 0xFFFFu);
+  uint32_t h;
+  if (F == FMT_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(c));
+  float2 v;
+  asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(v.x), "=f"(v.y)
+      : "r"(h));
+  return mul2(v, both(act_scale(VEC ? x.s : (x.s >> (8 * (k >> 1))) & 0xFFu)));
 }
 
 // Walks the row pieces of a T x (pieces per row) grid in steps of a fixed number of warps, without a

@@ -4,9 +4,8 @@
 // byte once; HBM bounds them (forward 4 bytes an element for BF16, 5 with the checkpoint; backward 6,
 // or 5 from the checkpoint).
 //
-// Forward: a row belongs to one warp up to 2048 columns (no barrier at all), to 4, 8 or 16 warps
-// above.  The mean, then the squared deviations from it, are reduced from registers; y and the
-// checkpoint are written from them.
+// Forward: a row belongs to a group of warps, one per piece up to 8192 columns.  Its mean and squared
+// deviations are reduced from registers; y and the checkpoint are written from them.
 //
 // Backward: sums over a row (h and h n) for dx, and sums over tokens (dy n and dy) for the gain's and
 // offset's gradients.  The latter stay in the registers of the thread that owns the column: a CTA
@@ -43,81 +42,117 @@ struct RowGroup {
     w = warp - id * nw;
     sh = &shared[id][0][0];
   }
-  __device__ __forceinline__ float2 sum(float2 v) {
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
-    if (nw == 1) return v;
+  // every warp's v; lane k < nw gets warp k's, the others zeros
+  __device__ __forceinline__ float2 share(float2 v) {
     const int lane = threadIdx.x & 31;
     float2 *b = sh + 16 * turn;
     turn ^= 1;
     if (lane == 0) b[w] = v;
     asm volatile("bar.sync %0, %1;\n" ::"r"(1 + id), "r"(32 * nw) : "memory");
-    v = lane < nw ? b[lane] : make_float2(0.0f, 0.0f);
+    return lane < nw ? b[lane] : make_float2(0.0f, 0.0f);
+  }
+  __device__ __forceinline__ float2 sum(float2 v) {
+    v.x = warp_sum(v.x);
+    v.y = warp_sum(v.y);
+    if (nw == 1) return v;
+    v = share(v);
     return make_float2(warp_sum(v.x), warp_sum(v.y));
+  }
+  // The row's mean and sum of squared deviations from the warps' (warp k holds `width` columns from
+  // k width on, as far as the row goes).
+  __device__ __forceinline__ float2 moments(float mean, float m2, int d, int width, float inv_d) {
+    if (nw == 1) return make_float2(mean, m2);
+    const float2 v = share(make_float2(mean, m2));
+    const float n = (float)min(max(d - (int)(threadIdx.x & 31) * width, 0), width);
+    const float m = warp_sum(v.x * n) * inv_d, dev = v.x - m;
+    return make_float2(m, warp_sum(fmaf(n * dev, dev, v.y)));
   }
 };
 
-template <bool VEC>
-__device__ __forceinline__ bool in_row(int n, int lane, int e) { return (VEC ? 16 * lane : 32 * e + lane) < n; }
-
 // 16 per-column factors of a lane (c0: the piece's first column)
 template <bool VEC>
-__device__ __forceinline__ void load_cols(const float *p, int c0, int n, int lane, float fill, float *v) {
+__device__ __forceinline__ void load_cols(const float *p, int c0, int n, int lane, float fill, float2 *v) {
   if (p == nullptr) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = fill;
+    for (int k = 0; k < 8; ++k) v[k] = both(fill);
   } else if (VEC) {
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-      const float4 f = 16 * lane < n ? __ldg(reinterpret_cast<const float4 *>(p + c0 + 16 * lane + e))
+    for (int k = 0; k < 8; k += 2) {
+      const float4 f = 16 * lane < n ? __ldg(reinterpret_cast<const float4 *>(p + c0 + 16 * lane + 2 * k))
                                      : make_float4(fill, fill, fill, fill);
-      v[e] = f.x;
-      v[e + 1] = f.y;
-      v[e + 2] = f.z;
-      v[e + 3] = f.w;
+      v[k] = make_float2(f.x, f.y);
+      v[k + 1] = make_float2(f.z, f.w);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = 32 * e + lane < n ? __ldg(p + c0 + 32 * e + lane) : fill;
+    for (int k = 0; k < 8; ++k) {
+      const int c = 64 * k + lane;
+      v[k] = make_float2(c < n ? __ldg(p + c0 + c) : fill, c + 32 < n ? __ldg(p + c0 + c + 32) : fill);
+    }
   }
 }
+// v where the lane's pair k lies in the row, 0 elsewhere
+template <bool VEC>
+__device__ __forceinline__ float2 in_row2(int n, int lane, int k, float2 v) {
+  if (VEC) return 16 * lane < n ? v : both(0.0f);
+  return make_float2(64 * k + lane < n ? v.x : 0.0f, 64 * k + 32 + lane < n ? v.y : 0.0f);
+}
+__device__ __forceinline__ float sum2(float2 v) { return v.x + v.y; }
 
+// Mean and squared deviations of a row: each warp's own by two passes over its registers, then the
+// warps' joined (mean = sum n_w mean_w / d, M2 = sum M2_w + n_w (mean_w - mean)^2), so that no large
+// mean is squared and the row group meets at one barrier only.  U = 1 holds gain and offset in
+// registers and loads the next row before it waits for the sums of this one.
 template <typename E, bool VEC, int U>
 __global__ void __launch_bounds__(512) k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt,
                                                       int *status) {
   __shared__ float2 red[16][2][16];
   const int lane = threadIdx.x & 31, T = a.T, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
   RowGroup G(nw, red);
-  const int per_cta = (int)(blockDim.x >> 5) / nw;
-  const float inv_d = __frcp_rn((float)d);
-  for (int t = blockIdx.x * per_cta + G.id; t < T; t += gridDim.x * per_cta) {
-    const size_t row = (size_t)t * d;
-    Raw<E> r[U];
+  const int per_cta = (int)(blockDim.x >> 5) / nw, step = gridDim.x * per_cta;
+  const int first = G.w * U * kPiece, mine = min(max(d - first, 0), U * kPiece);   // the warp's columns
+  const float inv_d = __frcp_rn((float)d), inv_mine = mine ? __frcp_rn((float)mine) : 0.0f;
+  float2 g[8], b[8];
+  if (U == 1) {
+    load_cols<VEC>(a.gamma, first, d - first, lane, 1.0f, g);
+    load_cols<VEC>(a.beta, first, d - first, lane, 0.0f, b);
+  }
+  Raw<E> now[U], next[1];
+  auto load = [&](int t, Raw<E> *r) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c0 = (G.w * U + u) * kPiece;
-      load_piece<VEC>(static_cast<const E *>(a.x) + row + c0, d - c0, lane, r[u]);
+      const int c0 = first + u * kPiece;
+      load_piece<VEC>(static_cast<const E *>(a.x) + (size_t)t * d + c0, t < T ? d - c0 : 0, lane, r[u]);
     }
-    float x[U][16], s = 0.0f;
+  };
+  int t = blockIdx.x * per_cta + G.id;
+  if (U == 1) load(t, next);
+  for (; t < T; t += step) {
+    const size_t row = (size_t)t * d;
+    if (U == 1) {
+      now[0] = next[0];
+      load(t + step, next);
+    } else {
+      load(t, now);
+    }
+    float2 x[U][8], s = both(0.0f), q = both(0.0f);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[u][e] = r[u].get(e);
-        s += x[u][e];
+      for (int k = 0; k < 8; ++k) {
+        x[u][k] = now[u].pair(k);
+        s = add2(s, x[u][k]);
       }
-    const float mean = G.sum(make_float2(s, 0.0f)).x * inv_d;
-    float q = 0.0f;
+    const float wmean = warp_sum(sum2(s)) * inv_mine;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int n = d - (G.w * U + u) * kPiece;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[u][e] = in_row<VEC>(n, lane, e) ? x[u][e] - mean : 0.0f;
-        q = fmaf(x[u][e], x[u][e], q);
+      for (int k = 0; k < 8; ++k) {
+        const float2 v = in_row2<VEC>(d - first - u * kPiece, lane, k, add2(x[u][k], both(-wmean)));
+        q = fma2(v, v, q);
       }
-    }
-    const float rstd = __frcp_rn(__fsqrt_rn(fmaf(G.sum(make_float2(q, 0.0f)).x, inv_d, a.eps)));
+    const float2 st = G.moments(wmean, warp_sum(sum2(q)), d, U * kPiece, inv_d);
+    const float mean = st.x, rstd = __frcp_rn(__fsqrt_rn(fmaf(st.y, inv_d, a.eps)));
     if (G.w == 0 && lane == 0) {
       if (a.mean) a.mean[t] = mean;
       if (a.rstd) a.rstd[t] = rstd;
@@ -125,15 +160,17 @@ __global__ void __launch_bounds__(512) k_norm_forward(const __grid_constant__ No
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c0 = (G.w * U + u) * kPiece, n = d - c0;
+      const int c0 = first + u * kPiece, n = d - c0;
       if (n > 0) {
-        float g[16], b[16], y[16];
-        load_cols<VEC>(a.gamma, c0, n, lane, 1.0f, g);
-        load_cols<VEC>(a.beta, c0, n, lane, 0.0f, b);
+        if (U > 1) {
+          load_cols<VEC>(a.gamma, c0, n, lane, 1.0f, g);
+          load_cols<VEC>(a.beta, c0, n, lane, 0.0f, b);
+        }
+        float2 y[8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[u][e] *= rstd;
-          y[e] = fmaf(x[u][e], g[e], b[e]);
+        for (int k = 0; k < 8; ++k) {
+          x[u][k] = in_row2<VEC>(n, lane, k, mul2(add2(x[u][k], both(-mean)), both(rstd)));
+          y[k] = fma2(x[u][k], g[k], b[k]);
         }
         store_piece<VEC>(static_cast<E *>(a.y) + row + c0, n, lane, y);
         if (a.codes) {
@@ -170,10 +207,10 @@ __global__ void __launch_bounds__(512) k_norm_backward(const __grid_constant__ N
   RowGroup G(nw, red);
   const int per_cta = (int)(blockDim.x >> 5) / nw, step = gridDim.x * per_cta;
   const float inv_d = __frcp_rn((float)d);
-  float g[16], dg[16], db[16];   // U = 1: held for the CTA's rows
+  float2 g[8], dg[8], db[8];   // U = 1: held for the CTA's rows
   if (U == 1) load_cols<VEC>(a.gamma, G.w * kPiece, d - G.w * kPiece, lane, 1.0f, g);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dg[e] = db[e] = 0.0f;
+  for (int k = 0; k < 8; ++k) dg[k] = db[k] = both(0.0f);
   RowPiece<E, SAVED> now[U], next[1];
   auto load = [&](int t, RowPiece<E, SAVED> *p) {
 #pragma unroll
@@ -195,41 +232,39 @@ __global__ void __launch_bounds__(512) k_norm_backward(const __grid_constant__ N
     } else {
       load(t, now);
     }
-    auto n_of = [&](int u, int e) -> float {
-      if constexpr (SAVED)
-        return fmt == FMT_E4M3 ? code_value<FMT_E4M3, VEC>(now[u].x, e) : code_value<FMT_E5M2, VEC>(now[u].x, e);
-      else
-        return (now[u].x.get(e) - mean) * rstd;
+    auto n_of = [&](int u, int k) -> float2 {
+      if constexpr (SAVED) return fmt == FMT_E4M3 ? code_pair<FMT_E4M3, VEC>(now[u].x, k) : code_pair<FMT_E5M2, VEC>(now[u].x, k);
+      else return mul2(add2(now[u].x.pair(k), both(-mean)), both(rstd));
     };
-    float2 s = make_float2(0.0f, 0.0f);
-    float keep[16];   // U = 1: n
+    float2 sh = both(0.0f), shn = both(0.0f);
+    float2 keep[8];   // U = 1: n
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (U > 1) load_cols<VEC>(a.gamma, (G.w * U + u) * kPiece, d - (G.w * U + u) * kPiece, lane, 1.0f, g);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float dy = now[u].dy.get(e), h = dy * g[e], n = n_of(u, e);
+      for (int k = 0; k < 8; ++k) {
+        const float2 dy = now[u].dy.pair(k), h = mul2(dy, g[k]), n = n_of(u, k);
         if (U == 1) {
-          keep[e] = n;
-          dg[e] = fmaf(dy, n, dg[e]);
-          db[e] += dy;
+          keep[k] = n;
+          dg[k] = fma2(dy, n, dg[k]);
+          db[k] = add2(db[k], dy);
         }
-        s.x += h;
-        s.y = fmaf(h, n, s.y);
+        sh = add2(sh, h);
+        shn = fma2(h, n, shn);
       }
     }
-    s = G.sum(s);
+    const float2 s = G.sum(make_float2(sum2(sh), sum2(shn)));
     if (G.w == 0 && lane == 0 && !(isfinite(s.x) && isfinite(s.y) && isfinite(rstd)))
       set_status(status, GIFT_ERR_NONFINITE);
-    const float ma = s.x * inv_d, mb = s.y * inv_d;
+    const float2 ma = both(-s.x * inv_d), mb = both(-s.y * inv_d);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int c0 = (G.w * U + u) * kPiece;
       if (U > 1) load_cols<VEC>(a.gamma, c0, d - c0, lane, 1.0f, g);
-      float dx[16];
+      float2 dx[8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        dx[e] = rstd * (fmaf(now[u].dy.get(e), g[e], -ma) - (U == 1 ? keep[e] : n_of(u, e)) * mb);
+      for (int k = 0; k < 8; ++k)
+        dx[k] = mul2(both(rstd), fma2(U == 1 ? keep[k] : n_of(u, k), mb, fma2(now[u].dy.pair(k), g[k], ma)));
       store_piece<VEC>(static_cast<E *>(a.dx) + (size_t)t * d + c0, d - c0, lane, dx);
     }
   }
@@ -243,16 +278,17 @@ __global__ void __launch_bounds__(512) k_norm_backward(const __grid_constant__ N
       for (int e = 0; e < 16; ++e) {
         const int c = G.w * kPiece + piece_col<VEC>(lane, e);
         float *sg = acc_sh + c, *sb = acc_sh + nw * kPiece + c;
+        float vg = e & 1 ? dg[e / 2].y : dg[e / 2].x, vb = e & 1 ? db[e / 2].y : db[e / 2].x;
         if (k > 0) {
-          dg[e] = *sg + dg[e];
-          db[e] = *sb + db[e];
+          vg += *sg;
+          vb += *sb;
         }
         if (k + 1 < per_cta) {
-          *sg = dg[e];
-          *sb = db[e];
+          *sg = vg;
+          *sb = vb;
         } else if (c < d) {
-          out[c] = dg[e];
-          out[d + c] = db[e];
+          out[c] = vg;
+          out[d + c] = vb;
         }
       }
     }
@@ -267,9 +303,9 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_cols(const __grid_constan
   const int c0 = (blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5)) * kPiece, n = d - c0;
   grid_release();
   if (n <= 0) return;
-  float dg[16], db[16];
+  float2 dg[8], db[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dg[e] = db[e] = 0.0f;
+  for (int k = 0; k < 8; ++k) dg[k] = db[k] = both(0.0f);
   const int t1 = min(a.T, (int)(blockIdx.y + 1) * rows);
 #pragma unroll 2
   for (int t = blockIdx.y * rows; t < t1; ++t) {
@@ -285,15 +321,13 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_cols(const __grid_constan
       mean = a.mean[t];
     }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float dy = p.dy.get(e);
-      float v;
-      if constexpr (SAVED)
-        v = fmt == FMT_E4M3 ? code_value<FMT_E4M3, VEC>(p.x, e) : code_value<FMT_E5M2, VEC>(p.x, e);
-      else
-        v = (p.x.get(e) - mean) * rstd;
-      dg[e] = fmaf(dy, v, dg[e]);
-      db[e] += dy;
+    for (int k = 0; k < 8; ++k) {
+      const float2 dy = p.dy.pair(k);
+      float2 v;
+      if constexpr (SAVED) v = fmt == FMT_E4M3 ? code_pair<FMT_E4M3, VEC>(p.x, k) : code_pair<FMT_E5M2, VEC>(p.x, k);
+      else v = mul2(add2(p.x.pair(k), both(-mean)), both(rstd));
+      dg[k] = fma2(dy, v, dg[k]);
+      db[k] = add2(db[k], dy);
     }
   }
   float *out = a.part + (size_t)2 * blockIdx.y * d;
@@ -301,17 +335,18 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_cols(const __grid_constan
   for (int e = 0; e < 16; ++e) {
     const int c = c0 + piece_col<VEC>(lane, e);
     if (c < d) {
-      out[c] = dg[e];
-      out[d + c] = db[e];
+      out[c] = e & 1 ? dg[e / 2].y : dg[e / 2].x;
+      out[d + c] = e & 1 ? db[e / 2].y : db[e / 2].x;
     }
   }
 }
 
-// out[c] = sum over partials of part[k stride + c]: 32 columns per CTA, eight warps take every eighth
-// partial, their sums are added in order.  blockIdx.y: the first or the second output.
-__global__ void __launch_bounds__(kNormThreads) k_norm_sums(const float *__restrict__ part, int parts, size_t stride,
-                                                            size_t second, int d, float *out0, float *out1) {
-  __shared__ float sh[8][32];
+// out[c] = sum over partials of part[k stride + c]: 32 columns per CTA, 32 warps take every 32nd
+// partial (their loads are all in flight at once: latency is what this kernel costs), and their sums
+// are added in order.  blockIdx.y: the first or the second output.
+__global__ void __launch_bounds__(1024) k_norm_sums(const float *__restrict__ part, int parts, size_t stride,
+                                                    size_t second, int d, float *out0, float *out1) {
+  __shared__ float sh[32][33];
   grid_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float *out = blockIdx.y ? out1 : out0;
@@ -320,15 +355,12 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_sums(const float *__restr
   float s = 0.0f;
   if (c < d) {
 #pragma unroll 8
-    for (int k = w; k < parts; k += 8) s += p[k * stride];
+    for (int k = w; k < parts; k += 32) s += p[k * stride];
   }
   sh[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < d) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) s += sh[k][lane];
-    out[c] = s;
-  }
+  const float v = warp_sum(sh[lane][w]);   // column w of the block
+  if (lane == 0 && blockIdx.x * 32 + w < d) out[blockIdx.x * 32 + w] = v;
 }
 
 // ---- rows too long for registers: column by column, the row read once per sum --------------------------
@@ -370,13 +402,13 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_forward_long(const __grid
       const int n = d - c0;
       Raw<E> r;
       load_piece<false>(xr + c0, n, lane, r);
-      float x[16], g[16], b[16], y[16];
+      float2 x[8], g[8], b[8], y[8];
       load_cols<false>(a.gamma, c0, n, lane, 1.0f, g);
       load_cols<false>(a.beta, c0, n, lane, 0.0f, b);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = in_row<false>(n, lane, e) ? (r.get(e) - mean) * rstd : 0.0f;
-        y[e] = fmaf(x[e], g[e], b[e]);
+      for (int k = 0; k < 8; ++k) {
+        x[k] = in_row2<false>(n, lane, k, mul2(add2(r.pair(k), both(-mean)), both(rstd)));
+        y[k] = fma2(x[k], g[k], b[k]);
       }
       store_piece<false>(static_cast<E *>(a.y) + row + c0, n, lane, y);
       if (a.codes) {
@@ -476,26 +508,14 @@ struct RowPlan {
   int u, nw, threads;
 };
 
-// Forward: up to 4 pieces in one warp (2048 columns); then 2 or 4 pieces in 4, 8 or 16 warps.
-bool forward_plan(int d, RowPlan *p) {
-  const int pieces = (d + kPiece - 1) / kPiece;
-  if (pieces > 64) return false;
-  if (pieces <= 4) *p = {pieces, 1, 256};
-  else if (pieces <= 8) *p = {2, 4, 256};
-  else if (pieces <= 16) *p = {2, 8, 256};
-  else if (pieces <= 32) *p = {4, 8, 256};
-  else *p = {4, 16, 512};
-  return true;
-}
-
-// Backward: up to 8192 columns one piece per lane and as many warps per row as pieces (CTAs of 8 to
-// 16 warps), with the column sums; up to 32768 two or four pieces per lane, without them.
-bool backward_plan(int d, RowPlan *p) {
+// As many warps per row as pieces up to 8192 columns, then two or four pieces per lane; CTAs of about
+// `warps` warps, at most 16.
+bool row_plan(int d, RowPlan *p, int warps = 8) {
   const int pieces = (d + kPiece - 1) / kPiece;
   if (pieces > 64) return false;
   p->u = pieces <= 16 ? 1 : pieces <= 32 ? 2 : 4;
   p->nw = (pieces + p->u - 1) / p->u;
-  p->threads = 32 * p->nw * (p->nw >= 8 ? 1 : 8 / p->nw);
+  p->threads = 32 * p->nw * (p->nw >= warps ? 1 : warps / p->nw);
   return true;
 }
 
@@ -512,7 +532,6 @@ cudaError_t forward_u(const Launch &L, int fmt, const NormForward &a, const RowP
   switch (p.u) {
     case 1: return forward<E, VEC, 1>(L, fmt, a, p);
     case 2: return forward<E, VEC, 2>(L, fmt, a, p);
-    case 3: return forward<E, VEC, 3>(L, fmt, a, p);
     default: return forward<E, VEC, 4>(L, fmt, a, p);
   }
 }
@@ -520,7 +539,7 @@ cudaError_t forward_u(const Launch &L, int fmt, const NormForward &a, const RowP
 template <typename E>
 cudaError_t forward_e(const Launch &L, int fmt, const NormForward &a) {
   RowPlan p;
-  if (!forward_plan(a.d, &p)) {
+  if (!row_plan(a.d, &p)) {
     const int grid = a.T < L.sms * 8 ? a.T : L.sms * 8;
     k_norm_forward_long<E><<<grid, kNormThreads, 0, L.stream>>>(a, fmt, L.status);
     return cudaGetLastError();
@@ -531,7 +550,7 @@ cudaError_t forward_e(const Launch &L, int fmt, const NormForward &a) {
 }
 
 cudaError_t sums_after(const Launch &L, const NormBackward &a, int parts) {
-  return launch_after(L.stream, k_norm_sums, dim3((a.d + 31) / 32, 2), kNormThreads, a.part, parts, (size_t)2 * a.d,
+  return launch_after(L.stream, k_norm_sums, dim3((a.d + 31) / 32, 2), 1024, a.part, parts, (size_t)2 * a.d,
                       (size_t)a.d, a.d, a.dgamma, a.dbeta);
 }
 
@@ -558,8 +577,9 @@ cudaError_t backward(const Launch &L, int fmt, const NormBackward &a, const RowP
 
 template <typename E, bool VEC, bool SAVED>
 cudaError_t backward_s(const Launch &L, int fmt, const NormBackward &a) {
+  // long batches: 16 warps per CTA, so that there are fewer partials
   RowPlan p;
-  if (backward_plan(a.d, &p)) {
+  if (row_plan(a.d, &p, (long long)a.T * ((a.d + kPiece - 1) / kPiece) >= 32LL * L.sms ? 16 : 8)) {
     switch (p.u) {
       case 1: return backward<E, VEC, SAVED, 1>(L, fmt, a, p);
       case 2: return backward<E, VEC, SAVED, 2>(L, fmt, a, p);
@@ -590,7 +610,7 @@ int norm_partials(int sms, int T) {
 
 size_t norm_part_floats(int sms, int T, int d) {
   RowPlan p;
-  if (backward_plan(d, &p) && p.u == 1) return (size_t)2 * norm_partials(sms, T) * d;
+  if (row_plan(d, &p) && p.u == 1) return (size_t)2 * norm_partials(sms, T) * d;
   const int rows = col_rows(T);
   return (size_t)2 * ((T + rows - 1) / rows) * d;
 }
@@ -606,7 +626,7 @@ cudaError_t launch_col_sums(const Launch &L, const void *x, bool bf16, int T, in
     k_col_sums<<<dim3(cb, slices), kNormThreads, 0, L.stream>>>(static_cast<const __nv_bfloat16 *>(x), T, d, rows, part);
   else
     k_col_sums<<<dim3(cb, slices), kNormThreads, 0, L.stream>>>(static_cast<const float *>(x), T, d, rows, part);
-  return launch_after(L.stream, k_norm_sums, dim3((d + 31) / 32, 1), kNormThreads, part, slices, (size_t)d, (size_t)0,
+  return launch_after(L.stream, k_norm_sums, dim3((d + 31) / 32, 1), 1024, part, slices, (size_t)d, (size_t)0,
                       d, out, static_cast<float *>(nullptr));
 }
 
