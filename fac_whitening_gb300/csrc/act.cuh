@@ -148,6 +148,36 @@ __device__ __forceinline__ void load_piece(const __nv_bfloat16 *p, int n, int la
   }
 }
 
+// A ring of pieces on their way to one lane: asynchronous 16-byte copies into shared memory that only
+// this lane reads, so that many rows are in flight without a register or a barrier for them.  DEPTH
+// slots of CHUNKS x 32 lanes x 16 bytes per warp.
+template <int CHUNKS, int DEPTH>
+struct LaneRing {
+  static constexpr int bytes = CHUNKS * DEPTH * 512;   // per warp
+  uint32_t base;
+  __device__ __forceinline__ LaneRing(void *warp_base, int lane)
+      : base((uint32_t)__cvta_generic_to_shared(warp_base) + 16 * lane) {}
+  __device__ __forceinline__ void clear() const {   // lanes past the row's end never copy: they read zeros
+#pragma unroll
+    for (int k = 0; k < CHUNKS * DEPTH; ++k)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + 512 * k), "r"(0u) : "memory");
+  }
+  __device__ __forceinline__ void copy(int slot, int chunk, const void *src) const {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + 512 * (slot * CHUNKS + chunk)), "l"(src)
+                 : "memory");
+  }
+  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ static void wait_oldest() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+  }
+  __device__ __forceinline__ void read(int slot, int chunk, uint32_t *r) const {
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(base + 512 * (slot * CHUNKS + chunk))
+                 : "memory");
+  }
+};
+
 template <bool VEC>
 __device__ __forceinline__ void store_piece(float *p, int n, int lane, const float2 *v) {
   if (VEC) {

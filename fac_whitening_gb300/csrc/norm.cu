@@ -19,11 +19,24 @@ namespace gift {
 namespace {
 
 constexpr int kNormThreads = 256;
+#ifndef FWD_CTAS
+#define FWD_CTAS 3
+#endif
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+
+// Two sums over the warp in six shuffles: the halves of the warp take one each after the first step.
+__device__ __forceinline__ float2 warp_sum2(float2 v) {
+  const bool upper = threadIdx.x & 16;
+  float s = (upper ? v.y : v.x) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v.x : v.y, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  const float other = __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+  return upper ? make_float2(other, s) : make_float2(s, other);
 }
 
 // wait for the programmatic predecessor's results / let the successor launch
@@ -52,11 +65,9 @@ struct RowGroup {
     return lane < nw ? b[lane] : make_float2(0.0f, 0.0f);
   }
   __device__ __forceinline__ float2 sum(float2 v) {
-    v.x = warp_sum(v.x);
-    v.y = warp_sum(v.y);
+    v = warp_sum2(v);
     if (nw == 1) return v;
-    v = share(v);
-    return make_float2(warp_sum(v.x), warp_sum(v.y));
+    return warp_sum2(share(v));
   }
   // The row's mean and sum of squared deviations from the warps' (warp k holds `width` columns from
   // k width on, as far as the row goes).
@@ -103,8 +114,8 @@ __device__ __forceinline__ float sum2(float2 v) { return v.x + v.y; }
 // warps' joined (mean = sum n_w mean_w / d, M2 = sum M2_w + n_w (mean_w - mean)^2), so that no large
 // mean is squared and the row group meets at one barrier only.  U = 1 holds gain and offset in
 // registers and loads the next row before it waits for the sums of this one.
-template <typename E, bool VEC, int U>
-__global__ void __launch_bounds__(512) k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt,
+template <typename E, bool VEC, int U, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 && U == 1 ? FWD_CTAS : 1) k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt,
                                                       int *status) {
   __shared__ float2 red[16][2][16];
   const int lane = threadIdx.x & 31, T = a.T, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
@@ -197,8 +208,8 @@ struct RowPiece<E, true> {
 
 // U = 1: dx and the column sums.  U > 1 (rows over 8192 columns): dx alone, the column sums take
 // a pass of their own (k_norm_cols), since their 32 registers a piece do not fit beside the row's.
-template <typename E, bool VEC, bool SAVED, int U>
-__global__ void __launch_bounds__(512) k_norm_backward(const __grid_constant__ NormBackward a, int nw, int fmt,
+template <typename E, bool VEC, bool SAVED, int U, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 && U == 1 ? 2 : 1) k_norm_backward(const __grid_constant__ NormBackward a, int nw, int fmt,
                                                        int *status) {
   extern __shared__ float acc_sh[];
   __shared__ float2 red[16][2][16];
@@ -469,11 +480,10 @@ __global__ void __launch_bounds__(kNormThreads) k_col_sums(const E *__restrict__
 }
 
 // ---- host ---------------------------------------------------------------------------------------------
-constexpr int kColRows = 128;      // tokens of a slice, at least
-
-int col_rows(int T) {   // at most 256 slices
+// tokens of a slice of a column pass: at least 16, at most 256 slices
+int col_rows(int T) {
   const int r = (T + 255) / 256;
-  return r < kColRows ? kColRows : r;
+  return r < 16 ? 16 : r;
 }
 
 bool cols_aligned(const float *p) { return !p || aligned16(p); }
@@ -508,23 +518,28 @@ struct RowPlan {
   int u, nw, threads;
 };
 
-// As many warps per row as pieces up to 8192 columns, then two or four pieces per lane; CTAs of about
-// `warps` warps, at most 16.
-bool row_plan(int d, RowPlan *p, int warps = 8) {
+// As many warps per row as pieces up to 8192 columns, then two or four pieces per lane; CTAs of 8 to
+// 16 warps.
+bool row_plan(int d, RowPlan *p) {
   const int pieces = (d + kPiece - 1) / kPiece;
   if (pieces > 64) return false;
   p->u = pieces <= 16 ? 1 : pieces <= 32 ? 2 : 4;
   p->nw = (pieces + p->u - 1) / p->u;
-  p->threads = 32 * p->nw * (p->nw >= warps ? 1 : warps / p->nw);
+  p->threads = 32 * p->nw * (p->nw >= 8 ? 1 : 8 / p->nw);
   return true;
+}
+
+template <typename E, bool VEC, int U, int MAXT>
+cudaError_t forward_t(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
+  constexpr auto kernel = k_norm_forward<E, VEC, U, MAXT>;
+  kernel<<<resident(kernel, L, p.threads, 0, a.T, p.threads / 32 / p.nw), p.threads, 0, L.stream>>>(a, p.nw, fmt,
+                                                                                                   L.status);
+  return cudaGetLastError();
 }
 
 template <typename E, bool VEC, int U>
 cudaError_t forward(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
-  const int per_cta = p.threads / 32 / p.nw;
-  const int grid = resident(k_norm_forward<E, VEC, U>, L, p.threads, 0, a.T, per_cta);
-  k_norm_forward<E, VEC, U><<<grid, p.threads, 0, L.stream>>>(a, p.nw, fmt, L.status);
-  return cudaGetLastError();
+  return p.threads <= 256 ? forward_t<E, VEC, U, 256>(L, fmt, a, p) : forward_t<E, VEC, U, 512>(L, fmt, a, p);
 }
 
 template <typename E, bool VEC>
@@ -563,23 +578,29 @@ cudaError_t column_pass(const Launch &L, int fmt, const NormBackward &a) {
   return e != cudaSuccess ? e : sums_after(L, a, slices);
 }
 
-template <typename E, bool VEC, bool SAVED, int U>
-cudaError_t backward(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
+template <typename E, bool VEC, bool SAVED, int U, int MAXT>
+cudaError_t backward_t(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
+  constexpr auto kernel = k_norm_backward<E, VEC, SAVED, U, MAXT>;
   const int per_cta = p.threads / 32 / p.nw, smem = U == 1 && per_cta > 1 ? 2 * p.nw * kPiece * 4 : 0;
-  int grid = resident(k_norm_backward<E, VEC, SAVED, U>, L, p.threads, smem, a.T, per_cta);
+  int grid = resident(kernel, L, p.threads, smem, a.T, per_cta);
   if (grid > norm_partials(L.sms, a.T)) grid = norm_partials(L.sms, a.T);
-  k_norm_backward<E, VEC, SAVED, U><<<grid, p.threads, smem, L.stream>>>(a, p.nw, fmt, L.status);
+  kernel<<<grid, p.threads, smem, L.stream>>>(a, p.nw, fmt, L.status);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (U > 1) return column_pass<E, VEC, SAVED>(L, fmt, a);
   return a.part ? sums_after(L, a, grid) : cudaSuccess;
 }
 
+template <typename E, bool VEC, bool SAVED, int U>
+cudaError_t backward(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
+  return p.threads <= 256 ? backward_t<E, VEC, SAVED, U, 256>(L, fmt, a, p)
+                          : backward_t<E, VEC, SAVED, U, 512>(L, fmt, a, p);
+}
+
 template <typename E, bool VEC, bool SAVED>
 cudaError_t backward_s(const Launch &L, int fmt, const NormBackward &a) {
-  // long batches: 16 warps per CTA, so that there are fewer partials
   RowPlan p;
-  if (row_plan(a.d, &p, (long long)a.T * ((a.d + kPiece - 1) / kPiece) >= 32LL * L.sms ? 16 : 8)) {
+  if (row_plan(a.d, &p)) {
     switch (p.u) {
       case 1: return backward<E, VEC, SAVED, 1>(L, fmt, a, p);
       case 2: return backward<E, VEC, SAVED, 2>(L, fmt, a, p);
