@@ -19,9 +19,6 @@ namespace gift {
 namespace {
 
 constexpr int kNormThreads = 256;
-#ifndef FWD_CTAS
-#define FWD_CTAS 3
-#endif
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -115,7 +112,7 @@ __device__ __forceinline__ float sum2(float2 v) { return v.x + v.y; }
 // mean is squared and the row group meets at one barrier only.  U = 1 holds gain and offset in
 // registers and loads the next row before it waits for the sums of this one.
 template <typename E, bool VEC, int U, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 && U == 1 ? FWD_CTAS : 1) k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt,
+__global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 384 ? 2 : 1) k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt,
                                                       int *status) {
   __shared__ float2 red[16][2][16];
   const int lane = threadIdx.x & 31, T = a.T, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
@@ -206,6 +203,18 @@ struct RowPiece<E, true> {
   RawCodes x;
 };
 
+constexpr int kColWords = 16 * 33;   // a warp's 512 column sums in shared memory
+
+// a lane's 16 column sums of a piece to out (n columns are left)
+template <bool VEC>
+__device__ __forceinline__ void write_cols(float *out, int n, int lane, const float2 *v) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int c = piece_col<VEC>(lane, e);
+    if (c < n) out[c] = e & 1 ? v[e / 2].y : v[e / 2].x;
+  }
+}
+
 // U = 1: dx and the column sums.  U > 1 (rows over 8192 columns): dx alone, the column sums take
 // a pass of their own (k_norm_cols), since their 32 registers a piece do not fit beside the row's.
 template <typename E, bool VEC, bool SAVED, int U, int MAXT>
@@ -280,29 +289,30 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && U == 1 ? 2 : 1) k_norm_ba
     }
   }
   if (U > 1 || !a.part) return;
-  // the CTA's partial: the row groups' sums in order, through shared memory where there are several
+  // The CTA's partial.  Several row groups: every warp leaves its sums in shared memory (a lane's 16
+  // columns 33 words apart, so that neither the writes by lane nor the reads by column conflict), then
+  // each thread adds the groups' values of its columns in order.
   float *out = a.part + (size_t)2 * blockIdx.x * d;
-  for (int k = 0; k < per_cta; ++k) {
-    if (k > 0) __syncthreads();
-    if (G.id == k) {
+  const int first = G.w * kPiece;
+  if (per_cta == 1) {
+    write_cols<VEC>(out + first, d - first, lane, dg);
+    write_cols<VEC>(out + d + first, d - first, lane, db);
+    return;
+  }
+  float *mine = acc_sh + 2 * kColWords * (G.id * nw + G.w);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int c = G.w * kPiece + piece_col<VEC>(lane, e);
-        float *sg = acc_sh + c, *sb = acc_sh + nw * kPiece + c;
-        float vg = e & 1 ? dg[e / 2].y : dg[e / 2].x, vb = e & 1 ? db[e / 2].y : db[e / 2].x;
-        if (k > 0) {
-          vg += *sg;
-          vb += *sb;
-        }
-        if (k + 1 < per_cta) {
-          *sg = vg;
-          *sb = vb;
-        } else if (c < d) {
-          out[c] = vg;
-          out[d + c] = vb;
-        }
-      }
-    }
+  for (int e = 0; e < 16; ++e) {
+    mine[33 * e + lane] = e & 1 ? dg[e / 2].y : dg[e / 2].x;
+    mine[kColWords + 33 * e + lane] = e & 1 ? db[e / 2].y : db[e / 2].x;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * d; i += blockDim.x) {
+    const int c = i < d ? i : i - d, in = c % kPiece;
+    const int e = VEC ? in % 16 : in / 32, l = VEC ? in / 16 : in % 32;
+    const float *p = acc_sh + 2 * kColWords * (c / kPiece) + (i < d ? 0 : kColWords) + 33 * e + l;
+    float v = p[0];
+    for (int k = 1; k < per_cta; ++k) v += p[2 * kColWords * nw * k];
+    out[i] = v;
   }
 }
 
@@ -488,12 +498,19 @@ int col_rows(int T) {
 
 bool cols_aligned(const float *p) { return !p || aligned16(p); }
 
-// CTAs of a persistent launch: what is resident on the context's SMs, at most one per `per_cta` rows
-template <typename K>
-int resident(K kernel, const Launch &L, int threads, int smem, int T, int per_cta) {
-  int per_sm = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
-    per_sm = 1;
+// CTAs of a persistent launch: what is resident on the context's SMs, at most one per `per_cta` rows.
+// The occupancy of a kernel is looked up once per CTA size (warps) and device.
+template <auto Kernel>
+int resident(const Launch &L, int threads, int smem, int T, int per_cta) {
+  static int known[64][17] = {};
+  int dev = 0, per_sm = 0;
+  const bool keep = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+  if (keep) per_sm = known[dev][threads / 32];
+  if (per_sm < 1) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, Kernel, threads, smem) != cudaSuccess || per_sm < 1)
+      per_sm = 1;
+    if (keep) known[dev][threads / 32] = per_sm;
+  }
   const long long most = (long long)L.sms * per_sm, need = ((long long)T + per_cta - 1) / per_cta;
   return (int)(need < most ? need : most);
 }
@@ -532,14 +549,15 @@ bool row_plan(int d, RowPlan *p) {
 template <typename E, bool VEC, int U, int MAXT>
 cudaError_t forward_t(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
   constexpr auto kernel = k_norm_forward<E, VEC, U, MAXT>;
-  kernel<<<resident(kernel, L, p.threads, 0, a.T, p.threads / 32 / p.nw), p.threads, 0, L.stream>>>(a, p.nw, fmt,
+  kernel<<<resident<kernel>(L, p.threads, 0, a.T, p.threads / 32 / p.nw), p.threads, 0, L.stream>>>(a, p.nw, fmt,
                                                                                                    L.status);
   return cudaGetLastError();
 }
 
 template <typename E, bool VEC, int U>
 cudaError_t forward(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
-  return p.threads <= 256 ? forward_t<E, VEC, U, 256>(L, fmt, a, p) : forward_t<E, VEC, U, 512>(L, fmt, a, p);
+  if (p.threads <= 256) return forward_t<E, VEC, U, 256>(L, fmt, a, p);
+  return U == 1 && p.threads <= 384 ? forward_t<E, VEC, U, 384>(L, fmt, a, p) : forward_t<E, VEC, U, 512>(L, fmt, a, p);
 }
 
 template <typename E, bool VEC>
@@ -581,8 +599,8 @@ cudaError_t column_pass(const Launch &L, int fmt, const NormBackward &a) {
 template <typename E, bool VEC, bool SAVED, int U, int MAXT>
 cudaError_t backward_t(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
   constexpr auto kernel = k_norm_backward<E, VEC, SAVED, U, MAXT>;
-  const int per_cta = p.threads / 32 / p.nw, smem = U == 1 && per_cta > 1 ? 2 * p.nw * kPiece * 4 : 0;
-  int grid = resident(kernel, L, p.threads, smem, a.T, per_cta);
+  const int per_cta = p.threads / 32 / p.nw, smem = U == 1 && per_cta > 1 ? per_cta * p.nw * 2 * kColWords * 4 : 0;
+  int grid = resident<kernel>(L, p.threads, smem, a.T, per_cta);
   if (grid > norm_partials(L.sms, a.T)) grid = norm_partials(L.sms, a.T);
   kernel<<<grid, p.threads, smem, L.stream>>>(a, p.nw, fmt, L.status);
   const cudaError_t e = cudaGetLastError();
