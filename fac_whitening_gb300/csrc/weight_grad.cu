@@ -149,6 +149,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
+// a float of CTA r's copy of a shared variable
+__device__ __forceinline__ float ld_cluster(const float *p, int r) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 ra;\n\t"
+      "mapa.shared::cluster.u32 ra, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [ra];\n\t}\n"
+      : "=f"(v)
+      : "r"(tc::smem_u32(p)), "r"(r)
+      : "memory");
+  return v;
+}
 // Arrive on the pair's first CTA's copy of `bar`.  What the barrier orders is tensor memory (its
 // own fences) and TMA's writes, no thread's stores, so no cluster-wide release is asked for: one
 // (.release.cluster) held every arriving warp for hundreds of cycles, 531 -> 457 us for
@@ -229,16 +241,6 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
-}
-// two FP32 sums at once, each to nearest
-__device__ __forceinline__ void add_f32x2(float2 &to, uint32_t x, uint32_t y) {
-  asm("{\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%0, %1};\n\t"
-      "mov.b64 b, {%2, %3};\n\t"
-      "add.rn.f32x2 a, a, b;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}\n"
-      : "+f"(to.x), "+f"(to.y)
-      : "f"(__uint_as_float(x)), "f"(__uint_as_float(y)));
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   __nv_bfloat162 x, y;
@@ -518,7 +520,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc::tmem_ld16_nowait(tmem + off + 128 * b + e, raw);
           tc::tmem_wait_ld16(raw);
 #pragma unroll
-          for (int x = 0; x < 16; x += 2) add_f32x2(to[(e + x) / 2], raw[x], raw[x + 1]);
+          for (int x = 0; x < 16; x += 2) {
+            float2 &s = to[(e + x) / 2];
+            s = add2(s, make_float2(__uint_as_float(raw[x]), __uint_as_float(raw[x + 1])));
+          }
         }
         tc::fence_before_sync();
         __syncwarp();
@@ -564,6 +569,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     dealloc_pair(tmem);
   }
+}
+
+// ---- few outputs: FP32 SIMT in one launch ----------------------------------------------------------
+// 32 x 32 tiles of dW, a cluster of eight CTAs each: a CTA takes every eighth 64 tokens through shared
+// memory, eight of them per warp, each lane 4 x 8 outputs in packed FP32.  A warp's sums are folded
+// every 64 tokens of the batch, the eight warps' joined in order, then the eight CTAs' through
+// distributed shared memory; db alongside.  Bound by latency.
+#ifndef SMALL_TOKENS
+#define SMALL_TOKENS 2048
+#endif
+constexpr long long kSmallTokens = SMALL_TOKENS;
+constexpr int kSmTok = 64, kSmTile = 32, kSmThreads = 256, kSmCtas = 8;
+
+template <int F, typename E>
+__global__ void __cluster_dims__(kSmCtas, 1, 1) __launch_bounds__(kSmThreads, 1)
+    k_weight_grad_small(const E *__restrict__ delta, const uint8_t *__restrict__ codes,
+                        const uint8_t *__restrict__ scales, int T, int d_out, int d_in, int groups,
+                        const float *__restrict__ gamma, const float *__restrict__ beta, float *__restrict__ db_out,
+                        float *__restrict__ dW) {
+  __shared__ __align__(16) union {
+    struct {
+      float delta[kSmTok][kSmTile], v[kSmTok][kSmTile];
+    } in;
+    float out[8][kSmTile][kSmTile + 1];
+  } sh;
+  __shared__ float sh_db[8][kSmTile];
+  __shared__ float cta[kSmTile][kSmTile + 1];   // the CTA's sums; column 32: db
+  const int rank = (int)cluster_rank();
+  const int i0 = blockIdx.x / kSmCtas * kSmTile, o0 = blockIdx.y * kSmTile;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, lo = 4 * (lane >> 2), li = 8 * (lane & 3);
+  const bool o_in = o0 + lane < d_out, i_in = i0 + lane < d_in;
+  const E *dp = delta + o0 + lane;
+  const uint8_t *cp = codes + i0 + lane, *sp = scales + i0 / kActGroup;   // a tile lies in one group
+  float2 tot[4][4];
+  float db = 0.0f;
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) tot[a][b] = make_float2(0.0f, 0.0f);
+  constexpr int kPer = kSmTok / 8;
+  float rd[kPer];
+  uint32_t rc[kPer], rs[kPer];
+  auto load = [&](int t0) {   // token t0 + w + 8 k of the chunk, this lane's column
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int t = t0 + w + 8 * k;
+      rd[k] = t < T && o_in ? ld1(dp + (size_t)t * d_out) : 0.0f;
+      rc[k] = t < T && i_in ? cp[(size_t)t * d_in] : 0u;
+      rs[k] = t < T ? sp[(size_t)t * groups] : 127u;
+    }
+  };
+  load(rank * kSmTok);
+  for (int t0 = rank * kSmTok; t0 < T; t0 += kSmTok * kSmCtas) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      sh.in.delta[w + 8 * k][lane] = rd[k];
+      sh.in.v[w + 8 * k][lane] = dec_fp8<F>(rc[k]) * act_scale(rs[k]);
+    }
+    __syncthreads();
+    load(t0 + kSmTok * kSmCtas);
+    float2 acc[4][4];
+    float dsum = 0.0f;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) acc[a][b] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = 0; k < kPer; ++k) {
+      const int r = kPer * w + k;
+      const float4 d4 = *reinterpret_cast<const float4 *>(&sh.in.delta[r][lo]);
+      const float4 va = *reinterpret_cast<const float4 *>(&sh.in.v[r][li]),
+                   vb = *reinterpret_cast<const float4 *>(&sh.in.v[r][li + 4]);
+      const float2 v[4] = {make_float2(va.x, va.y), make_float2(va.z, va.w), make_float2(vb.x, vb.y),
+                           make_float2(vb.z, vb.w)};
+      const float d[4] = {d4.x, d4.y, d4.z, d4.w};
+      dsum += sh.in.delta[r][lane];
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) acc[a][b] = fma2(both(d[a]), v[b], acc[a][b]);
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tot[a][b] = add2(tot[a][b], acc[a][b]);
+    db += dsum;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      sh.out[w][lo + a][li + 2 * b] = tot[a][b].x;
+      sh.out[w][lo + a][li + 2 * b + 1] = tot[a][b].y;
+    }
+  sh_db[w][lane] = db;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int o = w + 8 * k;
+    float v = sh.out[0][o][lane], b = sh_db[0][o];
+#pragma unroll
+    for (int x = 1; x < 8; ++x) {
+      v += sh.out[x][o][lane];
+      b += sh_db[x][o];
+    }
+    cta[o][lane] = v;
+    if (lane == 0) cta[o][kSmTile] = b;
+  }
+  cluster_sync();
+  // rows 4 rank .. 4 rank + 3 of the tile are joined and stored by this CTA, a warp each
+  if (w < 4) {
+    const int o = 4 * rank + w;
+    float v = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kSmCtas; ++r) {
+      v += ld_cluster(&cta[o][lane], r);
+      b += ld_cluster(&cta[o][kSmTile], r);
+    }
+    if (o0 + o < d_out) {
+      if (db_out && i0 == 0 && lane == 0) db_out[o0 + o] = b;
+      if (i_in) {
+        if (gamma) v *= gamma[i0 + lane];
+        if (beta) v = fmaf(beta[i0 + lane], b, v);
+        dW[(size_t)(o0 + o) * d_in + i0 + lane] = v;
+      }
+    }
+  }
+  cluster_sync();   // no CTA leaves while another reads its sums
 }
 
 // dW = gamma * (the slices' sums in order) + beta db
@@ -752,7 +887,28 @@ WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) 
   return w;
 }
 
+// Where the tensor-core kernel's fixed cost (its first loads, and the kernels before it) outweighs the
+// small kernel's: its clusters all run at once, over a few chunks each.
+bool small_product(int sms, int T, int d_out, int d_in) {
+  const long long tiles = (long long)((d_out + kSmTile - 1) / kSmTile) * ((d_in + kSmTile - 1) / kSmTile);
+  return tiles * kSmCtas <= 2 * sms && T <= kSmallTokens;
+}
+
+template <int F, typename E>
+cudaError_t launch_small(const Launch &L, const WeightGrad &a) {
+  const dim3 grid((a.d_in + kSmTile - 1) / kSmTile * kSmCtas, (a.d_out + kSmTile - 1) / kSmTile);
+  k_weight_grad_small<F, E><<<grid, kSmThreads, 0, L.stream>>>(static_cast<const E *>(a.delta), a.codes, a.scales, a.T,
+                                                               a.d_out, a.d_in, (a.d_in + kActGroup - 1) / kActGroup,
+                                                               a.gamma, a.beta, a.db, a.dW);
+  return cudaGetLastError();
+}
+
 cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const WeightGrad &a) {
+  if (small_product(L.sms, a.T, a.d_out, a.d_in)) {
+    if (fmt == FMT_E4M3)
+      return bf16 ? launch_small<FMT_E4M3, __nv_bfloat16>(L, a) : launch_small<FMT_E4M3, float>(L, a);
+    return bf16 ? launch_small<FMT_E5M2, __nv_bfloat16>(L, a) : launch_small<FMT_E5M2, float>(L, a);
+  }
   const Plan p = plan_of(L.sms, a.T, a.d_out, a.d_in);
   const float *db = nullptr;
   cudaError_t e;
