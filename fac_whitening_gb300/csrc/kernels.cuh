@@ -353,9 +353,8 @@ size_t norm_part_floats(int sms, int T, int d);
 int norm_partials(int sms, int T);
 cudaError_t launch_norm_forward(const Launch &L, int fmt, bool bf16, const NormForward &a);
 cudaError_t launch_norm_backward(const Launch &L, int fmt, bool bf16, const NormBackward &a);
-// out[c] = sum_t x[t][c], slices of tokens added in order; part: col_part_floats
-size_t col_part_floats(int T, int d);
-cudaError_t launch_col_sums(const Launch &L, const void *x, bool bf16, int T, int d, float *part, float *out);
+// out[c] = sum_k part[k d + c], in order
+cudaError_t launch_sum_parts(const Launch &L, const float *part, int parts, int d, float *out);
 // ---- weight_grad.cu -------------------------------------------------------------------------
 struct WeightGradWs {
   size_t part_floats = 0;      // column-sum partials of db

@@ -476,19 +476,6 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_dx_long(const __grid_cons
   }
 }
 
-// sums over tokens of one matrix, in slices
-template <typename E>
-__global__ void __launch_bounds__(kNormThreads) k_col_sums(const E *__restrict__ x, int T, int d, int rows,
-                                                           float *__restrict__ part) {
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
-  grid_release();
-  if (c >= d) return;
-  const int t0 = blockIdx.y * rows, t1 = min(T, t0 + rows);
-  float s = 0.0f;
-  for (int t = t0; t < t1; ++t) s += ld1(x + (size_t)t * d + c);
-  part[(size_t)blockIdx.y * d + c] = s;
-}
-
 // ---- host ---------------------------------------------------------------------------------------------
 // tokens of a slice of a column pass: at least 16, at most 256 slices
 int col_rows(int T) {
@@ -654,19 +641,9 @@ size_t norm_part_floats(int sms, int T, int d) {
   return (size_t)2 * ((T + rows - 1) / rows) * d;
 }
 
-size_t col_part_floats(int T, int d) {
-  const int rows = col_rows(T);
-  return (size_t)((T + rows - 1) / rows) * d;
-}
-
-cudaError_t launch_col_sums(const Launch &L, const void *x, bool bf16, int T, int d, float *part, float *out) {
-  const int rows = col_rows(T), slices = (T + rows - 1) / rows, cb = (d + kNormThreads - 1) / kNormThreads;
-  if (bf16)
-    k_col_sums<<<dim3(cb, slices), kNormThreads, 0, L.stream>>>(static_cast<const __nv_bfloat16 *>(x), T, d, rows, part);
-  else
-    k_col_sums<<<dim3(cb, slices), kNormThreads, 0, L.stream>>>(static_cast<const float *>(x), T, d, rows, part);
-  return launch_after(L.stream, k_norm_sums, dim3((d + 31) / 32, 1), 1024, part, slices, (size_t)d, (size_t)0,
-                      d, out, static_cast<float *>(nullptr));
+cudaError_t launch_sum_parts(const Launch &L, const float *part, int parts, int d, float *out) {
+  return launch_after(L.stream, k_norm_sums, dim3((d + 31) / 32, 1), 1024, part, parts, (size_t)d, (size_t)0, d, out,
+                      static_cast<float *>(nullptr));
 }
 
 cudaError_t launch_norm_forward(const Launch &L, int fmt, bool bf16, const NormForward &a) {

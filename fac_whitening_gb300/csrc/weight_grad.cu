@@ -149,6 +149,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
+// wait for the programmatic predecessor's results / let the successor launch
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // a float of CTA r's copy of a shared variable
 __device__ __forceinline__ float ld_cluster(const float *p, int r) {
   float v;
@@ -327,6 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---------------- TMA ----------------
       uint32_t g = 0;   // stages so far
       bool ok = true;
+      grid_wait();   // what the kernels before this one wrote is there
       if (warp == kCodesWarp) {
         for (int it = pair; it < P.items && ok; it += pairs) {
           const Item w(P, it, 128 * NH);
@@ -542,6 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (NH == 2) fold(1, sum[NH - 1]);
       if (!ok) break;
       const int i = w.i0 + 128 * rank + 32 * q + lane;
+      grid_wait();   // db, where a kernel before this one made it
       if (i < P.d_in) {
         const float ga = P.gamma ? P.gamma[i] : 1.0f, be = P.beta ? P.beta[i] : 0.0f;
         float *out = P.out + (size_t)w.slice * P.d_out * P.d_in + i;
@@ -719,30 +724,46 @@ __global__ void __launch_bounds__(256) k_join_slices(const float *__restrict__ p
   }
 }
 
-// Scale bytes [T][groups] -> StageScales [groups][stages] (NaN for a marked group, 1 past T): 256
-// tokens x 64 groups per CTA through shared memory, a warp writes a stage.
+// ---- what the tensor-core kernel reads, made by one launch -------------------------------------------
+struct Prepare {
+  const uint8_t *scales;       // [T][groups]
+  StageScales *stage_scales;   // [groups][stages]
+  int T, groups, stages;
+  int nscale, nsums, ndelta, ncodes;   // CTAs of each part, in this order
+  int sum_slices, sum_rows;    // nsums > 0: sums of delta over slices of consecutive tokens
+  bool sum_vec;
+  float *sum_part;             // [sum_slices][d_out]
+  const void *delta;           // ndelta > 0: FP32 -> three BF16 terms, or BF16 rows of another pitch
+  void *delta_out;
+  int d_out, delta_ld;         // delta_ld: elements
+  const uint8_t *codes;        // ncodes > 0: rows of another pitch
+  uint8_t *codes_out;
+  int d_in;
+  size_t codes_ld;
+};
+
+// Scale bytes -> StageScales (NaN for a marked group, 1 past T): a stage of 64 tokens x 64 groups per CTA
+// through shared memory, a warp writes a group.
 template <int F>
-__global__ void __launch_bounds__(256) k_stage_scales(const uint8_t *__restrict__ scales, int T, int groups,
-                                                      int stages, StageScales *__restrict__ out) {
-  __shared__ uint8_t tile[256][65];
+__device__ __forceinline__ void stage_scales(const Prepare &P, int cta) {
+  __shared__ uint8_t tile[kK][65];
   constexpr int up = F == FMT_E4M3 ? 120 : 112;
-  const int t0 = blockIdx.x * 256, g0 = blockIdx.y * 64, ng = min(64, groups - g0);
-  for (int e = threadIdx.x; e < 256 * ng; e += 256) {
-    const int r = e / ng, c = e - r * ng;
-    tile[r][c] = t0 + r < T ? scales[(size_t)(t0 + r) * groups + g0 + c] : 127;
-  }
-  __syncthreads();
+  const int stage = cta % P.stages, g0 = cta / P.stages * 64, ng = min(64, P.groups - g0), t0 = stage * kK;
   const int lane = threadIdx.x & 31;
-  for (int e = threadIdx.x >> 5; e < 4 * ng; e += 8) {
-    const int st = e & 3, c = e >> 2;
+  for (int r = threadIdx.x >> 5; r < kK; r += 8)
+#pragma unroll
+    for (int c = lane; c < 64; c += 32)
+      if (c < ng) tile[r][c] = t0 + r < P.T ? P.scales[(size_t)(t0 + r) * P.groups + g0 + c] : 127;
+  __syncthreads();
+  for (int c = threadIdx.x >> 5; c < ng; c += 8) {
     uint32_t first[2], over[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int b = tile[64 * st + 2 * lane + u][c];
+      const int b = tile[2 * lane + u][c];
       over[u] = b == (int)kActBad ? 0u : (uint32_t)max(0, b + up - 254);
       first[u] = b == (int)kActBad ? 0x7FC0u : (uint32_t)(b + up - (int)over[u]) << 7;
     }
-    StageScales &o = out[(size_t)(g0 + c) * stages + t0 / kK + st];
+    StageScales &o = P.stage_scales[(size_t)(g0 + c) * P.stages + stage];
     reinterpret_cast<uint32_t *>(o.first)[lane] = first[0] | first[1] << 16;
     reinterpret_cast<uint16_t *>(o.over)[lane] = (uint16_t)(over[0] | over[1] << 8);
     const bool any = __any_sync(0xFFFFFFFFu, (over[0] | over[1]) != 0);
@@ -750,22 +771,58 @@ __global__ void __launch_bounds__(256) k_stage_scales(const uint8_t *__restrict_
   }
 }
 
-// FP32 delta as three BF16 terms (exact), planes of T rows of ld columns
-__global__ void __launch_bounds__(256) k_delta_terms(const float *__restrict__ x, int T, int d, int ld,
-                                                     uint16_t *__restrict__ out) {
-  const size_t n = (size_t)T * d, plane = (size_t)T * ld, step = (size_t)gridDim.x * 256;
-  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < n; e += step) {
-    const size_t t = e / d, at = t * ld + (e - t * d);
-    tc::bf16_split3(x[e], out[at], out[plane + at], out[2 * plane + at]);
+// Sums over a slice of tokens of one piece of 512 columns: a warp takes every eighth token, the eight
+// warps' sums are joined in order.
+template <typename E, bool VEC>
+__device__ __forceinline__ void column_sums(const Prepare &P, int cta) {
+  __shared__ float sh[8][16 * 33];   // a lane's 16 columns 33 words apart: neither side conflicts
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c0 = cta / P.sum_slices * kPiece, slice = cta % P.sum_slices, n = P.d_out - c0;
+  const int t1 = min(P.T, (slice + 1) * P.sum_rows);
+  float2 s[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[k] = both(0.0f);
+#pragma unroll 4
+  for (int t = slice * P.sum_rows + w; t < t1; t += 8) {
+    Raw<E> r;
+    load_piece<VEC>(static_cast<const E *>(P.delta) + (size_t)t * P.d_out + c0, n, lane, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] = add2(s[k], r.pair(k));
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sh[w][33 * e + lane] = e & 1 ? s[e / 2].y : s[e / 2].x;
+  __syncthreads();
+  for (int c = threadIdx.x; c < kPiece && c < n; c += 256) {
+    const int at = VEC ? 33 * (c % 16) + c / 16 : 33 * (c / 32) + c % 32;
+    float v = sh[0][at];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += sh[k][at];
+    P.sum_part[(size_t)slice * P.d_out + c0 + c] = v;
+  }
+}
+
+// FP32 as three BF16 terms (exact), planes of T rows of ld columns
+__device__ __forceinline__ void bf16_terms(const float *x, int T, int d, int ld, uint16_t *out, int cta, int ctas) {
+  const size_t plane = (size_t)T * ld;
+  const int pairs = (d + 1) / 2;   // two columns at a time; ld is even
+  const size_t n = (size_t)T * pairs, step = (size_t)ctas * 256;
+  for (size_t e = (size_t)cta * 256 + threadIdx.x; e < n; e += step) {
+    const size_t t = e / pairs;
+    const int c = (int)(e - t * pairs) * 2;
+    const float *p = x + t * d + c;
+    uint32_t w[3];
+    tc::bf16_split3x2(p[0], c + 1 < d ? p[1] : 0.0f, w[0], w[1], w[2]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(out + k * plane + t * ld + c) = w[k];
   }
 }
 
 // Rows of `bytes` bytes at any alignment -> rows of ld (a multiple of 16) bytes, 16 at a time
-__global__ void __launch_bounds__(256) k_repitch(const uint8_t *__restrict__ src, int T, size_t bytes, size_t ld,
-                                                 uint8_t *__restrict__ dst) {
-  const size_t per = (bytes + 15) / 16, n = (size_t)T * per, step = (size_t)gridDim.x * 256;
+__device__ __forceinline__ void repitch(const uint8_t *src, int T, size_t bytes, size_t ld, uint8_t *dst, int cta,
+                                        int ctas) {
+  const size_t per = (bytes + 15) / 16, n = (size_t)T * per, step = (size_t)ctas * 256;
   const uintptr_t lo = (uintptr_t)src, hi = lo + (size_t)T * bytes;
-  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < n; e += step) {
+  for (size_t e = (size_t)cta * 256 + threadIdx.x; e < n; e += step) {
     const size_t t = e / per, c = (e - t * per) * 16;
     const uintptr_t a = lo + t * bytes + c, w0 = a & ~(uintptr_t)3;
     const int sh = (int)(a & 3) * 8;
@@ -788,6 +845,34 @@ __global__ void __launch_bounds__(256) k_repitch(const uint8_t *__restrict__ src
     v.w = __funnelshift_r(w[3], w[4], sh);
     *reinterpret_cast<uint4 *>(dst + t * ld + c) = v;   // past the row's end: never read (the tensor map's width)
   }
+}
+
+template <int F, bool BF16>
+__global__ void __launch_bounds__(256) k_prepare(const __grid_constant__ Prepare P) {
+  grid_release();
+  int cta = blockIdx.x;
+  if (cta < P.nscale) {
+    stage_scales<F>(P, cta);
+    return;
+  }
+  cta -= P.nscale;
+  if (cta < P.nsums) {
+    using E = typename std::conditional<BF16, __nv_bfloat16, float>::type;
+    if (P.sum_vec) column_sums<E, true>(P, cta);
+    else column_sums<E, false>(P, cta);
+    return;
+  }
+  cta -= P.nsums;
+  if (cta < P.ndelta) {
+    if (BF16)
+      repitch(static_cast<const uint8_t *>(P.delta), P.T, (size_t)P.d_out * 2, (size_t)P.delta_ld * 2,
+              static_cast<uint8_t *>(P.delta_out), cta, P.ndelta);
+    else
+      bf16_terms(static_cast<const float *>(P.delta), P.T, P.d_out, P.delta_ld, static_cast<uint16_t *>(P.delta_out),
+                 cta, P.ndelta);
+    return;
+  }
+  repitch(P.codes, P.T, P.d_in, P.codes_ld, P.codes_out, cta - P.ndelta, P.ncodes);
 }
 
 // ---- host ---------------------------------------------------------------------------------------
@@ -850,14 +935,30 @@ Plan plan_of(int sms, int T, int d_out, int d_in) {
   return p;
 }
 
+// Slices of tokens for delta's sums: about four CTAs per SM with all pieces, 64 tokens at least.
+int sum_slices(int sms, int T, int d_out) {
+  const int pieces = (d_out + kPiece - 1) / kPiece, most = (T + 63) / 64;
+  const int s = (4 * sms + pieces - 1) / pieces;
+  return s < most ? s : most;
+}
+
 template <int F, int NH, int TERMS>
 cudaError_t launch(const Launch &L, const Params &P, const CUtensorMap &tc_, const CUtensorMap &td, int pairs) {
   using C = Cfg<NH, TERMS>;
   const cudaError_t e = ensure_dynamic_smem<k_weight_grad<F, NH, TERMS>>(C::smem);
   if (e != cudaSuccess) return e;
-  k_weight_grad<F, NH, TERMS><<<2 * (P.items < pairs ? P.items : pairs), kThreads, C::smem, L.stream>>>(P, tc_, td,
-                                                                                                       L.status);
-  return cudaGetLastError();
+  // launched while k_prepare still runs (grid_wait)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * (P.items < pairs ? P.items : pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::smem;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_weight_grad<F, NH, TERMS>, P, tc_, td, L.status);
 }
 
 template <int F>
@@ -877,7 +978,7 @@ int stream_grid(const Launch &L, size_t n) {
 WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) {
   WeightGradWs w;
   const Plan p = plan_of(sms, T, d_out, d_in);
-  w.part_floats = col_part_floats(T, d_out);
+  w.part_floats = (size_t)sum_slices(sms, T, d_out) * d_out;
   w.slice_floats = p.slices > 1 ? (size_t)p.slices * d_out * d_in : 0;
   // a BF16 delta and the codes are copied only when their rows are not 16-byte aligned, which the
   // caller's pointers decide: room for both
@@ -910,38 +1011,55 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
     return bf16 ? launch_small<FMT_E5M2, __nv_bfloat16>(L, a) : launch_small<FMT_E5M2, float>(L, a);
   }
   const Plan p = plan_of(L.sms, a.T, a.d_out, a.d_in);
-  const float *db = nullptr;
+  const bool one = p.slices == 1, need_db = a.db || a.beta;
+  float *const db = need_db ? (a.db ? a.db : a.db_ws) : nullptr;
   cudaError_t e;
-  if (a.db || a.beta) {
-    float *out = a.db ? a.db : a.db_ws;
-    if ((e = launch_col_sums(L, a.delta, bf16, a.T, a.d_out, a.part, out)) != cudaSuccess) return e;
-    db = out;
+  // operands with 16-byte aligned rows, and the scales by group and stage
+  Prepare q{};
+  q.scales = a.scales;
+  q.stage_scales = static_cast<StageScales *>(a.scale_ws);
+  q.T = a.T;
+  q.groups = (a.d_in + kActGroup - 1) / kActGroup;
+  q.stages = p.ng * kGroup;
+  q.nscale = q.stages * ((q.groups + 63) / 64);
+  q.delta = a.delta;
+  q.delta_out = a.delta_ws;
+  q.d_out = a.d_out;
+  q.codes = a.codes;
+  q.codes_out = a.code_ws;
+  q.d_in = a.d_in;
+  if (need_db) {
+    q.sum_slices = sum_slices(L.sms, a.T, a.d_out);
+    q.sum_rows = (a.T + q.sum_slices - 1) / q.sum_slices;
+    q.sum_vec = rows_vec(a.d_out, a.delta, nullptr);
+    q.sum_part = a.part;
+    q.nsums = q.sum_slices * ((a.d_out + kPiece - 1) / kPiece);
   }
-  // operands with 16-byte aligned rows
   const void *delta = a.delta;
   size_t dpitch = (size_t)a.d_out * 2;
-  if (!bf16) {
+  if (!bf16 || dpitch % 16 || !aligned16(delta)) {
     dpitch = pad16(dpitch);
-    k_delta_terms<<<stream_grid(L, (size_t)a.T * a.d_out), 256, 0, L.stream>>>(
-        static_cast<const float *>(a.delta), a.T, a.d_out, (int)(dpitch / 2), static_cast<uint16_t *>(a.delta_ws));
+    q.delta_ld = (int)(dpitch / 2);
+    q.ndelta = stream_grid(L, bf16 ? (size_t)a.T * dpitch / 16 : (size_t)a.T * q.delta_ld / 2);
     delta = a.delta_ws;
-  } else if (dpitch % 16 || !aligned16(delta)) {
-    const size_t ld = pad16(dpitch);
-    k_repitch<<<stream_grid(L, (size_t)a.T * ld / 16), 256, 0, L.stream>>>(static_cast<const uint8_t *>(delta), a.T,
-                                                                           dpitch, ld,
-                                                                           static_cast<uint8_t *>(a.delta_ws));
-    delta = a.delta_ws;
-    dpitch = ld;
   }
   const uint8_t *codes = a.codes;
   size_t cpitch = a.d_in;
   if (cpitch % 16 || !aligned16(codes)) {
-    const size_t ld = pad16(cpitch);
-    k_repitch<<<stream_grid(L, (size_t)a.T * ld / 16), 256, 0, L.stream>>>(codes, a.T, cpitch, ld, a.code_ws);
+    cpitch = q.codes_ld = pad16(cpitch);
+    q.ncodes = stream_grid(L, (size_t)a.T * cpitch / 16);
     codes = a.code_ws;
-    cpitch = ld;
+  }
+  const int pgrid = q.nscale + q.nsums + q.ndelta + q.ncodes;
+  if (fmt == FMT_E4M3) {
+    if (bf16) k_prepare<FMT_E4M3, true><<<pgrid, 256, 0, L.stream>>>(q);
+    else k_prepare<FMT_E4M3, false><<<pgrid, 256, 0, L.stream>>>(q);
+  } else {
+    if (bf16) k_prepare<FMT_E5M2, true><<<pgrid, 256, 0, L.stream>>>(q);
+    else k_prepare<FMT_E5M2, false><<<pgrid, 256, 0, L.stream>>>(q);
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (need_db && (e = launch_sum_parts(L, a.part, q.sum_slices, a.d_out, db)) != cudaSuccess) return e;
 
   CUtensorMap tm_codes, tm_delta;
   if (!boxes(&tm_codes, false, codes, a.T, a.d_in, cpitch, 1) ||
@@ -951,19 +1069,14 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   P.T = a.T;
   P.d_out = a.d_out;
   P.d_in = a.d_in;
-  P.groups = (a.d_in + kActGroup - 1) / kActGroup;
+  P.groups = q.groups;
   P.ng = p.ng;
   P.mt = p.mt;
   P.nt = p.nt;
   P.slices = p.slices;
   P.items = p.mt * p.nt * p.slices;
-  StageScales *scales = static_cast<StageScales *>(a.scale_ws);
-  P.scales = scales;
-  P.stages = p.ng * kGroup;
-  const dim3 sgrid(p.ng, (P.groups + 63) / 64);
-  if (fmt == FMT_E4M3) k_stage_scales<FMT_E4M3><<<sgrid, 256, 0, L.stream>>>(a.scales, a.T, P.groups, P.stages, scales);
-  else k_stage_scales<FMT_E5M2><<<sgrid, 256, 0, L.stream>>>(a.scales, a.T, P.groups, P.stages, scales);
-  const bool one = p.slices == 1;
+  P.scales = q.stage_scales;
+  P.stages = q.stages;
   P.gamma = one ? a.gamma : nullptr;
   P.beta = one ? a.beta : nullptr;
   P.db = one ? db : nullptr;
