@@ -132,9 +132,7 @@ def _p(t) -> Optional[int]:
     """Address of a caller buffer for the library: None, a raw device address (int), or a
     contiguous CUDA tensor.  A host tensor or a strided view is refused here, since a kernel
     would read it as contiguous device memory."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     if not getattr(t, "is_cuda", False):
         raise ValueError("libgift buffers live in device memory: pass a CUDA tensor")
@@ -429,18 +427,37 @@ def _dt(t) -> int:
     raise ValueError(f"libgift takes float32 or bfloat16 activations and gradients, not {dt}")
 
 
-def _need(t, shape, what: str, dtype=None):
-    """Refuse a buffer whose shape or type is not what the call passes on to the library."""
-    if t is not None and (t.shape != shape or (dtype is not None and t.dtype != dtype)):
-        raise ValueError(f"{what}: expected {tuple(shape)}{'' if dtype is None else ' ' + str(dtype)}, "
-                         f"got {tuple(t.shape)} {t.dtype}")
+def _f32():
+    import torch
+    return torch.float32
 
 
-def _need_saved(codes, scales, T: int, d: int):
-    """Refuse checkpoint buffers that are not bytes or are smaller than a T x d checkpoint."""
-    for t, n, what in ((codes, T * d, "codes"), (scales, T * ((d + 127) // 128), "scales")):
-        if t.element_size() != 1 or t.numel() < n:
-            raise ValueError(f"{what}: expected at least {n} bytes, got {t.numel()} of {t.dtype}")
+def _buf(t, n: int, what: str, dtype) -> Optional[int]:
+    """Address of a dense device tensor of n elements of this type (None: NULL).  One call per buffer: these
+    checks are most of what a small call costs on the host."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n:
+        raise ValueError(f"{what}: expected {n} elements of {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        return _p(t)   # refuses it
+    return t.data_ptr()
+
+
+def _bytes(t, n: int, what: str) -> Optional[int]:
+    """Address of a dense device buffer of single bytes, at least n of them."""
+    if t is None:
+        return None
+    if t.element_size() != 1 or t.numel() < n:
+        raise ValueError(f"{what}: expected at least {n} bytes, got {t.numel()} of {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        return _p(t)
+    return t.data_ptr()
+
+
+def _ws(ws):
+    """Address and size of a workspace tensor."""
+    return (None, 0) if ws is None else (_p(ws), ws.numel() * ws.element_size())
 
 
 def gift_act_sizes(fmt: str, T: int, d: int):
@@ -459,61 +476,53 @@ def gift_act_workspace_bytes(ctx: Context, op: str, dtype, T: int, d_out: int, d
 
 def gift_act_encode(ctx: Context, x, fmt: str, codes, scales, status=None, stream=None):
     T, d = x.shape
-    _need_saved(codes, scales, T, d)
-    _check(lib().gift_act_encode(ctx.handle, _p(x), _dt(x), T, d, FMT[fmt], _p(codes), _p(scales), _p(status),
-                                 _stream(stream)), "gift_act_encode")
+    _check(lib().gift_act_encode(ctx.handle, _p(x), _dt(x), T, d, FMT[fmt], _bytes(codes, T * d, "codes"),
+                                 _bytes(scales, T * ((d + 127) // 128), "scales"), _p(status), _stream(stream)),
+           "gift_act_encode")
 
 
 def gift_act_decode(ctx: Context, codes, scales, fmt: str, x_out, status=None, stream=None):
     T, d = x_out.shape
-    _need_saved(codes, scales, T, d)
-    _check(lib().gift_act_decode(ctx.handle, _p(codes), _p(scales), FMT[fmt], T, d, _p(x_out), _dt(x_out),
-                                 _p(status), _stream(stream)), "gift_act_decode")
+    _check(lib().gift_act_decode(ctx.handle, _bytes(codes, T * d, "codes"),
+                                 _bytes(scales, T * ((d + 127) // 128), "scales"), FMT[fmt], T, d, _p(x_out),
+                                 _dt(x_out), _p(status), _stream(stream)), "gift_act_decode")
 
 
 def gift_layernorm_forward(ctx: Context, x, gamma, beta, eps: float, y, mean=None, rstd=None, fmt: str = "e4m3",
                            codes=None, scales=None, status=None, stream=None):
-    import torch
+    f32 = _f32()
     T, d = x.shape
-    _need(y, (T, d), "y", x.dtype)
-    for t, n, what in ((gamma, d, "gamma"), (beta, d, "beta"), (mean, T, "mean"), (rstd, T, "rstd")):
-        _need(t, (n,), what, torch.float32)
-    if codes is not None and scales is not None:
-        _need_saved(codes, scales, T, d)
-    _check(lib().gift_layernorm_forward(ctx.handle, _p(x), _dt(x), T, d, _p(gamma), _p(beta), eps, _p(y), _p(mean),
-                                        _p(rstd), FMT[fmt], _p(codes), _p(scales), _p(status), _stream(stream)),
-           "gift_layernorm_forward")
+    _check(lib().gift_layernorm_forward(ctx.handle, _p(x), _dt(x), T, d, _buf(gamma, d, "gamma", f32),
+                                        _buf(beta, d, "beta", f32), eps, _buf(y, T * d, "y", x.dtype),
+                                        _buf(mean, T, "mean", f32), _buf(rstd, T, "rstd", f32), FMT[fmt],
+                                        _bytes(codes, T * d, "codes"),
+                                        _bytes(scales, T * ((d + 127) // 128), "scales"), _p(status),
+                                        _stream(stream)), "gift_layernorm_forward")
 
 
 def gift_layernorm_backward(ctx: Context, dy, saved, gamma, rstd, dx, dgamma=None, dbeta=None, mean=None,
                             scales=None, fmt: str = "e4m3", ws=None, status=None, stream=None):
     """saved: the forward pass's x (with mean), or its checkpoint's codes (with scales)."""
-    import torch
+    f32 = _f32()
     T, d = dy.shape
-    _need(dx, (T, d), "dx", dy.dtype)
-    for t, n, what in ((gamma, d, "gamma"), (dgamma, d, "dgamma"), (dbeta, d, "dbeta"), (mean, T, "mean"),
-                       (rstd, T, "rstd")):
-        _need(t, (n,), what, torch.float32)
-    if scales is None:
-        _need(saved, (T, d), "saved", dy.dtype)
-    else:
-        _need_saved(saved, scales, T, d)
-    _check(lib().gift_layernorm_backward(ctx.handle, _p(dy), _dt(dy), T, d, _p(saved), int(scales is not None),
-                                         _p(scales), FMT[fmt], _p(mean), _p(rstd), _p(gamma), _p(dx), _p(dgamma),
-                                         _p(dbeta), _p(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+    kept = _buf(saved, T * d, "saved", dy.dtype) if scales is None else _bytes(saved, T * d, "codes")
+    w, wn = _ws(ws)
+    _check(lib().gift_layernorm_backward(ctx.handle, _p(dy), _dt(dy), T, d, kept, int(scales is not None),
+                                         _bytes(scales, T * ((d + 127) // 128), "scales"), FMT[fmt],
+                                         _buf(mean, T, "mean", f32), _buf(rstd, T, "rstd", f32),
+                                         _buf(gamma, d, "gamma", f32), _buf(dx, T * d, "dx", dy.dtype),
+                                         _buf(dgamma, d, "dgamma", f32), _buf(dbeta, d, "dbeta", f32), w, wn,
                                          _p(status), _stream(stream)), "gift_layernorm_backward")
 
 
 def gift_weight_grad(ctx: Context, delta, codes, scales, fmt: str, dW, db=None, gamma=None, beta=None, ws=None,
                      status=None, stream=None):
-    import torch
+    f32 = _f32()
     T, d_out = delta.shape
     d_in = dW.shape[1]
-    _need(dW, (d_out, d_in), "dW", torch.float32)
-    _need_saved(codes, scales, T, d_in)
-    for t, n, what in ((db, d_out, "db"), (gamma, d_in, "gamma"), (beta, d_in, "beta")):
-        _need(t, (n,), what, torch.float32)
-    _check(lib().gift_weight_grad(ctx.handle, _p(delta), _dt(delta), _p(codes), _p(scales), FMT[fmt], T, d_out, d_in,
-                                  _p(gamma), _p(beta), _p(dW), _p(db), _p(ws),
-                                  0 if ws is None else ws.numel() * ws.element_size(), _p(status), _stream(stream)),
-           "gift_weight_grad")
+    w, wn = _ws(ws)
+    _check(lib().gift_weight_grad(ctx.handle, _p(delta), _dt(delta), _bytes(codes, T * d_in, "codes"),
+                                  _bytes(scales, T * ((d_in + 127) // 128), "scales"), FMT[fmt], T, d_out, d_in,
+                                  _buf(gamma, d_in, "gamma", f32), _buf(beta, d_in, "beta", f32),
+                                  _buf(dW, d_out * d_in, "dW", f32), _buf(db, d_out, "db", f32), w, wn,
+                                  _p(status), _stream(stream)), "gift_weight_grad")
