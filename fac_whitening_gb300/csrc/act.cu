@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kActThreads) k_act_decode(const uint8_t *__res
        w.t < T; w.next()) {
     const int c0 = w.p * kPiece, n = d - c0;
     const size_t at = (size_t)w.t * d + c0;
-    RawCodes r;
+    RawCodes<> r;
     load_codes<VEC>(codes + at, scales + (size_t)w.t * groups + w.p * 4, n, lane, r);
     float2 v[8];
 #pragma unroll

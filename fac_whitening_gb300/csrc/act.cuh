@@ -39,17 +39,22 @@ __device__ __forceinline__ void st1(float *p, float v) { *p = v; }
 __device__ __forceinline__ void st1(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // ------------------------------------------------------------------------------------------------
-// Row pieces.  A warp handles a row in pieces of 512 columns, 16 per lane, so that a piece holds
-// four whole scale groups.  Two layouts: VEC, for rows whose pitch and base allow 32-byte accesses
-// (d a multiple of 16), lane l holds columns 16 l .. 16 l + 15 (a group is eight lanes); otherwise
+// Row pieces.  A warp handles a row in pieces of 32 C columns, C = 16 or 8 per lane, so that a piece
+// holds whole scale groups.  Two layouts: VEC, for rows whose pitch and base allow 32-byte accesses
+// (d a multiple of 16), lane l holds columns C l .. C l + C - 1 (a group is 128 / C lanes); otherwise
 // lane l holds columns l, l + 32, ... (a group is four consecutive registers of the warp), each
 // access one element wide and consecutive over the warp.
 // ------------------------------------------------------------------------------------------------
-constexpr int kPiece = 512;
+constexpr int kPiece = 512;   // C = 16
 
 __device__ __forceinline__ void ld256(const void *p, uint32_t *r) {
   asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void ld128(const void *p, uint32_t *r) {
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "l"(p));
 }
 __device__ __forceinline__ void st256(void *p, const uint32_t *r) {
@@ -91,124 +96,96 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// The element type's registers for a lane's 16 columns of a piece, as loaded.
-template <typename E>
+// The element type's registers for a lane's C columns of a piece, as loaded.
+template <typename E, int C = 16>
 struct Raw;
-template <>
-struct Raw<float> {
-  uint32_t r[16];
+template <int C>
+struct Raw<float, C> {
+  uint32_t r[C];
   __device__ __forceinline__ float2 pair(int k) const {   // elements 2 k and 2 k + 1
     return make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
   }
 };
-template <>
-struct Raw<__nv_bfloat16> {
-  uint32_t r[8];
+template <int C>
+struct Raw<__nv_bfloat16, C> {
+  uint32_t r[C / 2];
   __device__ __forceinline__ float2 pair(int k) const {
     return make_float2(__uint_as_float(r[k] << 16), __uint_as_float(r[k] & 0xFFFF0000u));
   }
 };
 
 // column of a lane's e-th value within its piece
-template <bool VEC>
-__device__ __forceinline__ int piece_col(int lane, int e) { return VEC ? 16 * lane + e : 32 * e + lane; }
+template <bool VEC, int C = 16>
+__device__ __forceinline__ int piece_col(int lane, int e) { return VEC ? C * lane + e : 32 * e + lane; }
 
 // Load a lane's values of the piece at p (n columns of the row are left, zeros past them).
-template <bool VEC>
-__device__ __forceinline__ void load_piece(const float *p, int n, int lane, Raw<float> &x) {
+template <bool VEC, int C>
+__device__ __forceinline__ void load_piece(const float *p, int n, int lane, Raw<float, C> &x) {
   if (VEC) {
-    if (16 * lane < n) {
-      ld256(p + 16 * lane, x.r);
-      ld256(p + 16 * lane + 8, x.r + 8);
+    if (C * lane < n) {
+#pragma unroll
+      for (int e = 0; e < C; e += 8) ld256(p + C * lane + e, x.r + e);
     } else {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x.r[e] = 0u;
+      for (int e = 0; e < C; ++e) x.r[e] = 0u;
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x.r[e] = 32 * e + lane < n ? __float_as_uint(p[32 * e + lane]) : 0u;
+    for (int e = 0; e < C; ++e) x.r[e] = 32 * e + lane < n ? __float_as_uint(p[32 * e + lane]) : 0u;
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void load_piece(const __nv_bfloat16 *p, int n, int lane, Raw<__nv_bfloat16> &x) {
+template <bool VEC, int C>
+__device__ __forceinline__ void load_piece(const __nv_bfloat16 *p, int n, int lane, Raw<__nv_bfloat16, C> &x) {
   if (VEC) {
-    if (16 * lane < n) {
-      ld256(p + 16 * lane, x.r);
+    if (C * lane < n) {
+      if constexpr (C == 16) ld256(p + C * lane, x.r);
+      else ld128(p + C * lane, x.r);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x.r[e] = 0u;
+      for (int e = 0; e < C / 2; ++e) x.r[e] = 0u;
     }
   } else {
     const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
-    uint32_t v[16];
+    uint32_t v[C];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = 32 * e + lane < n ? (uint32_t)q[32 * e + lane] : 0u;
+    for (int e = 0; e < C; ++e) v[e] = 32 * e + lane < n ? (uint32_t)q[32 * e + lane] : 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x.r[e] = v[2 * e] | v[2 * e + 1] << 16;
+    for (int e = 0; e < C / 2; ++e) x.r[e] = v[2 * e] | v[2 * e + 1] << 16;
   }
 }
 
-// A ring of pieces on their way to one lane: asynchronous 16-byte copies into shared memory that only
-// this lane reads, so that many rows are in flight without a register or a barrier for them.  DEPTH
-// slots of CHUNKS x 32 lanes x 16 bytes per warp.
-template <int CHUNKS, int DEPTH>
-struct LaneRing {
-  static constexpr int bytes = CHUNKS * DEPTH * 512;   // per warp
-  uint32_t base;
-  __device__ __forceinline__ LaneRing(void *warp_base, int lane)
-      : base((uint32_t)__cvta_generic_to_shared(warp_base) + 16 * lane) {}
-  __device__ __forceinline__ void clear() const {   // lanes past the row's end never copy: they read zeros
-#pragma unroll
-    for (int k = 0; k < CHUNKS * DEPTH; ++k)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + 512 * k), "r"(0u) : "memory");
-  }
-  __device__ __forceinline__ void copy(int slot, int chunk, const void *src) const {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + 512 * (slot * CHUNKS + chunk)), "l"(src)
-                 : "memory");
-  }
-  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-  __device__ __forceinline__ static void wait_oldest() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-  }
-  __device__ __forceinline__ void read(int slot, int chunk, uint32_t *r) const {
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(base + 512 * (slot * CHUNKS + chunk))
-                 : "memory");
-  }
-};
-
-template <bool VEC>
+template <bool VEC, int C = 16>
 __device__ __forceinline__ void store_piece(float *p, int n, int lane, const float2 *v) {
   if (VEC) {
-    if (16 * lane < n) {
-      uint32_t r[16];
+    if (C * lane < n) {
+      uint32_t r[C];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < C / 2; ++k) {
         r[2 * k] = __float_as_uint(v[k].x);
         r[2 * k + 1] = __float_as_uint(v[k].y);
       }
-      st256(p + 16 * lane, r);
-      st256(p + 16 * lane + 8, r + 8);
+#pragma unroll
+      for (int e = 0; e < C; e += 8) st256(p + C * lane + e, r + e);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < C; ++e)
       if (32 * e + lane < n) p[32 * e + lane] = e & 1 ? v[e / 2].y : v[e / 2].x;
   }
 }
-template <bool VEC>
+template <bool VEC, int C = 16>
 __device__ __forceinline__ void store_piece(__nv_bfloat16 *p, int n, int lane, const float2 *v) {
   if (VEC) {
-    if (16 * lane < n) {
-      uint32_t r[8];
+    if (C * lane < n) {
+      uint32_t r[C / 2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) r[k] = pack_bf16(v[k].x, v[k].y);
-      st256(p + 16 * lane, r);
+      for (int k = 0; k < C / 2; ++k) r[k] = pack_bf16(v[k].x, v[k].y);
+      if constexpr (C == 16) st256(p + C * lane, r);
+      else *reinterpret_cast<uint4 *>(p + C * lane) = make_uint4(r[0], r[1], r[2], r[3]);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < C; ++e)
       if (32 * e + lane < n) p[32 * e + lane] = __float2bfloat16_rn(e & 1 ? v[e / 2].y : v[e / 2].x);
   }
 }
@@ -254,42 +231,41 @@ __device__ __forceinline__ bool encode_piece(const float2 *v, int n, int lane, u
   return bad;
 }
 
-// A lane's 16 codes of a piece and their scales, as loaded.
+// A lane's C codes of a piece and their scales, as loaded.
+template <int C = 16>
 struct RawCodes {
-  uint32_t c[4];   // VEC: 16 bytes in order; otherwise byte k of c[g] is element 4 g + k
-  uint32_t s;      // VEC: the lane's scale byte; otherwise the four groups' bytes
+  uint32_t c[C / 4];   // VEC: the bytes in order; otherwise byte k of c[g] is element 4 g + k
+  uint32_t s;          // VEC: the lane's scale byte; otherwise the groups' bytes
 };
-template <bool VEC>
-__device__ __forceinline__ void load_codes(const uint8_t *cp, const uint8_t *sp, int n, int lane, RawCodes &x) {
+template <bool VEC, int C>
+__device__ __forceinline__ void load_codes(const uint8_t *cp, const uint8_t *sp, int n, int lane, RawCodes<C> &x) {
   if (VEC) {
-    x.c[0] = x.c[1] = x.c[2] = x.c[3] = 0u;
+#pragma unroll
+    for (int k = 0; k < C / 4; ++k) x.c[k] = 0u;
     x.s = 127u;
-    if (16 * lane < n) {
-      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(x.c[0]), "=r"(x.c[1]), "=r"(x.c[2]), "=r"(x.c[3])
-                   : "l"(cp + 16 * lane));
-      x.s = sp[lane >> 3];
+    if (C * lane < n) {
+      if constexpr (C == 16) ld128(cp + C * lane, x.c);
+      else asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];" : "=r"(x.c[0]), "=r"(x.c[1]) : "l"(cp + C * lane));
+      x.s = sp[lane * C / kActGroup];
     }
   } else {
-    x.s = 0x7F7F7F7Fu;
+    uint32_t mine = 127u;
+    if (lane < C / 4 && kActGroup * lane < n) mine = sp[lane];
+    x.s = 0;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < C / 4; ++g) {
+      x.s |= __shfl_sync(0xFFFFFFFFu, mine, g) << (8 * g);
       x.c[g] = 0u;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (32 * (4 * g + k) + lane < n) x.c[g] |= (uint32_t)cp[32 * (4 * g + k) + lane] << (8 * k);
     }
-    if (lane < 4 && kActGroup * lane < n) x.s = sp[lane];   // gathered below
-    uint32_t s = 0;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) s |= (__shfl_sync(0xFFFFFFFFu, x.s, g) & 0xFFu) << (8 * g);
-    x.s = s;
   }
 }
 // The values of elements 2 k and 2 k + 1 (of one group in either layout): the hardware's conversion to
 // FP16 holds every code exactly, and so does FP32.
-template <int F, bool VEC>
-__device__ __forceinline__ float2 code_pair(const RawCodes &x, int k) {
+template <int F, bool VEC, int C>
+__device__ __forceinline__ float2 code_pair(const RawCodes<C> &x, int k) {
   const uint16_t c = (uint16_t)(k & 1 ? x.c[k >> 1] >> 16 : x.c[k >> 1] & 0xFFFFu);
   uint32_t h;
   if (F == FMT_E4M3) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));

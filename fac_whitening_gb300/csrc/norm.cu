@@ -77,23 +77,23 @@ struct RowGroup {
   }
 };
 
-// 16 per-column factors of a lane (c0: the piece's first column)
-template <bool VEC>
+// C per-column factors of a lane (c0: the piece's first column)
+template <bool VEC, int C = 16>
 __device__ __forceinline__ void load_cols(const float *p, int c0, int n, int lane, float fill, float2 *v) {
   if (p == nullptr) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = both(fill);
+    for (int k = 0; k < C / 2; ++k) v[k] = both(fill);
   } else if (VEC) {
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      const float4 f = 16 * lane < n ? __ldg(reinterpret_cast<const float4 *>(p + c0 + 16 * lane + 2 * k))
-                                     : make_float4(fill, fill, fill, fill);
+    for (int k = 0; k < C / 2; k += 2) {
+      const float4 f = C * lane < n ? __ldg(reinterpret_cast<const float4 *>(p + c0 + C * lane + 2 * k))
+                                    : make_float4(fill, fill, fill, fill);
       v[k] = make_float2(f.x, f.y);
       v[k + 1] = make_float2(f.z, f.w);
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < C / 2; ++k) {
       const int c = 64 * k + lane;
       v[k] = make_float2(c < n ? __ldg(p + c0 + c) : fill, c + 32 < n ? __ldg(p + c0 + c + 32) : fill);
     }
@@ -191,55 +191,64 @@ __global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 38
   }
 }
 
-// What the backward pass needs of a lane's 16 columns of a row, as loaded.
-template <typename E, bool SAVED>
+// What the backward pass needs of a lane's C columns of a row, as loaded.
+template <typename E, bool SAVED, int C>
 struct RowPiece {
-  Raw<E> dy;
-  Raw<E> x;
+  Raw<E, C> dy;
+  Raw<E, C> x;
 };
-template <typename E>
-struct RowPiece<E, true> {
-  Raw<E> dy;
-  RawCodes x;
+template <typename E, int C>
+struct RowPiece<E, true, C> {
+  Raw<E, C> dy;
+  RawCodes<C> x;
 };
 
-constexpr int kColWords = 16 * 33;   // a warp's 512 column sums in shared memory
+template <int C>
+constexpr int kColWords = C * 33;   // a warp's column sums in shared memory
 
-// a lane's 16 column sums of a piece to out (n columns are left)
-template <bool VEC>
+// a lane's C column sums of a piece to out (n columns are left)
+template <bool VEC, int C>
 __device__ __forceinline__ void write_cols(float *out, int n, int lane, const float2 *v) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int c = piece_col<VEC>(lane, e);
+  for (int e = 0; e < C; ++e) {
+    const int c = piece_col<VEC, C>(lane, e);
     if (c < n) out[c] = e & 1 ? v[e / 2].y : v[e / 2].x;
   }
 }
 
-// U = 1: dx and the column sums.  U > 1 (rows over 8192 columns): dx alone, the column sums take
-// a pass of their own (k_norm_cols), since their 32 registers a piece do not fit beside the row's.
-template <typename E, bool VEC, bool SAVED, int U, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 256 && U == 1 ? 2 : 1) k_norm_backward(const __grid_constant__ NormBackward a, int nw, int fmt,
-                                                       int *status) {
+// U = 1 (up to 8192 columns): dx and the column sums.  The two sums, the gain and two rows take eight
+// registers a column, so 16 warps per SM with C = 16 columns per lane, 24 with C = 8.  With 32-byte
+// accesses C = 16 is faster (32768 x 4096 BF16: 160-173 us against 203; 16384 x 1536 from the
+// checkpoint 38 against 41), with element accesses C = 8 (5003 x 1361 FP32 from the checkpoint: 29 us
+// against 37; 30324 x 20: 16 against 22).
+// U > 1 (longer rows): dx alone, the column sums take a pass of their own (k_norm_cols).
+template <typename E, bool VEC, bool SAVED, int U, int C, int MAXT>
+__global__ void __launch_bounds__(MAXT, U > 1 || MAXT == 512 ? 1 : C == 16 ? 2 : 3)
+    k_norm_backward(const __grid_constant__ NormBackward a, int nw, int fmt, int *status) {
   extern __shared__ float acc_sh[];
   __shared__ float2 red[16][2][16];
   grid_release();
+  constexpr int kWide = 32 * C;   // columns of a piece
   const int lane = threadIdx.x & 31, T = a.T, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
   RowGroup G(nw, red);
   const int per_cta = (int)(blockDim.x >> 5) / nw, step = gridDim.x * per_cta;
+  const int first = G.w * U * kWide;
   const float inv_d = __frcp_rn((float)d);
-  float2 g[8], dg[8], db[8];   // U = 1: held for the CTA's rows
-  if (U == 1) load_cols<VEC>(a.gamma, G.w * kPiece, d - G.w * kPiece, lane, 1.0f, g);
+  float2 g[C / 2], dg[C / 2], db[C / 2];   // U = 1: held for the CTA's rows
+  if (U == 1) load_cols<VEC, C>(a.gamma, first, d - first, lane, 1.0f, g);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) dg[k] = db[k] = both(0.0f);
-  RowPiece<E, SAVED> now[U], next[1];
-  auto load = [&](int t, RowPiece<E, SAVED> *p) {
+  for (int k = 0; k < C / 2; ++k) dg[k] = db[k] = both(0.0f);
+  RowPiece<E, SAVED, C> now[U], next[1];
+  auto load = [&](int t, RowPiece<E, SAVED, C> *p) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c0 = (G.w * U + u) * kPiece, n = t < T ? d - c0 : 0;
+      const int c0 = first + u * kWide, n = t < T ? d - c0 : 0;
       const size_t at = (size_t)t * d + c0;
       load_piece<VEC>(static_cast<const E *>(a.dy) + at, n, lane, p[u].dy);
-      if constexpr (SAVED) load_codes<VEC>(a.codes + at, a.scales + (size_t)t * groups + c0 / kActGroup, n, lane, p[u].x);
-      else load_piece<VEC>(static_cast<const E *>(a.x) + at, n, lane, p[u].x);
+      if constexpr (SAVED)
+        load_codes<VEC>(a.codes + at, a.scales + (size_t)t * groups + c0 / kActGroup, n, lane, p[u].x);
+      else
+        load_piece<VEC>(static_cast<const E *>(a.x) + at, n, lane, p[u].x);
     }
   };
   int t = blockIdx.x * per_cta + G.id;
@@ -253,16 +262,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && U == 1 ? 2 : 1) k_norm_ba
       load(t, now);
     }
     auto n_of = [&](int u, int k) -> float2 {
-      if constexpr (SAVED) return fmt == FMT_E4M3 ? code_pair<FMT_E4M3, VEC>(now[u].x, k) : code_pair<FMT_E5M2, VEC>(now[u].x, k);
-      else return mul2(add2(now[u].x.pair(k), both(-mean)), both(rstd));
+      if constexpr (SAVED)
+        return fmt == FMT_E4M3 ? code_pair<FMT_E4M3, VEC>(now[u].x, k) : code_pair<FMT_E5M2, VEC>(now[u].x, k);
+      else
+        return mul2(add2(now[u].x.pair(k), both(-mean)), both(rstd));
     };
     float2 sh = both(0.0f), shn = both(0.0f);
-    float2 keep[8];   // U = 1: n
+    float2 keep[C / 2];   // U = 1: n
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (U > 1) load_cols<VEC>(a.gamma, (G.w * U + u) * kPiece, d - (G.w * U + u) * kPiece, lane, 1.0f, g);
+      if (U > 1) load_cols<VEC, C>(a.gamma, first + u * kWide, d - first - u * kWide, lane, 1.0f, g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < C / 2; ++k) {
         const float2 dy = now[u].dy.pair(k), h = mul2(dy, g[k]), n = n_of(u, k);
         if (U == 1) {
           keep[k] = n;
@@ -279,39 +290,39 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 && U == 1 ? 2 : 1) k_norm_ba
     const float2 ma = both(-s.x * inv_d), mb = both(-s.y * inv_d);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c0 = (G.w * U + u) * kPiece;
-      if (U > 1) load_cols<VEC>(a.gamma, c0, d - c0, lane, 1.0f, g);
-      float2 dx[8];
+      const int c0 = first + u * kWide;
+      if (U > 1) load_cols<VEC, C>(a.gamma, c0, d - c0, lane, 1.0f, g);
+      float2 dx[C / 2];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < C / 2; ++k)
         dx[k] = mul2(both(rstd), fma2(U == 1 ? keep[k] : n_of(u, k), mb, fma2(now[u].dy.pair(k), g[k], ma)));
-      store_piece<VEC>(static_cast<E *>(a.dx) + (size_t)t * d + c0, d - c0, lane, dx);
+      store_piece<VEC, C>(static_cast<E *>(a.dx) + (size_t)t * d + c0, d - c0, lane, dx);
     }
   }
   if (U > 1 || !a.part) return;
-  // The CTA's partial.  Several row groups: every warp leaves its sums in shared memory (a lane's 16
-  // columns 33 words apart, so that neither the writes by lane nor the reads by column conflict), then
-  // each thread adds the groups' values of its columns in order.
+  // The CTA's partial.  Several row groups: every warp leaves its sums in shared memory (a lane's columns
+  // 33 words apart, so that neither the writes by lane nor the reads by column conflict), then each
+  // thread adds the groups' values of its columns in order.
   float *out = a.part + (size_t)2 * blockIdx.x * d;
-  const int first = G.w * kPiece;
   if (per_cta == 1) {
-    write_cols<VEC>(out + first, d - first, lane, dg);
-    write_cols<VEC>(out + d + first, d - first, lane, db);
+    write_cols<VEC, C>(out + first, d - first, lane, dg);
+    write_cols<VEC, C>(out + d + first, d - first, lane, db);
     return;
   }
-  float *mine = acc_sh + 2 * kColWords * (G.id * nw + G.w);
+  constexpr int kWords = kColWords<C>;
+  float *mine = acc_sh + 2 * kWords * (G.id * nw + G.w);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
+  for (int e = 0; e < C; ++e) {
     mine[33 * e + lane] = e & 1 ? dg[e / 2].y : dg[e / 2].x;
-    mine[kColWords + 33 * e + lane] = e & 1 ? db[e / 2].y : db[e / 2].x;
+    mine[kWords + 33 * e + lane] = e & 1 ? db[e / 2].y : db[e / 2].x;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * d; i += blockDim.x) {
-    const int c = i < d ? i : i - d, in = c % kPiece;
-    const int e = VEC ? in % 16 : in / 32, l = VEC ? in / 16 : in % 32;
-    const float *p = acc_sh + 2 * kColWords * (c / kPiece) + (i < d ? 0 : kColWords) + 33 * e + l;
+    const int c = i < d ? i : i - d, in = c % kWide;
+    const int e = VEC ? in % C : in / 32, l = VEC ? in / C : in % 32;
+    const float *p = acc_sh + 2 * kWords * (c / kWide) + (i < d ? 0 : kWords) + 33 * e + l;
     float v = p[0];
-    for (int k = 1; k < per_cta; ++k) v += p[2 * kColWords * nw * k];
+    for (int k = 1; k < per_cta; ++k) v += p[2 * kWords * nw * k];
     out[i] = v;
   }
 }
@@ -331,7 +342,7 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_cols(const __grid_constan
 #pragma unroll 2
   for (int t = blockIdx.y * rows; t < t1; ++t) {
     const size_t at = (size_t)t * d + c0;
-    RowPiece<E, SAVED> p;
+    RowPiece<E, SAVED, 16> p;
     load_piece<VEC>(static_cast<const E *>(a.dy) + at, n, lane, p.dy);
     float rstd = 1.0f, mean = 0.0f;
     if constexpr (SAVED) {
@@ -520,7 +531,11 @@ cudaError_t launch_after(cudaStream_t s, void (*kernel)(P...), dim3 grid, int th
 // Rows by registers: pieces per lane and warps per row.
 struct RowPlan {
   int u, nw, threads;
+  int c = 16;   // columns per lane
 };
+
+// CTAs of whole row groups, about eight warps
+int group_threads(int nw) { return 32 * nw * (nw >= 8 ? 1 : 8 / nw); }
 
 // As many warps per row as pieces up to 8192 columns, then two or four pieces per lane; CTAs of 8 to
 // 16 warps.
@@ -529,7 +544,23 @@ bool row_plan(int d, RowPlan *p) {
   if (pieces > 64) return false;
   p->u = pieces <= 16 ? 1 : pieces <= 32 ? 2 : 4;
   p->nw = (pieces + p->u - 1) / p->u;
-  p->threads = 32 * p->nw * (p->nw >= 8 ? 1 : 8 / p->nw);
+  p->threads = group_threads(p->nw);
+  return true;
+}
+
+// Backward: element accesses up to 4096 columns by 256 columns and warp, else as the forward pass; where
+// the warps of a row do not divide eight, all the row groups that 16 warps hold in one CTA (three
+// warps per row: 15 warps per SM instead of 12).
+bool backward_plan(int d, bool vec, RowPlan *p) {
+  if (!vec && d <= 16 * 256) {
+    p->u = 1;
+    p->c = 8;
+    p->nw = (d + 255) / 256;
+    p->threads = group_threads(p->nw);
+    return true;
+  }
+  if (!row_plan(d, p)) return false;
+  if (p->u == 1 && p->nw < 8 && 8 % p->nw) p->threads = 32 * p->nw * (16 / p->nw);
   return true;
 }
 
@@ -583,29 +614,34 @@ cudaError_t column_pass(const Launch &L, int fmt, const NormBackward &a) {
   return e != cudaSuccess ? e : sums_after(L, a, slices);
 }
 
-template <typename E, bool VEC, bool SAVED, int U, int MAXT>
+template <typename E, bool VEC, bool SAVED, int U, int C, int MAXT>
 cudaError_t backward_t(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
-  constexpr auto kernel = k_norm_backward<E, VEC, SAVED, U, MAXT>;
-  const int per_cta = p.threads / 32 / p.nw, smem = U == 1 && per_cta > 1 ? per_cta * p.nw * 2 * kColWords * 4 : 0;
+  constexpr auto kernel = k_norm_backward<E, VEC, SAVED, U, C, MAXT>;
+  const int warps = p.threads / 32, per_cta = warps / p.nw, smem = U == 1 && per_cta > 1 ? warps * 2 * kColWords<C> * 4 : 0;
+  cudaError_t e = smem ? ensure_dynamic_smem<kernel>(smem) : cudaSuccess;
+  if (e != cudaSuccess) return e;
   int grid = resident<kernel>(L, p.threads, smem, a.T, per_cta);
   if (grid > norm_partials(L.sms, a.T)) grid = norm_partials(L.sms, a.T);
   kernel<<<grid, p.threads, smem, L.stream>>>(a, p.nw, fmt, L.status);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (U > 1) return column_pass<E, VEC, SAVED>(L, fmt, a);
   return a.part ? sums_after(L, a, grid) : cudaSuccess;
 }
 
 template <typename E, bool VEC, bool SAVED, int U>
 cudaError_t backward(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
-  return p.threads <= 256 ? backward_t<E, VEC, SAVED, U, 256>(L, fmt, a, p)
-                          : backward_t<E, VEC, SAVED, U, 512>(L, fmt, a, p);
+  constexpr int kC8 = U == 1 && !VEC ? 8 : 16;
+  if (p.c == 8)
+    return p.threads <= 256 ? backward_t<E, VEC, SAVED, U, kC8, 256>(L, fmt, a, p)
+                            : backward_t<E, VEC, SAVED, U, kC8, 512>(L, fmt, a, p);
+  return p.threads <= 256 ? backward_t<E, VEC, SAVED, U, 16, 256>(L, fmt, a, p)
+                          : backward_t<E, VEC, SAVED, U, 16, 512>(L, fmt, a, p);
 }
 
 template <typename E, bool VEC, bool SAVED>
 cudaError_t backward_s(const Launch &L, int fmt, const NormBackward &a) {
   RowPlan p;
-  if (row_plan(a.d, &p)) {
+  if (backward_plan(a.d, VEC, &p)) {
     switch (p.u) {
       case 1: return backward<E, VEC, SAVED, 1>(L, fmt, a, p);
       case 2: return backward<E, VEC, SAVED, 2>(L, fmt, a, p);

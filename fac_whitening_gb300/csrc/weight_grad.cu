@@ -801,49 +801,55 @@ __device__ __forceinline__ void column_sums(const Prepare &P, int cta) {
   }
 }
 
-// FP32 as three BF16 terms (exact), planes of T rows of ld columns
+// FP32 as three BF16 terms (exact), planes of T rows of ld columns; a warp per row, two columns per lane
 __device__ __forceinline__ void bf16_terms(const float *x, int T, int d, int ld, uint16_t *out, int cta, int ctas) {
   const size_t plane = (size_t)T * ld;
-  const int pairs = (d + 1) / 2;   // two columns at a time; ld is even
-  const size_t n = (size_t)T * pairs, step = (size_t)ctas * 256;
-  for (size_t e = (size_t)cta * 256 + threadIdx.x; e < n; e += step) {
-    const size_t t = e / pairs;
-    const int c = (int)(e - t * pairs) * 2;
-    const float *p = x + t * d + c;
-    uint32_t w[3];
-    tc::bf16_split3x2(p[0], c + 1 < d ? p[1] : 0.0f, w[0], w[1], w[2]);
+  for (int t = cta * 8 + (threadIdx.x >> 5); t < T; t += ctas * 8) {
+    const float *p = x + (size_t)t * d;
+    uint16_t *o = out + (size_t)t * ld;
+    for (int c = 2 * (threadIdx.x & 31); c < d; c += 64) {   // ld is even
+      uint32_t w[3];
+      tc::bf16_split3x2(p[c], c + 1 < d ? p[c + 1] : 0.0f, w[0], w[1], w[2]);
 #pragma unroll
-    for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(out + k * plane + t * ld + c) = w[k];
+      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(o + k * plane + c) = w[k];
+    }
   }
 }
 
-// Rows of `bytes` bytes at any alignment -> rows of ld (a multiple of 16) bytes, 16 at a time
+// Rows of `bytes` bytes at any alignment -> rows of ld (a multiple of 16) bytes; a warp per row, 16 bytes
+// per lane from the two aligned blocks that hold them.  Past a row's end nothing is read again (the
+// tensor map's width).
+__device__ __forceinline__ uint4 aligned_block(uintptr_t p, uintptr_t lo, uintptr_t hi) {
+  if (p >= lo && p + 16 <= hi) return *reinterpret_cast<const uint4 *>(p);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};   // the ends of the matrix
+#pragma unroll
+  for (int b = 0; b < 16; ++b)
+    if (p + b >= lo && p + b < hi) w[b / 4] |= (uint32_t)*reinterpret_cast<const uint8_t *>(p + b) << (8 * (b % 4));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
 __device__ __forceinline__ void repitch(const uint8_t *src, int T, size_t bytes, size_t ld, uint8_t *dst, int cta,
                                         int ctas) {
-  const size_t per = (bytes + 15) / 16, n = (size_t)T * per, step = (size_t)ctas * 256;
   const uintptr_t lo = (uintptr_t)src, hi = lo + (size_t)T * bytes;
-  for (size_t e = (size_t)cta * 256 + threadIdx.x; e < n; e += step) {
-    const size_t t = e / per, c = (e - t * per) * 16;
-    const uintptr_t a = lo + t * bytes + c, w0 = a & ~(uintptr_t)3;
-    const int sh = (int)(a & 3) * 8;
-    uint32_t w[5];
+  for (int t = cta * 8 + (threadIdx.x >> 5); t < T; t += ctas * 8) {
+    const uintptr_t row = lo + (size_t)t * bytes;
+    const int off = (int)(row & 15), sh = 8 * (off & 3);
+#pragma unroll 2
+    for (size_t c = 16 * (threadIdx.x & 31); c < bytes; c += 512) {
+      const uintptr_t at = row + c - off;
+      const uint4 a = aligned_block(at, lo, hi), b = off ? aligned_block(at + 16, lo, hi) : a;
+      uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+      if (off & 8) {   // the same for the whole row
 #pragma unroll
-    for (int k = 0; k < 5; ++k) {
-      const uintptr_t p = w0 + 4 * k;
-      w[k] = 0;
-      if (p >= lo && p + 4 <= hi) {
-        w[k] = *reinterpret_cast<const uint32_t *>(p);
-      } else {
-        for (int b = 0; b < 4; ++b)
-          if (p + b >= lo && p + b < hi) w[k] |= (uint32_t)*reinterpret_cast<const uint8_t *>(p + b) << (8 * b);
+        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
       }
+      if (off & 4) {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+      }
+      *reinterpret_cast<uint4 *>(dst + t * ld + c) =
+          make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                     __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
     }
-    uint4 v;
-    v.x = __funnelshift_r(w[0], w[1], sh);
-    v.y = __funnelshift_r(w[1], w[2], sh);
-    v.z = __funnelshift_r(w[2], w[3], sh);
-    v.w = __funnelshift_r(w[3], w[4], sh);
-    *reinterpret_cast<uint4 *>(dst + t * ld + c) = v;   // past the row's end: never read (the tensor map's width)
   }
 }
 
@@ -968,6 +974,12 @@ cudaError_t launch_fmt(const Launch &L, const Params &P, const CUtensorMap &tc_,
   return p.nh == 1 ? launch<F, 1, 3>(L, P, tc_, td, p.pairs) : launch<F, 2, 3>(L, P, tc_, td, p.pairs);
 }
 
+// CTAs of eight warps, a row each, up to eight per SM
+int row_grid(const Launch &L, int T) {
+  const int c = (T + 7) / 8;
+  return c < L.sms * 8 ? c : L.sms * 8;
+}
+
 int stream_grid(const Launch &L, size_t n) {
   const size_t c = (n + 255) / 256, most = (size_t)L.sms * 8;
   return (int)(c < most ? c : most);
@@ -1040,14 +1052,14 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   if (!bf16 || dpitch % 16 || !aligned16(delta)) {
     dpitch = pad16(dpitch);
     q.delta_ld = (int)(dpitch / 2);
-    q.ndelta = stream_grid(L, bf16 ? (size_t)a.T * dpitch / 16 : (size_t)a.T * q.delta_ld / 2);
+    q.ndelta = row_grid(L, a.T);
     delta = a.delta_ws;
   }
   const uint8_t *codes = a.codes;
   size_t cpitch = a.d_in;
   if (cpitch % 16 || !aligned16(codes)) {
     cpitch = q.codes_ld = pad16(cpitch);
-    q.ncodes = stream_grid(L, (size_t)a.T * cpitch / 16);
+    q.ncodes = row_grid(L, a.T);
     codes = a.code_ws;
   }
   const int pgrid = q.nscale + q.nsums + q.ndelta + q.ncodes;
