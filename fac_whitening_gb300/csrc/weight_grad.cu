@@ -745,8 +745,7 @@ struct Prepare {
 // Scale bytes -> StageScales (NaN for a marked group, 1 past T): a stage of 64 tokens x 64 groups per CTA
 // through shared memory, a warp writes a group.
 template <int F>
-__device__ __forceinline__ void stage_scales(const Prepare &P, int cta) {
-  __shared__ uint8_t tile[kK][65];
+__device__ __forceinline__ void stage_scales(const Prepare &P, int cta, uint8_t (*tile)[65]) {
   constexpr int up = F == FMT_E4M3 ? 120 : 112;
   const int stage = cta % P.stages, g0 = cta / P.stages * 64, ng = min(64, P.groups - g0), t0 = stage * kK;
   const int lane = threadIdx.x & 31;
@@ -774,8 +773,7 @@ __device__ __forceinline__ void stage_scales(const Prepare &P, int cta) {
 // Sums over a slice of tokens of one piece of 512 columns: a warp takes every eighth token, the eight
 // warps' sums are joined in order.
 template <typename E, bool VEC>
-__device__ __forceinline__ void column_sums(const Prepare &P, int cta) {
-  __shared__ float sh[8][16 * 33];   // a lane's 16 columns 33 words apart: neither side conflicts
+__device__ __forceinline__ void column_sums(const Prepare &P, int cta, float (*sh)[16 * 33]) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int c0 = cta / P.sum_slices * kPiece, slice = cta % P.sum_slices, n = P.d_out - c0;
   const int t1 = min(P.T, (slice + 1) * P.sum_rows);
@@ -833,7 +831,7 @@ __device__ __forceinline__ void repitch(const uint8_t *src, int T, size_t bytes,
   for (int t = cta * 8 + (threadIdx.x >> 5); t < T; t += ctas * 8) {
     const uintptr_t row = lo + (size_t)t * bytes;
     const int off = (int)(row & 15), sh = 8 * (off & 3);
-#pragma unroll 2
+#pragma unroll 4
     for (size_t c = 16 * (threadIdx.x & 31); c < bytes; c += 512) {
       const uintptr_t at = row + c - off;
       const uint4 a = aligned_block(at, lo, hi), b = off ? aligned_block(at + 16, lo, hi) : a;
@@ -855,17 +853,21 @@ __device__ __forceinline__ void repitch(const uint8_t *src, int T, size_t bytes,
 
 template <int F, bool BF16>
 __global__ void __launch_bounds__(256) k_prepare(const __grid_constant__ Prepare P) {
+  __shared__ union {
+    uint8_t tile[kK][65];
+    float sums[8][16 * 33];   // a lane's 16 columns 33 words apart: neither side conflicts
+  } sh;
   grid_release();
   int cta = blockIdx.x;
   if (cta < P.nscale) {
-    stage_scales<F>(P, cta);
+    stage_scales<F>(P, cta, sh.tile);
     return;
   }
   cta -= P.nscale;
   if (cta < P.nsums) {
     using E = typename std::conditional<BF16, __nv_bfloat16, float>::type;
-    if (P.sum_vec) column_sums<E, true>(P, cta);
-    else column_sums<E, false>(P, cta);
+    if (P.sum_vec) column_sums<E, true>(P, cta, sh.sums);
+    else column_sums<E, false>(P, cta, sh.sums);
     return;
   }
   cta -= P.nsums;
