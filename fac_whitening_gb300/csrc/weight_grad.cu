@@ -12,14 +12,22 @@
 //                the CTA's; transposed and made BF16 by a kernel before); its 64 x 64 delta boxes;
 //   warps 4-19   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
 //                tokens of one column, which is tcgen05.st's 16x256b layout; the code's bits placed
-//                in the BF16 fields times 2^120 (2^112 for E5M2) and times 2^k, both exact;
+//                in the BF16 fields times 2^(120 + k) (2^(112 + k) for E5M2), exact;
 //   warps 1, 3   the pair's first CTA issues 256 x 128 x 16 MMAs, a warp for each half of the tile;
 //   warps 20-27  fold: the tensor core truncates its sums, so a segment of at most 256 tokens goes
 //                into one of three 128-column accumulators and is added to FP32 registers to
 //                nearest; the two halves of a tile change accumulators half a segment apart, so
 //                that one is always being drained while two are being filled.
-// What bounds it: the MMA rate; the operand bytes a pair needs from L2 are 48 per clock and SM.
 // Few tiles: the tokens are cut into slices whose sums a second kernel adds in order.
+//
+// What bounds it.  The MMAs take 512 clocks a stage (measured back to back, N = 128 halves as well as
+// N = 256).  One CTA alone would need 80 bytes of operands per clock from L2, a pair needs 48 per SM.
+// The conversion costs the SM's integer pipes about 250 clocks a stage, and every warp's waits and
+// issues around it are latency: the numbers of warps, the two rings and the two MMA warps come from
+// there.  16384 x 1536 x 6144 (tokens x d_out x d_in): 180 us for this kernel, 1.72 PFLOP/s; 65536
+// tokens 707 us, 1.75 PFLOP/s; 32768 x 4096 x 16384 run over and over (power cap) 3.0 ms, 1.46
+// PFLOP/s.  Converting in a pass of its own would move 300 MB more for the first of these, 45 us at the
+// copy rate.
 // Every mbarrier wait is clock-bounded and reports GIFT_ERR_TIMEOUT.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -48,8 +56,8 @@ constexpr long long kWait = 4000000000LL;
 
 // Two rings in shared memory.  A code box is free as soon as it is converted; delta's boxes are held
 // until their MMAs are done, up to four stages later.  So delta gets the deeper part of the 224 KB:
-// with one ring of eight stages for both, four were left for loads in flight, which the L2's
-// latency under load outlasted (65536 tokens: 818 us; with both rings as below ...).
+// with one ring of eight stages for both, four were left for loads in flight (65536 x 1536 x 6144: 818
+// us with one ring, 790 with two and a TMA warp for each; one TMA warp for both took 1030).
 template <int NH, int TERMS>
 struct Cfg {
   static constexpr int delta_bytes = kBox * NH * TERMS;       // of a stage
@@ -580,11 +588,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // 32 x 32 tiles of dW, a cluster of eight CTAs each: a CTA takes every eighth 64 tokens through shared
 // memory, eight of them per warp, each lane 4 x 8 outputs in packed FP32.  A warp's sums are folded
 // every 64 tokens of the batch, the eight warps' joined in order, then the eight CTAs' through
-// distributed shared memory; db alongside.  Bound by latency.
-#ifndef SMALL_TOKENS
-#define SMALL_TOKENS 2048
-#endif
-constexpr long long kSmallTokens = SMALL_TOKENS;
+// distributed shared memory; db alongside.  Bound by latency: 512 x 64 x 256 takes about 6 us.
+constexpr int kSmallTokens = 2048;   // see small_product
 constexpr int kSmTok = 64, kSmTile = 32, kSmThreads = 256, kSmCtas = 8;
 
 template <int F, typename E>
@@ -706,7 +711,7 @@ __global__ void __cluster_dims__(kSmCtas, 1, 1) __launch_bounds__(kSmThreads, 1)
   cluster_sync();   // no CTA leaves while another reads its sums
 }
 
-// dW = gamma * (the slices' sums in order) + beta db
+// dW = gamma * (the slices' sums in order) + beta db; streams the slices from L2
 __global__ void __launch_bounds__(256) k_join_slices(const float *__restrict__ part, int slices, int d_out, int d_in,
                                                      const float *__restrict__ gamma, const float *__restrict__ beta,
                                                      const float *__restrict__ db, float *__restrict__ dW) {
@@ -1003,7 +1008,8 @@ WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) 
 }
 
 // Where the tensor-core kernel's fixed cost (its first loads, and the kernels before it) outweighs the
-// small kernel's: its clusters all run at once, over a few chunks each.
+// small kernel's, whose clusters all run at once over a few chunks each.  A call with db: 512 x 64 x 256
+// FP32 10.4 us here, 17.8 there; 2048 x 64 x 256 BF16 16.6 and 20.7; 4096 x 64 x 256 24.8 and 20.5.
 bool small_product(int sms, int T, int d_out, int d_in) {
   const long long tiles = (long long)((d_out + kSmTile - 1) / kSmTile) * ((d_in + kSmTile - 1) / kSmTile);
   return tiles * kSmCtas <= 2 * sms && T <= kSmallTokens;

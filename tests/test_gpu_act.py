@@ -459,6 +459,23 @@ def test_weight_grad_extreme_scales(dt):
     assert np.array_equal(host(dW), want)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_weight_grad_extreme_scales_of_a_wide_layer(dt, fmt):
+    # the same through the tensor-core kernel, with single tokens at the ends of the range among others
+    T, d_out, d_in = 300, 264, 528
+    rng = np.random.default_rng(9)
+    v = rng.choice([-1.0, 1.0, 0.5, 3.0], (T, d_in))
+    delta = rng.integers(-3, 4, (T, d_out)).astype(np.float64)
+    k = np.zeros(T, dtype=int)
+    k[[3, 64, 200, 299]] = [100, -90, 60, -100]
+    v, delta = np.ldexp(v, k[:, None]), np.ldexp(delta, -k[:, None])
+    codes, scales = R.encode(v, fmt)
+    want, _ = R.weight_grad(delta, R.decode(codes, scales, fmt))
+    dW, _ = weight_grad(dev(delta, DT[dt]), dev(codes, torch.uint8), dev(scales, torch.uint8), fmt, d_in)
+    assert np.array_equal(host(dW), want)
+
+
 # ---- what every call holds to -----------------------------------------------------------------
 def test_calls_repeat_bit_for_bit_and_keep_to_their_stream():
     T, d, d_out = 700, 520, 136
