@@ -303,4 +303,22 @@ inline bool rows_vec(int d, const void *x, const void *codes) {
   return d % 16 == 0 && ((uintptr_t)x & 31u) == 0 && ((uintptr_t)codes & 15u) == 0;
 }
 
+// wait for the programmatic predecessor's results / let the successor launch
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// launch with the programmatic dependency that grid_wait() ends
+template <typename... P, typename... Q>
+inline cudaError_t launch_after(cudaStream_t s, void (*kernel)(P...), dim3 grid, int threads, Q... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 }  // namespace gift

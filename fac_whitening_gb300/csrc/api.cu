@@ -1312,7 +1312,7 @@ bool valid_extent(int n) { return n >= 1 && n <= kMaxExtent; }
 // The workspace of one call, carved from the first 256-byte boundary (the size has room for it).
 struct ActWs {
   float *part = nullptr;    // slice partials of the sums over tokens
-  float *db = nullptr;      // weight gradient: db when only the call itself needs it
+  float *db = nullptr;      // weight gradient: db, by token slice
   float *slices = nullptr;  // sums of token slices
   uint8_t *delta = nullptr, *codes = nullptr;   // operands with aligned rows
   uint8_t *scales = nullptr;                    // scales by group
@@ -1327,7 +1327,7 @@ ActWs act_layout(void *base, const gift_ctx *ctx, gift_op op, gift_dtype dt, int
   } else {
     const WeightGradWs g = weight_grad_layout(ctx->sms, dt == GIFT_DT_BF16, T, d_out, d_in);
     w.part = c.take<float>(g.part_floats);
-    w.db = c.take<float>(d_out);
+    w.db = c.take<float>(g.db_floats);
     w.slices = c.take<float>(g.slice_floats);
     w.delta = c.take<uint8_t>(g.delta_bytes);
     w.codes = c.take<uint8_t>(g.code_bytes);

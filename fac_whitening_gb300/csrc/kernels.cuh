@@ -355,9 +355,11 @@ cudaError_t launch_norm_forward(const Launch &L, int fmt, bool bf16, const NormF
 cudaError_t launch_norm_backward(const Launch &L, int fmt, bool bf16, const NormBackward &a);
 // out[c] = sum_k part[k d + c], in order
 cudaError_t launch_sum_parts(const Launch &L, const float *part, int parts, int d, float *out);
+
 // ---- weight_grad.cu -------------------------------------------------------------------------
 struct WeightGradWs {
   size_t part_floats = 0;      // column-sum partials of db
+  size_t db_floats = 0;        // db, by slice
   size_t slice_floats = 0;     // sums of the token slices
   size_t delta_bytes = 0;      // delta's BF16 terms, or its copy with aligned rows
   size_t code_bytes = 0;       // the codes' copy with aligned rows
@@ -369,7 +371,7 @@ struct WeightGrad {
   int T, d_out, d_in;
   const float *gamma, *beta;   // nullable
   float *dW, *db;              // db nullable
-  float *part, *db_ws;         // workspace: column-sum partials, db when the caller wants none
+  float *part, *db_ws;         // workspace, as in WeightGradWs
   float *slices;
   void *delta_ws;
   uint8_t *code_ws;

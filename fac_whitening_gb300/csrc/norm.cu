@@ -42,10 +42,6 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
   return upper ? make_float2(other, s) : make_float2(s, other);
 }
 
-// wait for the programmatic predecessor's results / let the successor launch
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Row groups of `nw` warps within a CTA, and their sums: every warp of the group gets the total.  Two
 // buffers in turn, so that one barrier per sum is enough.
 struct RowGroup {
@@ -519,21 +515,6 @@ int resident(const Launch &L, int threads, int smem, int T, int per_cta) {
   return (int)(need < most ? need : most);
 }
 
-// launch with the programmatic dependency that grid_wait() ends
-template <typename... P, typename... Q>
-cudaError_t launch_after(cudaStream_t s, void (*kernel)(P...), dim3 grid, int threads, Q... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-}
-
 // Rows by registers: pieces per lane and warps per row.
 struct RowPlan {
   int u, nw, threads;
@@ -683,17 +664,17 @@ size_t norm_part_floats(int sms, int T, int d) {
   return (size_t)2 * ((T + rows - 1) / rows) * d;
 }
 
-cudaError_t launch_sum_parts(const Launch &L, const float *part, int parts, int d, float *out) {
-  return launch_after(L.stream, k_norm_sums, dim3((d + 31) / 32, 1), 1024, part, parts, (size_t)d, (size_t)0, d, out,
-                      static_cast<float *>(nullptr));
-}
-
 cudaError_t launch_norm_forward(const Launch &L, int fmt, bool bf16, const NormForward &a) {
   return bf16 ? forward_e<__nv_bfloat16>(L, fmt, a) : forward_e<float>(L, fmt, a);
 }
 
 cudaError_t launch_norm_backward(const Launch &L, int fmt, bool bf16, const NormBackward &a) {
   return bf16 ? backward_e<__nv_bfloat16>(L, fmt, a) : backward_e<float>(L, fmt, a);
+}
+
+cudaError_t launch_sum_parts(const Launch &L, const float *part, int parts, int d, float *out) {
+  return launch_after(L.stream, k_norm_sums, dim3((d + 31) / 32, 1), 1024, part, parts, (size_t)d, (size_t)0, d, out,
+                      static_cast<float *>(nullptr));
 }
 
 }  // namespace gift

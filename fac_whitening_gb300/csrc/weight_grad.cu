@@ -78,13 +78,16 @@ struct StageScales {
 constexpr int kScaleBytes = sizeof(StageScales);
 
 struct Params {
-  int T, d_out, d_in, groups;
+  int T, d_out, d_in, last_group;
   int ng;                      // groups of stages (256 tokens) over all tokens; tokens past T are zeros
   int mt, nt, slices, items;
-  const StageScales *scales;   // groups rows of `stages`
+  const StageScales *scales;   // last_group + 1 rows of `stages`
   int stages;
-  const float *gamma, *beta, *db;   // nullable; only with one slice
+  const float *gamma;          // nullable
   float *out;                  // dW, or the slices' sums (slice s at s d_out d_in)
+  int ones;                    // the row whose values are 1 (-1: none)
+  const uint8_t *one_codes;    // a box of the code of 1
+  float *db;                   // where that row's sums go
 };
 
 // One work item: an output tile and a range of groups.
@@ -158,8 +161,6 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 // wait for the programmatic predecessor's results / let the successor launch
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // a float of CTA r's copy of a shared variable
 __device__ __forceinline__ float ld_cluster(const float *p, int r) {
   float v;
@@ -289,6 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  grid_release();   // k_join_slices
 
   if (warp == 0) alloc_pair(&tmem_sh);
   if (tid == 32) {
@@ -342,16 +344,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (warp == kCodesWarp) {
         for (int it = pair; it < P.items && ok; it += pairs) {
           const Item w(P, it, 128 * NH);
-          // the CTA's columns are one group; past d_in there are only zero codes, of any scale
+          // the CTA's columns are one group; past d_in the codes are ones for db, otherwise zeros
           const int i = w.i0 + 128 * rank;
-          const StageScales *scales = P.scales + (size_t)min(i / kActGroup, P.groups - 1) * P.stages + w.t0 / kK;
+          const bool ones = P.ones >= 0 && i >= P.ones;
+          const StageScales *scales = P.scales + (size_t)min(i / kActGroup, P.last_group) * P.stages + w.t0 / kK;
           for (int t = w.t0; t < w.t0 + kGroup * kK * w.ng; t += kK, ++g, ++scales) {
             const Slot<kCodes> c(g);
             if (!(ok = wait(&cempty[c.at], c.parity ^ 1u))) break;
             __syncwarp();
             if (one) {
               tc::mbar_arrive_expect_tx(&cfull[c.at], kBox + kScaleBytes);
-              tc::tma_load_2d(sm + c.at * kBox, &tm_codes, i, t, &cfull[c.at]);
+              if (ones) bulk_load(sm + c.at * kBox, P.one_codes, kBox, &cfull[c.at]);
+              else tc::tma_load_2d(sm + c.at * kBox, &tm_codes, i, t, &cfull[c.at]);
               bulk_load(&scale_sh[c.at], scales, kScaleBytes, &cfull[c.at]);
             }
           }
@@ -554,23 +558,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (NH == 2) fold(1, sum[NH - 1]);
       if (!ok) break;
       const int i = w.i0 + 128 * rank + 32 * q + lane;
-      grid_wait();   // db, where a kernel before this one made it
-      if (i < P.d_in) {
-        const float ga = P.gamma ? P.gamma[i] : 1.0f, be = P.beta ? P.beta[i] : 0.0f;
-        float *out = P.out + (size_t)w.slice * P.d_out * P.d_in + i;
+      auto store = [&](float *p, size_t step, float ga) {
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const int o = w.o0 + 128 * h + 64 * c;
-          float *p = out + (size_t)o * P.d_in;
+          float *r = p + o * step;
 #pragma unroll
-          for (int e = 0; e < 64; ++e, p += P.d_in) {
+          for (int e = 0; e < 64; ++e, r += step) {
             if (o + e >= P.d_out) break;
-            float v = (e & 1 ? sum[h][e / 2].y : sum[h][e / 2].x) * ga;
-            if (P.beta) v = fmaf(be, P.db[o + e], v);
-            *p = v;
+            *r = (e & 1 ? sum[h][e / 2].y : sum[h][e / 2].x) * ga;
           }
         }
-      }
+      };
+      if (i < P.d_in) store(P.out + (size_t)w.slice * P.d_out * P.d_in + i, P.d_in, P.gamma ? P.gamma[i] : 1.0f);
+      else if (i == P.ones) store(P.db + (size_t)w.slice * P.d_out, 1, 1.0f);
     }
   }
 
@@ -711,29 +712,49 @@ __global__ void __cluster_dims__(kSmCtas, 1, 1) __launch_bounds__(kSmThreads, 1)
   cluster_sync();   // no CTA leaves while another reads its sums
 }
 
-// dW = gamma * (the slices' sums in order) + beta db; streams the slices from L2
-__global__ void __launch_bounds__(256) k_join_slices(const float *__restrict__ part, int slices, int d_out, int d_in,
-                                                     const float *__restrict__ gamma, const float *__restrict__ beta,
-                                                     const float *__restrict__ db, float *__restrict__ dW) {
-  const size_t n = (size_t)d_out * d_in, step = (size_t)gridDim.x * 256;
-  for (size_t e = (size_t)blockIdx.x * 256 + threadIdx.x; e < n; e += step) {
-    float v = part[e];
-    for (int s = 1; s < slices; ++s) v += part[s * n + e];
-    if (gamma || beta) {
-      const size_t o = e / d_in;
-      const int i = (int)(e - o * d_in);
-      if (gamma) v *= gamma[i];
-      if (beta) v = fmaf(beta[i], db[o], v);
+// dW = gamma * (the slices' sums in order) + beta db; db likewise from its slices.  `part` may be dW
+// (one slice).  A CTA takes 2048 columns of every gridDim.y-th row.  L2 holds what it reads where
+// that is below its size.
+constexpr int kJoinCols = 8;   // per thread
+__global__ void __launch_bounds__(256) k_join_slices(const float *part, int slices, int d_out, int d_in,
+                                                     const float *gamma, const float *beta, const float *db_part,
+                                                     int db_slices, float *db, float *dW) {
+  grid_wait();
+  const size_t n = (size_t)d_out * d_in;
+  const int c0 = blockIdx.x * 256 * kJoinCols + threadIdx.x;
+  float ga[kJoinCols], be[kJoinCols];
+#pragma unroll
+  for (int k = 0; k < kJoinCols; ++k) {
+    const int i = c0 + 256 * k;
+    ga[k] = gamma && i < d_in ? gamma[i] : 1.0f;
+    be[k] = beta && i < d_in ? beta[i] : 0.0f;
+  }
+  for (int o = blockIdx.y; o < d_out; o += gridDim.y) {
+    const size_t row = (size_t)o * d_in;
+    float v[kJoinCols], b = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) v[k] = c0 + 256 * k < d_in ? part[row + c0 + 256 * k] : 0.0f;
+    if (db_part) b = db_part[o];
+    for (int s = 1; s < slices; ++s) {
+#pragma unroll
+      for (int k = 0; k < kJoinCols; ++k)
+        if (c0 + 256 * k < d_in) v[k] += part[s * n + row + c0 + 256 * k];
+      if (s < db_slices) b += db_part[(size_t)s * d_out + o];
     }
-    dW[e] = v;
+    if (db && c0 == 0) db[o] = b;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k)
+      if (c0 + 256 * k < d_in) dW[row + c0 + 256 * k] = beta ? fmaf(be[k], b, v[k] * ga[k]) : v[k] * ga[k];
   }
 }
 
 // ---- what the tensor-core kernel reads, made by one launch -------------------------------------------
 struct Prepare {
   const uint8_t *scales;       // [T][groups]
-  StageScales *stage_scales;   // [groups][stages]
+  StageScales *stage_scales;   // [rows][stages]
+  uint8_t *one_codes;          // a box of the code of 1
   int T, groups, stages;
+  int rows;                    // groups, or one more: the group of ones
   int nscale, nsums, ndelta, ncodes;   // CTAs of each part, in this order
   int sum_slices, sum_rows;    // nsums > 0: sums of delta over slices of consecutive tokens
   bool sum_vec;
@@ -747,17 +768,17 @@ struct Prepare {
   size_t codes_ld;
 };
 
-// Scale bytes -> StageScales (NaN for a marked group, 1 past T): a stage of 64 tokens x 64 groups per CTA
+// Scale bytes -> StageScales (NaN for a marked group, 1 past T and for ones): a stage of 64 tokens x 64 groups per CTA
 // through shared memory, a warp writes a group.
 template <int F>
 __device__ __forceinline__ void stage_scales(const Prepare &P, int cta, uint8_t (*tile)[65]) {
   constexpr int up = F == FMT_E4M3 ? 120 : 112;
-  const int stage = cta % P.stages, g0 = cta / P.stages * 64, ng = min(64, P.groups - g0), t0 = stage * kK;
+  const int stage = cta % P.stages, g0 = cta / P.stages * 64, ng = min(64, P.rows - g0), t0 = stage * kK;
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < kK; r += 8)
 #pragma unroll
     for (int c = lane; c < 64; c += 32)
-      if (c < ng) tile[r][c] = t0 + r < P.T ? P.scales[(size_t)(t0 + r) * P.groups + g0 + c] : 127;
+      if (c < ng) tile[r][c] = t0 + r < P.T && g0 + c < P.groups ? P.scales[(size_t)(t0 + r) * P.groups + g0 + c] : 127;
   __syncthreads();
   for (int c = threadIdx.x >> 5; c < ng; c += 8) {
     uint32_t first[2], over[2];
@@ -865,6 +886,10 @@ __global__ void __launch_bounds__(256) k_prepare(const __grid_constant__ Prepare
   grid_release();
   int cta = blockIdx.x;
   if (cta < P.nscale) {
+    constexpr uint32_t one = F == FMT_E4M3 ? 0x38383838u : 0x3C3C3C3Cu;
+    if (cta == 0)
+      for (int e = threadIdx.x; e < kBox / 16; e += 256)
+        reinterpret_cast<uint4 *>(P.one_codes)[e] = make_uint4(one, one, one, one);
     stage_scales<F>(P, cta, sh.tile);
     return;
   }
@@ -920,32 +945,48 @@ size_t pad16(size_t bytes) { return (bytes + 15) / 16 * 16; }
 
 struct Plan {
   int nh, mt, nt, ng, slices, pairs;
+  bool ones;
+  double cost;   // in the time of a group, 1.1 us at 256 columns
 };
 
-// Tiles of 256 x 256, or 256 x 128 where one half covers d_out.  Tokens are cut into slices where
-// the tiles alone leave pairs of SMs idle: the count with the least waves x (groups of an item +
-// its start and end, about 1 group) + the slices' own traffic (written and read once, about 4 MB in
-// the time of a group, 1.1 us at 256 columns; the join kernel's launch about 2 groups).
-Plan plan_of(int sms, int T, int d_out, int d_in) {
+// Tiles of 256 x 256, or 256 x 128 where one half covers d_out; with `ones`, the columns' groups are
+// followed by one of ones, whose sums are db.  Tokens are cut into slices where the tiles alone leave
+// pairs of SMs idle: the count with the least waves x (groups of an item + its start and end, about 1
+// group) + the slices' own traffic (written and read once, about 4 MB in the time of a group; the join
+// kernel's launch about 2 groups).
+Plan plan_of(int sms, int T, int d_out, int d_in, bool ones) {
   Plan p;
   p.nh = d_out <= 128 ? 1 : 2;
-  p.mt = (d_in + 255) / 256;
+  p.mt = ((d_in + kActGroup - 1) / kActGroup + ones + 1) / 2;
   p.nt = (d_out + 128 * p.nh - 1) / (128 * p.nh);
   p.ng = (T + kGroup * kK - 1) / (kGroup * kK);
   p.pairs = sms / 2 > 1 ? sms / 2 : 1;
   const long long tiles = (long long)p.mt * p.nt;
   const double traffic = 8.0 * d_out * d_in / 4.0e6;
+  p.ones = ones;
   p.slices = 1;
-  double best = 1e300;
+  p.cost = 1e300;
   for (int s = 1; s <= 64 && s <= p.ng; ++s) {
     const long long waves = (tiles * s + p.pairs - 1) / p.pairs;
     const double cost = (double)waves * ((p.ng + s - 1) / s + 1) + (s > 1 ? 2.0 + s * traffic : 0.0);
-    if (cost < best) {
-      best = cost;
+    if (cost < p.cost) {
+      p.cost = cost;
       p.slices = s;
     }
   }
   return p;
+}
+
+// With db: from the group of ones, which is free where the last tile has room for it (5003 x 1021 x 2731
+// BF16: 42 us with db and without; by a pass over delta 49) or there is an idle pair of SMs in the last
+// wave (16384 x 1536 x 6144: 209 and 213 us), or by the pass over delta, about 5 MB in the time of a
+// group and 4 groups for its second kernel, where the tiles of ones would take a wave more (16384 x
+// 6144 x 1536: 278 us with them, 236 by the pass).
+Plan plan_for(int sms, bool bf16, int T, int d_out, int d_in, bool need_db) {
+  const Plan p = plan_of(sms, T, d_out, d_in, false);
+  if (!need_db) return p;
+  const Plan ones = plan_of(sms, T, d_out, d_in, true);
+  return ones.cost <= p.cost + 4.0 + (double)T * d_out * (bf16 ? 2 : 4) / 5.0e6 ? ones : p;
 }
 
 // Slices of tokens for delta's sums: about four CTAs per SM with all pieces, 64 tokens at least.
@@ -987,23 +1028,20 @@ int row_grid(const Launch &L, int T) {
   return c < L.sms * 8 ? c : L.sms * 8;
 }
 
-int stream_grid(const Launch &L, size_t n) {
-  const size_t c = (n + 255) / 256, most = (size_t)L.sms * 8;
-  return (int)(c < most ? c : most);
-}
-
 }  // namespace
 
 WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) {
   WeightGradWs w;
-  const Plan p = plan_of(sms, T, d_out, d_in);
-  w.part_floats = (size_t)sum_slices(sms, T, d_out) * d_out;
-  w.slice_floats = p.slices > 1 ? (size_t)p.slices * d_out * d_in : 0;
+  const Plan p = plan_for(sms, bf16, T, d_out, d_in, false), with_db = plan_for(sms, bf16, T, d_out, d_in, true);
+  const int slices = p.slices > with_db.slices ? p.slices : with_db.slices;
+  w.part_floats = with_db.ones ? 0 : (size_t)sum_slices(sms, T, d_out) * d_out;
+  w.db_floats = (size_t)with_db.slices * d_out;
+  w.slice_floats = slices > 1 ? (size_t)slices * d_out * d_in : 0;
   // a BF16 delta and the codes are copied only when their rows are not 16-byte aligned, which the
   // caller's pointers decide: room for both
   w.delta_bytes = (size_t)T * pad16((size_t)d_out * 2) * (bf16 ? 1 : 3);
   w.code_bytes = (size_t)T * pad16(d_in);
-  w.scale_bytes = (size_t)p.ng * kGroup * kScaleBytes * ((d_in + kActGroup - 1) / kActGroup);
+  w.scale_bytes = (size_t)p.ng * kGroup * kScaleBytes * ((d_in + kActGroup - 1) / kActGroup + 1) + kBox;
   return w;
 }
 
@@ -1030,10 +1068,9 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
       return bf16 ? launch_small<FMT_E4M3, __nv_bfloat16>(L, a) : launch_small<FMT_E4M3, float>(L, a);
     return bf16 ? launch_small<FMT_E5M2, __nv_bfloat16>(L, a) : launch_small<FMT_E5M2, float>(L, a);
   }
-  const Plan p = plan_of(L.sms, a.T, a.d_out, a.d_in);
-  const bool one = p.slices == 1, need_db = a.db || a.beta;
-  float *const db = need_db ? (a.db ? a.db : a.db_ws) : nullptr;
-  cudaError_t e;
+  const bool need_db = a.db || a.beta;
+  const Plan p = plan_for(L.sms, bf16, a.T, a.d_out, a.d_in, need_db);
+  const bool join = p.slices > 1 || a.beta;
   // operands with 16-byte aligned rows, and the scales by group and stage
   Prepare q{};
   q.scales = a.scales;
@@ -1041,14 +1078,16 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   q.T = a.T;
   q.groups = (a.d_in + kActGroup - 1) / kActGroup;
   q.stages = p.ng * kGroup;
-  q.nscale = q.stages * ((q.groups + 63) / 64);
+  q.rows = q.groups + p.ones;
+  q.one_codes = reinterpret_cast<uint8_t *>(q.stage_scales + (size_t)q.stages * q.rows);
+  q.nscale = q.stages * ((q.rows + 63) / 64);
   q.delta = a.delta;
   q.delta_out = a.delta_ws;
   q.d_out = a.d_out;
   q.codes = a.codes;
   q.codes_out = a.code_ws;
   q.d_in = a.d_in;
-  if (need_db) {
+  if (need_db && !p.ones) {
     q.sum_slices = sum_slices(L.sms, a.T, a.d_out);
     q.sum_rows = (a.T + q.sum_slices - 1) / q.sum_slices;
     q.sum_vec = rows_vec(a.d_out, a.delta, nullptr);
@@ -1078,8 +1117,12 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
     if (bf16) k_prepare<FMT_E5M2, true><<<pgrid, 256, 0, L.stream>>>(q);
     else k_prepare<FMT_E5M2, false><<<pgrid, 256, 0, L.stream>>>(q);
   }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (need_db && (e = launch_sum_parts(L, a.part, q.sum_slices, a.d_out, db)) != cudaSuccess) return e;
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // db in slices where the product makes it in slices
+  const int db_slices = p.ones ? p.slices : 1;
+  float *const db = db_slices > 1 || !a.db ? a.db_ws : a.db;
+  if (q.nsums && (e = launch_sum_parts(L, a.part, q.sum_slices, a.d_out, db)) != cudaSuccess) return e;
 
   CUtensorMap tm_codes, tm_delta;
   if (!boxes(&tm_codes, false, codes, a.T, a.d_in, cpitch, 1) ||
@@ -1089,7 +1132,7 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   P.T = a.T;
   P.d_out = a.d_out;
   P.d_in = a.d_in;
-  P.groups = q.groups;
+  P.last_group = q.rows - 1;
   P.ng = p.ng;
   P.mt = p.mt;
   P.nt = p.nt;
@@ -1097,16 +1140,18 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   P.items = p.mt * p.nt * p.slices;
   P.scales = q.stage_scales;
   P.stages = q.stages;
-  P.gamma = one ? a.gamma : nullptr;
-  P.beta = one ? a.beta : nullptr;
-  P.db = one ? db : nullptr;
-  P.out = one ? a.dW : a.slices;
+  P.gamma = join ? nullptr : a.gamma;
+  P.out = p.slices > 1 ? a.slices : a.dW;
+  P.ones = p.ones ? q.groups * kActGroup : -1;
+  P.one_codes = q.one_codes;
+  P.db = db;
   e = fmt == FMT_E4M3 ? launch_fmt<FMT_E4M3>(L, P, tm_codes, tm_delta, p, bf16)
                       : launch_fmt<FMT_E5M2>(L, P, tm_codes, tm_delta, p, bf16);
-  if (e != cudaSuccess || one) return e;
-  k_join_slices<<<stream_grid(L, (size_t)a.d_out * a.d_in), 256, 0, L.stream>>>(a.slices, p.slices, a.d_out, a.d_in,
-                                                                               a.gamma, a.beta, db, a.dW);
-  return cudaGetLastError();
+  if (e != cudaSuccess || !join) return e;
+  const int wide = (a.d_in + 256 * kJoinCols - 1) / (256 * kJoinCols), rows = (L.sms * 8 + wide - 1) / wide;
+  return launch_after(L.stream, k_join_slices, dim3(wide, a.d_out < rows ? a.d_out : rows), 256, P.out, p.slices,
+                      a.d_out, a.d_in, a.gamma, a.beta, need_db ? db : nullptr, db_slices, db_slices > 1 ? a.db : nullptr,
+                      a.dW);
 }
 
 }  // namespace gift

@@ -459,6 +459,28 @@ def test_weight_grad_extreme_scales(dt):
     assert np.array_equal(host(dW), want)
 
 
+# db beside a full last tile and one with room, with tokens in one slice and in several, and where a tile
+# more would cost another wave of tiles on 152 SMs
+@pytest.mark.parametrize("affine", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(300, 264, 512), (300, 264, 640), (9000, 100, 512), (9000, 100, 640),
+                                   (1100, 1024, 4864)], ids=str)
+def test_weight_grad_bias_gradient_of_every_tiling(shape, dt, affine):
+    T, d_out, d_in = shape
+    rng = np.random.default_rng(T + d_in)
+    delta = rng.integers(-3, 4, (T, d_out)).astype(np.float64)
+    codes, scales = R.encode(rng.integers(-7, 8, (T, d_in)).astype(np.float64), "e4m3")
+    v = R.decode(codes, scales, "e4m3")
+    gamma = rng.choice([-1.0, 0.5, 2.0], d_in).astype(np.float32) if affine else None
+    beta = rng.integers(-4, 5, d_in).astype(np.float32) if affine else None
+    want, wb = R.weight_grad(delta, v, gamma, beta)   # halves of integers below 2^23: exact in FP32
+    d, c, s = dev(delta, DT[dt]), dev(codes, torch.uint8), dev(scales, torch.uint8)
+    dW, db = weight_grad(d, c, s, "e4m3", d_in, gamma, beta)
+    assert np.array_equal(host(dW), want) and np.array_equal(host(db), wb)
+    dW, _ = weight_grad(d, c, s, "e4m3", d_in, gamma, beta, db=False)
+    assert np.array_equal(host(dW), want)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_weight_grad_extreme_scales_of_a_wide_layer(dt, fmt):
