@@ -9,7 +9,7 @@
 // A pair of CTAs (a cluster of two SMs, cta_group::2) owns a 256 (i) x 128 NH (o) tile and walks
 // its tokens 64 at a time; each CTA holds 128 of the i and half of the o columns:
 //   warps 0, 2   TMA: a stage's 64 x 128 code tile and its tokens' scales (one group of 128 columns:
-//                the CTA's; transposed and made BF16 by a kernel before); its 64 x 64 delta boxes;
+//                the CTA's; transposed and made BF16 by k_prepare); its 64 x 64 delta boxes;
 //   warps 4-19   codes -> BF16: ldmatrix transposes 16 x 16 bytes so that a register holds four
 //                tokens of one column, which is tcgen05.st's 16x256b layout; the code's bits placed
 //                in the BF16 fields times 2^(120 + k) (2^(112 + k) for E5M2), exact;
@@ -18,7 +18,8 @@
 //                into one of three 128-column accumulators and is added to FP32 registers to
 //                nearest; the two halves of a tile change accumulators half a segment apart, so
 //                that one is always being drained while two are being filled.
-// Few tiles: the tokens are cut into slices whose sums a second kernel adds in order.
+// Few tiles: the tokens are cut into slices whose sums a second kernel adds in order.  db is the row
+// that a value of 1 for every token gives: a group of ones after the last columns (plan_for).
 //
 // What bounds it.  The MMAs take 512 clocks a stage (measured back to back, N = 128 halves as well as
 // N = 256).  One CTA alone would need 80 bytes of operands per clock from L2, a pair needs 48 per SM.
@@ -713,8 +714,9 @@ __global__ void __cluster_dims__(kSmCtas, 1, 1) __launch_bounds__(kSmThreads, 1)
 }
 
 // dW = gamma * (the slices' sums in order) + beta db; db likewise from its slices.  `part` may be dW
-// (one slice).  A CTA takes 2048 columns of every gridDim.y-th row.  L2 holds what it reads where
-// that is below its size.
+// (one slice).  A CTA takes 2048 columns of every gridDim.y-th row; eight loads a thread are in flight.
+// Bound by L2 where that holds the sums: gain and offset onto 1536 x 6144 outputs take 16 us more
+// (75 MB, 4.7 TB/s), onto 1021 x 2731 5 us.
 constexpr int kJoinCols = 8;   // per thread
 __global__ void __launch_bounds__(256) k_join_slices(const float *part, int slices, int d_out, int d_in,
                                                      const float *gamma, const float *beta, const float *db_part,
@@ -749,6 +751,10 @@ __global__ void __launch_bounds__(256) k_join_slices(const float *part, int slic
 }
 
 // ---- what the tensor-core kernel reads, made by one launch -------------------------------------------
+// Independent parts share the launch, each on its own CTAs: scales by group and stage (16384 x 6144: about
+// 3 us), copies with aligned rows (5003 x 1021 BF16 and 5003 x 2731 codes: 42 us a call with them, 37
+// without), FP32 delta's terms, delta's sums over tokens (16384 x 1536 BF16: 16 us).  Bound by HBM and
+// by the launch; the product's launch overlaps its end (griddepcontrol).
 struct Prepare {
   const uint8_t *scales;       // [T][groups]
   StageScales *stage_scales;   // [rows][stages]
@@ -775,10 +781,18 @@ __device__ __forceinline__ void stage_scales(const Prepare &P, int cta, uint8_t 
   constexpr int up = F == FMT_E4M3 ? 120 : 112;
   const int stage = cta % P.stages, g0 = cta / P.stages * 64, ng = min(64, P.rows - g0), t0 = stage * kK;
   const int lane = threadIdx.x & 31;
-  for (int r = threadIdx.x >> 5; r < kK; r += 8)
+  uint8_t b[kK / 8][2];   // all loads before the first store
 #pragma unroll
-    for (int c = lane; c < 64; c += 32)
-      if (c < ng) tile[r][c] = t0 + r < P.T && g0 + c < P.groups ? P.scales[(size_t)(t0 + r) * P.groups + g0 + c] : 127;
+  for (int k = 0; k < kK / 8; ++k)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = t0 + (threadIdx.x >> 5) + 8 * k, g = g0 + lane + 32 * u;
+      b[k][u] = t < P.T && g < P.groups ? P.scales[(size_t)t * P.groups + g] : 127;
+    }
+#pragma unroll
+  for (int k = 0; k < kK / 8; ++k)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) tile[(threadIdx.x >> 5) + 8 * k][lane + 32 * u] = b[k][u];
   __syncthreads();
   for (int c = threadIdx.x >> 5; c < ng; c += 8) {
     uint32_t first[2], over[2];
