@@ -113,7 +113,7 @@ __device__ __forceinline__ float sum2(float2 v) { return v.x + v.y; }
 // warps' joined (mean = sum n_w mean_w / d, M2 = sum M2_w + n_w (mean_w - mean)^2), so that no large
 // mean is squared and the row group meets at one barrier only.  U = 1 holds gain and offset in
 // registers; U <= 2 (up to 16384 columns) loads the next row before it waits for the sums of this one
-// (8192 x 16384 BF16: 231 us without, see below with).
+// (8192 x 16384 BF16: 179 us, 231 without; gain and offset come from L1 and L2 there).
 template <typename E, bool VEC, int U, int MAXT>
 __global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 384 ? 2 : 1) k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt,
                                                       int *status) {
@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(MAXT, U > 1 || MAXT == 512 ? 1 : C == 16 ? 2 :
 }
 
 // The column sums alone: a warp takes one piece of the columns over a slice of consecutive tokens;
-// part[2 slice] = sum dy n, part[2 slice + 1] = sum dy.
+// part[2 slice] = sum dy n, part[2 slice + 1] = sum dy.  It reads dy and x a second time, HBM-bound: 8192 x
+// 16384 BF16 take 199 us for dx and 124 us here (4.3 TB/s).
 template <typename E, bool VEC, bool SAVED>
 __global__ void __launch_bounds__(kNormThreads) k_norm_cols(const __grid_constant__ NormBackward a, int fmt, int rows) {
   const int lane = threadIdx.x & 31, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
@@ -379,8 +380,8 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_cols(const __grid_constan
 }
 
 // out[c] = sum over partials of part[k stride + c]: 32 columns per CTA, 32 warps take every 32nd
-// partial (their loads are all in flight at once: latency is what this kernel costs), and their sums
-// are added in order.  blockIdx.y: the first or the second output.
+// partial (their loads are all in flight at once: latency is what this kernel costs, 5 us for 152
+// partials of 2 x 1536 columns), and their sums are added in order.  blockIdx.y: the first or the second output.
 __global__ void __launch_bounds__(1024) k_norm_sums(const float *__restrict__ part, int parts, size_t stride,
                                                     size_t second, int d, float *out0, float *out1) {
   __shared__ float sh[32][33];
@@ -401,6 +402,8 @@ __global__ void __launch_bounds__(1024) k_norm_sums(const float *__restrict__ pa
 }
 
 // ---- rows too long for registers: column by column, the row read once per sum --------------------------
+// (above 32768 columns.)  A row is read three times forward and twice backward, L2 serves the repeats:
+// 4096 x 40960 BF16 285 us forward, 855 us backward with both sums over tokens.
 __device__ __forceinline__ float cta_sum(float v, float *sh /* kNormThreads / 32 */) {
   v = warp_sum(v);
   __syncthreads();
