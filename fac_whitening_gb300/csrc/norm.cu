@@ -128,6 +128,20 @@ __global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 38
     load_cols<VEC>(a.gamma, first, d - first, lane, 1.0f, g);
     load_cols<VEC>(a.beta, first, d - first, lane, 0.0f, b);
   }
+  extern __shared__ float4 cols_sh[];
+  float4 *const own = cols_sh + G.w * U * 2 * 128 + lane;   // [piece][gain, offset][4][32]: no bank conflicts
+  if (U == 2) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      load_cols<VEC>(a.gamma, first + u * kPiece, d - first - u * kPiece, lane, 1.0f, g);
+      load_cols<VEC>(a.beta, first + u * kPiece, d - first - u * kPiece, lane, 0.0f, b);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        own[(8 * u + k) * 32] = make_float4(g[2 * k].x, g[2 * k].y, g[2 * k + 1].x, g[2 * k + 1].y);
+        own[(8 * u + 4 + k) * 32] = make_float4(b[2 * k].x, b[2 * k].y, b[2 * k + 1].x, b[2 * k + 1].y);
+      }
+    }
+  }
   constexpr bool kAhead = U <= 2;
   Raw<E> now[U], next[kAhead ? U : 1];
   auto load = [&](int t, Raw<E> *r) {
@@ -175,7 +189,16 @@ __global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 38
     for (int u = 0; u < U; ++u) {
       const int c0 = first + u * kPiece, n = d - c0;
       if (n > 0) {
-        if (U > 1) {
+        if (U == 2) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 gv = own[(8 * u + k) * 32], bv = own[(8 * u + 4 + k) * 32];
+            g[2 * k] = make_float2(gv.x, gv.y);
+            g[2 * k + 1] = make_float2(gv.z, gv.w);
+            b[2 * k] = make_float2(bv.x, bv.y);
+            b[2 * k + 1] = make_float2(bv.z, bv.w);
+          }
+        } else if (U > 2) {
           load_cols<VEC>(a.gamma, c0, n, lane, 1.0f, g);
           load_cols<VEC>(a.beta, c0, n, lane, 0.0f, b);
         }
@@ -560,8 +583,13 @@ bool backward_plan(int d, bool vec, RowPlan *p) {
 template <typename E, bool VEC, int U, int MAXT>
 cudaError_t forward_t(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
   constexpr auto kernel = k_norm_forward<E, VEC, U, MAXT>;
-  kernel<<<resident<kernel>(L, p.threads, 0, a.T, p.threads / 32 / p.nw), p.threads, 0, L.stream>>>(a, p.nw, fmt,
-                                                                                                   L.status);
+  const int smem = U == 2 ? p.nw * U * 2 * kPiece * (int)sizeof(float) : 0;   // gain and offset
+  if (smem) {
+    const cudaError_t e = ensure_dynamic_smem<kernel>(16 * U * 2 * kPiece * (int)sizeof(float));
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<resident<kernel>(L, p.threads, smem, a.T, p.threads / 32 / p.nw), p.threads, smem, L.stream>>>(
+      a, p.nw, fmt, L.status);
   return cudaGetLastError();
 }
 
