@@ -2,12 +2,12 @@
 //
 // Both hold a row's share in registers (pieces of act.cuh) and move each byte once: forward 4 bytes an
 // element for BF16, 5 with the checkpoint; backward 6, or 5 from the checkpoint.  A row belongs to a
-// group of warps, one per piece up to 8192 columns, and the next row is loaded before this one's sums
-// are waited for.
+// group of warps (row_plan, forward_plan, backward_plan), and the next row is loaded before this one's
+// sums are waited for.
 //
 // Forward: the mean and the squared deviations from it, reduced from registers; y and the checkpoint are
-// written from them.  32768 x 4096 BF16: 101 us, 5.3 TB/s; with the checkpoint 130 us, 5.2 TB/s: HBM, at
-// 0.78 of the copy rate.
+// written from them.  32768 x 4096 BF16: 91 us, 5.9 TB/s; with the checkpoint 111 us, 6.0 TB/s: HBM, at
+// 0.87 of the copy rate; 16384 x 1536 with the checkpoint 26.8 us, 4.7 TB/s.
 //
 // Backward: sums over a row (h and h n) for dx, and sums over tokens (dy n and dy) for the gain's and
 // offset's gradients.  The latter stay in the registers of the thread that owns the column: a CTA
@@ -112,11 +112,12 @@ __device__ __forceinline__ float sum2(float2 v) { return v.x + v.y; }
 // Mean and squared deviations of a row: each warp's own by two passes over its registers, then the
 // warps' joined (mean = sum n_w mean_w / d, M2 = sum M2_w + n_w (mean_w - mean)^2), so that no large
 // mean is squared and the row group meets at one barrier only.  U = 1 holds gain and offset in
-// registers; U <= 2 (up to 16384 columns) loads the next row before it waits for the sums of this one
-// (8192 x 16384 BF16: 179 us, 231 without; gain and offset come from L1 and L2 there).
+// registers, U = 2 and 3 in shared memory where no bank conflicts (8192 x 16384 BF16: 97 us, 179 with
+// loads from L1 and L2, whose lines 32 lanes' 64 bytes each cross); both load the next row before they
+// wait for the sums of this one (231 us without either).  U = 4 has room for neither.
 template <typename E, bool VEC, int U, int MAXT>
-__global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 384 ? 2 : 1) k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt,
-                                                      int *status) {
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (U == 1 ? 3 : 2) : MAXT == 384 ? 2 : 1)
+    k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt, int *status) {
   __shared__ float2 red[16][2][16];
   const int lane = threadIdx.x & 31, T = a.T, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
   RowGroup G(nw, red);
@@ -130,9 +131,9 @@ __global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 38
   }
   extern __shared__ float4 cols_sh[];
   float4 *const own = cols_sh + G.w * U * 2 * 128 + lane;   // [piece][gain, offset][4][32]: no bank conflicts
-  if (U == 2) {
+  if (U == 2 || U == 3) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U && G.id == 0; ++u) {
       load_cols<VEC>(a.gamma, first + u * kPiece, d - first - u * kPiece, lane, 1.0f, g);
       load_cols<VEC>(a.beta, first + u * kPiece, d - first - u * kPiece, lane, 0.0f, b);
 #pragma unroll
@@ -141,8 +142,9 @@ __global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 38
         own[(8 * u + 4 + k) * 32] = make_float4(b[2 * k].x, b[2 * k].y, b[2 * k + 1].x, b[2 * k + 1].y);
       }
     }
+    __syncthreads();
   }
-  constexpr bool kAhead = U <= 2;
+  constexpr bool kAhead = U <= 3;
   Raw<E> now[U], next[kAhead ? U : 1];
   auto load = [&](int t, Raw<E> *r) {
 #pragma unroll
@@ -189,7 +191,7 @@ __global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 38
     for (int u = 0; u < U; ++u) {
       const int c0 = first + u * kPiece, n = d - c0;
       if (n > 0) {
-        if (U == 2) {
+        if (U == 2 || U == 3) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float4 gv = own[(8 * u + k) * 32], bv = own[(8 * u + 4 + k) * 32];
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(MAXT, U > 1 ? 1 : MAXT == 256 ? 3 : MAXT == 38
             b[2 * k] = make_float2(bv.x, bv.y);
             b[2 * k + 1] = make_float2(bv.z, bv.w);
           }
-        } else if (U > 2) {
+        } else if (U > 3) {
           load_cols<VEC>(a.gamma, c0, n, lane, 1.0f, g);
           load_cols<VEC>(a.beta, c0, n, lane, 0.0f, b);
         }
@@ -580,10 +582,31 @@ bool backward_plan(int d, bool vec, RowPlan *p) {
   return true;
 }
 
+// Forward: with 32-byte accesses two pieces per lane where that leaves at most a sixth of the lanes idle (fewer
+// warps to a row, twice the loads of a lane in flight: 32768 x 4096 BF16 91 us against 101, 111 against
+// 131 with the checkpoint; 8192 x 8192 52 against 62), and a whole row of three pieces in one BF16 warp,
+// which needs no barrier (16384 x 1536: 20.3 against 22.8, 26.8 against 28.9; FP32 would not fit the
+// registers).  With element accesses one piece was faster (4099 x 7001 BF16 72 us against 87).
+bool forward_plan(int d, bool vec, bool bf16, RowPlan *p) {
+  if (!row_plan(d, p)) return false;
+  const int pieces = (d + kPiece - 1) / kPiece;
+  if (!vec || p->u > 1 || pieces == 1) return true;
+  if (pieces == 3 && bf16) {
+    p->u = 3;
+    p->nw = 1;
+    p->threads = 256;
+  } else if (pieces % 2 == 0 || pieces >= 5) {
+    p->u = 2;
+    p->nw = (pieces + 1) / 2;
+    p->threads = group_threads(p->nw);
+  }
+  return true;
+}
+
 template <typename E, bool VEC, int U, int MAXT>
 cudaError_t forward_t(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
   constexpr auto kernel = k_norm_forward<E, VEC, U, MAXT>;
-  const int smem = U == 2 ? p.nw * U * 2 * kPiece * (int)sizeof(float) : 0;   // gain and offset
+  const int smem = U == 2 || U == 3 ? p.nw * U * 2 * kPiece * (int)sizeof(float) : 0;   // gain and offset
   if (smem) {
     const cudaError_t e = ensure_dynamic_smem<kernel>(16 * U * 2 * kPiece * (int)sizeof(float));
     if (e != cudaSuccess) return e;
@@ -595,12 +618,15 @@ cudaError_t forward_t(const Launch &L, int fmt, const NormForward &a, const RowP
 
 template <typename E, bool VEC, int U>
 cudaError_t forward(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
-  if (p.threads <= 256) return forward_t<E, VEC, U, 256>(L, fmt, a, p);
+  if constexpr (U < 4)
+    if (p.threads <= 256) return forward_t<E, VEC, U, 256>(L, fmt, a, p);
   return U == 1 && p.threads <= 384 ? forward_t<E, VEC, U, 384>(L, fmt, a, p) : forward_t<E, VEC, U, 512>(L, fmt, a, p);
 }
 
 template <typename E, bool VEC>
 cudaError_t forward_u(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
+  if constexpr (VEC && sizeof(E) == 2)
+    if (p.u == 3) return forward_t<E, VEC, 3, 256>(L, fmt, a, p);
   switch (p.u) {
     case 1: return forward<E, VEC, 1>(L, fmt, a, p);
     case 2: return forward<E, VEC, 2>(L, fmt, a, p);
@@ -611,13 +637,13 @@ cudaError_t forward_u(const Launch &L, int fmt, const NormForward &a, const RowP
 template <typename E>
 cudaError_t forward_e(const Launch &L, int fmt, const NormForward &a) {
   RowPlan p;
-  if (!row_plan(a.d, &p)) {
+  const bool vec = rows_vec(a.d, a.x, a.codes) && rows_vec(a.d, a.y, nullptr) && cols_aligned(a.gamma) &&
+                   cols_aligned(a.beta);
+  if (!forward_plan(a.d, vec, sizeof(E) == 2, &p)) {
     const int grid = a.T < L.sms * 8 ? a.T : L.sms * 8;
     k_norm_forward_long<E><<<grid, kNormThreads, 0, L.stream>>>(a, fmt, L.status);
     return cudaGetLastError();
   }
-  const bool vec = rows_vec(a.d, a.x, a.codes) && rows_vec(a.d, a.y, nullptr) && cols_aligned(a.gamma) &&
-                   cols_aligned(a.beta);
   return vec ? forward_u<E, true>(L, fmt, a, p) : forward_u<E, false>(L, fmt, a, p);
 }
 
