@@ -213,6 +213,17 @@ def test_norm_forward_checkpoint_is_the_encode_of_n(shape, fmt, off):
     assert st == 0 and np.all(np.abs(v - wn) <= half * np.abs(wn) + lowest * amax + (d + 16) * 4 * R.U32)
 
 
+# aligned rows by every number of pieces per lane and of warps per row, whole and partial last pieces, and
+# more rows than are resident at once
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(5000, 528), (3001, 1040), (2600, 1536), (700, 2064), (641, 3600), (400, 4112),
+                                   (200, 8208), (320, 10000), (170, 16384), (160, 16400)], ids=str)
+def test_norm_forward_of_many_aligned_rows(shape, dt):
+    test_norm_forward(shape, dt, True, False)
+    if dt == "bf16":
+        test_norm_forward_checkpoint_is_the_encode_of_n(shape, "e4m3", False)
+
+
 def test_norm_forward_constant_and_nonfinite_rows():
     x = rows(6, 200, "f32", 9)
     x[1] = 3.25
