@@ -751,8 +751,8 @@ __global__ void __launch_bounds__(256) k_join_slices(const float *part, int slic
 }
 
 // ---- what the tensor-core kernel reads, made by one launch -------------------------------------------
-// Independent parts share the launch, each on its own CTAs: scales by group and stage (16384 x 6144: about
-// 3 us), copies with aligned rows (5003 x 1021 BF16 and 5003 x 2731 codes: 42 us a call with them, 37
+// Independent parts share the launch, each on its own CTAs: scales by group and stage (16384 x 6144: 5 us
+// cold), copies with aligned rows (5003 x 1021 BF16 and 5003 x 2731 codes: 42 us a call with them, 37
 // without), FP32 delta's terms, delta's sums over tokens (16384 x 1536 BF16: 16 us).  Bound by HBM and
 // by the launch; the product's launch overlaps its end (griddepcontrol).
 struct Prepare {
