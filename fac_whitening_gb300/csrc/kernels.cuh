@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "kernel_attrs.cuh"
 
 // Host context behind the opaque gift_ctx handle.
 struct gift_ctx {
@@ -210,21 +211,6 @@ cudaError_t launch_ritz_rotate(const Launch &L, float *Y, const float *Q, int d,
 cudaError_t launch_ritz_check(const Launch &L, const float *res_parts, int nparts, const float *theta, int r,
                               int *flag);
 cudaError_t launch_trace_diag(const Launch &L, const float *A, int d, double *tr);
-
-// Sets a kernel's opt-in dynamic shared-memory size once per device and kernel (so no
-// attribute call happens inside a stream capture after the first eager call).  Keyed on the
-// kernel itself: instantiations that share a function type keep separate flags.
-template <auto Kernel>
-cudaError_t ensure_dynamic_smem(int bytes) {
-  static int done[64] = {};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev] >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = bytes;
-  return e;
-}
 
 // Last CUDA error seen by a libgift call on this thread (see gift_last_error).
 void record_cuda_error(cudaError_t e);

@@ -665,7 +665,7 @@ template <typename E, bool VEC, bool SAVED, int U, int C, int MAXT>
 cudaError_t backward_t(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
   constexpr auto kernel = k_norm_backward<E, VEC, SAVED, U, C, MAXT>;
   const int warps = p.threads / 32, per_cta = warps / p.nw, smem = U == 1 && per_cta > 1 ? warps * 2 * kColWords<C> * 4 : 0;
-  cudaError_t e = smem ? ensure_dynamic_smem<kernel>(smem) : cudaSuccess;
+  cudaError_t e = smem ? ensure_dynamic_smem<kernel>(MAXT / 32 * 2 * kColWords<C> * 4) : cudaSuccess;
   if (e != cudaSuccess) return e;
   int grid = resident<kernel>(L, p.threads, smem, a.T, per_cta);
   if (grid > norm_partials(L.sms, a.T)) grid = norm_partials(L.sms, a.T);
