@@ -530,19 +530,10 @@ int col_rows(int T) {
 bool cols_aligned(const float *p) { return !p || aligned16(p); }
 
 // CTAs of a persistent launch: what is resident on the context's SMs, at most one per `per_cta` rows.
-// The occupancy of a kernel is looked up once per CTA size (warps) and device.
 template <auto Kernel>
 int resident(const Launch &L, int threads, int smem, int T, int per_cta) {
-  static int known[64][17] = {};
-  int dev = 0, per_sm = 0;
-  const bool keep = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
-  if (keep) per_sm = known[dev][threads / 32];
-  if (per_sm < 1) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, Kernel, threads, smem) != cudaSuccess || per_sm < 1)
-      per_sm = 1;
-    if (keep) known[dev][threads / 32] = per_sm;
-  }
-  const long long most = (long long)L.sms * per_sm, need = ((long long)T + per_cta - 1) / per_cta;
+  const long long most = (long long)L.sms * resident_per_sm<Kernel>(threads, smem);
+  const long long need = ((long long)T + per_cta - 1) / per_cta;
   return (int)(need < most ? need : most);
 }
 

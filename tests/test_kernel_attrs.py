@@ -24,3 +24,7 @@ def _run(tmp_path, name):
 
 def test_two_first_calls_of_one_kernel_keep_the_larger_limit(tmp_path):
     _run(tmp_path, "kernel_attrs_test")
+
+
+def test_the_resident_ctas_are_those_of_the_launch_asked_about(tmp_path):
+    _run(tmp_path, "resident_test")
