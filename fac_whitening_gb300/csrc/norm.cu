@@ -108,6 +108,10 @@ __device__ __forceinline__ float2 in_row2(int n, int lane, int k, float2 v) {
   return make_float2(64 * k + lane < n ? v.x : 0.0f, 64 * k + 32 + lane < n ? v.y : 0.0f);
 }
 __device__ __forceinline__ float sum2(float2 v) { return v.x + v.y; }
+// Whether a row's statistics are numbers.  A variance that overflowed leaves rstd at 0, which is finite.
+__device__ __forceinline__ bool norm_row_ok(float mean, float var, float rstd) {
+  return isfinite(mean) && isfinite(var) && isfinite(rstd);
+}
 
 // Mean and squared deviations of a row: each warp's own by two passes over its registers, then the
 // warps' joined (mean = sum n_w mean_w / d, M2 = sum M2_w + n_w (mean_w - mean)^2), so that no large
@@ -181,11 +185,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (U == 1 ? 3 : 2) : MAXT ==
         q = fma2(v, v, q);
       }
     const float2 st = G.moments(wmean, warp_sum(sum2(q)), d, U * kPiece, inv_d);
-    const float mean = st.x, rstd = __frcp_rn(__fsqrt_rn(fmaf(st.y, inv_d, a.eps)));
+    const float mean = st.x, var = fmaf(st.y, inv_d, a.eps), rstd = __frcp_rn(__fsqrt_rn(var));
     if (G.w == 0 && lane == 0) {
       if (a.mean) a.mean[t] = mean;
       if (a.rstd) a.rstd[t] = rstd;
-      if (!isfinite(mean) || !isfinite(rstd)) set_status(status, GIFT_ERR_NONFINITE);
+      if (!norm_row_ok(mean, var, rstd)) set_status(status, GIFT_ERR_NONFINITE);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -457,11 +461,11 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_forward_long(const __grid
       const float u = ld1(xr + c) - mean;
       q = fmaf(u, u, q);
     }
-    const float rstd = __frcp_rn(__fsqrt_rn(__fdiv_rn(cta_sum(q, sh), (float)d) + a.eps));
+    const float var = __fdiv_rn(cta_sum(q, sh), (float)d) + a.eps, rstd = __frcp_rn(__fsqrt_rn(var));
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[t] = mean;
       if (a.rstd) a.rstd[t] = rstd;
-      if (!isfinite(mean) || !isfinite(rstd)) set_status(status, GIFT_ERR_NONFINITE);
+      if (!norm_row_ok(mean, var, rstd)) set_status(status, GIFT_ERR_NONFINITE);
     }
     for (int c0 = warp * kPiece; c0 < d; c0 += kNormThreads / 32 * kPiece) {
       const int n = d - c0;

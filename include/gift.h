@@ -527,7 +527,8 @@ gift_status gift_act_decode(gift_ctx *ctx, const void *codes, const void *scales
  *           beta, gift_weight_grad of the linear layer that reads y.
  *  eps    : finite, >= 0.
  * INVALID_ARG: null x or y, one of codes and scales without the other, T or d < 1, a bad type,
- * format or eps.  d_status: NONFINITE when a row's mean or rstd is not finite. */
+ * format or eps.  d_status: NONFINITE when a row's mean, variance or rstd is not finite in FP32
+ * (finite deviations whose squares sum past FP32's largest value among them). */
 gift_status gift_layernorm_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d, const float *gamma,
                                    const float *beta, float eps, void *y, float *mean, float *rstd, gift_format fmt,
                                    void *codes, void *scales, int *d_status, cudaStream_t stream);
