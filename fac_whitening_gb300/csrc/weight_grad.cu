@@ -839,7 +839,26 @@ __device__ __forceinline__ void column_sums(const Prepare &P, int cta, float (*s
   }
 }
 
-// FP32 as three BF16 terms (exact), planes of T rows of ld columns; a warp per row, two columns per lane
+// The terms of one value at the end of FP32's range, where rounding to BF16 gives an infinity.  A finite
+// value is cut into its bits instead (8 + 8 + 8 of them, exact), so that no sum of the first terms passes it; an
+// infinity or NaN is its own first term and has no others (Inf - Inf would make it NaN).
+__device__ __forceinline__ void bf16_terms_of_large(float x, uint16_t *t) {
+  const uint32_t bits = __float_as_uint(x), size = bits & 0x7FFFFFFFu;
+  if (size < 0x7F7F8000u) {
+    tc::bf16_split3(x, t[0], t[1], t[2]);
+  } else if (size < 0x7F800000u) {
+    const float r = __fsub_rn(x, __uint_as_float(bits & 0xFFFF0000u));
+    t[0] = (uint16_t)(bits >> 16);
+    t[1] = (uint16_t)(__float_as_uint(r) >> 16);
+    t[2] = __bfloat16_as_ushort(__float2bfloat16_rn(__fsub_rn(r, __uint_as_float(__float_as_uint(r) & 0xFFFF0000u))));
+  } else {
+    t[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    t[1] = t[2] = 0;
+  }
+}
+
+// FP32 as three BF16 terms (exact from 2^-110 up; below, the last ends at BF16's smallest step), planes of
+// T rows of ld columns; a warp per row, two columns per lane
 __device__ __forceinline__ void bf16_terms(const float *x, int T, int d, int ld, uint16_t *out, int cta, int ctas) {
   const size_t plane = (size_t)T * ld;
   for (int t = cta * 8 + (threadIdx.x >> 5); t < T; t += ctas * 8) {
@@ -847,7 +866,16 @@ __device__ __forceinline__ void bf16_terms(const float *x, int T, int d, int ld,
     uint16_t *o = out + (size_t)t * ld;
     for (int c = 2 * (threadIdx.x & 31); c < d; c += 64) {   // ld is even
       uint32_t w[3];
-      tc::bf16_split3x2(p[c], c + 1 < d ? p[c + 1] : 0.0f, w[0], w[1], w[2]);
+      const float x0 = p[c], x1 = c + 1 < d ? p[c + 1] : 0.0f;
+      if (max(abs_bits(x0), abs_bits(x1)) < 0x7F7F8000u) {
+        tc::bf16_split3x2(x0, x1, w[0], w[1], w[2]);
+      } else {
+        uint16_t a[3], b[3];
+        bf16_terms_of_large(x0, a);
+        bf16_terms_of_large(x1, b);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) w[k] = (uint32_t)a[k] | (uint32_t)b[k] << 16;
+      }
 #pragma unroll
       for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(o + k * plane + c) = w[k];
     }

@@ -558,8 +558,10 @@ gift_status gift_layernorm_backward(gift_ctx *ctx, const void *dy, gift_dtype dt
  * by T), v the checkpoint's values, and the bias gradient db = sum_t delta.  For a checkpoint of a
  * norm's n the layer's input was gamma n + beta: with gamma (and beta)
  *   dW[o][i] = gamma[i] sum_t delta[t][o] n[t][i] + beta[i] db[o].
- * Products are exact (an FP32 delta enters as three BF16 terms); sums are FP32, rounded to
- * nearest at least every 256 tokens, in an order fixed by the shape and the context.
+ * Products are exact (an FP32 delta enters as three BF16 terms; below 2^-110 it may lose up to
+ * 2^-134); sums are FP32, rounded to nearest at least every 256 tokens, in an order fixed by the
+ * shape and the context.  An infinity or NaN in delta reaches its own row of dW and entry of db
+ * as the formula has it, a marked group (NaN) its own columns.
  *  delta  : device, T x d_out of type delta_dt.
  *  codes, scales : the checkpoint (T x d_in, format fmt).
  *  gamma, beta   : device, d_in FP32, each nullable (1 and 0).
