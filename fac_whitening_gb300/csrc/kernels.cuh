@@ -10,7 +10,7 @@ struct gift_ctx {
   int device_sms;           // SMs of the device
   int sms;                  // SMs this context's launches size their grids for (<= device_sms)
   int subspace_iters;
-  long long barrier_wait;   // clock cycles a CTA waits at a streaming grid barrier
+  long long barrier_wait;   // clock cycles of a settable wait (GIFT_OPT_BARRIER_WAIT)
   int sketch;               // rank-r refresh: 0 implicit a^T (a Q) / T, 1 explicit A Q
 };
 
@@ -22,7 +22,7 @@ struct Launch {
   cudaStream_t stream;
   int sms;       // streaming multiprocessors of the device
   int *status;   // caller's device status word (nullable)
-  long long barrier_wait = kDefaultBarrierWait;   // bounded wait of the streaming grid barriers
+  long long barrier_wait = kDefaultBarrierWait;   // clock cycles of a settable wait
 };
 
 struct ReduceArgs {

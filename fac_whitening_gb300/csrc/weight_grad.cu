@@ -29,7 +29,9 @@
 // tokens 707 us, 1.75 PFLOP/s; 32768 x 4096 x 16384 run over and over (power cap) 3.0 ms, 1.46
 // PFLOP/s.  Converting in a pass of its own would move 300 MB more for the first of these, 45 us at the
 // copy rate.
-// Every mbarrier wait is clock-bounded and reports GIFT_ERR_TIMEOUT.
+// Every mbarrier wait is bounded by the context's GIFT_OPT_BARRIER_WAIT and reports GIFT_ERR_TIMEOUT.  A
+// warp leaves as one, and however its loop ended, the copies it issued and the MMAs on the CTA's
+// memory are waited for before the CTA leaves.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -53,7 +55,7 @@ constexpr int kDeqWarp = 4, kDeqWarps = 16;  // warps 4-19: four per stage, by t
 constexpr int kFoldWarp = kDeqWarp + kDeqWarps;
 constexpr int kCodesWarp = 0, kMmaWarp = 1, kDeltaWarp = 2;   // and the second half's MMA warp, 3
 constexpr int kThreads = 896;
-constexpr long long kWait = 4000000000LL;
+constexpr long long kDrain = 4000000000LL;   // clocks that a leaving warp waits for what is in flight, about 2 s
 
 // Two rings in shared memory.  A code box is free as soon as it is converted; delta's boxes are held
 // until their MMAs are done, up to four stages later.  So delta gets the deeper part of the 224 KB:
@@ -78,6 +80,20 @@ struct StageScales {
 };
 constexpr int kScaleBytes = sizeof(StageScales);
 
+// The kernel's static shared memory: 2048 bytes for two halves of BF16 delta, which is all that its rings leave.
+template <int NH, int TERMS>
+struct __align__(16) Shared {
+  using C = Cfg<NH, TERMS>;
+  StageScales scales[C::codes];
+  uint64_t cfull[C::codes], cempty[C::codes];     // codes with their scales: loaded, converted
+  uint64_t bfull[C::deltas], bempty[C::deltas];   // delta: loaded, multiplied
+  uint64_t ready[kGroup];                         // A slot: converted in both CTAs
+  uint64_t dfull[3], dempty[3];                   // accumulators: summed, folded
+  uint64_t drained;                               // every MMA issued is done
+  uint32_t tmem;
+  volatile int failed;
+};
+
 struct Params {
   int T, d_out, d_in, last_group;
   int ng;                      // groups of stages (256 tokens) over all tokens; tokens past T are zeros
@@ -89,6 +105,7 @@ struct Params {
   int ones;                    // the row whose values are 1 (-1: none)
   const uint8_t *one_codes;    // a box of the code of 1
   float *db;                   // where that row's sums go
+  long long budget;            // clocks of a wait
 };
 
 // One work item: an output tile and a range of groups.
@@ -153,6 +170,15 @@ struct Slot {
   __device__ __forceinline__ explicit Slot(uint32_t g) : at(g % N), parity(g / N & 1u) {}
 };
 
+// Wait (bounded) until what a ring of N was filled with in its last uses, of g in all, has arrived.
+template <int N>
+__device__ __forceinline__ void landed(uint64_t *full, uint32_t g) {
+  for (uint32_t r = 1; r <= N && r <= g; ++r) {
+    const Slot<N> s(g - r);
+    if (!tc::mbar_wait_bounded(&full[s.at], s.parity, kDrain)) return;
+  }
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
@@ -161,7 +187,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
-// wait for the programmatic predecessor's results / let the successor launch
 // a float of CTA r's copy of a shared variable
 __device__ __forceinline__ float ld_cluster(const float *p, int r) {
   float v;
@@ -184,6 +209,18 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar) {
       "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
       "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(tc::smem_u32(bar))
       : "memory");
+}
+// whether the barrier's phase is over, without waiting for it
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
   asm volatile(
@@ -278,22 +315,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_weight_grad(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap tm_codes,
                   const __grid_constant__ CUtensorMap tm_delta, int *status) {
   using C = Cfg<NH, TERMS>;
+  static_assert(C::smem + sizeof(Shared<NH, TERMS>) <= 227 * 1024, "a CTA's shared memory");
   constexpr int kCodes = C::codes, kDeltas = C::deltas, kPeriod = C::period;
   extern __shared__ uint8_t dsm[];
   uint8_t *sm = reinterpret_cast<uint8_t *>(((uintptr_t)dsm + 1023) & ~(uintptr_t)1023);
   uint8_t *const sm_delta = sm + kCodes * kBox;
-  // codes (with their scales): loaded, converted; delta: loaded, multiplied; A slot: converted in both
-  // CTAs; accumulators: summed, folded
-  __shared__ uint64_t cfull[kCodes], cempty[kCodes], bfull[kDeltas], bempty[kDeltas], ready[kGroup], dfull[3], dempty[3];
-  __shared__ __align__(16) StageScales scale_sh[kCodes];
-  __shared__ uint32_t tmem_sh;
-  __shared__ volatile int failed;
+  __shared__ Shared<NH, TERMS> sh;
+  auto &cfull = sh.cfull, &cempty = sh.cempty;
+  auto &bfull = sh.bfull, &bempty = sh.bempty;
+  auto &dfull = sh.dfull, &dempty = sh.dempty;
+  uint64_t *const ready = sh.ready;
+  auto &scale_sh = sh.scales;
+  volatile int &failed = sh.failed;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   grid_release();   // k_join_slices
 
-  if (warp == 0) alloc_pair(&tmem_sh);
+  if (warp == 0) alloc_pair(&sh.tmem);
   if (tid == 32) {
     for (int s = 0; s < kCodes; ++s) {
       tc::mbar_init(&cfull[s], 1);
@@ -308,6 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(&dfull[b], 1);
       tc::mbar_init(&dempty[b], 2 * kFoldWarps);
     }
+    tc::mbar_init(&sh.drained, NH);
     tc::fence_mbar_init();
     failed = 0;
   }
@@ -315,21 +355,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();
   tc::fence_after_sync();
-  const uint32_t tmem = tmem_sh;
+  const uint32_t tmem = sh.tmem;
 
+  // called by whole warps: the lanes go on together, or none does
   auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!tc::mbar_try_wait(bar, parity)) {
-      if (failed || clock64() - t0 > kWait) {
-        failed = 1;
-        set_status(status, GIFT_ERR_TIMEOUT);
-        return false;
-      }
+    bool done = mbar_test_wait(bar, parity);
+    if (!done) {
+      const long long t0 = clock64();
+      do {
+        if (failed || clock64() - t0 > P.budget) {
+          failed = 1;
+          set_status(status, GIFT_ERR_TIMEOUT);
+          break;
+        }
+        done = tc::mbar_try_wait(bar, parity);
+      } while (!done);
     }
-    return true;
+    return __all_sync(0xFFFFFFFFu, done) != 0;
   };
-
   // registers: 72 per thread at launch (504 over the seven groups of four warps), redistributed as
   // 2 x 152 + 5 x 40
   if (warp < kDeqWarp) {
@@ -352,7 +395,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int t = w.t0; t < w.t0 + kGroup * kK * w.ng; t += kK, ++g, ++scales) {
             const Slot<kCodes> c(g);
             if (!(ok = wait(&cempty[c.at], c.parity ^ 1u))) break;
-            __syncwarp();
             if (one) {
               tc::mbar_arrive_expect_tx(&cfull[c.at], kBox + kScaleBytes);
               if (ones) bulk_load(sm + c.at * kBox, P.one_codes, kBox, &cfull[c.at]);
@@ -361,13 +403,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+        landed<kCodes>(cfull, g);
       } else {
         for (int it = pair; it < P.items && ok; it += pairs) {
           const Item w(P, it, 128 * NH);
           for (int t = w.t0; t < w.t0 + kGroup * kK * w.ng; t += kK, ++g) {
             const Slot<kDeltas> d(g);
             if (!(ok = wait(&bempty[d.at], d.parity ^ 1u))) break;
-            __syncwarp();
             if (one) {
               uint64_t *bar = &bfull[d.at];
               uint8_t *st = sm_delta + d.at * C::delta_bytes;
@@ -381,13 +423,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // leave no arrival of the MMAs' commits behind: the last stages'
         for (uint32_t r = 1; ok && r <= kDeltas && r <= g; ++r) {
           const Slot<kDeltas> d(g - r);
-          wait(&bempty[d.at], d.parity);
+          ok = wait(&bempty[d.at], d.parity);
         }
-      }
-      if (!ok) {   // leave no copy in flight: whichever parity a barrier is in, one of the two waits is for it
-        for (int s = 0; s < kCodes + kDeltas; ++s)
-          for (uint32_t par = 0; par < 2; ++par)
-            tc::mbar_wait_bounded(s < kCodes ? &cfull[s] : &bfull[s - kCodes], par, kWait / 16);
+        landed<kDeltas>(bfull, g);
+        tc::mbar_wait_bounded(&sh.drained, 0, P.budget + kDrain);   // the pair's first CTA may have a wait of its own to end
       }
     } else if ((warp == kMmaWarp || (NH == 2 && warp == kMmaWarp + 2)) && rank == 0) {
       // ---------------- MMA, a warp per half of the tile: a warp's waits and commits cost about as
@@ -421,7 +460,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const uint32_t db = (kGroup * n + j) % kDeltas;
               const uint32_t b0 = b_first + (db * NH + half) * TERMS * (kBox >> 4);
               if (!wait(&ready[j], n & 1u)) return;
-              __syncwarp();
               tc::fence_after_sync();
               if (one) {
 #pragma unroll
@@ -441,6 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       if (warp == kMmaWarp) walk(std::integral_constant<int, 0>());
       else walk(std::integral_constant<int, 1>());
+      if (one) commit_pair(&sh.drained);
     }
   } else if (warp < kFoldWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
@@ -454,7 +493,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Slot<kCodes> c(g);
       const Slot<kDeltas> d(g);
       if (!wait(&cfull[c.at], c.parity)) break;
-      __syncwarp();
       const StageScales &sc = scale_sh[c.at];
       bool ok = true;
 #pragma unroll
@@ -496,7 +534,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ok = wait(&bfull[d.at], d.parity);
           }
           if (!ok) break;
-          __syncwarp();
           tc::fence_after_sync();
         }
         tmem_st_16x256b_x4(slot + ((uint32_t)(16 * hh) << 16), x);
@@ -529,7 +566,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto fold = [&](int h, float2(&to)[32]) {
         const int b = acc.cur(h);
         if (!(ok = ok && wait(&dfull[b], acc.use(b)))) return;
-        __syncwarp();
         tc::fence_after_sync();
 #pragma unroll
         for (int e = 0; e < 64; e += 16) {
@@ -1184,6 +1220,7 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   P.stages = q.stages;
   P.gamma = join ? nullptr : a.gamma;
   P.out = p.slices > 1 ? a.slices : a.dW;
+  P.budget = L.barrier_wait;
   P.ones = p.ones ? q.groups * kActGroup : -1;
   P.one_codes = q.one_codes;
   P.db = db;

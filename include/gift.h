@@ -159,10 +159,12 @@ typedef enum {
                                   K-FAC product) and multiplies it.  Set it before
                                   gift_workspace_bytes: the two need different workspaces. */
   GIFT_OPT_BARRIER_WAIT = 1,   /* SM clock cycles a CTA of the shared-scale encode waits at its
-                                  grid-wide barrier before it gives up, writes GIFT_ERR_TIMEOUT
-                                  to d_status and stores no codes (default 2e9, about a second;
-                                  0..2e10).  A small value makes the wait run out on purpose: the
-                                  kernel still ends and the context stays usable. */
+                                  grid-wide barrier, and a warp of gift_weight_grad's tensor-core
+                                  kernel at a barrier of its pipeline, before it gives up and writes
+                                  GIFT_ERR_TIMEOUT to d_status (the encode then stores no codes,
+                                  the weight gradient leaves its outputs undefined; default 2e9,
+                                  about a second; 0..2e10).  A small value makes the wait run out
+                                  on purpose: the kernel still ends and the context stays usable. */
   GIFT_OPT_SMS = 3             /* SMs the context's launches size their grids for (default and
                                   maximum: the device's SM count).  With a fraction of the SMs per
                                   context, calls on several streams run side by side on disjoint
