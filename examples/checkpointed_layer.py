@@ -6,8 +6,9 @@ One layer, norm -> linear -> squared error, for R data-parallel replicas modelle
              of the layer's input is kept;
   backward   gift_weight_grad makes the linear layer's weight gradient from the checkpoint (the norm's
              gain and offset folded in), gift_layernorm_backward the norm's own gradients from it;
-  codec      the layer's K-FAC factor from the checkpoint's values, then every replica's weight
-             gradient whitened, packed to E4M3, averaged and mapped back (GIFT's Algorithm 1).
+  codec      the layer's K-FAC factor from replica 0's inputs (the checkpoint's values with the norm's
+             gain and offset), then every replica's weight gradient whitened, packed to E4M3,
+             averaged and mapped back (GIFT's Algorithm 1).
 
     python examples/checkpointed_layer.py [--tokens 4096] [--d-in 1536] [--d-out 384] [--steps 10]
 """
@@ -39,7 +40,7 @@ class NormLinear(torch.autograd.Function):
         c.save_for_backward(codes, scales, rstd, gamma, beta, W)
         c.ctx = ctx
         kept["bytes"] = codes.numel() + scales.numel() + 4 * T
-        kept["checkpoint"] = (codes, scales)
+        kept["checkpoint"], kept["gain"], kept["offset"] = (codes, scales), gamma.detach(), beta.detach()
         return y @ W.to(x.dtype).t()
 
     @staticmethod
@@ -59,15 +60,22 @@ class NormLinear(torch.autograd.Function):
         return dx, dgamma, dbeta, dW, None, None
 
 
-def average_through_codec(ctx, grads, checkpoint, T):
-    """The replicas' weight gradients whitened with the factor of the checkpointed activations, packed to
-    E4M3, averaged and mapped back."""
+def layer_inputs(ctx, kept, T, d_in, status):
+    """What the linear layer read, a = gamma n + beta in BF16, from the checkpoint of the norm's rows n."""
+    n = torch.empty(T, d_in, device=kept["gain"].device)
+    G.gift_act_decode(ctx, *kept["checkpoint"], FMT, n, status=status)
+    return torch.addcmul(kept["offset"], n, kept["gain"]).to(torch.bfloat16)
+
+
+def average_through_codec(ctx, grads, kept, T):
+    """The replicas' weight gradients whitened with the factor of the activations that `kept` stands for (one
+    factor for all of them: a single decode maps the average back), packed to E4M3, averaged and mapped
+    back."""
     d_out, d_in = grads[0].shape
     dev = grads[0].device
     new = lambda n: torch.empty(max(n, 256), dtype=torch.uint8, device=dev)  # noqa: E731
-    acts = torch.empty(T, d_in, dtype=torch.bfloat16, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev)
-    G.gift_act_decode(ctx, *checkpoint, FMT, acts, status=status)
+    acts = layer_inputs(ctx, kept, T, d_in, status)
     fac = G.Factor.empty("lowrank", d_out, d_in, planes=True)
     G.gift_factor_update(ctx, fac, acts, seed=1, status=status,
                          ws=new(G.gift_workspace_bytes(ctx, "factor_update", "lowrank", "e4m3", "tensor", d_out, d_in, T)))
@@ -97,17 +105,17 @@ def train(tokens=4096, d_in=1536, d_out=384, steps=10, replicas=2, lr=0.1, seed=
     with torch.no_grad():   # the goal sees normalised rows
         norm = lambda x: (x.float() - x.float().mean(1, keepdim=True)) / x.float().std(1, keepdim=True)  # noqa: E731
         ys = [norm(x) @ goal.t() for x in xs]
-    losses, error, kept = [], 0.0, {}
+    losses, error, kept = [], 0.0, [{} for _ in range(replicas)]
     for _ in range(steps):
         gW, total = [], 0.0
-        for x, y in zip(xs, ys):
+        for x, y, k in zip(xs, ys, kept):
             W.grad = None
-            out = NormLinear.apply(x, gamma, beta, W, ctx, kept)
+            out = NormLinear.apply(x, gamma, beta, W, ctx, k)
             loss = (out.float() - y).square().mean()
             loss.backward()
             gW.append(W.grad)
             total += loss.item() / replicas
-        avg = average_through_codec(ctx, gW, kept["checkpoint"], tokens)
+        avg = average_through_codec(ctx, gW, kept[0], tokens)
         exact = sum(gW) / replicas
         error = ((avg - exact).norm() / exact.norm()).item()
         with torch.no_grad():
@@ -115,7 +123,7 @@ def train(tokens=4096, d_in=1536, d_out=384, steps=10, replicas=2, lr=0.1, seed=
                 p -= lr * g * (d_out if p is W else 1.0)
         gamma.grad = beta.grad = None
         losses.append(total)
-    return losses, error, kept["bytes"]
+    return losses, error, kept[0]["bytes"]
 
 
 def main():

@@ -514,7 +514,8 @@ gift_status gift_act_encode(gift_ctx *ctx, const void *x, gift_dtype x_dt, int T
 
 /* The values of an 8-bit checkpoint (exact, NaN for a group marked so) into x_out (device, T x d
  * of type out_dt), for callers that take plain activations (gift_factor_update,
- * gift_kfac_factor).  INVALID_ARG as gift_act_encode.  d_status: NONFINITE when a group is marked. */
+ * gift_kfac_factor; a norm's checkpoint gives its rows n, and the linear layer behind it read
+ * gamma n + beta).  INVALID_ARG as gift_act_encode.  d_status: NONFINITE when a group is marked. */
 gift_status gift_act_decode(gift_ctx *ctx, const void *codes, const void *scales, gift_format fmt, int T, int d,
                             void *x_out, gift_dtype out_dt, int *d_status, cudaStream_t stream);
 
