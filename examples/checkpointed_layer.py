@@ -27,7 +27,8 @@ FMT, EPS = "e4m3", 1e-5
 
 
 class NormLinear(torch.autograd.Function):
-    """y = norm(x; gamma, beta) W^T, keeping an 8-bit checkpoint of the norm's rows between the passes."""
+    """y = norm(x; gamma, beta) W^T, keeping an 8-bit checkpoint of the norm's rows between the passes.
+    `kept` gets the checkpoint; its "status" word, where there is one, gets what only the device sees."""
 
     @staticmethod
     def forward(c, x, gamma, beta, W, ctx, kept):
@@ -36,9 +37,10 @@ class NormLinear(torch.autograd.Function):
         cb, sb = G.gift_act_sizes(FMT, T, d)
         codes, scales = torch.empty(cb, dtype=torch.uint8, device=dev), torch.empty(sb, dtype=torch.uint8, device=dev)
         y, rstd = torch.empty_like(x), torch.empty(T, device=dev)
-        G.gift_layernorm_forward(ctx, x, gamma, beta, EPS, y, rstd=rstd, fmt=FMT, codes=codes, scales=scales)
+        G.gift_layernorm_forward(ctx, x, gamma, beta, EPS, y, rstd=rstd, fmt=FMT, codes=codes, scales=scales,
+                                 status=kept.get("status"))
         c.save_for_backward(codes, scales, rstd, gamma, beta, W)
-        c.ctx = ctx
+        c.ctx, c.status = ctx, kept.get("status")
         kept["bytes"] = codes.numel() + scales.numel() + 4 * T
         kept["checkpoint"], kept["gain"], kept["offset"] = (codes, scales), gamma.detach(), beta.detach()
         return y @ W.to(x.dtype).t()
@@ -51,11 +53,12 @@ class NormLinear(torch.autograd.Function):
         d, dev = W.shape[1], delta.device
         new = lambda n: torch.empty(max(n, 1), dtype=torch.uint8, device=dev)  # noqa: E731
         dW = torch.empty_like(W)
-        G.gift_weight_grad(c.ctx, delta, codes, scales, FMT, dW, gamma=gamma, beta=beta,
+        G.gift_weight_grad(c.ctx, delta, codes, scales, FMT, dW, gamma=gamma, beta=beta, status=c.status,
                            ws=new(G.gift_act_workspace_bytes(c.ctx, "weight_grad", delta.dtype, T, d_out, d)))
         dy = delta @ W.to(delta.dtype)
         dx, dgamma, dbeta = torch.empty_like(dy), torch.empty_like(gamma), torch.empty_like(beta)
         G.gift_layernorm_backward(c.ctx, dy, codes, gamma, rstd, dx, dgamma, dbeta, scales=scales, fmt=FMT,
+                                  status=c.status,
                                   ws=new(G.gift_act_workspace_bytes(c.ctx, "layernorm_backward", dy.dtype, T, d, d)))
         return dx, dgamma, dbeta, dW, None, None
 
@@ -74,7 +77,7 @@ def average_through_codec(ctx, grads, kept, T):
     d_out, d_in = grads[0].shape
     dev = grads[0].device
     new = lambda n: torch.empty(max(n, 256), dtype=torch.uint8, device=dev)  # noqa: E731
-    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    status = kept["status"]
     acts = layer_inputs(ctx, kept, T, d_in, status)
     fac = G.Factor.empty("lowrank", d_out, d_in, planes=True)
     G.gift_factor_update(ctx, fac, acts, seed=1, status=status,
@@ -86,8 +89,6 @@ def average_through_codec(ctx, grads, kept, T):
     out = torch.empty(d_out, d_in, device=dev)
     G.gift_reduce_decode(ctx, fac, codes, scales, "e4m3", "tensor", d_out, d_in, out, status=status,
                          ws=new(G.gift_workspace_bytes(ctx, "reduce_decode", "lowrank", "e4m3", "tensor", d_out, d_in)))
-    if int(status.item()):
-        raise G.GiftError(int(status.item()), "average_through_codec")
     return out
 
 
@@ -105,7 +106,8 @@ def train(tokens=4096, d_in=1536, d_out=384, steps=10, replicas=2, lr=0.1, seed=
     with torch.no_grad():   # the goal sees normalised rows
         norm = lambda x: (x.float() - x.float().mean(1, keepdim=True)) / x.float().std(1, keepdim=True)  # noqa: E731
         ys = [norm(x) @ goal.t() for x in xs]
-    losses, error, kept = [], 0.0, [{} for _ in range(replicas)]
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    losses, error, kept = [], 0.0, [{"status": status} for _ in range(replicas)]
     for _ in range(steps):
         gW, total = [], 0.0
         for x, y, k in zip(xs, ys, kept):
@@ -116,6 +118,8 @@ def train(tokens=4096, d_in=1536, d_out=384, steps=10, replicas=2, lr=0.1, seed=
             gW.append(W.grad)
             total += loss.item() / replicas
         avg = average_through_codec(ctx, gW, kept[0], tokens)
+        if int(status.item()):   # of the passes as well as the codec
+            raise G.GiftError(int(status.item()), "a training step")
         exact = sum(gW) / replicas
         error = ((avg - exact).norm() / exact.norm()).item()
         with torch.no_grad():
