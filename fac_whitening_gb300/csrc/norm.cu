@@ -611,11 +611,19 @@ cudaError_t forward_t(const Launch &L, int fmt, const NormForward &a, const RowP
   return cudaGetLastError();
 }
 
+// The CTA sizes that forward_plan gives: one piece, 8 warps at most with wide accesses and up to 16 with
+// element ones; two pieces, 8 warps for 5 to 16 pieces (wide) and 9 to 16 warps above; four pieces, 9 to 16.
 template <typename E, bool VEC, int U>
 cudaError_t forward(const Launch &L, int fmt, const NormForward &a, const RowPlan &p) {
-  if constexpr (U < 4)
-    if (p.threads <= 256) return forward_t<E, VEC, U, 256>(L, fmt, a, p);
-  return U == 1 && p.threads <= 384 ? forward_t<E, VEC, U, 384>(L, fmt, a, p) : forward_t<E, VEC, U, 512>(L, fmt, a, p);
+  if constexpr (VEC && U == 1) {
+    return forward_t<E, VEC, U, 256>(L, fmt, a, p);
+  } else {
+    if constexpr (U == 1 || (VEC && U == 2))
+      if (p.threads <= 256) return forward_t<E, VEC, U, 256>(L, fmt, a, p);
+    if constexpr (U == 1)
+      if (p.threads <= 384) return forward_t<E, VEC, U, 384>(L, fmt, a, p);
+    return forward_t<E, VEC, U, 512>(L, fmt, a, p);
+  }
 }
 
 template <typename E, bool VEC>
@@ -670,14 +678,17 @@ cudaError_t backward_t(const Launch &L, int fmt, const NormBackward &a, const Ro
   return a.part ? sums_after(L, a, grid) : cudaSuccess;
 }
 
+// The CTA sizes that backward_plan gives: 8 columns per lane for element accesses up to 4096 columns; 16
+// elsewhere, in 9 to 16 warps but for wide accesses to up to 8 pieces.
 template <typename E, bool VEC, bool SAVED, int U>
 cudaError_t backward(const Launch &L, int fmt, const NormBackward &a, const RowPlan &p) {
-  constexpr int kC8 = U == 1 && !VEC ? 8 : 16;
-  if (p.c == 8)
-    return p.threads <= 256 ? backward_t<E, VEC, SAVED, U, kC8, 256>(L, fmt, a, p)
-                            : backward_t<E, VEC, SAVED, U, kC8, 512>(L, fmt, a, p);
-  return p.threads <= 256 ? backward_t<E, VEC, SAVED, U, 16, 256>(L, fmt, a, p)
-                          : backward_t<E, VEC, SAVED, U, 16, 512>(L, fmt, a, p);
+  if constexpr (U == 1) {
+    constexpr int kSmall = VEC ? 16 : 8;   // columns per lane of the CTAs of 256 threads
+    if (p.threads <= 256) return backward_t<E, VEC, SAVED, U, kSmall, 256>(L, fmt, a, p);
+    if constexpr (!VEC)
+      if (p.c == 8) return backward_t<E, VEC, SAVED, U, 8, 512>(L, fmt, a, p);
+  }
+  return backward_t<E, VEC, SAVED, U, 16, 512>(L, fmt, a, p);
 }
 
 template <typename E, bool VEC, bool SAVED>
