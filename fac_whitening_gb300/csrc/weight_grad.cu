@@ -210,18 +210,6 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar) {
       "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(tc::smem_u32(bar))
       : "memory");
 }
-// whether the barrier's phase is over, without waiting for it
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(tc::smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
@@ -357,9 +345,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem;
 
-  // called by whole warps: the lanes go on together, or none does
+  // Called by whole warps: the lanes go on together, or none does.  A try waits up to 4 us itself (to look first
+  // and try then cost the 16384 x 1536 x 6144 product 1.5 %).
   auto wait = [&](uint64_t *bar, uint32_t parity) {
-    bool done = mbar_test_wait(bar, parity);
+    bool done = tc::mbar_try_wait(bar, parity);
     if (!done) {
       const long long t0 = clock64();
       do {
