@@ -7,16 +7,19 @@
 //
 // Forward: the mean and the squared deviations from it, reduced from registers; y and the checkpoint are
 // written from them.  32768 x 4096 BF16: 91 us, 5.9 TB/s; with the checkpoint 111 us, 6.0 TB/s: HBM, at
-// 0.87 of the copy rate; 16384 x 1536 with the checkpoint 26.8 us, 4.7 TB/s.
+// 0.87 of the copy rate; 16384 x 1536 with the checkpoint 26.8 us, 4.7 TB/s; 16384 x 4096 FP32 97 us, 5.5
+// TB/s, with the checkpoint 108 us, 5.6 TB/s.  Element accesses: 4099 x 7001 BF16 72 us, 1.6 TB/s.
 //
 // Backward: sums over a row (h and h n) for dx, and sums over tokens (dy n and dy) for the gain's and
 // offset's gradients.  The latter stay in the registers of the thread that owns the column: a CTA
 // takes every gridDim-th row, adds its row groups' sums through shared memory at the end and writes
-// one partial; k_norm_sums adds the partials.  The order is fixed by the shape and the grid.  32768 x
-// 4096 BF16: 160 to 171 us, 4.7 to 5.0 TB/s; 16384 x 1536 from the checkpoint 34 us, 3.7 TB/s: the
-// registers of the column sums leave 15 or 16 warps per SM, which do not hide a row's two reductions and
-// its barrier altogether (a third of the issue slots are used).  Rings of asynchronous copies in
-// shared memory and batches of two to four rows per reduction were measured and were no faster.
+// one partial; k_norm_sums adds the partials.  The order is fixed by the shape, the accesses (rows_vec)
+// and the grid.  32768 x 4096 BF16: 171 us, 4.7 TB/s (dx alone, same kernel: 158); 16384 x 1536 from
+// the checkpoint 34 us, 3.7 TB/s.  One row ahead in registers, 12 to 16 warps per SM up to 4096 columns:
+// at most 32 KB in flight, which wait at each row's barrier; a third of the issue slots are used.  From
+// 4097 columns a CTA is one row and the registers hold one CTA per SM, 9 to 16 warps: 32768 x 4608 BF16
+// 261 us (3.5 TB/s), 5120 273, 6144 297, 16384 x 8192 181 (4.5 TB/s).  Rings of per-thread asynchronous
+// copies in shared memory and batches of two to four rows per reduction were measured and were no faster.
 #include "act.cuh"
 #include "kernels.cuh"
 
@@ -118,7 +121,8 @@ __device__ __forceinline__ bool norm_row_ok(float mean, float var, float rstd) {
 // mean is squared and the row group meets at one barrier only.  U = 1 holds gain and offset in
 // registers, U = 2 and 3 in shared memory where no bank conflicts (8192 x 16384 BF16: 97 us, 179 with
 // loads from L1 and L2, whose lines 32 lanes' 64 bytes each cross); both load the next row before they
-// wait for the sums of this one (231 us without either).  U = 4 has room for neither.
+// wait for the sums of this one (231 us without either).  U = 4 has room for neither.  The 80 registers of
+// U = 1 (three CTAs per SM) spill 12 to 52 bytes.
 template <typename E, bool VEC, int U, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? (U == 1 ? 3 : 2) : MAXT == 384 ? 2 : 1)
     k_norm_forward(const __grid_constant__ NormForward a, int nw, int fmt, int *status) {
@@ -251,11 +255,13 @@ __device__ __forceinline__ void write_cols(float *out, int n, int lane, const fl
 }
 
 // U = 1 (up to 8192 columns): dx and the column sums.  The two sums, the gain and two rows take eight
-// registers a column, so 16 warps per SM with C = 16 columns per lane, 24 with C = 8.  With 32-byte
-// accesses C = 16 is faster (32768 x 4096 BF16: 160-173 us against 203; 16384 x 1536 from the
-// checkpoint 38 against 41), with element accesses C = 8 (5003 x 1361 FP32 from the checkpoint: 29 us
-// against 37; 30324 x 20: 16 against 22).
+// registers a column, so at most 16 warps per SM with C = 16 columns per lane (120 to 128 registers), 24
+// with C = 8 up to 2048 columns (80); from 2049 to 4096 C = 8 takes 97 to 103 in CTAs of one row, 9 to 16
+// warps per SM.  With 32-byte accesses C = 16 is faster (32768 x 4096 BF16: 171 us against 203; 16384
+// x 1536 from the checkpoint 38 against 41), with element accesses C = 8 (5003 x 1361 FP32 from the
+// checkpoint: 29 us against 37; 30324 x 20: 16 against 22).
 // U > 1 (longer rows): dx alone, the column sums take a pass of their own (k_norm_cols).
+// Spilled (bytes stored): FP32 with wide accesses 16, elements 8 to 96; U = 2 up to 40, U = 4 190 to 310.
 template <typename E, bool VEC, bool SAVED, int U, int C, int MAXT>
 __global__ void __launch_bounds__(MAXT, U > 1 || MAXT == 512 ? 1 : C == 16 ? 2 : 3)
     k_norm_backward(const __grid_constant__ NormBackward a, int nw, int fmt, int *status) {
@@ -362,8 +368,8 @@ __global__ void __launch_bounds__(MAXT, U > 1 || MAXT == 512 ? 1 : C == 16 ? 2 :
 }
 
 // The column sums alone: a warp takes one piece of the columns over a slice of consecutive tokens;
-// part[2 slice] = sum dy n, part[2 slice + 1] = sum dy.  It reads dy and x a second time, HBM-bound: 8192 x
-// 16384 BF16 take 199 us for dx and 124 us here (4.3 TB/s).
+// part[2 slice] = sum dy n, part[2 slice + 1] = sum dy.  It reads dy and x a second time: 8192 x 16384 BF16
+// take 200 us for dx (4.0 TB/s; no row is loaded ahead) and 124 us here (4.3 TB/s), 324 of a floor of 119.
 template <typename E, bool VEC, bool SAVED>
 __global__ void __launch_bounds__(kNormThreads) k_norm_cols(const __grid_constant__ NormBackward a, int fmt, int rows) {
   const int lane = threadIdx.x & 31, d = a.d, groups = (d + kActGroup - 1) / kActGroup;
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(1024) k_norm_sums(const float *__restrict__ pa
 
 // ---- rows too long for registers: column by column, the row read once per sum --------------------------
 // (above 32768 columns.)  A row is read three times forward and twice backward, L2 serves the repeats:
-// 4096 x 40960 BF16 285 us forward, 855 us backward with both sums over tokens.
+// 4096 x 40960 BF16 287 us forward, 863 us backward with both sums over tokens, 1046 from the checkpoint.
 __device__ __forceinline__ float cta_sum(float v, float *sh /* kNormThreads / 32 */) {
   v = warp_sum(v);
   __syncthreads();
@@ -580,8 +586,10 @@ bool backward_plan(int d, bool vec, RowPlan *p) {
 // Forward: with 32-byte accesses two pieces per lane where that leaves at most a sixth of the lanes idle (fewer
 // warps to a row, twice the loads of a lane in flight: 32768 x 4096 BF16 91 us against 101, 111 against
 // 131 with the checkpoint; 8192 x 8192 52 against 62), and a whole row of three pieces in one BF16 warp,
-// which needs no barrier (16384 x 1536: 20.3 against 22.8, 26.8 against 28.9; FP32 would not fit the
-// registers).  With element accesses one piece was faster (4099 x 7001 BF16 72 us against 87).
+// which needs no barrier (16384 x 1536: 20.3 against 22.8, 26.8 against 28.9; also where the third piece is
+// mostly empty, 32768 rows of 1040 columns 35.5 against 41.6, 45.7 against 51.8, of 1280 35.5 against
+// 41.6, 45.7 against 53.9; FP32 would not fit the registers).  With element accesses one piece was faster
+// (4099 x 7001 BF16 72 us against 87).
 bool forward_plan(int d, bool vec, bool bf16, RowPlan *p) {
   if (!row_plan(d, p)) return false;
   const int pieces = (d + kPiece - 1) / kPiece;

@@ -25,10 +25,14 @@
 // N = 256).  One CTA alone would need 80 bytes of operands per clock from L2, a pair needs 48 per SM.
 // The conversion costs the SM's integer pipes about 250 clocks a stage, and every warp's waits and
 // issues around it are latency: the numbers of warps, the two rings and the two MMA warps come from
-// there.  16384 x 1536 x 6144 (tokens x d_out x d_in): 180 us for this kernel, 1.72 PFLOP/s; 65536
-// tokens 707 us, 1.75 PFLOP/s; 32768 x 4096 x 16384 run over and over (power cap) 3.0 ms, 1.46
-// PFLOP/s.  Converting in a pass of its own would move 300 MB more for the first of these, 45 us at the
-// copy rate.
+// there.  16384 x 1536 x 6144 (tokens x d_out x d_in): 185 us for this kernel with cold caches, 1.67
+// PFLOP/s (a call 193 us alone, 212 to 219 in passes one after the other); 65536 tokens 712 to 724 us a
+// call, 1.72 PFLOP/s; 32768 x 4096 x 16384 run over and over (power cap) 3.0 to 3.1 ms, 1.42 to 1.46
+// PFLOP/s; FP32 delta 16384 x 1536 x 6144 with db 522 us a call, 0.94 of its threefold products at the
+// measured rate.  Converting in a pass of its own would move 300 MB more for the first of these, 45 us
+// at the copy rate.
+// The 72 registers of a launch spill 52 bytes stored and 116 loaded for BF16, 144 and 148 for FP32 delta
+// (two halves).
 // Every mbarrier wait is bounded by the context's GIFT_OPT_BARRIER_WAIT and reports GIFT_ERR_TIMEOUT.  A
 // warp leaves as one, and however its loop ended, the copies it issued and the MMAs on the CTA's
 // memory are waited for before the CTA leaves.
@@ -1045,10 +1049,11 @@ Plan plan_of(int sms, int T, int d_out, int d_in, bool ones) {
 }
 
 // With db: from the group of ones, which is free where the last tile has room for it (5003 x 1021 x 2731
-// BF16: 42 us with db and without; by a pass over delta 49) or there is an idle pair of SMs in the last
-// wave (16384 x 1536 x 6144: 209 and 213 us), or by the pass over delta, about 5 MB in the time of a
-// group and 4 groups for its second kernel, where the tiles of ones would take a wave more (16384 x
-// 6144 x 1536: 278 us with them, 236 by the pass).
+// BF16: 54 us, by a pass over delta 63) or there is an idle pair of SMs in the last wave (16384 x 1536 x
+// 6144: 194 us, 193 without db, 204 by the pass; FP32 521 and 534), or by the pass over delta, about 5
+// MB in the time of a group and 4 groups for its second kernel, where the tiles of ones would take a
+// wave more (16384 x 6144 x 1536: 271 us with them, 234 by the pass, 192 without db).  Single calls,
+// caches flushed between them.
 Plan plan_for(int sms, bool bf16, int T, int d_out, int d_in, bool need_db) {
   const Plan p = plan_of(sms, T, d_out, d_in, false);
   if (!need_db) return p;

@@ -34,8 +34,12 @@
  *              the first error wins, the library never clears the word.  Pass
  *              d_status = NULL to ignore them.  Outputs are undefined when the word
  *              is non-zero.
- *   Alignment  Any alignment works; 16-byte aligned buffers with d_in a multiple of
- *              4 (FP32) or 16 (codes) take the vectorised paths.
+ *   Alignment  Any alignment works (to the element).  The codec's calls take their
+ *              vectorised paths for 16-byte aligned buffers with d_in a multiple of 4 (FP32)
+ *              or 16 (codes).  The checkpoint and norm calls take theirs for rows of a
+ *              multiple of 16 elements (of either type) in 32-byte aligned buffers, with
+ *              16-byte aligned codes, gain and offset; gift_weight_grad reads BF16 delta and
+ *              codes in place where their rows and pointers are 16-byte aligned, copies else.
  *   Aliasing   Outputs must not alias inputs unless a parameter says otherwise.
  */
 #ifndef GIFT_H_
@@ -164,7 +168,8 @@ typedef enum {
                                   GIFT_ERR_TIMEOUT to d_status (the encode then stores no codes,
                                   the weight gradient leaves its outputs undefined; default 2e9,
                                   about a second; 0..2e10).  A small value makes the wait run out
-                                  on purpose: the kernel still ends and the context stays usable. */
+                                  on purpose (the weight gradient's after a few microseconds): the
+                                  kernel still ends and the context stays usable. */
   GIFT_OPT_SMS = 3             /* SMs the context's launches size their grids for (default and
                                   maximum: the device's SM count).  With a fraction of the SMs per
                                   context, calls on several streams run side by side on disjoint
@@ -492,7 +497,9 @@ gift_status gift_encode_lowrank_noalloc(gift_ctx *ctx, const gift_factor *f, con
  *   code   : x 2^-k rounded to nearest even, saturating; the value it stands for is code 2^k.
  * The scale is a power of two, so no element loses mantissa bits to it and every value is exact
  * in BF16 (the tensor cores multiply it as it is) and in FP32.  A group that holds NaN or Inf has
- * the scale byte 255 and stands for NaN.
+ * the scale byte 255 and stands for NaN.  Bytes that gift_act_encode never writes (codes 0x7F and
+ * 0xFF of E4M3, 0x7C to 0x7F and 0xFC to 0xFF of E5M2 in a group not marked; other scale bytes) have
+ * no value: the calls that read a checkpoint need not agree on one.
  * In all of them T, d, d_out and d_in are at most 2^30 (INVALID_ARG above); their products may
  * pass 2^32. */
 
@@ -547,7 +554,7 @@ gift_status gift_layernorm_forward(gift_ctx *ctx, const void *x, gift_dtype dt, 
  *  rstd   : device, T FP32, the forward pass's.
  *  gamma  : device, d FP32, nullable (1).
  *  dgamma, dbeta : device, d FP32, each nullable.  Sums over tokens are FP32, in an order fixed
- *           by the shape and the context: equal calls give equal bits.
+ *           by the shape, the buffers' alignment and the context: equal calls give equal bits.
  *  ws     : gift_act_workspace_bytes(GIFT_OP_LAYERNORM_BACKWARD, dt, T, d, d) bytes (may be NULL
  *           when dgamma and dbeta both are).
  * INVALID_ARG: a null dy, saved, rstd or dx, a missing mean or scales, T or d < 1, a bad type or
@@ -564,7 +571,7 @@ gift_status gift_layernorm_backward(gift_ctx *ctx, const void *dy, gift_dtype dt
  * Products are exact (an FP32 delta enters as three BF16 terms; below 2^-110 it may lose up to
  * 2^-134); sums are FP32, rounded to nearest at least every 256 tokens, in an order fixed by the
  * shape and the context.  An infinity or NaN in delta reaches its own row of dW and entry of db
- * as the formula has it, a marked group (NaN) its own columns.
+ * as the formula has it, a marked group (NaN) its own columns; neither is reported (d_status).
  *  delta  : device, T x d_out of type delta_dt.
  *  codes, scales : the checkpoint (T x d_in, format fmt).
  *  gamma, beta   : device, d_in FP32, each nullable (1 and 0).
