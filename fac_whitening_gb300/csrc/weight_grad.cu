@@ -366,6 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     return __all_sync(0xFFFFFFFFu, done) != 0;
   };
+
   // registers: 72 per thread at launch (504 over the seven groups of four warps), redistributed as
   // 2 x 152 + 5 x 40
   if (warp < kDeqWarp) {
@@ -419,7 +420,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = wait(&bempty[d.at], d.parity);
         }
         landed<kDeltas>(bfull, g);
-        tc::mbar_wait_bounded(&sh.drained, 0, P.budget + kDrain);   // the pair's first CTA may have a wait of its own to end
+        // the pair's first CTA may have a wait of its own to end before its last commit
+        tc::mbar_wait_bounded(&sh.drained, 0, P.budget + kDrain);
       }
     } else if ((warp == kMmaWarp || (NH == 2 && warp == kMmaWarp + 2)) && rank == 0) {
       // ---------------- MMA, a warp per half of the tile: a warp's waits and commits cost about as
