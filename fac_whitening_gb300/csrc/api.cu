@@ -1316,6 +1316,7 @@ struct ActWs {
   float *slices = nullptr;  // sums of token slices
   uint8_t *delta = nullptr, *codes = nullptr;   // operands with aligned rows
   uint8_t *scales = nullptr;                    // scales by group
+  uint8_t *operands = nullptr;                  // products: operands with aligned rows
   size_t bytes = 0;
 };
 
@@ -1324,6 +1325,16 @@ ActWs act_layout(void *base, const gift_ctx *ctx, gift_op op, gift_dtype dt, int
   Carve c(base ? reinterpret_cast<void *>(((uintptr_t)base + kAlign - 1) / kAlign * kAlign) : nullptr);
   if (op == GIFT_OP_LAYERNORM_BACKWARD) {
     w.part = c.take<float>(norm_part_floats(ctx->sms, T, d_in));
+  } else if (op == GIFT_OP_DROPOUT_BACKWARD) {
+    w.part = c.take<float>(dropout_part_floats(ctx->sms, T, d_in));
+  } else if (op != GIFT_OP_WEIGHT_GRAD) {
+    const bool bf16 = dt == GIFT_DT_BF16;
+    const MlpWs m = op == GIFT_OP_GATED_FORWARD    ? gated_forward_layout(bf16, T, d_out, d_in)
+                    : op == GIFT_OP_GATED_BACKWARD ? gated_backward_layout(bf16, T, d_out, d_in)
+                    : op == GIFT_OP_LINEAR_FORWARD ? linear_forward_layout(ctx->sms, bf16, T, d_out, d_in)
+                                                   : input_grad_layout(ctx->sms, bf16, T, d_out, d_in);
+    w.operands = c.take<uint8_t>(m.operand_bytes);
+    w.slices = c.take<float>(m.part_floats);
   } else {
     const WeightGradWs g = weight_grad_layout(ctx->sms, dt == GIFT_DT_BF16, T, d_out, d_in);
     w.part = c.take<float>(g.part_floats);
@@ -1349,7 +1360,9 @@ gift_status gift_act_sizes(gift_format fmt, int T, int d, size_t *code_bytes, si
 
 size_t gift_act_workspace_bytes(const gift_ctx *ctx, gift_op op, gift_dtype dt, int T, int d_out, int d_in) {
   if (!ctx || !valid_dt(dt) || !valid_extent(T) || !valid_extent(d_in)) return (size_t)-1;
-  if (op != GIFT_OP_LAYERNORM_BACKWARD && (op != GIFT_OP_WEIGHT_GRAD || !valid_extent(d_out))) return (size_t)-1;
+  if (op < GIFT_OP_LAYERNORM_BACKWARD || op > GIFT_OP_DROPOUT_BACKWARD) return (size_t)-1;
+  const bool rows_only = op == GIFT_OP_LAYERNORM_BACKWARD || op == GIFT_OP_DROPOUT_BACKWARD;
+  if (!rows_only && !valid_extent(d_out)) return (size_t)-1;
   return act_layout(nullptr, ctx, op, dt, T, d_out, d_in).bytes;
 }
 
@@ -1451,6 +1464,169 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
   a.code_ws = w.codes;
   a.scale_ws = w.scales;
   CK(launch_weight_grad(mk(ctx, d_status, stream), fmt8(fmt), delta_dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
+// -----------------------------------------------------------------------------------------
+// the feed-forward block: gated products, linear layer with dropout, input gradient, dropout
+// -----------------------------------------------------------------------------------------
+namespace {
+
+bool valid_gate(gift_gate g) { return g == GIFT_GATE_SILU || g == GIFT_GATE_GELU || g == GIFT_GATE_GELU_TANH; }
+
+// Whether an output of T x N has a countable number of tiles (256 x 128 at the least).
+bool valid_tiles(int T, int N) {
+  return ((long long)T + 255) / 256 * (((long long)N + 127) / 128) <= 0x7FFFFFFFll;
+}
+
+// P = round(65536 p), the share of 16-bit numbers that drop an element; false: p is not a probability below 1 that
+// leaves one.
+bool drop_below(float p, const unsigned long long *rng, uint32_t *below) {
+  if (!(p >= 0.0f) || !(p < 1.0f)) return false;
+  *below = (uint32_t)(65536.0 * (double)p + 0.5);
+  return *below < 65536u && (!*below || rng);
+}
+
+}  // namespace
+
+gift_status gift_gated_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d, const void *Wg,
+                               const void *Wu, int f, const float *bg, const float *bu, gift_gate fn, void *h,
+                               void *gate, void *up, gift_format fmt, void *codes, void *scales, void *ws,
+                               size_t ws_bytes, int *d_status, cudaStream_t stream) {
+  if (!ctx || !x || !Wg || !Wu || !h || !ws || !valid_extent(T) || !valid_extent(d) || !valid_extent(f) ||
+      !valid_tiles(T, f) || !valid_dt(dt) || !valid_gate(fn))
+    return GIFT_ERR_INVALID_ARG;
+  if (!gate != !up || !codes != !scales || (codes && !valid_act_fmt(fmt))) return GIFT_ERR_INVALID_ARG;
+  if (ws_bytes < act_layout(nullptr, ctx, GIFT_OP_GATED_FORWARD, dt, T, f, d).bytes) return GIFT_ERR_INVALID_ARG;
+  GatedForward a{};
+  a.x = x;
+  a.Wg = Wg;
+  a.Wu = Wu;
+  a.T = T;
+  a.d = d;
+  a.f = f;
+  a.fn = (int)fn;
+  a.fmt = fmt8(fmt);
+  a.bg = bg;
+  a.bu = bu;
+  a.h = h;
+  a.gate = gate;
+  a.up = up;
+  a.codes = static_cast<uint8_t *>(codes);
+  a.scales = static_cast<uint8_t *>(scales);
+  a.ws = act_layout(ws, ctx, GIFT_OP_GATED_FORWARD, dt, T, f, d).operands;
+  CK(launch_gated_forward(mk(ctx, d_status, stream), dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
+gift_status gift_gated_backward(gift_ctx *ctx, const void *dy, gift_dtype dt, int T, int d_out, const void *W, int f,
+                                const void *gate, const void *up, gift_gate fn, void *dgate, void *dup, void *ws,
+                                size_t ws_bytes, int *d_status, cudaStream_t stream) {
+  if (!ctx || !dy || !W || !gate || !up || !dgate || !dup || !ws || !valid_extent(T) || !valid_extent(d_out) ||
+      !valid_extent(f) || !valid_tiles(T, f) || !valid_dt(dt) || !valid_gate(fn))
+    return GIFT_ERR_INVALID_ARG;
+  if (ws_bytes < act_layout(nullptr, ctx, GIFT_OP_GATED_BACKWARD, dt, T, d_out, f).bytes) return GIFT_ERR_INVALID_ARG;
+  GatedBackward a{};
+  a.dy = dy;
+  a.W = W;
+  a.T = T;
+  a.d_out = d_out;
+  a.f = f;
+  a.fn = (int)fn;
+  a.gate = gate;
+  a.up = up;
+  a.dgate = dgate;
+  a.dup = dup;
+  a.ws = act_layout(ws, ctx, GIFT_OP_GATED_BACKWARD, dt, T, d_out, f).operands;
+  CK(launch_gated_backward(mk(ctx, d_status, stream), dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
+gift_status gift_linear_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d_in, const void *W, int d_out,
+                                const float *bias, const void *residual, float p, const unsigned long long *rng,
+                                unsigned int site, void *y, void *ws, size_t ws_bytes, int *d_status,
+                                cudaStream_t stream) {
+  LinearForward a{};
+  if (!ctx || !x || !W || !y || !ws || !valid_extent(T) || !valid_extent(d_in) || !valid_extent(d_out) ||
+      !valid_tiles(T, d_out) || !valid_dt(dt) || !drop_below(p, rng, &a.below))
+    return GIFT_ERR_INVALID_ARG;
+  if (ws_bytes < act_layout(nullptr, ctx, GIFT_OP_LINEAR_FORWARD, dt, T, d_out, d_in).bytes)
+    return GIFT_ERR_INVALID_ARG;
+  const ActWs w = act_layout(ws, ctx, GIFT_OP_LINEAR_FORWARD, dt, T, d_out, d_in);
+  a.x = x;
+  a.W = W;
+  a.T = T;
+  a.d_out = d_out;
+  a.d_in = d_in;
+  a.bias = bias;
+  a.residual = residual;
+  a.rng = rng;
+  a.site = site;
+  a.y = y;
+  a.ws = w.operands;
+  a.part = w.slices;
+  CK(launch_linear_forward(mk(ctx, d_status, stream), dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
+gift_status gift_input_grad(gift_ctx *ctx, const void *delta, const void *W, const void *delta2, const void *W2,
+                            gift_dtype dt, int T, int d_out, int d_in, void *dx, void *ws, size_t ws_bytes,
+                            int *d_status, cudaStream_t stream) {
+  if (!ctx || !delta || !W || !delta2 != !W2 || !dx || !ws || !valid_extent(T) || !valid_extent(d_out) ||
+      !valid_extent(d_in) || !valid_tiles(T, d_in) || !valid_dt(dt))
+    return GIFT_ERR_INVALID_ARG;
+  if (ws_bytes < act_layout(nullptr, ctx, GIFT_OP_INPUT_GRAD, dt, T, d_out, d_in).bytes) return GIFT_ERR_INVALID_ARG;
+  const ActWs w = act_layout(ws, ctx, GIFT_OP_INPUT_GRAD, dt, T, d_out, d_in);
+  InputGrad a{};
+  a.delta = delta;
+  a.W = W;
+  a.delta2 = delta2;
+  a.W2 = W2;
+  a.T = T;
+  a.d_out = d_out;
+  a.d_in = d_in;
+  a.dx = dx;
+  a.ws = w.operands;
+  a.part = w.slices;
+  CK(launch_input_grad(mk(ctx, d_status, stream), dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
+gift_status gift_dropout_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d, const float *bias,
+                                 const void *residual, float p, const unsigned long long *rng, unsigned int site,
+                                 void *y, cudaStream_t stream) {
+  DropoutCall a{};
+  if (!ctx || !x || !y || !valid_extent(T) || !valid_extent(d) || !valid_dt(dt) || !drop_below(p, rng, &a.below))
+    return GIFT_ERR_INVALID_ARG;
+  a.x = x;
+  a.residual = residual;
+  a.bias = bias;
+  a.T = T;
+  a.d = d;
+  a.rng = rng;
+  a.site = site;
+  a.y = y;
+  CK(launch_dropout_forward(mk(ctx, nullptr, stream), dt == GIFT_DT_BF16, a));
+  return GIFT_OK;
+}
+
+gift_status gift_dropout_backward(gift_ctx *ctx, const void *dy, gift_dtype dt, int T, int d, float p,
+                                  const unsigned long long *rng, unsigned int site, void *dx, float *dbias, void *ws,
+                                  size_t ws_bytes, cudaStream_t stream) {
+  DropoutCall a{};
+  if (!ctx || !dy || !dx || !valid_extent(T) || !valid_extent(d) || !valid_dt(dt) || !drop_below(p, rng, &a.below))
+    return GIFT_ERR_INVALID_ARG;
+  if (dbias && (!ws || ws_bytes < act_layout(nullptr, ctx, GIFT_OP_DROPOUT_BACKWARD, dt, T, d, d).bytes))
+    return GIFT_ERR_INVALID_ARG;
+  a.x = dy;
+  a.T = T;
+  a.d = d;
+  a.rng = rng;
+  a.site = site;
+  a.y = dx;
+  a.dbias = dbias;
+  a.part = dbias ? act_layout(ws, ctx, GIFT_OP_DROPOUT_BACKWARD, dt, T, d, d).part : nullptr;
+  CK(launch_dropout_backward(mk(ctx, nullptr, stream), dt == GIFT_DT_BF16, a));
   return GIFT_OK;
 }
 

@@ -1,0 +1,138 @@
+// Dropout by itself: y = residual + drop(x + bias), and its backward pass dx = drop(dy), dbias = sum_t dx.
+//
+// HBM bounds it.  A warp keeps one piece of 512 columns (16 a lane, so that a lane draws two counters for its own
+// columns) and walks down the rows of its CTA's slice; the bits are drawn where they are used.
+#include "act.cuh"
+#include "dropout.cuh"
+#include "kernels.cuh"
+
+namespace gift {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+// The lane's 16 bits as its registers hold the columns: VEC bit e is column 16 lane + e; otherwise column
+// 32 e + lane, whose bit lane (32 e + lane) / 16 drew.
+template <bool VEC>
+__device__ __forceinline__ uint32_t keep16(const Draw &d, uint32_t row, uint32_t c0, int lane) {
+  const uint32_t g = c0 / 8 + 2 * lane;
+  const uint32_t m = d.keep8(row, g) | d.keep8(row, g + 1) << 8;
+  if (VEC) return m;
+  uint32_t k = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) k |= (__shfl_sync(0xFFFFFFFFu, m, 2 * e + (lane >> 4)) >> (lane & 15) & 1u) << e;
+  return k;
+}
+
+struct Args {
+  const void *x, *residual;   // residual nullable
+  const float *bias;          // nullable
+  void *y;
+  int T, d, rows;             // rows of a slice
+  Dropout drop;
+  float *part;                // nullable: [slices][d] sums of y over the slice's rows
+};
+
+template <typename E, bool VEC, bool SUMS>
+__global__ void __launch_bounds__(kThreads) k_dropout(const Args a) {
+  __shared__ float sh[SUMS ? kWarps : 1][SUMS ? 16 * 33 : 1];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * kPiece, n = a.d - c0;
+  const int t0 = blockIdx.y * a.rows, t1 = min(a.T, t0 + a.rows);
+  const Draw draw(a.drop);
+  float2 bias[8], sum[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    bias[k] = sum[k] = both(0.0f);
+    if (!SUMS && a.bias) {
+      const int c = piece_col<VEC>(lane, 2 * k), c1 = piece_col<VEC>(lane, 2 * k + 1);
+      bias[k] = make_float2(c < n ? a.bias[c0 + c] : 0.0f, c1 < n ? a.bias[c0 + c1] : 0.0f);
+    }
+  }
+  const E *x = static_cast<const E *>(a.x) + c0, *res = static_cast<const E *>(a.residual);
+#pragma unroll 2
+  for (int t = t0 + w; t < t1; t += kWarps) {
+    const size_t at = (size_t)t * a.d;
+    Raw<E> r, q;
+    load_piece<VEC>(x + at, n, lane, r);
+    if (!SUMS && res) load_piece<VEC>(res + c0 + at, n, lane, q);
+    const uint32_t keep = draw.below ? keep16<VEC>(draw, t, c0, lane) : 0xFFFFu;
+    float2 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      v[k] = SUMS ? r.pair(k) : add2(r.pair(k), bias[k]);
+      if (draw.below) {
+        v[k].x = keep >> (2 * k) & 1u ? v[k].x * draw.scale : 0.0f;
+        v[k].y = keep >> (2 * k + 1) & 1u ? v[k].y * draw.scale : 0.0f;
+      }
+      if (SUMS) sum[k] = add2(sum[k], v[k]);
+      else if (res) v[k] = add2(v[k], q.pair(k));
+    }
+    store_piece<VEC>(static_cast<E *>(a.y) + c0 + at, n, lane, v);
+  }
+  if constexpr (SUMS) {
+    if (!a.part) return;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sh[w][33 * e + lane] = e & 1 ? sum[e / 2].y : sum[e / 2].x;
+    __syncthreads();
+    for (int c = threadIdx.x; c < kPiece && c < n; c += kThreads) {
+      const int at = VEC ? 33 * (c % 16) + c / 16 : 33 * (c / 32) + c % 32;
+      float v = sh[0][at];
+#pragma unroll
+      for (int k = 1; k < kWarps; ++k) v += sh[k][at];
+      a.part[(size_t)blockIdx.y * a.d + c0 + c] = v;
+    }
+  }
+}
+
+// Slices of rows: about four CTAs per SM with all pieces, a row per warp at least.
+int slices_of(int sms, int T, int d) {
+  const int pieces = (d + kPiece - 1) / kPiece, most = (T + kWarps - 1) / kWarps;
+  const int s = (4 * sms + pieces - 1) / pieces;
+  return s < most ? s : most;
+}
+
+template <typename E, bool SUMS>
+cudaError_t launch(const Launch &L, const Args &a, int slices) {
+  const dim3 grid((a.d + kPiece - 1) / kPiece, slices);
+  const bool vec = rows_vec(a.d, a.x, nullptr) && rows_vec(a.d, a.y, nullptr) && rows_vec(a.d, a.residual, nullptr);
+  if (vec) k_dropout<E, true, SUMS><<<grid, kThreads, 0, L.stream>>>(a);
+  else k_dropout<E, false, SUMS><<<grid, kThreads, 0, L.stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t dropout_part_floats(int sms, int T, int d) { return (size_t)slices_of(sms, T, d) * d; }
+
+cudaError_t launch_dropout_forward(const Launch &L, bool bf16, const DropoutCall &c) {
+  Args a{};
+  a.x = c.x;
+  a.residual = c.residual;
+  a.bias = c.bias;
+  a.y = c.y;
+  a.T = c.T;
+  a.d = c.d;
+  a.drop = Dropout{c.rng, c.below, c.site, 65536.0f / (float)(65536 - c.below)};
+  const int s = slices_of(L.sms, c.T, c.d);
+  a.rows = (c.T + s - 1) / s;
+  return bf16 ? launch<__nv_bfloat16, false>(L, a, s) : launch<float, false>(L, a, s);
+}
+
+cudaError_t launch_dropout_backward(const Launch &L, bool bf16, const DropoutCall &c) {
+  Args a{};
+  a.x = c.x;
+  a.y = c.y;
+  a.T = c.T;
+  a.d = c.d;
+  a.drop = Dropout{c.rng, c.below, c.site, 65536.0f / (float)(65536 - c.below)};
+  a.part = c.dbias ? c.part : nullptr;
+  const int s = slices_of(L.sms, c.T, c.d);
+  a.rows = (c.T + s - 1) / s;
+  const cudaError_t e = bf16 ? launch<__nv_bfloat16, true>(L, a, s) : launch<float, true>(L, a, s);
+  if (e != cudaSuccess || !c.dbias) return e;
+  return launch_sum_parts(L, c.part, s, c.d, c.dbias);
+}
+
+}  // namespace gift

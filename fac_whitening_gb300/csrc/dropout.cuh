@@ -1,0 +1,46 @@
+// Dropout from a counter: which elements are dropped is a function of the seed, the step, the site (which
+// dropout of the model) and the element's row and column, so no mask is ever stored.
+//
+// Philox's key is the seed, its counter (column / 8, row, site, step): 128 bits for eight columns of a row,
+// 16 for each (word j / 2's lower, then upper half).  An element is dropped where its 16 bits are below
+// P = round(65536 p).  Sixteen bits resolve p to 2^-17, and half the calls of 32 bits an element are left: at
+// 16384 x 1536 BF16 the rounds of one call per four elements would take as long as the memory traffic.
+#pragma once
+
+#include "act.cuh"
+#include "philox.cuh"
+
+namespace gift {
+
+struct Dropout {
+  const unsigned long long *rng;   // device: seed, step
+  uint32_t below;                  // P; 0: nothing is dropped and rng is not read
+  uint32_t site;
+  float scale;                     // 65536 / (65536 - P)
+};
+
+// What a thread draws with: loaded once per kernel.
+struct Draw {
+  uint32_t k0 = 0, k1 = 0, site, step = 0, below;
+  float scale;
+  __device__ __forceinline__ explicit Draw(const Dropout &d) : site(d.site), below(d.below), scale(d.scale) {
+    if (below) {
+      const unsigned long long seed = d.rng[0];
+      k0 = (uint32_t)seed;
+      k1 = (uint32_t)(seed >> 32);
+      step = (uint32_t)d.rng[1];
+    }
+  }
+  // bit j: column 8 group + j of the row is kept
+  __device__ __forceinline__ uint32_t keep8(uint32_t row, uint32_t group) const {
+    const U4 r = philox4x32_10(U4{group, row, site, step}, k0, k1);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m |= ((w[j] & 0xFFFFu) >= below ? 1u : 0u) << (2 * j) | ((w[j] >> 16) >= below ? 2u : 0u) << (2 * j);
+    return m;
+  }
+};
+
+}  // namespace gift

@@ -366,4 +366,65 @@ struct WeightGrad {
 WeightGradWs weight_grad_layout(int sms, bool bf16, int T, int d_out, int d_in);
 cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const WeightGrad &a);
 
+// ---- mlp.cu: the feed-forward block's products -----------------------------------------------
+struct MlpWs {
+  size_t operand_bytes = 0;    // operands' BF16 terms, or their copies with aligned rows
+  size_t part_floats = 0;      // sums of slices of k
+};
+struct GatedForward {
+  const void *x, *Wg, *Wu;
+  int T, d, f, fn, fmt;
+  const float *bg, *bu;        // nullable
+  void *h, *gate, *up;         // gate and up: both or neither
+  uint8_t *codes, *scales;     // both or neither
+  uint8_t *ws;
+};
+struct GatedBackward {
+  const void *dy, *W;
+  int T, d_out, f, fn;
+  const void *gate, *up;
+  void *dgate, *dup;
+  uint8_t *ws;
+};
+struct LinearForward {
+  const void *x, *W;
+  int T, d_out, d_in;
+  const float *bias;           // nullable
+  const void *residual;        // nullable
+  const unsigned long long *rng;
+  uint32_t below, site;
+  void *y;
+  uint8_t *ws;
+  float *part;
+};
+struct InputGrad {
+  const void *delta, *W, *delta2, *W2;   // the second pair nullable
+  int T, d_out, d_in;
+  void *dx;
+  uint8_t *ws;
+  float *part;
+};
+MlpWs gated_forward_layout(bool bf16, int T, int f, int d);
+MlpWs gated_backward_layout(bool bf16, int T, int d_out, int f);
+MlpWs linear_forward_layout(int sms, bool bf16, int T, int d_out, int d_in);
+MlpWs input_grad_layout(int sms, bool bf16, int T, int d_out, int d_in);
+cudaError_t launch_gated_forward(const Launch &L, bool bf16, const GatedForward &a);
+cudaError_t launch_gated_backward(const Launch &L, bool bf16, const GatedBackward &a);
+cudaError_t launch_linear_forward(const Launch &L, bool bf16, const LinearForward &a);
+cudaError_t launch_input_grad(const Launch &L, bool bf16, const InputGrad &a);
+
+// ---- dropout.cu ---------------------------------------------------------------------------------
+struct DropoutCall {
+  const void *x, *residual;    // residual nullable (forward)
+  const float *bias;           // nullable (forward)
+  int T, d;
+  const unsigned long long *rng;
+  uint32_t below, site;
+  void *y;
+  float *dbias, *part;         // nullable (backward)
+};
+size_t dropout_part_floats(int sms, int T, int d);
+cudaError_t launch_dropout_forward(const Launch &L, bool bf16, const DropoutCall &c);
+cudaError_t launch_dropout_backward(const Launch &L, bool bf16, const DropoutCall &c);
+
 }  // namespace gift

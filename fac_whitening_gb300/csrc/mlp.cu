@@ -1,0 +1,327 @@
+// The feed-forward block's products, host side: operands as the tensor-core kernel reads them (product.cuh), its
+// tiles and slices, and the kernels before and after it.
+#include "operand.cuh"
+#include "product.cuh"
+
+namespace gift {
+
+namespace {
+
+using product::Params;
+
+// ---- operands with 16-byte aligned rows, made by one launch -------------------------------------------
+// FP32 -> three BF16 terms, or BF16 rows of another pitch; each operand has CTAs of its own.
+struct Operands {
+  int n;
+  struct One {
+    const void *src;
+    uint8_t *dst;
+    int rows, cols, ld;   // ld: elements
+    int ctas;
+  } op[4];
+};
+
+__global__ void __launch_bounds__(256) k_operands(const __grid_constant__ Operands O, bool bf16) {
+  grid_release();
+  int cta = blockIdx.x;
+  for (int i = 0; i < O.n; ++i) {
+    const Operands::One &o = O.op[i];
+    if (cta < o.ctas) {
+      if (bf16)
+        repitch(static_cast<const uint8_t *>(o.src), o.rows, (size_t)o.cols * 2, (size_t)o.ld * 2, o.dst, cta, o.ctas);
+      else
+        bf16_terms(static_cast<const float *>(o.src), o.rows, o.cols, o.ld, reinterpret_cast<uint16_t *>(o.dst), cta,
+                   o.ctas);
+      return;
+    }
+    cta -= o.ctas;
+  }
+}
+
+// ---- sums of slices of k -> the linear forward product's epilogue ----------------------------------------
+// A thread has eight columns of one row (one draw of dropout's bits); slices are added in order.
+template <typename E>
+__global__ void __launch_bounds__(256) k_join_linear(const float *__restrict__ part, int slices, int ld, int T, int N,
+                                                     const float *__restrict__ bias, const Dropout drop,
+                                                     const E *residual, E *y) {
+  const int groups = (N + 7) / 8;
+  const size_t all = (size_t)T * groups, plane = (size_t)T * ld;
+  grid_wait();
+  const Draw draw(drop);
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
+    const size_t t = i / groups;
+    const int g = (int)(i - t * groups), n = N - 8 * g;
+    const float4 *p = reinterpret_cast<const float4 *>(part + t * ld + 8 * g);
+    float4 a = p[0], b = p[1];
+    for (int s = 1; s < slices; ++s) {
+      const float4 *q = reinterpret_cast<const float4 *>(part + s * plane + t * ld + 8 * g);
+      const float4 x = q[0], z = q[1];
+      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      b = make_float4(b.x + z.x, b.y + z.y, b.z + z.z, b.w + z.w);
+    }
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint32_t keep = draw.below ? draw.keep8((uint32_t)t, g) : 0xFFu;
+    const size_t at = t * N + 8 * (size_t)g;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e >= n) break;
+      float x = bias ? v[e] + bias[8 * g + e] : v[e];
+      if (draw.below) x = keep >> e & 1u ? x * draw.scale : 0.0f;
+      if (residual) x += ld1(residual + at + e);
+      st1(y + at + e, x);
+    }
+  }
+}
+
+// ---- host ---------------------------------------------------------------------------------------------
+constexpr int kSegment = 8, kSegment6 = 6;   // stages of a segment: 512 k, or one block of 64 k of FP32's terms
+
+// `planes` matrices of rows x cols BF16, rows `pitch` bytes apart, read in boxes of 64 columns x `box` rows
+bool boxes(CUtensorMap *m, const void *base, int rows, int cols, size_t pitch, int planes, int box) {
+  const auto enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {pitch, pitch * (cuuint64_t)rows};
+  const cuuint32_t size[3] = {64, (cuuint32_t)box, 1}, one[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, size, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Source {
+  const void *p;
+  int rows, cols;
+  int box;   // rows of a TMA box
+};
+
+size_t operand_bytes(bool bf16, int rows, int cols) {
+  return ((size_t)rows * pad16((size_t)cols * 2) * (bf16 ? 1 : 3) + 255) / 256 * 256;
+}
+
+// The tensor maps of up to four operands; those that TMA cannot read as they lie are made in `ws`, in their
+// order, by one launch (`made`).
+cudaError_t operands(const Launch &L, bool bf16, const Source *src, int n, uint8_t *ws, CUtensorMap *maps, bool &made) {
+  Operands O{};
+  int grid = 0;
+  for (int i = 0; i < n; ++i) {
+    const Source &s = src[i];
+    size_t pitch = (size_t)s.cols * 2;
+    const void *at = s.p;
+    if (!bf16 || pitch % 16 || !aligned16(at)) {
+      pitch = pad16(pitch);
+      Operands::One &o = O.op[O.n++];
+      o.src = s.p;
+      o.dst = ws;
+      o.rows = s.rows;
+      o.cols = s.cols;
+      o.ld = (int)(pitch / 2);
+      const size_t all = spans(s.rows, s.cols, kSpan), ctas = (all + 7) / 8, most = (size_t)L.sms * 8;
+      o.ctas = (int)(ctas < most ? ctas : most);
+      grid += o.ctas;
+      at = ws;
+    }
+    ws += operand_bytes(bf16, s.rows, s.cols);
+    if (!boxes(&maps[i], at, s.rows, s.cols, pitch, bf16 ? 1 : 3, s.box)) return cudaErrorInvalidValue;
+  }
+  made = grid > 0;
+  if (made) k_operands<<<grid, 256, 0, L.stream>>>(O, bf16);
+  return cudaGetLastError();
+}
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// A launch's tiles: 256 rows x bn columns, k in `slices`.
+struct Plan {
+  int bn, slices;
+};
+
+// The width with the least waves x (an item's stages + its start and end); k cut into slices, joined by a kernel
+// of their own, where the tiles leave pairs of SMs idle.  In microseconds.
+Plan plan_linear(int sms, bool bf16, int T, int N, int kb) {
+  const int pairs = sms / 2 > 1 ? sms / 2 : 1;
+  const long long mt = ceil_div(T, product::kTileRows);
+  Plan best{256, 1};
+  double least = 1e300;
+  for (int bn = 256; bn >= 128; bn -= 64) {
+    const double stage = bn == 256 ? 0.28 : bn == 192 ? 0.23 : 0.18;
+    const long long tiles = mt * ceil_div(N, bn);
+    for (int s = 1; s <= 32 && s <= kb; ++s) {
+      const long long waves = (tiles * s + pairs - 1) / pairs;
+      const double cost = (double)waves * (ceil_div(kb, s) * (bf16 ? 1 : 6) * stage + 1.0) +
+                          (s > 1 ? 3.0 + s * 8.0 * T * N / 4.0e6 : 0.0);
+      if (cost < least) {
+        least = cost;
+        best = Plan{bn, s};
+      }
+    }
+  }
+  return best;
+}
+
+int pairs_of(const Launch &L) { return L.sms / 2 > 1 ? L.sms / 2 : 1; }
+
+Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, bool b_mn, int kb) {
+  Params P{};
+  P.T = T;
+  P.N = N;
+  P.mt = ceil_div(T, product::kTileRows);
+  P.nt = ceil_div(N, columns);
+  P.slices = 1;
+  P.items = P.mt * P.nt;
+  P.kb = P.kb1 = kb;
+  P.terms = bf16 ? 1 : 6;
+  P.seg = bf16 ? kSegment : kSegment6;
+  P.bn = bn;
+  P.b_mn = b_mn;
+  P.idesc = tc::idesc_bf16(256, bn) | (b_mn ? 1u << 16 : 0u);
+  P.budget = L.barrier_wait;
+  return P;
+}
+
+}  // namespace
+
+MlpWs gated_forward_layout(bool bf16, int T, int f, int d) {
+  MlpWs w;
+  w.operand_bytes = operand_bytes(bf16, T, d) + 2 * operand_bytes(bf16, f, d);
+  return w;
+}
+
+cudaError_t launch_gated_forward(const Launch &L, bool bf16, const GatedForward &a) {
+  CUtensorMap maps[4];
+  const Source src[3] = {{a.x, a.T, a.d, 128}, {a.Wg, a.f, a.d, 128}, {a.Wu, a.f, a.d, 128}};
+  CUtensorMap made_maps[3];
+  bool made;
+  const cudaError_t e = operands(L, bf16, src, 3, a.ws, made_maps, made);
+  if (e != cudaSuccess) return e;
+  maps[0] = maps[1] = made_maps[0];
+  maps[2] = made_maps[1];
+  maps[3] = made_maps[2];
+  Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK));
+  P.fn = a.fn;
+  P.fmt = a.fmt;
+  P.groups = ceil_div(a.f, kActGroup);
+  P.bias0 = a.bg;
+  P.bias1 = a.bu;
+  P.out0 = a.h;
+  P.out1 = a.gate;
+  P.out2 = a.up;
+  P.codes = a.codes;
+  P.scales = a.scales;
+  const bool vec = rows_vec(a.f, a.h, a.codes) && rows_vec(a.f, a.gate, nullptr) && rows_vec(a.f, a.up, nullptr);
+  return product::launch_gated_forward(L, bf16, vec, P, maps, pairs_of(L), made);
+}
+
+MlpWs gated_backward_layout(bool bf16, int T, int d_out, int f) {
+  MlpWs w;
+  w.operand_bytes = operand_bytes(bf16, T, d_out) + operand_bytes(bf16, d_out, f);
+  return w;
+}
+
+cudaError_t launch_gated_backward(const Launch &L, bool bf16, const GatedBackward &a) {
+  const Source src[2] = {{a.dy, a.T, a.d_out, 128}, {a.W, a.d_out, a.f, 64}};
+  CUtensorMap made_maps[2];
+  bool made;
+  const cudaError_t e = operands(L, bf16, src, 2, a.ws, made_maps, made);
+  if (e != cudaSuccess) return e;
+  const CUtensorMap maps[4] = {made_maps[0], made_maps[0], made_maps[1], made_maps[1]};
+  const int kb = ceil_div(a.d_out, product::kK);
+  const int bn = plan_linear(L.sms, bf16, a.T, a.f, kb).bn;
+  Params P = params_of(L, bf16, a.T, a.f, bn, bn, true, kb);
+  P.fn = a.fn;
+  P.in0 = a.gate;
+  P.in1 = a.up;
+  P.out0 = a.dgate;
+  P.out1 = a.dup;
+  const bool vec = rows_vec(a.f, a.gate, nullptr) && rows_vec(a.f, a.up, nullptr) && rows_vec(a.f, a.dgate, nullptr) &&
+                   rows_vec(a.f, a.dup, nullptr);
+  return product::launch_gated_backward(L, bf16, vec, P, maps, pairs_of(L), made);
+}
+
+namespace {
+
+// A product with the linear epilogue, whole or in slices.
+cudaError_t linear(const Launch &L, bool bf16, const Plan &p, Params P, const CUtensorMap *maps, bool made,
+                   float *part) {
+  P.drop.scale = P.drop.below ? P.drop.scale : 1.0f;
+  if (p.slices == 1) {
+    const bool vec = rows_vec(P.N, P.out0, nullptr) && rows_vec(P.N, P.in0, nullptr);
+    return product::launch_linear(L, bf16, vec, P, maps, pairs_of(L), made);
+  }
+  P.slices = p.slices;
+  P.items *= p.slices;
+  P.part = part;
+  P.part_ld = ceil_div(P.N, 16) * 16;
+  const cudaError_t e = product::launch_slices(L, P, maps, pairs_of(L), made);
+  if (e != cudaSuccess) return e;
+  const size_t ctas = ((size_t)P.T * ceil_div(P.N, 8) + 255) / 256, most = (size_t)L.sms * 8;
+  const dim3 grid((unsigned)(ctas < most ? ctas : most));
+  if (bf16)
+    return launch_after(L.stream, k_join_linear<__nv_bfloat16>, grid, 256, part, p.slices, P.part_ld, P.T, P.N,
+                        P.bias0, P.drop, static_cast<const __nv_bfloat16 *>(P.in0),
+                        static_cast<__nv_bfloat16 *>(P.out0));
+  return launch_after(L.stream, k_join_linear<float>, grid, 256, part, p.slices, P.part_ld, P.T, P.N, P.bias0, P.drop,
+                      static_cast<const float *>(P.in0), static_cast<float *>(P.out0));
+}
+
+size_t part_floats(const Plan &p, int T, int N) {
+  return p.slices > 1 ? (size_t)p.slices * T * (ceil_div(N, 16) * 16) : 0;
+}
+
+}  // namespace
+
+MlpWs linear_forward_layout(int sms, bool bf16, int T, int d_out, int d_in) {
+  MlpWs w;
+  w.operand_bytes = operand_bytes(bf16, T, d_in) + operand_bytes(bf16, d_out, d_in);
+  w.part_floats = part_floats(plan_linear(sms, bf16, T, d_out, ceil_div(d_in, product::kK)), T, d_out);
+  return w;
+}
+
+cudaError_t launch_linear_forward(const Launch &L, bool bf16, const LinearForward &a) {
+  const int kb = ceil_div(a.d_in, product::kK);
+  const Plan p = plan_linear(L.sms, bf16, a.T, a.d_out, kb);
+  const Source src[2] = {{a.x, a.T, a.d_in, 128}, {a.W, a.d_out, a.d_in, p.bn / 2}};
+  CUtensorMap made_maps[2];
+  bool made;
+  const cudaError_t e = operands(L, bf16, src, 2, a.ws, made_maps, made);
+  if (e != cudaSuccess) return e;
+  const CUtensorMap maps[4] = {made_maps[0], made_maps[0], made_maps[1], made_maps[1]};
+  Params P = params_of(L, bf16, a.T, a.d_out, p.bn, p.bn, false, kb);
+  P.bias0 = a.bias;
+  P.in0 = a.residual;
+  P.out0 = a.y;
+  P.drop.rng = a.rng;
+  P.drop.below = a.below;
+  P.drop.site = a.site;
+  P.drop.scale = 65536.0f / (float)(65536 - a.below);
+  return linear(L, bf16, p, P, maps, made, a.part);
+}
+
+MlpWs input_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) {
+  MlpWs w;
+  w.operand_bytes = 2 * (operand_bytes(bf16, T, d_out) + operand_bytes(bf16, d_out, d_in));
+  const int kb = ceil_div(d_out, product::kK);   // one pair of operands, or two
+  const size_t one = part_floats(plan_linear(sms, bf16, T, d_in, kb), T, d_in),
+               two = part_floats(plan_linear(sms, bf16, T, d_in, 2 * kb), T, d_in);
+  w.part_floats = one > two ? one : two;
+  return w;
+}
+
+cudaError_t launch_input_grad(const Launch &L, bool bf16, const InputGrad &a) {
+  const int kb = ceil_div(a.d_out, product::kK), n = a.delta2 ? 2 : 1;
+  const Plan p = plan_linear(L.sms, bf16, a.T, a.d_in, n * kb);
+  const Source src[4] = {{a.delta, a.T, a.d_out, 128},
+                         {a.W, a.d_out, a.d_in, 64},
+                         {a.delta2, a.T, a.d_out, 128},
+                         {a.W2, a.d_out, a.d_in, 64}};
+  CUtensorMap m[4];
+  bool made;
+  const cudaError_t e = operands(L, bf16, src, 2 * n, a.ws, m, made);
+  if (e != cudaSuccess) return e;
+  const CUtensorMap maps[4] = {m[0], m[n == 2 ? 2 : 0], m[1], m[n == 2 ? 3 : 1]};
+  Params P = params_of(L, bf16, a.T, a.d_in, p.bn, p.bn, true, n * kb);
+  P.kb1 = kb;
+  P.out0 = a.dx;
+  return linear(L, bf16, p, P, maps, made, a.part);
+}
+
+}  // namespace gift

@@ -36,14 +36,12 @@
 // Every mbarrier wait is bounded by the context's GIFT_OPT_BARRIER_WAIT and reports GIFT_ERR_TIMEOUT.  A
 // warp leaves as one, and however its loop ended, the copies it issued and the MMAs on the CTA's
 // memory are waited for before the CTA leaves.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <type_traits>
 
 #include "act.cuh"
 #include "kernels.cuh"
-#include "tc.cuh"
+#include "operand.cuh"
+#include "pair.cuh"
 
 namespace gift {
 
@@ -59,7 +57,6 @@ constexpr int kDeqWarp = 4, kDeqWarps = 16;  // warps 4-19: four per stage, by t
 constexpr int kFoldWarp = kDeqWarp + kDeqWarps;
 constexpr int kCodesWarp = 0, kMmaWarp = 1, kDeltaWarp = 2;   // and the second half's MMA warp, 3
 constexpr int kThreads = 896;
-constexpr long long kDrain = 4000000000LL;   // clocks that a leaving warp waits for what is in flight, about 2 s
 
 // Two rings in shared memory.  A code box is free as soon as it is converted; delta's boxes are held
 // until their MMAs are done, up to four stages later.  So delta gets the deeper part of the 224 KB:
@@ -167,30 +164,6 @@ struct Accumulators {
   }
 };
 
-// The slot of a ring of N that its g-th use takes, and the parity of that use.
-template <int N>
-struct Slot {
-  uint32_t at, parity;
-  __device__ __forceinline__ explicit Slot(uint32_t g) : at(g % N), parity(g / N & 1u) {}
-};
-
-// Wait (bounded) until what a ring of N was filled with in its last uses, of g in all, has arrived.
-template <int N>
-__device__ __forceinline__ void landed(uint64_t *full, uint32_t g) {
-  for (uint32_t r = 1; r <= N && r <= g; ++r) {
-    const Slot<N> s(g - r);
-    if (!tc::mbar_wait_bounded(&full[s.at], s.parity, kDrain)) return;
-  }
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-}
 // a float of CTA r's copy of a shared variable
 __device__ __forceinline__ float ld_cluster(const float *p, int r) {
   float v;
@@ -203,38 +176,12 @@ __device__ __forceinline__ float ld_cluster(const float *p, int r) {
       : "memory");
   return v;
 }
-// Arrive on the pair's first CTA's copy of `bar`.  What the barrier orders is tensor memory (its
-// own fences) and TMA's writes, no thread's stores, so no cluster-wide release is asked for: one
-// (.release.cluster) held every arriving warp for hundreds of cycles, 531 -> 457 us for
-// 16384 x 1536 x 6144 without it.
-__device__ __forceinline__ void arrive_first(uint64_t *bar) {
-  asm volatile(
-      "{\n\t.reg .b32 ra;\n\t"
-      "mapa.shared::cluster.u32 ra, %0, 0;\n\t"
-      "mbarrier.arrive.shared::cluster.b64 _, [ra];\n\t}\n" ::"r"(tc::smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int x, int y, int z, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
-          tc::smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
-      : "memory");
-}
 // untiled copy; both addresses and the size are multiples of 16 bytes
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
                    tc::smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                : "memory");
-}
-__device__ __forceinline__ void alloc_pair(uint32_t *dst) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n"
-               "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::"r"(tc::smem_u32(dst))
-               : "memory");
-}
-__device__ __forceinline__ void dealloc_pair(uint32_t taddr) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(taddr) : "memory");
 }
 // B: MN-major, 128-byte swizzle, one atom (64 BF16) wide, 8-token groups 1024 bytes apart.  The
 // descriptor's lower half holds the start address, the upper half is constant.
@@ -251,25 +198,6 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t bdesc_
       "r"(a), "r"(bdesc_lo), "n"(kDescHi), "n"(kIdesc), "r"(accumulate)
       : "memory");
 }
-// arrive on both CTAs' `bar` once the MMAs issued so far have completed
-__device__ __forceinline__ void commit_pair(uint64_t *bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
-          tc::smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-// one thread of a converged warp
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok));
-  return ok != 0;
-}
-
 __device__ __forceinline__ void ldmatrix_t8(uint32_t addr, uint32_t *r) {
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -870,86 +798,6 @@ __device__ __forceinline__ void column_sums(const Prepare &P, int cta, float (*s
   }
 }
 
-// The terms of one value at the end of FP32's range, where rounding to BF16 gives an infinity.  A finite
-// value is cut into its bits instead (8 + 8 + 8 of them, exact), so that no sum of the first terms passes it; an
-// infinity or NaN is its own first term and has no others (Inf - Inf would make it NaN).
-__device__ __forceinline__ void bf16_terms_of_large(float x, uint16_t *t) {
-  const uint32_t bits = __float_as_uint(x), size = bits & 0x7FFFFFFFu;
-  if (size < 0x7F7F8000u) {
-    tc::bf16_split3(x, t[0], t[1], t[2]);
-  } else if (size < 0x7F800000u) {
-    const float r = __fsub_rn(x, __uint_as_float(bits & 0xFFFF0000u));
-    t[0] = (uint16_t)(bits >> 16);
-    t[1] = (uint16_t)(__float_as_uint(r) >> 16);
-    t[2] = __bfloat16_as_ushort(__float2bfloat16_rn(__fsub_rn(r, __uint_as_float(__float_as_uint(r) & 0xFFFF0000u))));
-  } else {
-    t[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-    t[1] = t[2] = 0;
-  }
-}
-
-// FP32 as three BF16 terms (exact from 2^-110 up; below, the last ends at BF16's smallest step), planes of
-// T rows of ld columns; a warp per row, two columns per lane
-__device__ __forceinline__ void bf16_terms(const float *x, int T, int d, int ld, uint16_t *out, int cta, int ctas) {
-  const size_t plane = (size_t)T * ld;
-  for (int t = cta * 8 + (threadIdx.x >> 5); t < T; t += ctas * 8) {
-    const float *p = x + (size_t)t * d;
-    uint16_t *o = out + (size_t)t * ld;
-    for (int c = 2 * (threadIdx.x & 31); c < d; c += 64) {   // ld is even
-      uint32_t w[3];
-      const float x0 = p[c], x1 = c + 1 < d ? p[c + 1] : 0.0f;
-      if (max(abs_bits(x0), abs_bits(x1)) < 0x7F7F8000u) {
-        tc::bf16_split3x2(x0, x1, w[0], w[1], w[2]);
-      } else {
-        uint16_t a[3], b[3];
-        bf16_terms_of_large(x0, a);
-        bf16_terms_of_large(x1, b);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) w[k] = (uint32_t)a[k] | (uint32_t)b[k] << 16;
-      }
-#pragma unroll
-      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(o + k * plane + c) = w[k];
-    }
-  }
-}
-
-// Rows of `bytes` bytes at any alignment -> rows of ld (a multiple of 16) bytes; a warp per row, 16 bytes
-// per lane from the two aligned blocks that hold them.  Past a row's end nothing is read again (the
-// tensor map's width).
-__device__ __forceinline__ uint4 aligned_block(uintptr_t p, uintptr_t lo, uintptr_t hi) {
-  if (p >= lo && p + 16 <= hi) return *reinterpret_cast<const uint4 *>(p);
-  uint32_t w[4] = {0u, 0u, 0u, 0u};   // the ends of the matrix
-#pragma unroll
-  for (int b = 0; b < 16; ++b)
-    if (p + b >= lo && p + b < hi) w[b / 4] |= (uint32_t)*reinterpret_cast<const uint8_t *>(p + b) << (8 * (b % 4));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void repitch(const uint8_t *src, int T, size_t bytes, size_t ld, uint8_t *dst, int cta,
-                                        int ctas) {
-  const uintptr_t lo = (uintptr_t)src, hi = lo + (size_t)T * bytes;
-  for (int t = cta * 8 + (threadIdx.x >> 5); t < T; t += ctas * 8) {
-    const uintptr_t row = lo + (size_t)t * bytes;
-    const int off = (int)(row & 15), sh = 8 * (off & 3);
-#pragma unroll 4
-    for (size_t c = 16 * (threadIdx.x & 31); c < bytes; c += 512) {
-      const uintptr_t at = row + c - off;
-      const uint4 a = aligned_block(at, lo, hi), b = off ? aligned_block(at + 16, lo, hi) : a;
-      uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      if (off & 8) {   // the same for the whole row
-#pragma unroll
-        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
-      }
-      if (off & 4) {
-#pragma unroll
-        for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
-      }
-      *reinterpret_cast<uint4 *>(dst + t * ld + c) =
-          make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
-                     __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
-    }
-  }
-}
-
 template <int F, bool BF16>
 __global__ void __launch_bounds__(256) k_prepare(const __grid_constant__ Prepare P) {
   __shared__ union {
@@ -987,18 +835,6 @@ __global__ void __launch_bounds__(256) k_prepare(const __grid_constant__ Prepare
 }
 
 // ---- host ---------------------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
 // `planes` matrices of rows x cols elements, rows `pitch` bytes apart, read in 128-byte x 64-row boxes
 bool boxes(CUtensorMap *m, bool bf16, const void *base, int rows, int cols, size_t pitch, int planes) {
   const auto enc = encoder();
@@ -1013,8 +849,6 @@ bool boxes(CUtensorMap *m, bool bf16, const void *base, int rows, int cols, size
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-size_t pad16(size_t bytes) { return (bytes + 15) / 16 * 16; }
 
 struct Plan {
   int nh, mt, nt, ng, slices, pairs;

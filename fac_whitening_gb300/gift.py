@@ -26,7 +26,9 @@ XFORM = {"identity": 0, "lowrank": 1, "chol_input": 2, "chol_two_sided": 3}
 PREC = {"fp32": 0, "tc": 1}
 DTYPE = {"f32": 0, "bf16": 1}
 OP = {"factor_update": 0, "encode": 1, "decode": 2, "amax": 3, "kfac_factor": 4, "reduce_decode": 5,
-      "layernorm_backward": 6, "weight_grad": 7}
+      "layernorm_backward": 6, "weight_grad": 7, "gated_forward": 8, "gated_backward": 9, "linear_forward": 10,
+      "input_grad": 11, "dropout_backward": 12}
+GATE = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 OPT_SUBSPACE_ITERS = 0
 OPT_BARRIER_WAIT = 1
 OPT_SKETCH = 2
@@ -104,6 +106,15 @@ def _declare(lib):
         "gift_layernorm_backward": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                          _sz, _vp, _vp]),
         "gift_weight_grad": (_i, [_vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+        "gift_gated_forward": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp,
+                                    _sz, _vp, _vp]),
+        "gift_gated_backward": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp, _vp]),
+        "gift_linear_forward": (_i, [_vp, _vp, _i, _i, _i, _vp, _i, _vp, _vp, ctypes.c_float, _vp, ctypes.c_uint, _vp,
+                                     _vp, _sz, _vp, _vp]),
+        "gift_input_grad": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _sz, _vp, _vp]),
+        "gift_dropout_forward": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, ctypes.c_float, _vp, ctypes.c_uint, _vp, _vp]),
+        "gift_dropout_backward": (_i, [_vp, _vp, _i, _i, _i, ctypes.c_float, _vp, ctypes.c_uint, _vp, _vp, _vp, _sz,
+                                       _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -526,3 +537,83 @@ def gift_weight_grad(ctx: Context, delta, codes, scales, fmt: str, dW, db=None, 
                                   _buf(gamma, d_in, "gamma", f32), _buf(beta, d_in, "beta", f32),
                                   _buf(dW, d_out * d_in, "dW", f32), _buf(db, d_out, "db", f32), w, wn,
                                   _p(status), _stream(stream)), "gift_weight_grad")
+
+
+# ---- the feed-forward block: gated products, linear layer with dropout, input gradient, dropout ----------
+def _rng(rng) -> Optional[int]:
+    """Address of a device tensor of two 64-bit integers: dropout's seed and step."""
+    if rng is None:
+        return None
+    if rng.element_size() != 8 or rng.numel() != 2 or rng.is_floating_point():
+        raise ValueError(f"rng: expected two 64-bit integers, got {tuple(rng.shape)} {rng.dtype}")
+    return _p(rng)
+
+
+def gift_gated_forward(ctx: Context, x, Wg, Wu, fn: str, h, gate=None, up=None, bg=None, bu=None, fmt: str = "e4m3",
+                       codes=None, scales=None, ws=None, status=None, stream=None):
+    """h = a(x Wg^T + bg) (x Wu^T + bu); gate and up receive the two projections, codes and scales h's checkpoint."""
+    f32, dt = _f32(), x.dtype
+    T, d = x.shape
+    f = Wg.shape[0]
+    w, wn = _ws(ws)
+    _check(lib().gift_gated_forward(ctx.handle, _p(x), _dt(x), T, d, _buf(Wg, f * d, "Wg", dt),
+                                    _buf(Wu, f * d, "Wu", dt), f, _buf(bg, f, "bg", f32), _buf(bu, f, "bu", f32),
+                                    GATE[fn], _buf(h, T * f, "h", dt), _buf(gate, T * f, "gate", dt),
+                                    _buf(up, T * f, "up", dt), FMT[fmt], _bytes(codes, T * f, "codes"),
+                                    _bytes(scales, T * ((f + 127) // 128), "scales"), w, wn, _p(status),
+                                    _stream(stream)), "gift_gated_forward")
+
+
+def gift_gated_backward(ctx: Context, dy, W, gate, up, fn: str, dgate, dup, ws=None, status=None, stream=None):
+    """dgate and dup from dy, the gradient of what the linear layer W (d_out x f) made of h."""
+    dt = dy.dtype
+    T, d_out = dy.shape
+    f = W.shape[1]
+    n = T * f
+    w, wn = _ws(ws)
+    _check(lib().gift_gated_backward(ctx.handle, _p(dy), _dt(dy), T, d_out, _buf(W, d_out * f, "W", dt), f,
+                                     _buf(gate, n, "gate", dt), _buf(up, n, "up", dt), GATE[fn],
+                                     _buf(dgate, n, "dgate", dt), _buf(dup, n, "dup", dt), w, wn, _p(status),
+                                     _stream(stream)), "gift_gated_backward")
+
+
+def gift_linear_forward(ctx: Context, x, W, y, bias=None, residual=None, p: float = 0.0, rng=None, site: int = 0,
+                        ws=None, status=None, stream=None):
+    """y = residual + drop(x W^T + bias); rng: a device tensor of two 64-bit integers, the seed and the step."""
+    f32, dt = _f32(), x.dtype
+    T, d_in = x.shape
+    d_out = W.shape[0]
+    w, wn = _ws(ws)
+    _check(lib().gift_linear_forward(ctx.handle, _p(x), _dt(x), T, d_in, _buf(W, d_out * d_in, "W", dt), d_out,
+                                     _buf(bias, d_out, "bias", f32), _buf(residual, T * d_out, "residual", dt), p,
+                                     _rng(rng), site, _buf(y, T * d_out, "y", dt), w, wn, _p(status),
+                                     _stream(stream)), "gift_linear_forward")
+
+
+def gift_input_grad(ctx: Context, delta, W, dx, delta2=None, W2=None, ws=None, status=None, stream=None):
+    """dx = delta W, or delta W + delta2 W2."""
+    dt = delta.dtype
+    T, d_out = delta.shape
+    d_in = W.shape[1]
+    w, wn = _ws(ws)
+    _check(lib().gift_input_grad(ctx.handle, _p(delta), _buf(W, d_out * d_in, "W", dt),
+                                 _buf(delta2, T * d_out, "delta2", dt), _buf(W2, d_out * d_in, "W2", dt), _dt(delta),
+                                 T, d_out, d_in, _buf(dx, T * d_in, "dx", dt), w, wn, _p(status), _stream(stream)),
+           "gift_input_grad")
+
+
+def gift_dropout_forward(ctx: Context, x, y, p: float, rng, site: int = 0, bias=None, residual=None, stream=None):
+    """y = residual + drop(x + bias)."""
+    T, d = x.shape
+    _check(lib().gift_dropout_forward(ctx.handle, _p(x), _dt(x), T, d, _buf(bias, d, "bias", _f32()),
+                                      _buf(residual, T * d, "residual", x.dtype), p, _rng(rng), site,
+                                      _buf(y, T * d, "y", x.dtype), _stream(stream)), "gift_dropout_forward")
+
+
+def gift_dropout_backward(ctx: Context, dy, dx, p: float, rng, site: int = 0, dbias=None, ws=None, stream=None):
+    """dx = drop(dy) with the forward pass's bits, dbias = sum over tokens of dx."""
+    T, d = dy.shape
+    w, wn = _ws(ws)
+    _check(lib().gift_dropout_backward(ctx.handle, _p(dy), _dt(dy), T, d, p, _rng(rng), site,
+                                       _buf(dx, T * d, "dx", dy.dtype), _buf(dbias, d, "dbias", _f32()), w, wn,
+                                       _stream(stream)), "gift_dropout_backward")

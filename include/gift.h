@@ -142,7 +142,7 @@ typedef struct {
  * per-call state, so calls on different streams may run concurrently. */
 typedef struct gift_ctx gift_ctx;
 
-/* Operations for gift_workspace_bytes (the last two for gift_act_workspace_bytes). */
+/* Operations for gift_workspace_bytes and gift_act_workspace_bytes. */
 typedef enum {
   GIFT_OP_FACTOR_UPDATE = 0,
   GIFT_OP_ENCODE = 1,
@@ -150,8 +150,13 @@ typedef enum {
   GIFT_OP_AMAX = 3,
   GIFT_OP_KFAC_FACTOR = 4,
   GIFT_OP_REDUCE_DECODE = 5,
-  GIFT_OP_LAYERNORM_BACKWARD = 6, /* sized by gift_act_workspace_bytes */
-  GIFT_OP_WEIGHT_GRAD = 7         /* sized by gift_act_workspace_bytes */
+  GIFT_OP_LAYERNORM_BACKWARD = 6, /* this and what follows: sized by gift_act_workspace_bytes */
+  GIFT_OP_WEIGHT_GRAD = 7,
+  GIFT_OP_GATED_FORWARD = 8,
+  GIFT_OP_GATED_BACKWARD = 9,
+  GIFT_OP_LINEAR_FORWARD = 10,
+  GIFT_OP_INPUT_GRAD = 11,
+  GIFT_OP_DROPOUT_BACKWARD = 12
 } gift_op;
 
 /* Tunables for gift_set_option. */
@@ -507,9 +512,10 @@ gift_status gift_encode_lowrank_noalloc(gift_ctx *ctx, const gift_factor *f, con
  * format other than E4M3 or E5M2. */
 gift_status gift_act_sizes(gift_format fmt, int T, int d, size_t *code_bytes, size_t *scale_bytes);
 
-/* Bytes of device workspace of GIFT_OP_LAYERNORM_BACKWARD (d_out is ignored, d_in = d) or
- * GIFT_OP_WEIGHT_GRAD with gradients (dy, delta) of type dt.  Host-only; (size_t)-1 for invalid
- * arguments or another op. */
+/* Bytes of device workspace of a call with tensors (dy, delta, x) of type dt: GIFT_OP_LAYERNORM_BACKWARD and
+ * GIFT_OP_DROPOUT_BACKWARD (d_out is ignored, d_in = d), GIFT_OP_WEIGHT_GRAD, GIFT_OP_GATED_FORWARD (d_out = f,
+ * d_in = d), GIFT_OP_GATED_BACKWARD (d_in = f), GIFT_OP_LINEAR_FORWARD, GIFT_OP_INPUT_GRAD (with or without the
+ * second pair).  Host-only; (size_t)-1 for invalid arguments or another op. */
 size_t gift_act_workspace_bytes(const gift_ctx *ctx, gift_op op, gift_dtype dt, int T, int d_out, int d_in);
 
 /* Keep x (device, T x d of type x_dt) as an 8-bit checkpoint: codes and scales (device,
@@ -584,6 +590,113 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
                              const void *scales, gift_format fmt, int T, int d_out, int d_in, const float *gamma,
                              const float *beta, float *dW, float *db, void *ws, size_t ws_bytes, int *d_status,
                              cudaStream_t stream);
+
+/* ---- The feed-forward block around those layers ---------------------------------------------
+ * The method's fragile layers are the second products of the MLP blocks ([notes] simplification 3, the profile:
+ * all of the first 13 are fc2); the pages say nothing of the block itself.  These calls are one block of a
+ * training step between its norm and the codec, forward and backward:
+ *
+ *   g = x Wg^T + bg, u = x Wu^T + bu, h = a(g) u        gift_gated_forward
+ *   y = residual + drop(h W^T + bias)                   gift_linear_forward
+ *   dz = drop(dy), dbias = sum_t dz                     gift_dropout_backward
+ *   dh = dz W, dg = dh u a'(g), du = dh a(g)            gift_gated_backward
+ *   dx = dg Wg + du Wu                                  gift_input_grad
+ *
+ * and gift_weight_grad makes dW from h's checkpoint and dz, dWg and dWu from the norm's checkpoint and dg, du.
+ * Products are summed in FP32, rounded to nearest at least every 512 terms (the tensor core truncates in
+ * between), and each output is rounded once, to its type.  FP32 operands enter as three BF16 terms each with the
+ * six products i + j <= 4 of terms i and j (what is dropped is below 2^-23 of |x_k W_k|); operands below 2^-110 may lose
+ * up to 2^-134.  Orders of summation are fixed by the shape, the buffers' alignment and the context: equal calls
+ * give equal bits.  An infinity or NaN in a BF16 operand reaches the outputs as the formula has it; in an FP32
+ * operand it makes NaN or Inf of every output that the formula makes not finite, without telling which.
+ * T, d, f, d_in and d_out are at most 2^30 and an output has at most 2^31 - 1 tiles of 256 x 128 (INVALID_ARG above).
+ * Alignment: any to the element.  BF16 operands of the products are read in place where their rows and pointers are
+ * 16-byte aligned, copied into the workspace else; rows of the other tensors are moved by 32-byte accesses where
+ * they are a multiple of 16 elements in 32-byte aligned buffers (codes 16-byte aligned), through shared memory
+ * else. */
+
+/* The gate's activation a: g / (1 + exp(-g)); g Phi(g), Phi the normal distribution; g (1 + tanh(sqrt(2 / pi)
+ * (g + 0.044715 g^3))) / 2. */
+typedef enum { GIFT_GATE_SILU = 0, GIFT_GATE_GELU = 1, GIFT_GATE_GELU_TANH = 2 } gift_gate;
+
+/* The block's two projections, the activation and the product in one kernel.
+ *  x      : device, T x d of type dt.
+ *  Wg, Wu : device, f x d of type dt.
+ *  bg, bu : device, f FP32, each nullable (0).
+ *  h      : device, T x f of type dt.
+ *  gate, up : device, T x f of type dt, both or neither: g and u, kept for gift_gated_backward.
+ *  codes, scales : device, both or neither: the 8-bit checkpoint of h in `fmt` (ignored when NULL), made from h
+ *           in FP32, for gift_weight_grad of the layer that reads h.
+ *  ws     : gift_act_workspace_bytes(GIFT_OP_GATED_FORWARD, dt, T, f, d) bytes.
+ * INVALID_ARG: a null x, Wg, Wu, h or ws, one of a pair without the other, T, d or f < 1, a bad type, gate or
+ * format, a workspace too small.  d_status: NONFINITE when the checkpoint has a group with NaN or Inf; TIMEOUT. */
+gift_status gift_gated_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d, const void *Wg,
+                               const void *Wu, int f, const float *bg, const float *bu, gift_gate fn, void *h,
+                               void *gate, void *up, gift_format fmt, void *codes, void *scales, void *ws,
+                               size_t ws_bytes, int *d_status, cudaStream_t stream);
+
+/* The gradients of g and u from the gradient dy of what a linear layer W made of h: dh = dy W, dg = dh u a'(g),
+ * du = dh a(g), from the g and u that the forward pass kept; dh itself is not stored.
+ *  dy     : device, T x d_out of type dt.
+ *  W      : device, d_out x f of type dt.
+ *  gate, up   : device, T x f of type dt.
+ *  dgate, dup : device, T x f of type dt; dgate may be gate and dup may be up.
+ *  ws     : gift_act_workspace_bytes(GIFT_OP_GATED_BACKWARD, dt, T, d_out, f) bytes.
+ * INVALID_ARG: a null pointer, T, d_out or f < 1, a bad type or gate, a workspace too small.  d_status: TIMEOUT. */
+gift_status gift_gated_backward(gift_ctx *ctx, const void *dy, gift_dtype dt, int T, int d_out, const void *W, int f,
+                                const void *gate, const void *up, gift_gate fn, void *dgate, void *dup, void *ws,
+                                size_t ws_bytes, int *d_status, cudaStream_t stream);
+
+/* A linear layer with dropout and the residual stream: y = residual + drop(x W^T + bias).
+ *  x      : device, T x d_in of type dt.     W : device, d_out x d_in of type dt.
+ *  bias   : device, d_out FP32, nullable.    residual : device, T x d_out of type dt, nullable.
+ *  p, rng, site : as gift_dropout_forward.
+ *  y      : device, T x d_out of type dt; may be residual.
+ *  ws     : gift_act_workspace_bytes(GIFT_OP_LINEAR_FORWARD, dt, T, d_out, d_in) bytes.
+ * INVALID_ARG: a null x, W, y or ws, T, d_in or d_out < 1, a bad type, p or rng, a workspace too small.  d_status:
+ * TIMEOUT. */
+gift_status gift_linear_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d_in, const void *W, int d_out,
+                                const float *bias, const void *residual, float p, const unsigned long long *rng,
+                                unsigned int site, void *y, void *ws, size_t ws_bytes, int *d_status,
+                                cudaStream_t stream);
+
+/* A linear layer's input gradient dx = delta W, or of two layers that read the same input, delta W + delta2 W2.
+ *  delta, delta2 : device, T x d_out of type dt.     W, W2 : device, d_out x d_in of type dt.
+ *                  (delta2 and W2 both or neither.)
+ *  dx     : device, T x d_in of type dt.
+ *  ws     : gift_act_workspace_bytes(GIFT_OP_INPUT_GRAD, dt, T, d_out, d_in) bytes.
+ * INVALID_ARG: a null delta, W, dx or ws, one of delta2 and W2 without the other, T, d_out or d_in < 1, a bad type, a
+ * workspace too small.  d_status: TIMEOUT. */
+gift_status gift_input_grad(gift_ctx *ctx, const void *delta, const void *W, const void *delta2, const void *W2,
+                            gift_dtype dt, int T, int d_out, int d_in, void *dx, void *ws, size_t ws_bytes,
+                            int *d_status, cudaStream_t stream);
+
+/* Dropout with the residual stream: y = residual + drop(x + bias).  Which elements are dropped is drawn from a
+ * counter and never stored: with Philox4x32-10, the seed as its key and the counter (column / 8, row, site, step), an
+ * element has 16 of the 128 bits (column % 8 = 2 w or 2 w + 1: word w's lower or upper half) and is dropped, to 0, where
+ * they are below P = round(65536 p), otherwise multiplied with 65536 / (65536 - P).
+ *  x      : device, T x d of type dt.
+ *  bias   : device, d FP32, nullable.     residual : device, T x d of type dt, nullable.
+ *  p      : 0 <= p < 1 with P < 65536.
+ *  rng    : device, two 64-bit numbers, the seed and the step (its lower 32 bits count), read when the call runs: a
+ *           captured step draws new bits when the caller changes them.  May be NULL when P = 0.
+ *  site   : which dropout of the model this is; two sites of a step draw different bits.
+ *  y      : device, T x d of type dt; may be x or residual.
+ * INVALID_ARG: a null x or y, T or d < 1, a bad type, p or rng. */
+gift_status gift_dropout_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d, const float *bias,
+                                 const void *residual, float p, const unsigned long long *rng, unsigned int site,
+                                 void *y, cudaStream_t stream);
+
+/* Dropout's gradients with the bits that p, rng and site gave the forward pass (gift_dropout_forward or
+ * gift_linear_forward): dx = drop(dy) and dbias = sum_t dx, in FP32 from the unrounded dx, in a fixed order; the
+ * residual's gradient is dy.
+ *  dy, dx : device, T x d of type dt; dx may be dy.
+ *  dbias  : device, d FP32, nullable.
+ *  ws     : gift_act_workspace_bytes(GIFT_OP_DROPOUT_BACKWARD, dt, T, d, d) bytes (may be NULL when dbias is).
+ * INVALID_ARG: a null dy or dx, T or d < 1, a bad type, p or rng, a workspace too small. */
+gift_status gift_dropout_backward(gift_ctx *ctx, const void *dy, gift_dtype dt, int T, int d, float p,
+                                  const unsigned long long *rng, unsigned int site, void *dx, float *dbias, void *ws,
+                                  size_t ws_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }
