@@ -94,6 +94,32 @@ struct Source {
   int box;   // rows of a TMA box
 };
 
+// The tensor T x N that an epilogue's buffers are copied to or from: boxes of 32 rows x 128 bytes, or 64 codes.
+bool unit_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *base, int T, int N) {
+  const auto enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)T}, stride = (cuuint64_t)N * size;
+  const cuuint32_t box[2] = {size == 1 ? 64u : 128u / size, 32}, one[2] = {1, 1};
+  return enc(m, type, 2, const_cast<void *>(base), dims, &stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             size == 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An epilogue's tensors by TMA, where all their rows and pointers are 16-byte aligned (rows of 16 columns: of codes too);
+// null ones are not used.  vec: whether they are.
+bool unit_maps(product::IoMaps &io, bool bf16, int T, int N, const void *t0, const void *t1, const void *t2,
+               const void *t3, const void *codes, bool &vec) {
+  const void *t[4] = {t0, t1, t2, t3};
+  vec = N % 16 == 0 && aligned16(codes);
+  for (const void *p : t) vec = vec && aligned16(p);
+  if (!vec) return true;
+  for (int i = 0; i < 4; ++i)
+    if (t[i] && !unit_map(&io.m[i], bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                          bf16 ? 2 : 4, t[i], T, N))
+      return false;
+  return !codes || unit_map(&io.m[3], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, codes, T, N);
+}
+
 size_t operand_bytes(bool bf16, int rows, int cols) {
   return ((size_t)rows * pad16((size_t)cols * 2) * (bf16 ? 1 : 3) + 255) / 256 * 256;
 }
@@ -169,10 +195,8 @@ Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, 
   P.slices = 1;
   P.items = P.mt * P.nt;
   P.kb = P.kb1 = kb;
-  P.terms = bf16 ? 1 : 6;
   P.seg = bf16 ? kSegment : kSegment6;
   P.bn = bn;
-  P.b_mn = b_mn;
   P.idesc = tc::idesc_bf16(256, bn) | (b_mn ? 1u << 16 : 0u);
   P.budget = L.barrier_wait;
   return P;
@@ -207,8 +231,10 @@ cudaError_t launch_gated_forward(const Launch &L, bool bf16, const GatedForward 
   P.out2 = a.up;
   P.codes = a.codes;
   P.scales = a.scales;
-  const bool vec = rows_vec(a.f, a.h, a.codes) && rows_vec(a.f, a.gate, nullptr) && rows_vec(a.f, a.up, nullptr);
-  return product::launch_gated_forward(L, bf16, vec, P, maps, pairs_of(L), made);
+  product::IoMaps io{};
+  bool vec;
+  if (!unit_maps(io, bf16, a.T, a.f, a.h, a.gate, a.up, nullptr, a.codes, vec)) return cudaErrorInvalidValue;
+  return product::launch_gated_forward(L, bf16, vec, P, maps, io, pairs_of(L), made);
 }
 
 MlpWs gated_backward_layout(bool bf16, int T, int d_out, int f) {
@@ -232,26 +258,29 @@ cudaError_t launch_gated_backward(const Launch &L, bool bf16, const GatedBackwar
   P.in1 = a.up;
   P.out0 = a.dgate;
   P.out1 = a.dup;
-  const bool vec = rows_vec(a.f, a.gate, nullptr) && rows_vec(a.f, a.up, nullptr) && rows_vec(a.f, a.dgate, nullptr) &&
-                   rows_vec(a.f, a.dup, nullptr);
-  return product::launch_gated_backward(L, bf16, vec, P, maps, pairs_of(L), made);
+  product::IoMaps io{};
+  bool vec;
+  if (!unit_maps(io, bf16, a.T, a.f, a.gate, a.up, a.dgate, a.dup, nullptr, vec)) return cudaErrorInvalidValue;
+  return product::launch_gated_backward(L, bf16, vec, P, maps, io, pairs_of(L), made);
 }
 
 namespace {
 
 // A product with the linear epilogue, whole or in slices.
-cudaError_t linear(const Launch &L, bool bf16, const Plan &p, Params P, const CUtensorMap *maps, bool made,
+cudaError_t linear(const Launch &L, bool bf16, bool mn, const Plan &p, Params P, const CUtensorMap *maps, bool made,
                    float *part) {
   P.drop.scale = P.drop.below ? P.drop.scale : 1.0f;
   if (p.slices == 1) {
-    const bool vec = rows_vec(P.N, P.out0, nullptr) && rows_vec(P.N, P.in0, nullptr);
-    return product::launch_linear(L, bf16, vec, P, maps, pairs_of(L), made);
+    product::IoMaps io{};
+    bool vec;
+    if (!unit_maps(io, bf16, P.T, P.N, P.in0, nullptr, P.out0, nullptr, nullptr, vec)) return cudaErrorInvalidValue;
+    return product::launch_linear(L, bf16, vec, mn, P, maps, io, pairs_of(L), made);
   }
   P.slices = p.slices;
   P.items *= p.slices;
   P.part = part;
   P.part_ld = ceil_div(P.N, 16) * 16;
-  const cudaError_t e = product::launch_slices(L, P, maps, pairs_of(L), made);
+  const cudaError_t e = product::launch_slices(L, bf16, mn, P, maps, product::IoMaps{}, pairs_of(L), made);
   if (e != cudaSuccess) return e;
   const size_t ctas = ((size_t)P.T * ceil_div(P.N, 8) + 255) / 256, most = (size_t)L.sms * 8;
   const dim3 grid((unsigned)(ctas < most ? ctas : most));
@@ -293,7 +322,7 @@ cudaError_t launch_linear_forward(const Launch &L, bool bf16, const LinearForwar
   P.drop.below = a.below;
   P.drop.site = a.site;
   P.drop.scale = 65536.0f / (float)(65536 - a.below);
-  return linear(L, bf16, p, P, maps, made, a.part);
+  return linear(L, bf16, false, p, P, maps, made, a.part);
 }
 
 MlpWs input_grad_layout(int sms, bool bf16, int T, int d_out, int d_in) {
@@ -321,7 +350,7 @@ cudaError_t launch_input_grad(const Launch &L, bool bf16, const InputGrad &a) {
   Params P = params_of(L, bf16, a.T, a.d_in, p.bn, p.bn, true, n * kb);
   P.kb1 = kb;
   P.out0 = a.dx;
-  return linear(L, bf16, p, P, maps, made, a.part);
+  return linear(L, bf16, true, p, P, maps, made, a.part);
 }
 
 }  // namespace gift

@@ -4,7 +4,7 @@
 //
 // A pair of CTAs (a cluster of two SMs, cta_group::2) owns 256 tokens x up to 256 columns: each CTA holds 128 of
 // the tokens and half of B's columns.  Per CTA:
-//   warp 0       TMA: stages of 64 k, A's 128 x 64 and B's up to 128 x 64 elements;
+//   warps 0, 2   TMA: stages of 64 k, A's 128 x 64 and B's up to 128 x 64 elements;
 //   warp 1       the pair's first CTA issues 256 x N x 16 MMAs; the second one's reports its stages to the first;
 //   warps 4-11   fold and epilogue: a thread has one token and half of the tile's columns.
 // The tensor core truncates its sums, so a segment of at most 512 k goes into one of two accumulators in tensor
@@ -35,24 +35,33 @@ namespace product {
 constexpr int kK = 64;                      // k of a stage
 constexpr int kABytes = 128 * kK * 2;       // a CTA's rows of A in a stage, and its most columns of B
 constexpr int kStage = 2 * kABytes;
-constexpr int kStages = 6;
 constexpr int kBox = kK * 128;              // bytes of an MN-major box: 64 columns
 constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4, kEpiWarps = 8;
 constexpr int kTileRows = 256;
-constexpr int kPitch = 17;                  // floats of a row of the epilogue's 32 x 16 staging tiles
-constexpr int kSmem = kStages * kStage + kEpiWarps * 32 * kPitch * 4 + 1024;
+constexpr int kUnit = 32 * 128;             // bytes of an epilogue buffer: 32 rows of 64 BF16 or 32 FP32 columns
+constexpr int kPitch = 17;                  // floats of a row of the 32 x 16 tiles that rows of any alignment go through
 
 enum Op { GATED_FORWARD, GATED_BACKWARD, LINEAR, SLICE };
+
+// Shared memory: a ring of stages, and epilogue buffers for each of its warps (backward: the gate's and the other
+// projection's unit side by side, the gradients in their place).
+template <int OP>
+struct Cfg {
+  static constexpr int stages = OP == GATED_BACKWARD ? 5 : 6;
+  static constexpr int bufs = OP == GATED_BACKWARD ? 2 : 1;
+  static constexpr int smem = stages * kStage + kEpiWarps * bufs * kUnit + 1024;
+};
+struct IoMaps {
+  CUtensorMap m[4];   // boxes of 32 rows x 128 bytes: in0, in1, out0, out1; forward: out0 to out2 and the codes (64 bytes)
+};
 
 struct Params {
   int T, N;               // rows and columns of the output
   int mt, nt, slices, items;
   int kb, kb1;            // blocks of 64 k, and those of the first pair of operands
-  int terms;              // products per block: 1, or 6 of FP32's terms
   int seg;                // stages of a segment
   int bn;                 // columns of a tile, a multiple of 64
-  int b_mn;               // B is MN-major
   uint32_t idesc;
   long long budget;       // clocks of a wait
   // epilogue
@@ -81,13 +90,15 @@ struct Item {
   }
 };
 
+constexpr int kMostStages = 6;
 struct __align__(16) Shared {
-  uint64_t full[kStages], empty[kStages];   // loaded; multiplied (in both CTAs)
-  uint64_t other[kStages];                  // first CTA: the second one's stage is loaded
+  uint64_t full[kMostStages], empty[kMostStages];   // loaded; multiplied (in both CTAs)
+  uint64_t other[kMostStages];                      // first CTA: the second one's stage is loaded
+  uint64_t in[kEpiWarps][2];                        // an epilogue warp's buffers: loaded
   uint64_t dfull[2], dempty[2];             // accumulators: summed; folded by both CTAs
-  uint64_t met[4];                          // a row's two column halves have left their amax
+  uint64_t met[4];                          // a row's two column halves have left their scale bytes
   uint64_t drained;
-  uint32_t amax[2][2][128];                 // [tile parity][half][row]
+  uint8_t scale[2][2][128];                 // [tile parity][half][row]: the scale byte that the half's columns ask for
   uint32_t tmem;
   volatile int failed;
 };
@@ -107,108 +118,159 @@ __device__ __forceinline__ void mma_pair_ss(uint32_t d, uint32_t a_lo, uint32_t 
       : "memory");
 }
 
-// ---- a thread's 16 columns of one row, of 32 consecutive rows per warp ---------------------------------
-// VEC: rows of a multiple of 16 elements in 32-byte aligned buffers; a lane moves its own row's columns.  Otherwise
-// through the warp's staging tile, so that 16 lanes move 16 consecutive columns.
-template <typename E, bool VEC>
-struct Cols;
-template <>
-struct Cols<__nv_bfloat16, true> {
-  uint32_t r[8];
-  __device__ __forceinline__ void load(const void *base, size_t ld, int row0, int rows, int col, int n, float *) {
-    const int lane = threadIdx.x & 31;
-    if (lane < rows && n > 0) ld256(static_cast<const __nv_bfloat16 *>(base) + (size_t)(row0 + lane) * ld + col, r);
-    else
+// Barriers and copies by shared-memory address, for the loops of one thread
+__device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool test_wait_at(uint32_t bar, uint32_t parity) {   // looks, does not wait
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void expect_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void load_at(uint32_t dst, const CUtensorMap *tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+// The next slot of a ring of N, and the parity of its uses
+template <int N>
+__device__ __forceinline__ void advance(uint32_t &at, uint32_t &parity) {
+  if (++at == N) {
+    at = 0;
+    parity ^= 1u;
+  }
+}
+
+// ---- units: a thread's 128 bytes of one row, of 32 consecutive rows per warp ------------------------------
+// A warp's buffer holds them in the 128-byte swizzle of its tensor map: 16-byte piece j of row r at j ^ (r % 8), so that
+// eight lanes' pieces do not meet in a bank.  TMA moves whole buffers: a lane's own accesses to 32 rows cost the load
+// and store unit 67 clocks for each 32 bytes a lane (the stores of g and u 4300 clocks a tile, of 12300).
+__device__ __forceinline__ uint32_t piece_at(uint32_t buf, int lane, int j) {
+  return buf + lane * 128 + ((j ^ (lane & 7)) << 4);
+}
+__device__ __forceinline__ uint4 read_piece(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void write_piece(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// A piece's columns (8 BF16 or 4 FP32) as pairs
+template <typename E>
+struct Piece {
+  static constexpr int pairs = sizeof(E) == 2 ? 4 : 2;
+  float2 v[pairs];
+  Piece() = default;
+  __device__ __forceinline__ explicit Piece(uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = 0u;
-  }
-  __device__ __forceinline__ float2 pair(int k) const {
-    return make_float2(__uint_as_float(r[k] << 16), __uint_as_float(r[k] & 0xFFFF0000u));
-  }
-};
-template <>
-struct Cols<float, true> {
-  uint32_t r[16];
-  __device__ __forceinline__ void load(const void *base, size_t ld, int row0, int rows, int col, int n, float *) {
-    const int lane = threadIdx.x & 31;
-    if (lane < rows && n > 0) {
-      const float *p = static_cast<const float *>(base) + (size_t)(row0 + lane) * ld + col;
-      ld256(p, r);
-      ld256(p + 8, r + 8);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) r[e] = 0u;
-    }
-  }
-  __device__ __forceinline__ float2 pair(int k) const {
-    return make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+    for (int k = 0; k < pairs; ++k)
+      v[k] = sizeof(E) == 2 ? make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u))
+                            : make_float2(__uint_as_float(w[2 * k % 4]), __uint_as_float(w[(2 * k + 1) % 4]));
   }
 };
 template <typename E>
-struct Cols<E, false> {
+__device__ __forceinline__ uint4 pack_piece(const float2 *v) {
+  if (sizeof(E) == 2)
+    return make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
+                      pack_bf16(v[3].x, v[3].y));
+  return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+}
+// Copies between a buffer and its place in a tensor; stores of a thread are waited for in groups.
+__device__ __forceinline__ void load_unit(uint32_t buf, const CUtensorMap *map, int col, int row, uint32_t bar) {
+  expect_at(bar, kUnit);
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          buf),
+      "l"(map), "r"(col), "r"(row), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void store_unit(uint32_t buf, const CUtensorMap *map, int col, int row) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n"
+      "cp.async.bulk.commit_group;\n" ::"l"(map),
+      "r"(col), "r"(row), "r"(buf)
+      : "memory");
+}
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
+
+// ---- rows of any alignment: 16 columns at a time through a 32 x 16 tile, 16 lanes to a row -----------------------
+template <typename E>
+struct Cols {
   float2 v[8];
   __device__ __forceinline__ void load(const void *base, size_t ld, int row0, int rows, int col, int n, float *stage) {
     const int lane = threadIdx.x & 31, c = lane & 15;
     const E *p = static_cast<const E *>(base) + (size_t)row0 * ld + col + c;
+    float x[16];   // all loads before the first store
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const int r = 2 * k + (lane >> 4);
-      stage[r * kPitch + c] = r < rows && c < n ? ld1(p + (size_t)r * ld) : 0.0f;
+      x[k] = r < rows && c < n ? ld1(p + (size_t)r * ld) : 0.0f;
     }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) stage[(2 * k + (lane >> 4)) * kPitch + c] = x[k];
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = make_float2(stage[lane * kPitch + 2 * k], stage[lane * kPitch + 2 * k + 1]);
     __syncwarp();
   }
-  __device__ __forceinline__ float2 pair(int k) const { return v[k]; }
 };
 
-template <typename E, bool VEC>
+template <typename E>
 __device__ __forceinline__ void store16(void *base, size_t ld, int row0, int rows, int col, int n, const float2 *v,
                                         float *stage) {
-  const int lane = threadIdx.x & 31;
-  E *p = static_cast<E *>(base) + (size_t)row0 * ld + col;
-  if (VEC) {
-    if (lane < rows && n > 0) {
-      p += (size_t)lane * ld;
-      if constexpr (sizeof(E) == 2) {
-        uint32_t r[8];
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  E *p = static_cast<E *>(base) + (size_t)row0 * ld + col + c;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) r[k] = pack_bf16(v[k].x, v[k].y);
-        st256(p, r);
-      } else {
-        uint32_t r[16];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          r[2 * k] = __float_as_uint(v[k].x);
-          r[2 * k + 1] = __float_as_uint(v[k].y);
-        }
-        st256(p, r);
-        st256(p + 8, r + 8);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      stage[lane * kPitch + 2 * k] = v[k].x;
-      stage[lane * kPitch + 2 * k + 1] = v[k].y;
-    }
-    __syncwarp();
-    const int c = lane & 15;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int r = 2 * k + (lane >> 4);
-      if (r < rows && c < n) st1(p + (size_t)r * ld + c, stage[r * kPitch + c]);
-    }
-    __syncwarp();
+  for (int k = 0; k < 8; ++k) {
+    stage[lane * kPitch + 2 * k] = v[k].x;
+    stage[lane * kPitch + 2 * k + 1] = v[k].y;
   }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const int r = 2 * k + (lane >> 4);
+    if (r < rows && c < n) st1(p + (size_t)r * ld, stage[r * kPitch + c]);
+  }
+  __syncwarp();
 }
 
-// 16 codes of a row: VEC as above (and 16-byte aligned codes)
-template <int F, bool VEC>
-__device__ __forceinline__ void store_codes(uint8_t *base, size_t ld, int row0, int rows, int col, int n,
-                                            const float2 *v, float inv, float *stage) {
-  const int lane = threadIdx.x & 31;
+// 16 columns of a lane's own row, rows of a multiple of 16 FP32 in 32-byte aligned buffers
+__device__ __forceinline__ void store_own(float *p, const float2 *v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    r[2 * k] = __float_as_uint(v[k].x);
+    r[2 * k + 1] = __float_as_uint(v[k].y);
+  }
+  st256(p, r);
+  st256(p + 8, r + 8);
+}
+
+// 16 codes
+template <int F>
+__device__ __forceinline__ uint4 pack_codes(const float2 *v, float inv) {
   const float2 s = both(inv);
   uint32_t w[4];
 #pragma unroll
@@ -216,28 +278,39 @@ __device__ __forceinline__ void store_codes(uint8_t *base, size_t ld, int row0, 
     const float2 a = mul2(v[2 * k], s), b = mul2(v[2 * k + 1], s);
     w[k] = pack4_fp8<F>(a.x, a.y, b.x, b.y);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_codes(uint8_t *base, size_t ld, int row0, int rows, int col, int n, uint4 w,
+                                            float *stage) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
   uint8_t *p = base + (size_t)row0 * ld + col;
-  if (VEC) {
-    if (lane < rows && n > 0) *reinterpret_cast<uint4 *>(p + (size_t)lane * ld) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    uint32_t *t = reinterpret_cast<uint32_t *>(stage);   // rows of 5 words: 20 bytes
+  uint32_t *t = reinterpret_cast<uint32_t *>(stage) + lane * 5;   // rows of 20 bytes
+  t[0] = w.x;
+  t[1] = w.y;
+  t[2] = w.z;
+  t[3] = w.w;
+  __syncwarp();
+  const uint8_t *b = reinterpret_cast<const uint8_t *>(stage);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) t[lane * 5 + k] = w[k];
-    __syncwarp();
-    const uint8_t *b = reinterpret_cast<const uint8_t *>(stage);
-    const int c = lane & 15;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int r = 2 * k + (lane >> 4);
-      if (r < rows && c < n) p[(size_t)r * ld + c] = b[r * 20 + c];
-    }
-    __syncwarp();
+  for (int k = 0; k < 16; ++k) {
+    const int r = 2 * k + (lane >> 4);
+    if (r < rows && c < n) p[(size_t)r * ld + c] = b[r * 20 + c];
   }
+  __syncwarp();
 }
 
 // bias of 16 columns (the same for every lane), n of them in the matrix; nullable
 __device__ __forceinline__ void add_bias(float2 *v, const float *bias, int n) {
   if (!bias) return;
+  if (n >= 16 && aligned16(bias)) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 b = *reinterpret_cast<const float4 *>(bias + 4 * k);
+      v[2 * k] = add2(v[2 * k], make_float2(b.x, b.y));
+      v[2 * k + 1] = add2(v[2 * k + 1], make_float2(b.z, b.w));
+    }
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     v[k] = add2(v[k], make_float2(2 * k < n ? bias[2 * k] : 0.0f, 2 * k + 1 < n ? bias[2 * k + 1] : 0.0f));
@@ -254,27 +327,43 @@ __device__ __forceinline__ void gate_forward(float2 (&acc)[8][8]) {
       acc[i][k] = mul2(make_float2(gate_value<FN, ACCURATE>(g.x), gate_value<FN, ACCURATE>(g.y)), acc[4 + i][k]);
     }
 }
-// dh in `d`: the gate's gradient in its place, the other projection's in `du`
-template <int FN, bool ACCURATE, typename C>
-__device__ __forceinline__ void gate_backward(float2 *d, float2 *du, const C &g, const C &u) {
+// dh in `d`: the gate's gradient in its place, the other projection's in `du`; N pairs of columns
+template <int FN, bool ACCURATE, int N>
+__device__ __forceinline__ void gate_backward(float2 *d, float2 *du, const float2 *g, const float2 *u) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float2 gv = g.pair(k);
+  for (int k = 0; k < N; ++k) {
     float2 slope, a;
-    a.x = gate_slope<FN, ACCURATE>(gv.x, slope.x);
-    a.y = gate_slope<FN, ACCURATE>(gv.y, slope.y);
+    a.x = gate_slope<FN, ACCURATE>(g[k].x, slope.x);
+    a.y = gate_slope<FN, ACCURATE>(g[k].y, slope.y);
     du[k] = mul2(d[k], a);
-    d[k] = mul2(mul2(d[k], u.pair(k)), slope);
+    d[k] = mul2(mul2(d[k], u[k]), slope);
+  }
+}
+// 16 bits of dropout for a row's columns col to col + 15: dropped to 0, or scaled
+__device__ __forceinline__ void drop16(const Draw &draw, float2 *v, int row, int col) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t keep = draw.keep8(row, col / 8 + h);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float2 &x = v[4 * h + k];
+      x.x = keep >> (2 * k) & 1u ? x.x * draw.scale : 0.0f;
+      x.y = keep >> (2 * k + 1) & 1u ? x.y * draw.scale : 0.0f;
+    }
   }
 }
 
-template <int OP, typename E, bool VEC>
+// MN: B is MN-major.
+template <int OP, typename E, bool VEC, bool MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_product(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap tm_a0,
               const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b0,
-              const __grid_constant__ CUtensorMap tm_b1, int *status) {
+              const __grid_constant__ CUtensorMap tm_b1, const __grid_constant__ IoMaps io, int *status) {
+  constexpr int kStages = Cfg<OP>::stages, kBufs = Cfg<OP>::bufs;
+  static_assert(Cfg<OP>::smem + sizeof(Shared) <= 227 * 1024, "a CTA's shared memory");
   constexpr bool kGated = OP == GATED_FORWARD;
   constexpr bool kAccurate = sizeof(E) == 4;
+  constexpr int kTerms = sizeof(E) == 4 ? 6 : 1;
   extern __shared__ uint8_t dsm[];
   uint8_t *sm = reinterpret_cast<uint8_t *>(((uintptr_t)dsm + 1023) & ~(uintptr_t)1023);
   __shared__ Shared sh;
@@ -285,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) alloc_pair(&sh.tmem);
   if (tid == 32) {
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&sh.full[s], 1);
+      tc::mbar_init(&sh.full[s], 2);
       tc::mbar_init(&sh.empty[s], 1);
       tc::mbar_init(&sh.other[s], 1);
     }
@@ -294,6 +383,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(&sh.dempty[b], 2 * kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) tc::mbar_init(&sh.met[q], 2);
+    for (int e = 0; e < kEpiWarps; ++e)
+      for (int b = 0; b < 2; ++b) tc::mbar_init(&sh.in[e][b], 1);
     tc::mbar_init(&sh.drained, 1);
     tc::fence_mbar_init();
     sh.failed = 0;
@@ -321,121 +412,170 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return __all_sync(0xFFFFFFFFu, done) != 0;
   };
 
+  // The same for one thread by itself.
+  auto hold = [&](uint32_t bar, uint32_t parity) {
+    if (try_wait_at(bar, parity)) return true;
+    const long long t0 = clock64();
+    do {
+      if (sh.failed || clock64() - t0 > P.budget) {
+        sh.failed = 1;
+        set_status(status, GIFT_ERR_TIMEOUT);
+        return false;
+      }
+    } while (!try_wait_at(bar, parity));
+    return true;
+  };
+
   // registers: 168 per thread at launch (504 over the three groups of four warps), redistributed as 2 x 208 + 88
   if (warp < kEpiWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-    const bool one = elect_one();
-    if (warp == 0) {
+    // One thread each.  A stage's 512 clocks are few for what a single thread does between two of them, so these loops keep
+    // their addresses running, and A and B have a thread each (one for both, its slot and terms computed per stage, took
+    // 550 clocks a stage).
+    const uint32_t full = tc::smem_u32(sh.full), empty = tc::smem_u32(sh.empty), other = tc::smem_u32(sh.other);
+    const uint32_t ring = tc::smem_u32(sm);
+    if (!elect_one()) {
+    } else if (warp == 0 || warp == 2) {
       // ---------------- TMA ----------------
-      const int half = P.bn / 2, boxes = (half + 63) / 64;
-      const uint32_t bytes = kABytes + (P.b_mn ? boxes * kBox : half * 128);
-      uint32_t g = 0;
+      const bool is_a = warp == 0;
+      const int half = P.bn / 2, boxes = half > 64 ? 2 : 1;
+      const uint32_t bytes = is_a ? kABytes : MN ? boxes * kBox : half * 128;
+      const uint32_t base = ring + (is_a ? 0 : kABytes);
+      uint32_t at = 0, parity = 1, g = 0;
       bool ok = true;
       grid_wait();   // the operands that the launch before this one made
+      auto stage = [&](const CUtensorMap *map, int k, int y, int term) {
+        const uint32_t bar = full + 8 * at, dst = base + at * kStage;
+        if (!(ok = hold(empty + 8 * at, parity))) return;
+        expect_at(bar, bytes);
+        if (MN && !is_a) {
+          load_at(dst, map, y, k, term, bar);
+          if (boxes == 2) load_at(dst + kBox, map, y + 64, k, term, bar);
+        } else {
+          load_at(dst, map, k, y, term, bar);
+        }
+        advance<kStages>(at, parity);
+        ++g;
+      };
       for (int it = pair; it < P.items && ok; it += pairs) {
         const Item w(P, it);
-        const int row = w.m * kTileRows + 128 * rank;
-        const int col = kGated ? 128 * w.n : w.n * P.bn + half * rank;
-        const CUtensorMap *gate = rank ? &tm_b1 : &tm_b0;
-        for (int kb = w.k0; kb < w.k1 && ok; ++kb) {
-          const bool second = !kGated && kb >= P.kb1;
-          const int k = (second ? kb - P.kb1 : kb) * kK;
-          const CUtensorMap *a = second ? &tm_a1 : &tm_a0, *b = kGated ? gate : second ? &tm_b1 : &tm_b0;
-          for (int p = 6 - P.terms; p < 6; ++p, ++g) {   // terms (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
-            const int ta = (0x001012 >> (4 * p)) & 3, tb = (0x010210 >> (4 * p)) & 3;
-            const Slot<kStages> s(g);
-            if (!(ok = wait(&sh.empty[s.at], s.parity ^ 1u))) break;
-            if (one) {
-              uint8_t *st = sm + s.at * kStage;
-              tc::mbar_arrive_expect_tx(&sh.full[s.at], bytes);
-              tma_load_3d(st, a, k, row, ta, &sh.full[s.at]);
-              if (P.b_mn) {
-                for (int x = 0; x < boxes; ++x)
-                  tma_load_3d(st + kABytes + x * kBox, b, col + 64 * x, k, tb, &sh.full[s.at]);
-              } else {
-                tma_load_3d(st + kABytes, b, k, col, tb, &sh.full[s.at]);
-              }
+        const int y = is_a ? w.m * kTileRows + 128 * rank : kGated ? 128 * w.n : w.n * P.bn + half * rank;
+        auto walk = [&](const CUtensorMap *map, int k, int end) {
+          for (; k < end && ok; k += kK) {
+            if constexpr (kTerms == 1) {
+              stage(map, k, y, 0);
+            } else {   // terms (2,0) (1,1) (0,2) (1,0) (0,1) (0,0)
+              const int t[6] = {is_a ? 2 : 0, 1, is_a ? 0 : 2, is_a ? 1 : 0, is_a ? 0 : 1, 0};
+#pragma unroll
+              for (int p = 0; p < 6; ++p)
+                if (ok) stage(map, k, y, t[p]);
             }
           }
+        };
+        if (kGated) {
+          walk(is_a ? &tm_a0 : rank ? &tm_b1 : &tm_b0, w.k0 * kK, w.k1 * kK);
+        } else {
+          walk(is_a ? &tm_a0 : &tm_b0, w.k0 * kK, min(w.k1, P.kb1) * kK);
+          walk(is_a ? &tm_a1 : &tm_b1, max(w.k0 - P.kb1, 0) * kK, (w.k1 - P.kb1) * kK);
         }
       }
       // leave no arrival of the MMAs' commits behind: the last stages'
       for (uint32_t r = 1; ok && r <= kStages && r <= g; ++r) {
         const Slot<kStages> s(g - r);
-        ok = wait(&sh.empty[s.at], s.parity);
+        ok = hold(empty + 8 * s.at, s.parity);
       }
       landed<kStages>(sh.full, g);
       // the pair's first CTA may have a wait of its own to end before its last commit
       tc::mbar_wait_bounded(&sh.drained, 0, P.budget + kDrain);
     } else if (warp == 1 && rank == 0) {
       // ---------------- MMA ----------------
-      const uint32_t first = tc::smem_u32(sm) >> 4;
-      const uint32_t b_lead = P.b_mn ? (uint32_t)(kBox >> 4) << 16 : 1u << 16, b_step = P.b_mn ? 128u : 2u;
-      uint32_t g = 0, n = 0;   // stages, segments
-      bool ok = true;
+      const uint32_t b_lead = MN ? (uint32_t)(kBox >> 4) << 16 : 1u << 16, b_step = MN ? 128u : 2u;
+      const uint32_t dempty = tc::smem_u32(sh.dempty), idesc = P.idesc;
+      const int seg = P.seg;
+      uint32_t at = 0, parity = 0, n = 0;   // slot, segments
+      bool ok = true, there = false;        // there: the stage was seen to be loaded
       for (int it = pair; it < P.items && ok; it += pairs) {
         const Item w(P, it);
-        for (int left = (w.k1 - w.k0) * P.terms; left > 0 && ok; left -= P.seg, ++n) {
+        for (int left = (w.k1 - w.k0) * kTerms; left > 0 && ok; left -= seg, ++n) {
           const uint32_t d = tmem + 256 * (n & 1);
-          if (!(ok = wait(&sh.dempty[n & 1], (n >> 1 & 1u) ^ 1u))) break;
+          if (!(ok = hold(dempty + 8 * (n & 1), (n >> 1 & 1u) ^ 1u))) break;
           tc::fence_after_sync();
-          for (int j = 0; j < P.seg && j < left; ++j, ++g) {
-            const Slot<kStages> s(g);
-            if (!(ok = wait(&sh.full[s.at], s.parity) && wait(&sh.other[s.at], s.parity))) break;
+          uint32_t accumulate = 0;
+          for (int j = min(seg, left); j > 0; --j) {
+            if (!there && !(ok = hold(full + 8 * at, parity) && hold(other + 8 * at, parity))) break;
+            const uint32_t a = (ring + at * kStage) >> 4, b = a + (kABytes >> 4);
+            uint64_t *const done = &sh.empty[at];
+            advance<kStages>(at, parity);
+            there = test_wait_at(full + 8 * at, parity) && test_wait_at(other + 8 * at, parity);
             tc::fence_after_sync();
-            if (one) {
-              const uint32_t a = first + s.at * (kStage >> 4), b = a + (kABytes >> 4);
 #pragma unroll
-              for (int k = 0; k < kK / 16; ++k)
-                mma_pair_ss(d, (a + 2 * k) | 1u << 16, (b + b_step * k) | b_lead, P.idesc, j || k ? 1u : 0u);
-              commit_pair(&sh.empty[s.at]);
+            for (int k = 0; k < kK / 16; ++k) {
+              mma_pair_ss(d, (a + 2 * k) | 1u << 16, (b + b_step * k) | b_lead, idesc, accumulate);
+              accumulate = 1;
             }
+            commit_pair(done);
           }
-          if (ok && one) commit_pair(&sh.dfull[n & 1]);
+          if (ok) commit_pair(&sh.dfull[n & 1]);
         }
       }
-      if (one) commit_pair(&sh.drained);
+      commit_pair(&sh.drained);
     } else if (warp == 1) {
       // ---------------- the second CTA's stages ----------------
       uint32_t total = 0;
       for (int it = pair; it < P.items; it += pairs) {
         const Item w(P, it);
-        total += (uint32_t)(w.k1 - w.k0) * P.terms;
+        total += (uint32_t)(w.k1 - w.k0) * kTerms;
       }
-      for (uint32_t g = 0; g < total; ++g) {
-        const Slot<kStages> s(g);
-        if (!wait(&sh.full[s.at], s.parity)) break;
-        if (one) arrive_first(&sh.other[s.at]);
+      for (uint32_t g = 0, at = 0, parity = 0; g < total; ++g) {
+        if (!hold(full + 8 * at, parity)) break;
+        arrive_first(&sh.other[at]);
+        advance<kStages>(at, parity);
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-    // ---------------- fold and epilogue: 32 rows, half of the columns ----------------
-    const int q = warp & 3, c = (warp - kEpiWarp) >> 2;
-    const int half = P.bn / 2;
-    float *stage = reinterpret_cast<float *>(sm + kStages * kStage) + (warp - kEpiWarp) * 32 * kPitch;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    // ---------------- fold and epilogue: 32 rows, and a part of the columns in whole units (128 and 64 of 192,
+    // otherwise half) ----------------
+    const int e = warp - kEpiWarp, q = warp & 3, c = e >> 2;
+    const int first = (P.bn + 127) / 128 * 64, own = c ? P.bn - first : first;   // columns of the two parts, of this warp
+    uint8_t *const mine = sm + kStages * kStage + e * kBufs * kUnit;
+    float *const stage = reinterpret_cast<float *>(mine);
+    const uint32_t buf = tc::smem_u32(mine), lanes = tmem + ((uint32_t)(32 * q) << 16);
+    constexpr int kCols = 128 / sizeof(E);           // columns of a unit
+    constexpr int kPairs = Piece<E>::pairs;
+    const bool one = elect_one();
     const Draw draw(P.drop);
-    uint32_t n = 0, tile = 0;
+    uint32_t n = 0, tile = 0, loads = 0, issued = 0;   // loads: buffers filled and read
     bool ok = true, bad = false;
     for (int it = pair; it < P.items && ok; it += pairs, ++tile) {
       const Item w(P, it);
       const int row0 = w.m * kTileRows + 128 * rank + 32 * q, rows = P.T - row0;   // may be <= 0
+      const int col0 = kGated ? 128 * w.n + 64 * c : w.n * P.bn + first * c;
+      // the inputs of unit v into the warp's buffers, whose last contents have been stored
+      auto load_inputs = [&](int v) {
+        if (!one || rows <= 0 || col0 + kCols * v >= P.N) return;
+        ++issued;
+        stores_read();
+        load_unit(buf, &io.m[0], col0 + kCols * v, row0, tc::smem_u32(&sh.in[e][0]));
+        if (kBufs == 2) load_unit(buf + kUnit, &io.m[1], col0 + kCols * v, row0, tc::smem_u32(&sh.in[e][1]));
+      };
+      const bool inputs = VEC && (OP == GATED_BACKWARD || (OP == LINEAR && P.in0));
+      if (inputs) load_inputs(0);
       float2 acc[8][8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[i][k] = both(0.0f);
 #pragma unroll 1
-      for (int left = (w.k1 - w.k0) * P.terms; left > 0; left -= P.seg, ++n) {
+      for (int left = (w.k1 - w.k0) * kTerms; left > 0; left -= P.seg, ++n) {
         if (!(ok = wait(&sh.dfull[n & 1], n >> 1 & 1u))) break;
         tc::fence_after_sync();
         const uint32_t from = lanes + 256 * (n & 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (32 * j >= half) break;
+          if (32 * j >= own) break;
           uint32_t raw[32];
-          tc::tmem_ld32_nowait(from + (kGated ? (j < 2 ? 64 * c + 32 * j : 64 + 64 * c + 32 * j) : half * c + 32 * j), raw);
+          tc::tmem_ld32_nowait(from + (kGated ? (j < 2 ? 64 * c + 32 * j : 64 + 64 * c + 32 * j) : first * c + 32 * j), raw);
           tc::tmem_wait_ld(raw);
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
@@ -449,70 +589,135 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
+      // Unit v of 16-column groups `from` to a tensor: the buffer is written when its last contents have been stored.
+      auto put = [&](const float2 (*from)[8], const CUtensorMap *map, int v) {
+        if (rows <= 0 || col0 + kCols * v >= P.N) return;
+        if (one) stores_read();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          write_piece(piece_at(buf, lane, j), pack_piece<E>(&from[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8]));
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (one) store_unit(buf, map, col0 + kCols * v, row0);
+      };
+      // the same by elements, for rows of any alignment
+      auto put_any = [&](const float2 (*from)[8], void *to, int i) {
+        store16<E>(to, P.N, row0, rows, col0 + 16 * i, P.N - col0 - 16 * i, from[i], stage);
+      };
+
       if constexpr (OP == GATED_FORWARD) {
-        const int f0 = 128 * w.n + 64 * c;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int col = f0 + 16 * i, left = P.N - col;
+          const int col = col0 + 16 * i, left = P.N - col;
           add_bias(acc[i], P.bias0 ? P.bias0 + col : nullptr, left);
           add_bias(acc[4 + i], P.bias1 ? P.bias1 + col : nullptr, left);
-          if (P.out1) {
-            store16<E, VEC>(P.out1, P.N, row0, rows, col, left, acc[i], stage);
-            store16<E, VEC>(P.out2, P.N, row0, rows, col, left, acc[4 + i], stage);
+        }
+        if (P.out1) {
+          if constexpr (VEC) {
+#pragma unroll
+            for (int v = 0; v < 64 / kCols; ++v) {
+              put(acc, &io.m[1], v);
+              put(acc + 4, &io.m[2], v);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              put_any(acc, P.out1, i);
+              put_any(acc + 4, P.out2, i);
+            }
           }
         }
         if (P.fn == GATE_SILU) gate_forward<GATE_SILU, kAccurate>(acc);
         else if (P.fn == GATE_GELU) gate_forward<GATE_GELU, kAccurate>(acc);
         else gate_forward<GATE_GELU_TANH, kAccurate>(acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          store16<E, VEC>(P.out0, P.N, row0, rows, f0 + 16 * i, P.N - f0 - 16 * i, acc[i], stage);
+        uint8_t(&scale)[2][128] = sh.scale[tile & 1];
+        uint32_t sb = 0;
         if (P.codes) {
-          // a scale group is the tile's 128 columns: this warp's 64 and the other half's
+          // a scale group is the tile's 128 columns: this warp's 64 and the other warp's; the byte grows with the amax
           uint32_t m = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              if (f0 + 16 * i + 2 * k < P.N) {   // columns past the matrix are not its last group's
+              if (VEC ? col0 + 16 * i < P.N : col0 + 16 * i + 2 * k < P.N) {   // columns past the matrix do not count
                 m = max(m, abs_bits(acc[i][k].x));
-                if (f0 + 16 * i + 2 * k + 1 < P.N) m = max(m, abs_bits(acc[i][k].y));
+                if (VEC || col0 + 16 * i + 2 * k + 1 < P.N) m = max(m, abs_bits(acc[i][k].y));
               }
-          uint32_t(&amax)[2][128] = sh.amax[tile & 1];
-          amax[c][32 * q + lane] = m;
+          sb = P.fmt == FMT_E4M3 ? act_scale_byte<FMT_E4M3>(m) : act_scale_byte<FMT_E5M2>(m);
+          scale[c][32 * q + lane] = (uint8_t)sb;
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sh.met[q]);
+        }
+        if constexpr (VEC) {
+#pragma unroll
+          for (int v = 0; v < 64 / kCols; ++v) put(acc, &io.m[0], v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) put_any(acc, P.out0, i);
+        }
+        if (P.codes) {
           if (!(ok = wait(&sh.met[q], tile & 1u))) break;
-          m = max(m, amax[c ^ 1][32 * q + lane]);
-          const uint32_t sb = P.fmt == FMT_E4M3 ? act_scale_byte<FMT_E4M3>(m) : act_scale_byte<FMT_E5M2>(m);
+          sb = max(sb, (uint32_t)scale[c ^ 1][32 * q + lane]);
           const float inv = act_inv_scale(sb);
           if (lane < rows) {
             bad |= sb == kActBad;
             if (c == 0) P.scales[(size_t)(row0 + lane) * P.groups + w.n] = (uint8_t)sb;
           }
+          if (VEC && one) stores_read();
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int col = f0 + 16 * i, left = P.N - col;
-            if (P.fmt == FMT_E4M3)
-              store_codes<FMT_E4M3, VEC>(P.codes, P.N, row0, rows, col, left, acc[i], inv, stage);
-            else
-              store_codes<FMT_E5M2, VEC>(P.codes, P.N, row0, rows, col, left, acc[i], inv, stage);
+            const uint4 w4 = P.fmt == FMT_E4M3 ? pack_codes<FMT_E4M3>(acc[i], inv) : pack_codes<FMT_E5M2>(acc[i], inv);
+            if (VEC) write_piece(buf + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4), w4);   // 64-byte swizzle
+            else store_codes(P.codes, P.N, row0, rows, col0 + 16 * i, P.N - col0 - 16 * i, w4, stage);
+          }
+          if (VEC) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (one && rows > 0 && col0 < P.N) store_unit(buf, &io.m[3], col0, row0);
           }
         }
       } else if constexpr (OP == GATED_BACKWARD) {
         auto walk = [&](auto fn_c) {
           constexpr int FN = decltype(fn_c)::value;
+          if constexpr (VEC) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (16 * i >= half) break;
-            const int col = w.n * P.bn + half * c + 16 * i, left = P.N - col;
-            Cols<E, VEC> g, u;
-            g.load(P.in0, P.N, row0, rows, col, left, stage);
-            u.load(P.in1, P.N, row0, rows, col, left, stage);
-            float2 du[8];
-            gate_backward<FN, kAccurate>(acc[i], du, g, u);
-            store16<E, VEC>(P.out0, P.N, row0, rows, col, left, acc[i], stage);
-            store16<E, VEC>(P.out1, P.N, row0, rows, col, left, du, stage);
+            for (int v = 0; v < 128 / kCols; ++v) {
+              const int col = col0 + kCols * v;
+              if (kCols * v >= own || rows <= 0 || col >= P.N) break;
+              if (!(ok = wait(&sh.in[e][0], loads & 1u) && wait(&sh.in[e][1], loads & 1u))) break;
+              ++loads;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint32_t at = piece_at(buf, lane, j);
+                const Piece<E> g(read_piece(at)), u(read_piece(at + kUnit));
+                float2 *d = &acc[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8], du[kPairs];
+                gate_backward<FN, kAccurate, kPairs>(d, du, g.v, u.v);
+                write_piece(at, pack_piece<E>(d));
+                write_piece(at + kUnit, pack_piece<E>(du));
+              }
+              tc::fence_proxy_async_smem();
+              __syncwarp();
+              if (one) {
+                store_unit(buf, &io.m[2], col, row0);
+                store_unit(buf + kUnit, &io.m[3], col, row0);
+              }
+              if (kCols * (v + 1) < own) load_inputs(v + 1);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (16 * i >= own) break;
+              const int col = col0 + 16 * i, left = P.N - col;
+              Cols<E> g, u;
+              g.load(P.in0, P.N, row0, rows, col, left, stage);
+              u.load(P.in1, P.N, row0, rows, col, left, stage);
+              float2 du[8];
+              gate_backward<FN, kAccurate, 8>(acc[i], du, g.v, u.v);
+              store16<E>(P.out0, P.N, row0, rows, col, left, acc[i], stage);
+              store16<E>(P.out1, P.N, row0, rows, col, left, du, stage);
+            }
           }
         };
         if (P.fn == GATE_SILU) walk(std::integral_constant<int, GATE_SILU>());
@@ -521,38 +726,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if constexpr (OP == LINEAR) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (16 * i >= half) break;
-          const int col = w.n * P.bn + half * c + 16 * i, left = P.N - col;
-          add_bias(acc[i], P.bias0 ? P.bias0 + col : nullptr, left);
-          if (draw.below) {
+          if (16 * i >= own) break;
+          const int col = col0 + 16 * i;
+          add_bias(acc[i], P.bias0 ? P.bias0 + col : nullptr, P.N - col);
+          if (draw.below) drop16(draw, acc[i], row0 + lane, col);
+        }
+        if constexpr (VEC) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t keep = draw.keep8(row0 + lane, col / 8 + h);
+          for (int v = 0; v < 128 / kCols; ++v) {
+            const int col = col0 + kCols * v;
+            if (kCols * v >= own || rows <= 0 || col >= P.N) break;
+            if (inputs) {
+              if (!(ok = wait(&sh.in[e][0], loads & 1u))) break;
+              ++loads;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                float2 &v = acc[i][4 * h + k];
-                v.x = keep >> (2 * k) & 1u ? v.x * draw.scale : 0.0f;
-                v.y = keep >> (2 * k + 1) & 1u ? v.y * draw.scale : 0.0f;
+              for (int j = 0; j < 8; ++j) {
+                const uint32_t at = piece_at(buf, lane, j);
+                const Piece<E> r(read_piece(at));
+                float2 *x = &acc[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8];
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) x[k] = add2(x[k], r.v[k]);
               }
             }
+            put(acc, &io.m[2], v);
+            if (inputs && kCols * (v + 1) < own) load_inputs(v + 1);
           }
-          if (P.in0) {
-            Cols<E, VEC> r;
-            r.load(P.in0, P.N, row0, rows, col, left, stage);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[i][k] = add2(acc[i][k], r.pair(k));
+          for (int i = 0; i < 8; ++i) {
+            if (16 * i >= own) break;
+            if (P.in0) {
+              Cols<E> r;
+              r.load(P.in0, P.N, row0, rows, col0 + 16 * i, P.N - col0 - 16 * i, stage);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) acc[i][k] = add2(acc[i][k], r.v[k]);
+            }
+            put_any(acc, P.out0, i);
           }
-          store16<E, VEC>(P.out0, P.N, row0, rows, col, left, acc[i], stage);
         }
       } else {
+        float *p = P.part + ((size_t)w.slice * P.T + row0 + lane) * P.part_ld + col0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (16 * i >= half) break;
-          const int col = w.n * P.bn + half * c + 16 * i;
-          store16<float, true>(P.part + (size_t)w.slice * P.T * P.part_ld, P.part_ld, row0, rows, col,
-                               P.part_ld - col, acc[i], stage);
+          if (16 * i >= own) break;
+          if (lane < rows && col0 + 16 * i < P.part_ld) store_own(p + 16 * i, acc[i]);
         }
       }
+    }
+    // nothing of this warp's is in flight when the CTA leaves: its stores, and loads whose wait did not end
+    if (one) {
+      stores_done();
+      if (issued != loads)
+        for (int b = 0; b < kBufs; ++b) tc::mbar_wait_bounded(&sh.in[e][b], loads & 1u, kDrain);
     }
     if (bad) set_status(status, GIFT_ERR_NONFINITE);
   }
@@ -567,14 +792,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int OP, typename E, bool VEC>
-cudaError_t launch(const Launch &L, const Params &P, const CUtensorMap *maps, int pairs, bool after) {
-  const cudaError_t e = ensure_dynamic_smem<k_product<OP, E, VEC>>(kSmem);
+template <int OP, typename E, bool VEC, bool MN>
+cudaError_t launch(const Launch &L, const Params &P, const CUtensorMap *maps, const IoMaps &io, int pairs, bool after) {
+  const cudaError_t e = ensure_dynamic_smem<k_product<OP, E, VEC, MN>>(Cfg<OP>::smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2 * (P.items < pairs ? P.items : pairs));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = Cfg<OP>::smem;
   cfg.stream = L.stream;
   // `after` the launch that makes the operands, itself ordered behind everything before it: this one may
   // start beside it (grid_wait).  Without that launch the kernel waits for its predecessors as usual.
@@ -583,26 +808,31 @@ cudaError_t launch(const Launch &L, const Params &P, const CUtensorMap *maps, in
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_product<OP, E, VEC>, P, maps[0], maps[1], maps[2], maps[3], L.status);
+  return cudaLaunchKernelEx(&cfg, k_product<OP, E, VEC, MN>, P, maps[0], maps[1], maps[2], maps[3], io,
+                            L.status);
 }
 
-template <int OP>
-cudaError_t launch_typed(const Launch &L, bool bf16, bool vec, const Params &P, const CUtensorMap *maps, int pairs,
+template <int OP, bool MN>
+cudaError_t launch_typed(const Launch &L, bool bf16, bool vec, const Params &P, const CUtensorMap *maps, const IoMaps &io, int pairs,
                          bool after) {
   if (bf16)
-    return vec ? launch<OP, __nv_bfloat16, true>(L, P, maps, pairs, after)
-               : launch<OP, __nv_bfloat16, false>(L, P, maps, pairs, after);
-  return vec ? launch<OP, float, true>(L, P, maps, pairs, after) : launch<OP, float, false>(L, P, maps, pairs, after);
+    return vec ? launch<OP, __nv_bfloat16, true, MN>(L, P, maps, io, pairs, after)
+               : launch<OP, __nv_bfloat16, false, MN>(L, P, maps, io, pairs, after);
+  return vec ? launch<OP, float, true, MN>(L, P, maps, io, pairs, after)
+             : launch<OP, float, false, MN>(L, P, maps, io, pairs, after);
 }
 
 // One launch per file, so that they compile side by side.
 cudaError_t launch_gated_forward(const Launch &L, bool bf16, bool vec, const Params &P, const CUtensorMap *maps,
-                                 int pairs, bool after);
+                                 const IoMaps &io, int pairs, bool after);
 cudaError_t launch_gated_backward(const Launch &L, bool bf16, bool vec, const Params &P, const CUtensorMap *maps,
-                                  int pairs, bool after);
-cudaError_t launch_linear(const Launch &L, bool bf16, bool vec, const Params &P, const CUtensorMap *maps, int pairs,
+                                  const IoMaps &io, int pairs, bool after);
+cudaError_t launch_linear(const Launch &L, bool bf16, bool vec, bool mn, const Params &P, const CUtensorMap *maps,
+                          const IoMaps &io, int pairs, bool after);
+cudaError_t launch_linear_mn(const Launch &L, bool bf16, bool vec, const Params &P, const CUtensorMap *maps, const IoMaps &io, int pairs,
+                             bool after);
+cudaError_t launch_slices(const Launch &L, bool bf16, bool mn, const Params &P, const CUtensorMap *maps, const IoMaps &io, int pairs,
                           bool after);
-cudaError_t launch_slices(const Launch &L, const Params &P, const CUtensorMap *maps, int pairs, bool after);
 
 }  // namespace product
 

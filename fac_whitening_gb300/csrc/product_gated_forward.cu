@@ -4,8 +4,8 @@
 namespace gift {
 namespace product {
 cudaError_t launch_gated_forward(const Launch &L, bool bf16, bool vec, const Params &P, const CUtensorMap *maps,
-                                 int pairs, bool after) {
-  return launch_typed<GATED_FORWARD>(L, bf16, vec, P, maps, pairs, after);
+                                 const IoMaps &io, int pairs, bool after) {
+  return launch_typed<GATED_FORWARD, false>(L, bf16, vec, P, maps, io, pairs, after);
 }
 }  // namespace product
 }  // namespace gift
