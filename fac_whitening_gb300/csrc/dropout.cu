@@ -16,8 +16,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 // 32 e + lane, whose bit lane (32 e + lane) / 16 drew.
 template <bool VEC>
 __device__ __forceinline__ uint32_t keep16(const Draw &d, uint32_t row, uint32_t c0, int lane) {
-  const uint32_t g = c0 / 8 + 2 * lane;
-  const uint32_t m = d.keep8(row, g) | d.keep8(row, g + 1) << 8;
+  const uint32_t m = d.keep16(row, c0 / 8 + 2 * lane);
   if (VEC) return m;
   uint32_t k = 0;
 #pragma unroll

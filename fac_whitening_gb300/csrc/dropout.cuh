@@ -41,6 +41,10 @@ struct Draw {
       m |= ((w[j] & 0xFFFFu) >= below ? 1u : 0u) << (2 * j) | ((w[j] >> 16) >= below ? 2u : 0u) << (2 * j);
     return m;
   }
+  // of the 16 columns from 8 group
+  __device__ __forceinline__ uint32_t keep16(uint32_t row, uint32_t group) const {
+    return keep8(row, group) | keep8(row, group + 1) << 8;
+  }
 };
 
 }  // namespace gift

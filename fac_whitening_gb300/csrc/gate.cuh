@@ -10,19 +10,25 @@ namespace gift {
 
 enum GateFn { GATE_SILU = 0, GATE_GELU = 1, GATE_GELU_TANH = 2 };
 
-// FP32 results take the library's expf and division (a few units in the last place); results that are rounded to
-// BF16 the hardware's exponential and reciprocal (about 2^-21 off, 2^-13 of BF16's rounding).
+// FP32 results take the library's expf and division (a few units in the last place).  Results that are rounded to
+// BF16 take the hardware's exponential and reciprocal (about 2^-21 off, 2^-13 of BF16's rounding; results below 2^-126
+// are 0, where s is 1 to the last place): with expf and a rounded division the gate's arithmetic took half as long again.
 template <bool ACCURATE>
 __device__ __forceinline__ float sigmoid(float z) {
   if (ACCURATE) return 1.0f / (1.0f + expf(-z));
-  return __fdividef(1.0f, 1.0f + __expf(-z));   // 0 where the exponential is infinite or past 2^126
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));   // 0 where e is infinite
+  return s;
 }
+
+constexpr float kTanhScale = 1.5957691216057308f;   // 2 sqrt(2 / pi)
+__device__ __forceinline__ float tanh_inner(float g) { return kTanhScale * fmaf(0.044715f * g * g, g, g); }
 
 template <int FN, bool ACCURATE>
 __device__ __forceinline__ float gate_value(float g) {
   if (FN == GATE_GELU) return g * (0.5f * erfcf(g * -0.70710678118654752f));
-  const float c = 1.5957691216057308f;
-  return g * sigmoid<ACCURATE>(FN == GATE_SILU ? g : c * fmaf(0.044715f * g * g, g, g));
+  return g * sigmoid<ACCURATE>(FN == GATE_SILU ? g : tanh_inner(g));
 }
 
 // a(g), and a'(g) in `slope`
@@ -33,13 +39,14 @@ __device__ __forceinline__ float gate_slope(float g, float &slope) {
     slope = fmaf(g * 0.3989422804014327f, ACCURATE ? expf(e) : __expf(e), phi);
     return g * phi;
   }
-  const float c = 1.5957691216057308f;
-  const float s = sigmoid<ACCURATE>(FN == GATE_SILU ? g : c * fmaf(0.044715f * g * g, g, g));
-  const float t = s * (1.0f - s);
-  // z' may overflow where s is 0 or 1 already
-  if (FN == GATE_SILU) slope = fmaf(g, t, s);
-  else slope = t == 0.0f ? s : fmaf(g * (c * fmaf(3.0f * 0.044715f * g, g, 1.0f)), t, s);
-  return g * s;
+  const float s = sigmoid<ACCURATE>(FN == GATE_SILU ? g : tanh_inner(g)), a = g * s;
+  if (FN == GATE_SILU) {
+    slope = fmaf(a, 1.0f - s, s);
+  } else {   // z' may overflow where s is 0 or 1 already
+    const float t = s * (1.0f - s);
+    slope = t == 0.0f ? s : fmaf(g * (kTanhScale * fmaf(3.0f * 0.044715f * g, g, 1.0f)), t, s);
+  }
+  return a;
 }
 
 }  // namespace gift

@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(256) k_join_linear(const float *__restrict__ p
 }
 
 // ---- host ---------------------------------------------------------------------------------------------
-constexpr int kSegment = 8, kSegment6 = 6;   // stages of a segment: 512 k, or one block of 64 k of FP32's terms
+// Most stages of a segment: 1024 k, 768 for the forward product, or one block of 64 k of FP32's terms
+constexpr int kSegment = 16, kSegmentForward = 12, kSegment6 = 6;
 
 // `planes` matrices of rows x cols BF16, rows `pitch` bytes apart, read in boxes of 64 columns x `box` rows
 bool boxes(CUtensorMap *m, const void *base, int rows, int cols, size_t pitch, int planes, int box) {
@@ -186,16 +187,19 @@ Plan plan_linear(int sms, bool bf16, int T, int N, int kb) {
 
 int pairs_of(const Launch &L) { return L.sms / 2 > 1 ? L.sms / 2 : 1; }
 
-Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, bool b_mn, int kb) {
+Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, bool b_mn, int kb,
+                 int slices = 1, int segment = kSegment) {
   Params P{};
   P.T = T;
   P.N = N;
   P.mt = ceil_div(T, product::kTileRows);
   P.nt = ceil_div(N, columns);
-  P.slices = 1;
-  P.items = P.mt * P.nt;
+  P.slices = slices;
+  P.items = P.mt * P.nt * slices;
   P.kb = P.kb1 = kb;
-  P.seg = bf16 ? kSegment : kSegment6;
+  // segments of equal length, so that none ends long before the next is folded
+  const int most = ceil_div(kb, slices);
+  P.seg = bf16 ? ceil_div(most, ceil_div(most, segment)) : kSegment6;
   P.bn = bn;
   P.idesc = tc::idesc_bf16(256, bn) | (b_mn ? 1u << 16 : 0u);
   P.budget = L.barrier_wait;
@@ -220,7 +224,7 @@ cudaError_t launch_gated_forward(const Launch &L, bool bf16, const GatedForward 
   maps[0] = maps[1] = made_maps[0];
   maps[2] = made_maps[1];
   maps[3] = made_maps[2];
-  Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK));
+  Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK), 1, kSegmentForward);
   P.fn = a.fn;
   P.fmt = a.fmt;
   P.groups = ceil_div(a.f, kActGroup);
@@ -276,8 +280,6 @@ cudaError_t linear(const Launch &L, bool bf16, bool mn, const Plan &p, Params P,
     if (!unit_maps(io, bf16, P.T, P.N, P.in0, nullptr, P.out0, nullptr, nullptr, vec)) return cudaErrorInvalidValue;
     return product::launch_linear(L, bf16, vec, mn, P, maps, io, pairs_of(L), made);
   }
-  P.slices = p.slices;
-  P.items *= p.slices;
   P.part = part;
   P.part_ld = ceil_div(P.N, 16) * 16;
   const cudaError_t e = product::launch_slices(L, bf16, mn, P, maps, product::IoMaps{}, pairs_of(L), made);
@@ -314,7 +316,7 @@ cudaError_t launch_linear_forward(const Launch &L, bool bf16, const LinearForwar
   const cudaError_t e = operands(L, bf16, src, 2, a.ws, made_maps, made);
   if (e != cudaSuccess) return e;
   const CUtensorMap maps[4] = {made_maps[0], made_maps[0], made_maps[1], made_maps[1]};
-  Params P = params_of(L, bf16, a.T, a.d_out, p.bn, p.bn, false, kb);
+  Params P = params_of(L, bf16, a.T, a.d_out, p.bn, p.bn, false, kb, p.slices);
   P.bias0 = a.bias;
   P.in0 = a.residual;
   P.out0 = a.y;
@@ -347,7 +349,7 @@ cudaError_t launch_input_grad(const Launch &L, bool bf16, const InputGrad &a) {
   const cudaError_t e = operands(L, bf16, src, 2 * n, a.ws, m, made);
   if (e != cudaSuccess) return e;
   const CUtensorMap maps[4] = {m[0], m[n == 2 ? 2 : 0], m[1], m[n == 2 ? 3 : 1]};
-  Params P = params_of(L, bf16, a.T, a.d_in, p.bn, p.bn, true, n * kb);
+  Params P = params_of(L, bf16, a.T, a.d_in, p.bn, p.bn, true, n * kb, p.slices);
   P.kb1 = kb;
   P.out0 = a.dx;
   return linear(L, bf16, true, p, P, maps, made, a.part);

@@ -7,9 +7,10 @@
 //   warps 0, 2   TMA: stages of 64 k, A's 128 x 64 and B's up to 128 x 64 elements;
 //   warp 1       the pair's first CTA issues 256 x N x 16 MMAs; the second one's reports its stages to the first;
 //   warps 4-11   fold and epilogue: a thread has one token and half of the tile's columns.
-// The tensor core truncates its sums, so a segment of at most 512 k goes into one of two accumulators in tensor
-// memory and is added to FP32 registers to nearest while the other is filled.  The epilogue runs from those
-// registers while the next tile's first two segments are multiplied.
+// The tensor core truncates its sums, so a segment of at most 1024 k (768 for the forward product, whose 8-bit checkpoint
+// tells FP32's last bits) goes into one of two accumulators in tensor memory and is added to FP32 registers to
+// nearest while the other is filled.  The epilogue runs from those registers while the next tile's first two
+// segments are multiplied: 1536 k are two segments, and the epilogue has a tile's whole time.
 // The gated forward product takes its two projections as one product of 128 + 128 columns: the first CTA loads
 // the gate's rows, the second the other projection's, and both halves of a row meet in one thread.
 // FP32 operands are three BF16 terms each (operand.cuh); a block of 64 k then takes six stages, the products i + j <= 2
@@ -205,6 +206,10 @@ __device__ __forceinline__ void load_unit(uint32_t buf, const CUtensorMap *map, 
       "l"(map), "r"(col), "r"(row), "r"(bar)
       : "memory");
 }
+// bring a unit into L2 ahead of its load
+__device__ __forceinline__ void prefetch_unit(const CUtensorMap *map, int col, int row) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];\n" ::"l"(map), "r"(col), "r"(row) : "memory");
+}
 __device__ __forceinline__ void store_unit(uint32_t buf, const CUtensorMap *map, int col, int row) {
   asm volatile(
       "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n"
@@ -339,17 +344,12 @@ __device__ __forceinline__ void gate_backward(float2 *d, float2 *du, const float
     d[k] = mul2(mul2(d[k], u[k]), slope);
   }
 }
-// 16 bits of dropout for a row's columns col to col + 15: dropped to 0, or scaled
-__device__ __forceinline__ void drop16(const Draw &draw, float2 *v, int row, int col) {
+// dropped to 0, or scaled
+__device__ __forceinline__ void drop16(const Draw &draw, float2 *v, uint32_t keep) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t keep = draw.keep8(row, col / 8 + h);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float2 &x = v[4 * h + k];
-      x.x = keep >> (2 * k) & 1u ? x.x * draw.scale : 0.0f;
-      x.y = keep >> (2 * k + 1) & 1u ? x.y * draw.scale : 0.0f;
-    }
+  for (int k = 0; k < 8; ++k) {
+    v[k].x = keep >> (2 * k) & 1u ? v[k].x * draw.scale : 0.0f;
+    v[k].y = keep >> (2 * k + 1) & 1u ? v[k].y * draw.scale : 0.0f;
   }
 }
 
@@ -560,7 +560,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (kBufs == 2) load_unit(buf + kUnit, &io.m[1], col0 + kCols * v, row0, tc::smem_u32(&sh.in[e][1]));
       };
       const bool inputs = VEC && (OP == GATED_BACKWARD || (OP == LINEAR && P.in0));
-      if (inputs) load_inputs(0);
+      if (inputs) {
+        load_inputs(0);
+        if (one && rows > 0)
+          for (int col = kCols; col < own && col0 + col < P.N; col += kCols) {
+            prefetch_unit(&io.m[0], col0 + col, row0);
+            if (kBufs == 2) prefetch_unit(&io.m[1], col0 + col, row0);
+          }
+      }
+      // dropout's bits are drawn while the tile is multiplied: 16 columns each
+      uint32_t keep[8];
+      if (OP == LINEAR && draw.below) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (16 * i < own) keep[i] = draw.keep16(row0 + lane, (col0 + 16 * i) / 8);
+      }
       float2 acc[8][8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -613,24 +627,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           add_bias(acc[i], P.bias0 ? P.bias0 + col : nullptr, left);
           add_bias(acc[4 + i], P.bias1 ? P.bias1 + col : nullptr, left);
         }
+        // With one buffer, a store's read of it is covered by arithmetic: g, a(g) u in g's place, u.
         if (P.out1) {
-          if constexpr (VEC) {
 #pragma unroll
-            for (int v = 0; v < 64 / kCols; ++v) {
-              put(acc, &io.m[1], v);
-              put(acc + 4, &io.m[2], v);
-            }
-          } else {
+          for (int v = 0; v < 64 / kCols; ++v)
+            if constexpr (VEC) put(acc, &io.m[1], v);
+          if constexpr (!VEC) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              put_any(acc, P.out1, i);
-              put_any(acc + 4, P.out2, i);
-            }
+            for (int i = 0; i < 4; ++i) put_any(acc, P.out1, i);
           }
         }
         if (P.fn == GATE_SILU) gate_forward<GATE_SILU, kAccurate>(acc);
         else if (P.fn == GATE_GELU) gate_forward<GATE_GELU, kAccurate>(acc);
         else gate_forward<GATE_GELU_TANH, kAccurate>(acc);
+        if (P.out1) {
+#pragma unroll
+          for (int v = 0; v < 64 / kCols; ++v)
+            if constexpr (VEC) put(acc + 4, &io.m[2], v);
+          if constexpr (!VEC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put_any(acc + 4, P.out2, i);
+          }
+        }
         uint8_t(&scale)[2][128] = sh.scale[tile & 1];
         uint32_t sb = 0;
         if (P.codes) {
@@ -729,7 +747,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (16 * i >= own) break;
           const int col = col0 + 16 * i;
           add_bias(acc[i], P.bias0 ? P.bias0 + col : nullptr, P.N - col);
-          if (draw.below) drop16(draw, acc[i], row0 + lane, col);
+          if (draw.below) drop16(draw, acc[i], keep[i]);
         }
         if constexpr (VEC) {
 #pragma unroll
