@@ -5,7 +5,7 @@
 // A pair of CTAs (a cluster of two SMs, cta_group::2) owns 256 tokens x up to 256 columns: each CTA holds 128 of
 // the tokens and half of B's columns.  Per CTA:
 //   warps 0, 2   TMA: stages of 64 k, A's 128 x 64 and B's up to 128 x 64 elements;
-//   warp 1       the pair's first CTA issues 256 x N x 16 MMAs; the second one's reports its stages to the first;
+//   warp 1       the pair's first CTA issues 256 x N x 16 MMAs (both CTAs' copies complete on its barriers);
 //   warps 4-11   fold and epilogue: a thread has one token and half of the tile's columns.
 // The tensor core truncates its sums, so a segment of at most 1024 k (768 for the forward product, whose 8-bit checkpoint
 // tells FP32's last bits) goes into one of two accumulators in tensor memory and is added to FP32 registers to
@@ -93,16 +93,17 @@ struct Item {
 
 constexpr int kMostStages = 6;
 struct __align__(16) Shared {
-  uint64_t full[kMostStages], empty[kMostStages];   // loaded; multiplied (in both CTAs)
-  uint64_t other[kMostStages];                      // first CTA: the second one's stage is loaded
-  uint64_t in[kEpiWarps][2];                        // an epilogue warp's buffers: loaded
+  uint64_t full[kMostStages], empty[kMostStages];   // first CTA: loaded in both; multiplied (in both CTAs)
+  uint64_t in[kEpiWarps];                           // an epilogue warp's buffer: loaded
   uint64_t dfull[2], dempty[2];             // accumulators: summed; folded by both CTAs
   uint64_t met[4];                          // a row's two column halves have left their scale bytes
   uint64_t drained;
   uint8_t scale[2][2][128];                 // [tile parity][half][row]: the scale byte that the half's columns ask for
+  uint32_t issued[4];                       // copies that the pair's TMA threads made, and whether one gave up
   uint32_t tmem;
   volatile int failed;
 };
+constexpr uint32_t kGaveUp = 1u << 31;
 
 // D (+)= A[smem] B[smem], one 256 x N x 16 step over both CTAs
 __device__ __forceinline__ void mma_pair_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
@@ -145,10 +146,25 @@ __device__ __forceinline__ bool test_wait_at(uint32_t bar, uint32_t parity) {   
 __device__ __forceinline__ void expect_at(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void load_at(uint32_t dst, const CUtensorMap *tmap, int x, int y, int z, uint32_t bar) {
+// Of shared memory of the pair's CTA r: its address, an arrival with `bytes` to come, a word's write; and a copy into this
+// CTA that completes on a barrier of either.  A copy that the first CTA has to be told of by the second costs a
+// stage of latency: 16384 x 1536 x 6144 gated forward 378 us with a thread that passed them on, 365 without.
+__device__ __forceinline__ uint32_t of_cta(uint32_t at, uint32_t r) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(at), "r"(r));
+  return a;
+}
+__device__ __forceinline__ void expect_in_cluster(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void write_in_cluster(uint32_t at, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void load_in_cluster(uint32_t dst, const CUtensorMap *tmap, int x, int y, int z,
+                                                uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
-          dst),
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
+      "[%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
@@ -206,10 +222,6 @@ __device__ __forceinline__ void load_unit(uint32_t buf, const CUtensorMap *map, 
       "l"(map), "r"(col), "r"(row), "r"(bar)
       : "memory");
 }
-// bring a unit into L2 ahead of its load
-__device__ __forceinline__ void prefetch_unit(const CUtensorMap *map, int col, int row) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];\n" ::"l"(map), "r"(col), "r"(row) : "memory");
-}
 __device__ __forceinline__ void store_unit(uint32_t buf, const CUtensorMap *map, int col, int row) {
   asm volatile(
       "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n"
@@ -217,47 +229,59 @@ __device__ __forceinline__ void store_unit(uint32_t buf, const CUtensorMap *map,
       "r"(col), "r"(row), "r"(buf)
       : "memory");
 }
+// A unit by the warp's own copies (8 lanes to a row, 32 rows), for the gated backward product: TMA's queue serves the
+// product's operands there while these come from HBM (16384 x 1536 x 6144: 271 us by TMA, 248 so).
+template <typename E>
+__device__ __forceinline__ void load_rows(uint32_t buf, const void *base, size_t ld, int row0, int rows, int col, int n) {
+  const int lane = threadIdx.x & 31, j = lane & 7;
+  constexpr int per = 16 / sizeof(E);
+  const E *p = static_cast<const E *>(base) + (size_t)row0 * ld + col + per * j;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    if (r < rows && per * j < n)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(piece_at(buf, r, j)), "l"(p + (size_t)r * ld)
+                   : "memory");
+  }
+}
+__device__ __forceinline__ void loads_done() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
 // ---- rows of any alignment: 16 columns at a time through a 32 x 16 tile, 16 lanes to a row -----------------------
 template <typename E>
-struct Cols {
-  float2 v[8];
-  __device__ __forceinline__ void load(const void *base, size_t ld, int row0, int rows, int col, int n, float *stage) {
-    const int lane = threadIdx.x & 31, c = lane & 15;
-    const E *p = static_cast<const E *>(base) + (size_t)row0 * ld + col + c;
-    float x[16];   // all loads before the first store
+__device__ __forceinline__ void load_tile(const void *base, size_t ld, int row0, int rows, int col, int n,
+                                          float *stage) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  const E *p = static_cast<const E *>(base) + (size_t)(row0 + (lane >> 4)) * ld + col + c;
+  float x[16];   // all loads before the first store
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int r = 2 * k + (lane >> 4);
-      x[k] = r < rows && c < n ? ld1(p + (size_t)r * ld) : 0.0f;
-    }
+  for (int k = 0; k < 16; ++k, p += 2 * ld) x[k] = 2 * k + (lane >> 4) < rows && c < n ? ld1(p) : 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) stage[(2 * k + (lane >> 4)) * kPitch + c] = x[k];
-    __syncwarp();
+  for (int k = 0; k < 16; ++k) stage[(2 * k + (lane >> 4)) * kPitch + c] = x[k];
+}
+template <typename E>
+__device__ __forceinline__ void store_tile(void *base, size_t ld, int row0, int rows, int col, int n,
+                                           const float *stage) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  E *p = static_cast<E *>(base) + (size_t)(row0 + (lane >> 4)) * ld + col + c;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = make_float2(stage[lane * kPitch + 2 * k], stage[lane * kPitch + 2 * k + 1]);
-    __syncwarp();
+  for (int k = 0; k < 16; ++k, p += 2 * ld) {
+    const int r = 2 * k + (lane >> 4);
+    if (r < rows && c < n) st1(p, stage[r * kPitch + c]);
   }
-};
-
+}
 template <typename E>
 __device__ __forceinline__ void store16(void *base, size_t ld, int row0, int rows, int col, int n, const float2 *v,
                                         float *stage) {
-  const int lane = threadIdx.x & 31, c = lane & 15;
-  E *p = static_cast<E *>(base) + (size_t)row0 * ld + col + c;
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     stage[lane * kPitch + 2 * k] = v[k].x;
     stage[lane * kPitch + 2 * k + 1] = v[k].y;
   }
   __syncwarp();
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int r = 2 * k + (lane >> 4);
-    if (r < rows && c < n) st1(p + (size_t)r * ld, stage[r * kPitch + c]);
-  }
+  store_tile<E>(base, ld, row0, rows, col, n, stage);
   __syncwarp();
 }
 
@@ -374,17 +398,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) alloc_pair(&sh.tmem);
   if (tid == 32) {
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&sh.full[s], 2);
+      tc::mbar_init(&sh.full[s], 4);
       tc::mbar_init(&sh.empty[s], 1);
-      tc::mbar_init(&sh.other[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&sh.dfull[b], 1);
       tc::mbar_init(&sh.dempty[b], 2 * kEpiWarps);
     }
     for (int q = 0; q < 4; ++q) tc::mbar_init(&sh.met[q], 2);
-    for (int e = 0; e < kEpiWarps; ++e)
-      for (int b = 0; b < 2; ++b) tc::mbar_init(&sh.in[e][b], 1);
+    for (int e = 0; e < kEpiWarps; ++e) tc::mbar_init(&sh.in[e], 1);
     tc::mbar_init(&sh.drained, 1);
     tc::fence_mbar_init();
     sh.failed = 0;
@@ -432,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // One thread each.  A stage's 512 clocks are few for what a single thread does between two of them, so these loops keep
     // their addresses running, and A and B have a thread each (one for both, its slot and terms computed per stage, took
     // 550 clocks a stage).
-    const uint32_t full = tc::smem_u32(sh.full), empty = tc::smem_u32(sh.empty), other = tc::smem_u32(sh.other);
+    const uint32_t full = of_cta(tc::smem_u32(sh.full), 0), empty = tc::smem_u32(sh.empty);
     const uint32_t ring = tc::smem_u32(sm);
     if (!elect_one()) {
     } else if (warp == 0 || warp == 2) {
@@ -447,12 +469,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto stage = [&](const CUtensorMap *map, int k, int y, int term) {
         const uint32_t bar = full + 8 * at, dst = base + at * kStage;
         if (!(ok = hold(empty + 8 * at, parity))) return;
-        expect_at(bar, bytes);
+        expect_in_cluster(bar, bytes);
         if (MN && !is_a) {
-          load_at(dst, map, y, k, term, bar);
-          if (boxes == 2) load_at(dst + kBox, map, y + 64, k, term, bar);
+          load_in_cluster(dst, map, y, k, term, bar);
+          if (boxes == 2) load_in_cluster(dst + kBox, map, y + 64, k, term, bar);
         } else {
-          load_at(dst, map, k, y, term, bar);
+          load_in_cluster(dst, map, k, y, term, bar);
         }
         advance<kStages>(at, parity);
         ++g;
@@ -479,18 +501,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           walk(is_a ? &tm_a1 : &tm_b1, max(w.k0 - P.kb1, 0) * kK, (w.k1 - P.kb1) * kK);
         }
       }
-      // leave no arrival of the MMAs' commits behind: the last stages'
+      // The last stages' MMAs are done (and leave no arrival of their commits behind): all copies have landed.
       for (uint32_t r = 1; ok && r <= kStages && r <= g; ++r) {
         const Slot<kStages> s(g - r);
         ok = hold(empty + 8 * s.at, s.parity);
       }
-      landed<kStages>(sh.full, g);
       // the pair's first CTA may have a wait of its own to end before its last commit
       tc::mbar_wait_bounded(&sh.drained, 0, P.budget + kDrain);
+      const uint32_t at_issued = tc::smem_u32(&sh.issued[2 * rank + (is_a ? 0 : 1)]);
+      for (uint32_t r = 0; r < 2; ++r) write_in_cluster(of_cta(at_issued, r), g | (ok ? 0u : kGaveUp));
     } else if (warp == 1 && rank == 0) {
       // ---------------- MMA ----------------
       const uint32_t b_lead = MN ? (uint32_t)(kBox >> 4) << 16 : 1u << 16, b_step = MN ? 128u : 2u;
-      const uint32_t dempty = tc::smem_u32(sh.dempty), idesc = P.idesc;
+      const uint32_t loaded = tc::smem_u32(sh.full), dempty = tc::smem_u32(sh.dempty), idesc = P.idesc;
       const int seg = P.seg;
       uint32_t at = 0, parity = 0, n = 0;   // slot, segments
       bool ok = true, there = false;        // there: the stage was seen to be loaded
@@ -502,11 +525,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tc::fence_after_sync();
           uint32_t accumulate = 0;
           for (int j = min(seg, left); j > 0; --j) {
-            if (!there && !(ok = hold(full + 8 * at, parity) && hold(other + 8 * at, parity))) break;
+            if (!there && !(ok = hold(loaded + 8 * at, parity))) break;
             const uint32_t a = (ring + at * kStage) >> 4, b = a + (kABytes >> 4);
             uint64_t *const done = &sh.empty[at];
             advance<kStages>(at, parity);
-            there = test_wait_at(full + 8 * at, parity) && test_wait_at(other + 8 * at, parity);
+            there = test_wait_at(loaded + 8 * at, parity);
             tc::fence_after_sync();
 #pragma unroll
             for (int k = 0; k < kK / 16; ++k) {
@@ -519,18 +542,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       commit_pair(&sh.drained);
-    } else if (warp == 1) {
-      // ---------------- the second CTA's stages ----------------
-      uint32_t total = 0;
-      for (int it = pair; it < P.items; it += pairs) {
-        const Item w(P, it);
-        total += (uint32_t)(w.k1 - w.k0) * kTerms;
-      }
-      for (uint32_t g = 0, at = 0, parity = 0; g < total; ++g) {
-        if (!hold(full + 8 * at, parity)) break;
-        arrive_first(&sh.other[at]);
-        advance<kStages>(at, parity);
-      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
@@ -553,21 +564,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int col0 = kGated ? 128 * w.n + 64 * c : w.n * P.bn + first * c;
       // the inputs of unit v into the warp's buffers, whose last contents have been stored
       auto load_inputs = [&](int v) {
-        if (!one || rows <= 0 || col0 + kCols * v >= P.N) return;
-        ++issued;
-        stores_read();
-        load_unit(buf, &io.m[0], col0 + kCols * v, row0, tc::smem_u32(&sh.in[e][0]));
-        if (kBufs == 2) load_unit(buf + kUnit, &io.m[1], col0 + kCols * v, row0, tc::smem_u32(&sh.in[e][1]));
+        const int col = col0 + kCols * v;
+        if (rows <= 0 || col >= P.N) return;
+        if (one) stores_read();
+        __syncwarp();
+        if constexpr (OP == GATED_BACKWARD) {
+          load_rows<E>(buf, P.in0, P.N, row0, rows, col, P.N - col);
+          load_rows<E>(buf + kUnit, P.in1, P.N, row0, rows, col, P.N - col);
+        } else if (one) {
+          ++issued;
+          load_unit(buf, &io.m[0], col, row0, tc::smem_u32(&sh.in[e]));
+        }
       };
       const bool inputs = VEC && (OP == GATED_BACKWARD || (OP == LINEAR && P.in0));
-      if (inputs) {
-        load_inputs(0);
-        if (one && rows > 0)
-          for (int col = kCols; col < own && col0 + col < P.N; col += kCols) {
-            prefetch_unit(&io.m[0], col0 + col, row0);
-            if (kBufs == 2) prefetch_unit(&io.m[1], col0 + col, row0);
-          }
-      }
+      if (inputs) load_inputs(0);
       // dropout's bits are drawn while the tile is multiplied: 16 columns each
       uint32_t keep[8];
       if (OP == LINEAR && draw.below) {
@@ -704,8 +714,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int v = 0; v < 128 / kCols; ++v) {
               const int col = col0 + kCols * v;
               if (kCols * v >= own || rows <= 0 || col >= P.N) break;
-              if (!(ok = wait(&sh.in[e][0], loads & 1u) && wait(&sh.in[e][1], loads & 1u))) break;
-              ++loads;
+              loads_done();
+              __syncwarp();
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const uint32_t at = piece_at(buf, lane, j);
@@ -728,13 +738,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 8; ++i) {
               if (16 * i >= own) break;
               const int col = col0 + 16 * i, left = P.N - col;
-              Cols<E> g, u;
-              g.load(P.in0, P.N, row0, rows, col, left, stage);
-              u.load(P.in1, P.N, row0, rows, col, left, stage);
-              float2 du[8];
-              gate_backward<FN, kAccurate, 8>(acc[i], du, g.v, u.v);
-              store16<E>(P.out0, P.N, row0, rows, col, left, acc[i], stage);
-              store16<E>(P.out1, P.N, row0, rows, col, left, du, stage);
+              float *const other = stage + kUnit / 4;
+              load_tile<E>(P.in0, P.N, row0, rows, col, left, stage);
+              load_tile<E>(P.in1, P.N, row0, rows, col, left, other);
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int at = lane * kPitch + 2 * k;
+                const float2 g = make_float2(stage[at], stage[at + 1]), u = make_float2(other[at], other[at + 1]);
+                float2 du;
+                gate_backward<FN, kAccurate, 1>(&acc[i][k], &du, &g, &u);
+                stage[at] = acc[i][k].x;
+                stage[at + 1] = acc[i][k].y;
+                other[at] = du.x;
+                other[at + 1] = du.y;
+              }
+              __syncwarp();
+              store_tile<E>(P.out0, P.N, row0, rows, col, left, stage);
+              store_tile<E>(P.out1, P.N, row0, rows, col, left, other);
+              __syncwarp();
             }
           }
         };
@@ -755,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int col = col0 + kCols * v;
             if (kCols * v >= own || rows <= 0 || col >= P.N) break;
             if (inputs) {
-              if (!(ok = wait(&sh.in[e][0], loads & 1u))) break;
+              if (!(ok = wait(&sh.in[e], loads & 1u))) break;
               ++loads;
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -774,10 +796,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 8; ++i) {
             if (16 * i >= own) break;
             if (P.in0) {
-              Cols<E> r;
-              r.load(P.in0, P.N, row0, rows, col0 + 16 * i, P.N - col0 - 16 * i, stage);
+              load_tile<E>(P.in0, P.N, row0, rows, col0 + 16 * i, P.N - col0 - 16 * i, stage);
+              __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 8; ++k) acc[i][k] = add2(acc[i][k], r.v[k]);
+              for (int k = 0; k < 8; ++k) {
+                const int at = lane * kPitch + 2 * k;
+                acc[i][k] = add2(acc[i][k], make_float2(stage[at], stage[at + 1]));
+              }
+              __syncwarp();
             }
             put_any(acc, P.out0, i);
           }
@@ -794,9 +820,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // nothing of this warp's is in flight when the CTA leaves: its stores, and loads whose wait did not end
     if (one) {
       stores_done();
-      if (issued != loads)
-        for (int b = 0; b < kBufs; ++b) tc::mbar_wait_bounded(&sh.in[e][b], loads & 1u, kDrain);
+      if (issued != loads) tc::mbar_wait_bounded(&sh.in[e], loads & 1u, kDrain);
     }
+    if (OP == GATED_BACKWARD) loads_done();
     if (bad) set_status(status, GIFT_ERR_NONFINITE);
   }
 
@@ -804,6 +830,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   cluster_sync();   // the peer no longer arrives on this CTA's barriers, and its MMAs are done
+  const uint32_t most = max(max(sh.issued[0], sh.issued[1]), max(sh.issued[2], sh.issued[3]));
+  if (most & kGaveUp) {   // the same in both CTAs
+    // The copies that were made land on the first CTA's barriers: it arrives for those that were not, and waits.
+    if (rank == 0 && tid == 0) {
+      uint32_t g = 0;
+      for (int i = 0; i < 4; ++i) g = max(g, sh.issued[i] & ~kGaveUp);
+      for (int i = 0; i < 4; ++i)
+        for (uint32_t u = sh.issued[i] & ~kGaveUp; u < g; ++u) tc::mbar_arrive(&sh.full[u % kStages]);
+      landed<kStages>(sh.full, g);
+    }
+    cluster_sync();
+  }
   if (warp == 0) {
     tc::fence_after_sync();
     dealloc_pair(tmem);
