@@ -1,7 +1,7 @@
 // Dropout by itself: y = residual + drop(x + bias), and its backward pass dx = drop(dy), dbias = sum_t dx.
 //
-// HBM bounds it.  A warp keeps one piece of 512 columns (16 a lane, so that a lane draws two counters for its own
-// columns) and walks down the rows of its CTA's slice; the bits are drawn where they are used.
+// HBM bounds it.  A warp keeps one piece of 256 columns (8 a lane: one counter) and walks down the rows of its CTA's
+// slice, two at a time so that their loads are in flight together; the bits are drawn where they are used.
 #include "act.cuh"
 #include "dropout.cuh"
 #include "kernels.cuh"
@@ -11,17 +11,24 @@ namespace gift {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kC = 8, kCols = 32 * kC;   // columns of a lane, of a piece
+constexpr int kRows = 2;                 // rows of a step of a warp
 
-// The lane's 16 bits as its registers hold the columns: VEC bit e is column 16 lane + e; otherwise column
-// 32 e + lane, whose bit lane (32 e + lane) / 16 drew.
+// Drop a lane's values of a row: VEC, its own columns; otherwise value e is column 32 e + lane, whose bit lane
+// (32 e + lane) / 8 drew.
 template <bool VEC>
-__device__ __forceinline__ uint32_t keep16(const Draw &d, uint32_t row, uint32_t c0, int lane) {
-  const uint32_t m = d.keep16(row, c0 / 8 + 2 * lane);
-  if (VEC) return m;
-  uint32_t k = 0;
+__device__ __forceinline__ void drop(const Draw &d, float2 *v, uint32_t row, uint32_t c0, int lane) {
+  if (VEC) {
+    d.apply8(v, row, c0 / 8 + lane);
+    return;
+  }
+  const uint32_t m = d.keep8(row, c0 / 8 + lane);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) k |= (__shfl_sync(0xFFFFFFFFu, m, 2 * e + (lane >> 4)) >> (lane & 15) & 1u) << e;
-  return k;
+  for (int k = 0; k < kC / 2; ++k) {
+    const uint32_t a = __shfl_sync(0xFFFFFFFFu, m, 8 * k + (lane >> 3)), b = __shfl_sync(0xFFFFFFFFu, m, 8 * k + 4 + (lane >> 3));
+    v[k].x = a >> (lane & 7) & 1u ? v[k].x * d.scale : 0.0f;
+    v[k].y = b >> (lane & 7) & 1u ? v[k].y * d.scale : 0.0f;
+  }
 }
 
 struct Args {
@@ -35,48 +42,53 @@ struct Args {
 
 template <typename E, bool VEC, bool SUMS>
 __global__ void __launch_bounds__(kThreads) k_dropout(const Args a) {
-  __shared__ float sh[SUMS ? kWarps : 1][SUMS ? 16 * 33 : 1];
+  __shared__ float sh[SUMS ? kWarps : 1][SUMS ? kC * 33 : 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int c0 = blockIdx.x * kPiece, n = a.d - c0;
+  const int c0 = blockIdx.x * kCols, n = a.d - c0;
   const int t0 = blockIdx.y * a.rows, t1 = min(a.T, t0 + a.rows);
   const Draw draw(a.drop);
-  float2 bias[8], sum[8];
+  float2 bias[kC / 2], sum[kC / 2];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kC / 2; ++k) {
     bias[k] = sum[k] = both(0.0f);
     if (!SUMS && a.bias) {
-      const int c = piece_col<VEC>(lane, 2 * k), c1 = piece_col<VEC>(lane, 2 * k + 1);
+      const int c = piece_col<VEC, kC>(lane, 2 * k), c1 = piece_col<VEC, kC>(lane, 2 * k + 1);
       bias[k] = make_float2(c < n ? a.bias[c0 + c] : 0.0f, c1 < n ? a.bias[c0 + c1] : 0.0f);
     }
   }
   const E *x = static_cast<const E *>(a.x) + c0, *res = static_cast<const E *>(a.residual);
-#pragma unroll 2
-  for (int t = t0 + w; t < t1; t += kWarps) {
-    const size_t at = (size_t)t * a.d;
-    Raw<E> r, q;
-    load_piece<VEC>(x + at, n, lane, r);
-    if (!SUMS && res) load_piece<VEC>(res + c0 + at, n, lane, q);
-    const uint32_t keep = draw.below ? keep16<VEC>(draw, t, c0, lane) : 0xFFFFu;
-    float2 v[8];
+  for (int t = t0 + w; t < t1; t += kRows * kWarps) {
+    Raw<E, kC> r[kRows], q[kRows];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[k] = SUMS ? r.pair(k) : add2(r.pair(k), bias[k]);
-      if (draw.below) {
-        v[k].x = keep >> (2 * k) & 1u ? v[k].x * draw.scale : 0.0f;
-        v[k].y = keep >> (2 * k + 1) & 1u ? v[k].y * draw.scale : 0.0f;
-      }
-      if (SUMS) sum[k] = add2(sum[k], v[k]);
-      else if (res) v[k] = add2(v[k], q.pair(k));
+    for (int u = 0; u < kRows; ++u) {
+      const size_t at = (size_t)(t + u * kWarps) * a.d;
+      if (t + u * kWarps >= t1) break;
+      load_piece<VEC>(x + at, n, lane, r[u]);
+      if (!SUMS && res) load_piece<VEC>(res + c0 + at, n, lane, q[u]);
     }
-    store_piece<VEC>(static_cast<E *>(a.y) + c0 + at, n, lane, v);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int row = t + u * kWarps;
+      if (row >= t1) break;
+      float2 v[kC / 2];
+#pragma unroll
+      for (int k = 0; k < kC / 2; ++k) v[k] = SUMS ? r[u].pair(k) : add2(r[u].pair(k), bias[k]);
+      if (draw.below) drop<VEC>(draw, v, row, c0, lane);
+#pragma unroll
+      for (int k = 0; k < kC / 2; ++k) {
+        if (SUMS) sum[k] = add2(sum[k], v[k]);
+        else if (res) v[k] = add2(v[k], q[u].pair(k));
+      }
+      store_piece<VEC, kC>(static_cast<E *>(a.y) + c0 + (size_t)row * a.d, n, lane, v);
+    }
   }
   if constexpr (SUMS) {
     if (!a.part) return;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sh[w][33 * e + lane] = e & 1 ? sum[e / 2].y : sum[e / 2].x;
+    for (int e = 0; e < kC; ++e) sh[w][33 * e + lane] = e & 1 ? sum[e / 2].y : sum[e / 2].x;
     __syncthreads();
-    for (int c = threadIdx.x; c < kPiece && c < n; c += kThreads) {
-      const int at = VEC ? 33 * (c % 16) + c / 16 : 33 * (c / 32) + c % 32;
+    for (int c = threadIdx.x; c < kCols && c < n; c += kThreads) {
+      const int at = VEC ? 33 * (c % kC) + c / kC : 33 * (c / 32) + c % 32;
       float v = sh[0][at];
 #pragma unroll
       for (int k = 1; k < kWarps; ++k) v += sh[k][at];
@@ -85,16 +97,16 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const Args a) {
   }
 }
 
-// Slices of rows: about four CTAs per SM with all pieces, a row per warp at least.
+// Slices of rows: about eight CTAs per SM with all pieces, a step of the CTA's warps at least.
 int slices_of(int sms, int T, int d) {
-  const int pieces = (d + kPiece - 1) / kPiece, most = (T + kWarps - 1) / kWarps;
-  const int s = (4 * sms + pieces - 1) / pieces;
+  const int pieces = (d + kCols - 1) / kCols, most = (T + kRows * kWarps - 1) / (kRows * kWarps);
+  const int s = (8 * sms + pieces - 1) / pieces;
   return s < most ? s : most;
 }
 
 template <typename E, bool SUMS>
 cudaError_t launch(const Launch &L, const Args &a, int slices) {
-  const dim3 grid((a.d + kPiece - 1) / kPiece, slices);
+  const dim3 grid((a.d + kCols - 1) / kCols, slices);
   const bool vec = rows_vec(a.d, a.x, nullptr) && rows_vec(a.d, a.y, nullptr) && rows_vec(a.d, a.residual, nullptr);
   if (vec) k_dropout<E, true, SUMS><<<grid, kThreads, 0, L.stream>>>(a);
   else k_dropout<E, false, SUMS><<<grid, kThreads, 0, L.stream>>>(a);

@@ -31,15 +31,29 @@ struct Draw {
       step = (uint32_t)d.rng[1];
     }
   }
-  // bit j: column 8 group + j of the row is kept
+  // the bits of the eight columns from 8 group
+  __device__ __forceinline__ U4 bits(uint32_t row, uint32_t group) const {
+    return philox4x32_10(U4{group, row, site, step}, k0, k1);
+  }
+  // bit j: column 8 group + j of the row is kept.  A half is at least P where, in the upper half of a word, it is
+  // at least P 2^16.
   __device__ __forceinline__ uint32_t keep8(uint32_t row, uint32_t group) const {
-    const U4 r = philox4x32_10(U4{group, row, site, step}, k0, k1);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    const U4 r = bits(row, group);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w}, least = below << 16;
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      m |= ((w[j] & 0xFFFFu) >= below ? 1u : 0u) << (2 * j) | ((w[j] >> 16) >= below ? 2u : 0u) << (2 * j);
+    for (int j = 0; j < 4; ++j) m |= (w[j] << 16 >= least ? 1u << (2 * j) : 0u) | (w[j] >= least ? 2u << (2 * j) : 0u);
     return m;
+  }
+  // dropped to 0, or scaled: v[k] holds columns 2 k and 2 k + 1 of a group
+  __device__ __forceinline__ void apply8(float2 *v, uint32_t row, uint32_t group) const {
+    const U4 r = bits(row, group);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w}, least = below << 16;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j].x = w[j] << 16 >= least ? v[j].x * scale : 0.0f;
+      v[j].y = w[j] >= least ? v[j].y * scale : 0.0f;
+    }
   }
   // of the 16 columns from 8 group
   __device__ __forceinline__ uint32_t keep16(uint32_t row, uint32_t group) const {
