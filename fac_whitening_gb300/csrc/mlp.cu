@@ -106,12 +106,12 @@ bool unit_map(CUtensorMap *m, CUtensorMapDataType type, int size, const void *ba
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// An epilogue's tensors by TMA, where all their rows and pointers are 16-byte aligned (rows of 16 columns: of codes too);
-// null ones are not used.  vec: whether they are.
+// An epilogue's tensors by TMA, where all their rows and pointers are 16-byte aligned (the codes' too); null ones are not
+// used.  vec: whether they are.
 bool unit_maps(product::IoMaps &io, bool bf16, int T, int N, const void *t0, const void *t1, const void *t2,
                const void *t3, const void *codes, bool &vec) {
   const void *t[4] = {t0, t1, t2, t3};
-  vec = N % 16 == 0 && aligned16(codes);
+  vec = N % (codes ? 16 : bf16 ? 8 : 4) == 0 && aligned16(codes);
   for (const void *p : t) vec = vec && aligned16(p);
   if (!vec) return true;
   for (int i = 0; i < 4; ++i)

@@ -27,6 +27,7 @@
 #include "dropout.cuh"
 #include "gate.cuh"
 #include "kernels.cuh"
+#include "operand.cuh"
 #include "pair.cuh"
 
 namespace gift {
@@ -41,7 +42,6 @@ constexpr int kThreads = 384;
 constexpr int kEpiWarp = 4, kEpiWarps = 8;
 constexpr int kTileRows = 256;
 constexpr int kUnit = 32 * 128;             // bytes of an epilogue buffer: 32 rows of 64 BF16 or 32 FP32 columns
-constexpr int kPitch = 17;                  // floats of a row of the 32 x 16 tiles that rows of any alignment go through
 
 enum Op { GATED_FORWARD, GATED_BACKWARD, LINEAR, SLICE };
 
@@ -177,7 +177,7 @@ __device__ __forceinline__ void advance(uint32_t &at, uint32_t &parity) {
   }
 }
 
-// ---- units: a thread's 128 bytes of one row, of 32 consecutive rows per warp ------------------------------
+// ---- units: a lane's 128 bytes of one row, of 32 consecutive rows per warp ------------------------------
 // A warp's buffer holds them in the 128-byte swizzle of its tensor map: 16-byte piece j of row r at j ^ (r % 8), so that
 // eight lanes' pieces do not meet in a bank.  TMA moves whole buffers: a lane's own accesses to 32 rows cost the load
 // and store unit 67 clocks for each 32 bytes a lane (the stores of g and u 4300 clocks a tile, of 12300).
@@ -248,41 +248,93 @@ __device__ __forceinline__ void loads_done() { asm volatile("cp.async.wait_all;\
 __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
-// ---- rows of any alignment: 16 columns at a time through a 32 x 16 tile, 16 lanes to a row -----------------------
+// ---- units of rows of any alignment, 8 lanes to a row ------------------------------------------------------
+// Rows start anywhere in a 16-byte block.  A load takes the two aligned blocks that a piece lies in and shifts; a store
+// writes the aligned blocks that the unit's part of a row covers, and the elements before and after them one by one
+// (5003 x 1361 x 2731 gated backward, every access an element wide: 200 us).
 template <typename E>
-__device__ __forceinline__ void load_tile(const void *base, size_t ld, int row0, int rows, int col, int n,
-                                          float *stage) {
-  const int lane = threadIdx.x & 31, c = lane & 15;
-  const E *p = static_cast<const E *>(base) + (size_t)(row0 + (lane >> 4)) * ld + col + c;
-  float x[16];   // all loads before the first store
+__device__ __forceinline__ void load_any(uint32_t buf, const void *base, int T, int N, int row0, int rows, int col) {
+  const int lane = threadIdx.x & 31, j = lane & 7;
+  const uintptr_t lo = (uintptr_t)base, hi = lo + (size_t)T * N * sizeof(E);
+  const size_t step = (size_t)4 * N * sizeof(E);
+  uintptr_t at = lo + ((size_t)(row0 + (lane >> 3)) * N + col) * sizeof(E) + 16 * j;
+#pragma unroll 4
+  for (int r = lane >> 3; r < 32; r += 4, at += step) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows && at < hi) {   // past the row's end: what lies there, never stored
+      const int off = (int)(at & 15);
+      v = aligned_block(at - off, lo, hi);
+      if (off) {
+        const uint4 n = aligned_block(at - off + 16, lo, hi);
+        uint32_t w[8] = {v.x, v.y, v.z, v.w, n.x, n.y, n.z, n.w};
+        if (off & 8) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k, p += 2 * ld) x[k] = 2 * k + (lane >> 4) < rows && c < n ? ld1(p) : 0.0f;
+          for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+        }
+        if (off & 4) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) stage[(2 * k + (lane >> 4)) * kPitch + c] = x[k];
-}
-template <typename E>
-__device__ __forceinline__ void store_tile(void *base, size_t ld, int row0, int rows, int col, int n,
-                                           const float *stage) {
-  const int lane = threadIdx.x & 31, c = lane & 15;
-  E *p = static_cast<E *>(base) + (size_t)(row0 + (lane >> 4)) * ld + col + c;
-#pragma unroll
-  for (int k = 0; k < 16; ++k, p += 2 * ld) {
-    const int r = 2 * k + (lane >> 4);
-    if (r < rows && c < n) st1(p, stage[r * kPitch + c]);
+          for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+        }
+        const int sh = 8 * (off & 3);
+        v = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+      }
+    }
+    write_piece(piece_at(buf, r, j), v);
   }
 }
+// E's bytes of a buffer's row from byte `from`
 template <typename E>
-__device__ __forceinline__ void store16(void *base, size_t ld, int row0, int rows, int col, int n, const float2 *v,
-                                        float *stage) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    stage[lane * kPitch + 2 * k] = v[k].x;
-    stage[lane * kPitch + 2 * k + 1] = v[k].y;
+__device__ __forceinline__ void store_element(E *p, uint32_t buf, int r, int from) {
+  const uint32_t at = piece_at(buf, r, from >> 4) + (from & 15);
+  if constexpr (sizeof(E) == 1) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    *p = (E)v;
+  } else if constexpr (sizeof(E) == 2) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    *reinterpret_cast<uint16_t *>(p) = v;
+  } else {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    *reinterpret_cast<uint32_t *>(p) = v;
   }
-  __syncwarp();
-  store_tile<E>(base, ld, row0, rows, col, n, stage);
-  __syncwarp();
+}
+// COLS columns of the unit, n of them in the matrix
+template <typename E, int COLS>
+__device__ __forceinline__ void store_any(uint32_t buf, void *base, int N, int row0, int rows, int col, int n) {
+  constexpr int size = sizeof(E);
+  const int lane = threadIdx.x & 31, j = lane & 7, len = min(n, COLS) * size;
+  E *p = static_cast<E *>(base) + (size_t)(row0 + (lane >> 3)) * N + col;
+#pragma unroll 2
+  for (int r = lane >> 3; r < min(rows, 32); r += 4, p += (size_t)4 * N) {
+    const int head = min(len, (int)((0 - (uintptr_t)p) & 15)), blocks = (len - head) >> 4;
+    if (j < blocks) {
+      uint4 v = read_piece(piece_at(buf, r, j));
+      if (head) {
+        const uint4 m = read_piece(piece_at(buf, r, j + 1));
+        uint32_t w[8] = {v.x, v.y, v.z, v.w, m.x, m.y, m.z, m.w};
+        if (head & 8) {
+#pragma unroll
+          for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+        }
+        if (head & 4) {
+#pragma unroll
+          for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+        }
+        const int sh = 8 * (head & 3);
+        v = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
+                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+      }
+      *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p) + head + 16 * j) = v;
+    }
+    const int rest = (len - 16 * blocks) / size, before = head / size;
+    for (int i = j; i < rest; i += 8) {
+      const int c = i < before ? i : i + 16 * blocks / size;
+      store_element(p + c, buf, r, c * size);
+    }
+  }
 }
 
 // 16 columns of a lane's own row, rows of a multiple of 16 FP32 in 32-byte aligned buffers
@@ -309,25 +361,6 @@ __device__ __forceinline__ uint4 pack_codes(const float2 *v, float inv) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store_codes(uint8_t *base, size_t ld, int row0, int rows, int col, int n, uint4 w,
-                                            float *stage) {
-  const int lane = threadIdx.x & 31, c = lane & 15;
-  uint8_t *p = base + (size_t)row0 * ld + col;
-  uint32_t *t = reinterpret_cast<uint32_t *>(stage) + lane * 5;   // rows of 20 bytes
-  t[0] = w.x;
-  t[1] = w.y;
-  t[2] = w.z;
-  t[3] = w.w;
-  __syncwarp();
-  const uint8_t *b = reinterpret_cast<const uint8_t *>(stage);
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const int r = 2 * k + (lane >> 4);
-    if (r < rows && c < n) p[(size_t)r * ld + c] = b[r * 20 + c];
-  }
-  __syncwarp();
-}
-
 // bias of 16 columns (the same for every lane), n of them in the matrix; nullable
 __device__ __forceinline__ void add_bias(float2 *v, const float *bias, int n) {
   if (!bias) return;
@@ -550,7 +583,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int e = warp - kEpiWarp, q = warp & 3, c = e >> 2;
     const int first = (P.bn + 127) / 128 * 64, own = c ? P.bn - first : first;   // columns of the two parts, of this warp
     uint8_t *const mine = sm + kStages * kStage + e * kBufs * kUnit;
-    float *const stage = reinterpret_cast<float *>(mine);
     const uint32_t buf = tc::smem_u32(mine), lanes = tmem + ((uint32_t)(32 * q) << 16);
     constexpr int kCols = 128 / sizeof(E);           // columns of a unit
     constexpr int kPairs = Piece<E>::pairs;
@@ -566,9 +598,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto load_inputs = [&](int v) {
         const int col = col0 + kCols * v;
         if (rows <= 0 || col >= P.N) return;
-        if (one) stores_read();
+        if (VEC && one) stores_read();
         __syncwarp();
-        if constexpr (OP == GATED_BACKWARD) {
+        if constexpr (!VEC) {
+          load_any<E>(buf, P.in0, P.T, P.N, row0, rows, col);
+          if (OP == GATED_BACKWARD) load_any<E>(buf + kUnit, P.in1, P.T, P.N, row0, rows, col);
+        } else if constexpr (OP == GATED_BACKWARD) {
           load_rows<E>(buf, P.in0, P.N, row0, rows, col, P.N - col);
           load_rows<E>(buf + kUnit, P.in1, P.N, row0, rows, col, P.N - col);
         } else if (one) {
@@ -576,7 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           load_unit(buf, &io.m[0], col, row0, tc::smem_u32(&sh.in[e]));
         }
       };
-      const bool inputs = VEC && (OP == GATED_BACKWARD || (OP == LINEAR && P.in0));
+      const bool inputs = OP == GATED_BACKWARD || (OP == LINEAR && P.in0);
       if (inputs) load_inputs(0);
       // dropout's bits are drawn while the tile is multiplied: 16 columns each
       uint32_t keep[8];
@@ -613,21 +648,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
 
+      // a buffer to its place in a tensor
+      auto store = [&](uint32_t from, const CUtensorMap *map, void *to, int col) {
+        if constexpr (VEC) {
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (one) store_unit(from, map, col, row0);
+        } else {
+          __syncwarp();
+          store_any<E, kCols>(from, to, P.N, row0, rows, col, P.N - col);
+          __syncwarp();
+        }
+      };
       // Unit v of 16-column groups `from` to a tensor: the buffer is written when its last contents have been stored.
-      auto put = [&](const float2 (*from)[8], const CUtensorMap *map, int v) {
-        if (rows <= 0 || col0 + kCols * v >= P.N) return;
-        if (one) stores_read();
+      auto put = [&](const float2 (*from)[8], const CUtensorMap *map, void *to, int v) {
+        const int col = col0 + kCols * v;
+        if (rows <= 0 || col >= P.N) return;
+        if (VEC && one) stores_read();
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           write_piece(piece_at(buf, lane, j), pack_piece<E>(&from[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8]));
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (one) store_unit(buf, map, col0 + kCols * v, row0);
-      };
-      // the same by elements, for rows of any alignment
-      auto put_any = [&](const float2 (*from)[8], void *to, int i) {
-        store16<E>(to, P.N, row0, rows, col0 + 16 * i, P.N - col0 - 16 * i, from[i], stage);
+        store(buf, map, to, col);
       };
 
       if constexpr (OP == GATED_FORWARD) {
@@ -640,50 +682,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // With one buffer, a store's read of it is covered by arithmetic: g, a(g) u in g's place, u.
         if (P.out1) {
 #pragma unroll
-          for (int v = 0; v < 64 / kCols; ++v)
-            if constexpr (VEC) put(acc, &io.m[1], v);
-          if constexpr (!VEC) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) put_any(acc, P.out1, i);
-          }
+          for (int v = 0; v < 64 / kCols; ++v) put(acc, &io.m[1], P.out1, v);
         }
         if (P.fn == GATE_SILU) gate_forward<GATE_SILU, kAccurate>(acc);
         else if (P.fn == GATE_GELU) gate_forward<GATE_GELU, kAccurate>(acc);
         else gate_forward<GATE_GELU_TANH, kAccurate>(acc);
         if (P.out1) {
 #pragma unroll
-          for (int v = 0; v < 64 / kCols; ++v)
-            if constexpr (VEC) put(acc + 4, &io.m[2], v);
-          if constexpr (!VEC) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) put_any(acc + 4, P.out2, i);
-          }
+          for (int v = 0; v < 64 / kCols; ++v) put(acc + 4, &io.m[2], P.out2, v);
         }
         uint8_t(&scale)[2][128] = sh.scale[tile & 1];
         uint32_t sb = 0;
         if (P.codes) {
-          // a scale group is the tile's 128 columns: this warp's 64 and the other warp's; the byte grows with the amax
+          // A scale group is the tile's 128 columns: this warp's 64 and the other warp's; the byte grows with the amax.
+          // Columns past the matrix are zeros here.
           uint32_t m = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (VEC ? col0 + 16 * i < P.N : col0 + 16 * i + 2 * k < P.N) {   // columns past the matrix do not count
-                m = max(m, abs_bits(acc[i][k].x));
-                if (VEC || col0 + 16 * i + 2 * k + 1 < P.N) m = max(m, abs_bits(acc[i][k].y));
-              }
+            for (int k = 0; k < 8; ++k) m = max(m, max(abs_bits(acc[i][k].x), abs_bits(acc[i][k].y)));
           sb = P.fmt == FMT_E4M3 ? act_scale_byte<FMT_E4M3>(m) : act_scale_byte<FMT_E5M2>(m);
           scale[c][32 * q + lane] = (uint8_t)sb;
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sh.met[q]);
         }
-        if constexpr (VEC) {
 #pragma unroll
-          for (int v = 0; v < 64 / kCols; ++v) put(acc, &io.m[0], v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) put_any(acc, P.out0, i);
-        }
+        for (int v = 0; v < 64 / kCols; ++v) put(acc, &io.m[0], P.out0, v);
         if (P.codes) {
           if (!(ok = wait(&sh.met[q], tile & 1u))) break;
           sb = max(sb, (uint32_t)scale[c ^ 1][32 * q + lane]);
@@ -692,72 +716,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bad |= sb == kActBad;
             if (c == 0) P.scales[(size_t)(row0 + lane) * P.groups + w.n] = (uint8_t)sb;
           }
+          if (rows <= 0 || col0 >= P.N) continue;
           if (VEC && one) stores_read();
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint4 w4 = P.fmt == FMT_E4M3 ? pack_codes<FMT_E4M3>(acc[i], inv) : pack_codes<FMT_E5M2>(acc[i], inv);
-            if (VEC) write_piece(buf + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4), w4);   // 64-byte swizzle
-            else store_codes(P.codes, P.N, row0, rows, col0 + 16 * i, P.N - col0 - 16 * i, w4, stage);
+            // by TMA: rows of 64 bytes in the 64-byte swizzle
+            write_piece(VEC ? buf + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4) : piece_at(buf, lane, i), w4);
           }
-          if (VEC) {
+          if constexpr (VEC) {
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (one && rows > 0 && col0 < P.N) store_unit(buf, &io.m[3], col0, row0);
+            if (one) store_unit(buf, &io.m[3], col0, row0);
+          } else {
+            __syncwarp();
+            store_any<uint8_t, 64>(buf, P.codes, P.N, row0, rows, col0, P.N - col0);
+            __syncwarp();
           }
         }
       } else if constexpr (OP == GATED_BACKWARD) {
         auto walk = [&](auto fn_c) {
           constexpr int FN = decltype(fn_c)::value;
-          if constexpr (VEC) {
 #pragma unroll
-            for (int v = 0; v < 128 / kCols; ++v) {
-              const int col = col0 + kCols * v;
-              if (kCols * v >= own || rows <= 0 || col >= P.N) break;
-              loads_done();
-              __syncwarp();
+          for (int v = 0; v < 128 / kCols; ++v) {
+            const int col = col0 + kCols * v;
+            if (kCols * v >= own || rows <= 0 || col >= P.N) break;
+            if (VEC) loads_done();
+            __syncwarp();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint32_t at = piece_at(buf, lane, j);
-                const Piece<E> g(read_piece(at)), u(read_piece(at + kUnit));
-                float2 *d = &acc[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8], du[kPairs];
-                gate_backward<FN, kAccurate, kPairs>(d, du, g.v, u.v);
-                write_piece(at, pack_piece<E>(d));
-                write_piece(at + kUnit, pack_piece<E>(du));
-              }
-              tc::fence_proxy_async_smem();
-              __syncwarp();
-              if (one) {
-                store_unit(buf, &io.m[2], col, row0);
-                store_unit(buf + kUnit, &io.m[3], col, row0);
-              }
-              if (kCols * (v + 1) < own) load_inputs(v + 1);
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t at = piece_at(buf, lane, j);
+              const Piece<E> g(read_piece(at)), u(read_piece(at + kUnit));
+              float2 *d = &acc[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8], du[kPairs];
+              gate_backward<FN, kAccurate, kPairs>(d, du, g.v, u.v);
+              write_piece(at, pack_piece<E>(d));
+              write_piece(at + kUnit, pack_piece<E>(du));
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (16 * i >= own) break;
-              const int col = col0 + 16 * i, left = P.N - col;
-              float *const other = stage + kUnit / 4;
-              load_tile<E>(P.in0, P.N, row0, rows, col, left, stage);
-              load_tile<E>(P.in1, P.N, row0, rows, col, left, other);
-              __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int at = lane * kPitch + 2 * k;
-                const float2 g = make_float2(stage[at], stage[at + 1]), u = make_float2(other[at], other[at + 1]);
-                float2 du;
-                gate_backward<FN, kAccurate, 1>(&acc[i][k], &du, &g, &u);
-                stage[at] = acc[i][k].x;
-                stage[at + 1] = acc[i][k].y;
-                other[at] = du.x;
-                other[at + 1] = du.y;
-              }
-              __syncwarp();
-              store_tile<E>(P.out0, P.N, row0, rows, col, left, stage);
-              store_tile<E>(P.out1, P.N, row0, rows, col, left, other);
-              __syncwarp();
-            }
+            store(buf, &io.m[2], P.out0, col);
+            store(buf + kUnit, &io.m[3], P.out1, col);
+            if (kCols * (v + 1) < own) load_inputs(v + 1);
           }
         };
         if (P.fn == GATE_SILU) walk(std::integral_constant<int, GATE_SILU>());
@@ -771,42 +769,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           add_bias(acc[i], P.bias0 ? P.bias0 + col : nullptr, P.N - col);
           if (draw.below) drop16(draw, acc[i], keep[i]);
         }
-        if constexpr (VEC) {
 #pragma unroll
-          for (int v = 0; v < 128 / kCols; ++v) {
-            const int col = col0 + kCols * v;
-            if (kCols * v >= own || rows <= 0 || col >= P.N) break;
-            if (inputs) {
+        for (int v = 0; v < 128 / kCols; ++v) {
+          const int col = col0 + kCols * v;
+          if (kCols * v >= own || rows <= 0 || col >= P.N) break;
+          if (inputs) {
+            if (VEC) {
               if (!(ok = wait(&sh.in[e], loads & 1u))) break;
               ++loads;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint32_t at = piece_at(buf, lane, j);
-                const Piece<E> r(read_piece(at));
-                float2 *x = &acc[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8];
-#pragma unroll
-                for (int k = 0; k < kPairs; ++k) x[k] = add2(x[k], r.v[k]);
-              }
             }
-            put(acc, &io.m[2], v);
-            if (inputs && kCols * (v + 1) < own) load_inputs(v + 1);
-          }
-        } else {
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (16 * i >= own) break;
-            if (P.in0) {
-              load_tile<E>(P.in0, P.N, row0, rows, col0 + 16 * i, P.N - col0 - 16 * i, stage);
-              __syncwarp();
+            for (int j = 0; j < 8; ++j) {
+              const Piece<E> r(read_piece(piece_at(buf, lane, j)));
+              float2 *x = &acc[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int at = lane * kPitch + 2 * k;
-                acc[i][k] = add2(acc[i][k], make_float2(stage[at], stage[at + 1]));
-              }
-              __syncwarp();
+              for (int k = 0; k < kPairs; ++k) x[k] = add2(x[k], r.v[k]);
             }
-            put_any(acc, P.out0, i);
           }
+          put(acc, &io.m[2], P.out0, v);
+          if (inputs && kCols * (v + 1) < own) load_inputs(v + 1);
         }
       } else {
         float *p = P.part + ((size_t)w.slice * P.T + row0 + lane) * P.part_ld + col0;

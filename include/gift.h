@@ -612,7 +612,7 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
  * T, d, f, d_in and d_out are at most 2^30 and an output has at most 2^31 - 1 tiles of 256 x 128 (INVALID_ARG above).
  * Alignment: any to the element.  BF16 operands of the products are read in place where their rows and pointers are
  * 16-byte aligned, copied into the workspace else; the products' other tensors are moved by TMA where all their rows
- * are a multiple of 16 elements in 16-byte aligned buffers, by elements else; gift_dropout_forward and
+ * and pointers are 16-byte aligned, by shifted 16-byte accesses else; gift_dropout_forward and
  * gift_dropout_backward take 32-byte accesses for rows of a multiple of 16 elements in 32-byte aligned buffers. */
 
 /* The gate's activation a: g / (1 + exp(-g)); g Phi(g), Phi the normal distribution; g (1 + tanh(sqrt(2 / pi)
