@@ -39,28 +39,50 @@ __device__ __forceinline__ void bf16_terms(const float *x, int T, int d, int ld,
     const int c0 = (int)(i - t * per) * kSpan, c1 = min(d, c0 + kSpan);
     const float *p = x + t * d;
     uint16_t *o = out + t * ld;
-#pragma unroll 4
-    for (int c = c0 + 2 * (threadIdx.x & 31); c < c1; c += 64) {   // ld and kSpan are even
-      uint32_t w[3];
-      const float x0 = p[c], x1 = c + 1 < d ? p[c + 1] : 0.0f;
-      if (max(abs_bits(x0), abs_bits(x1)) < 0x7F7F8000u) {
-        tc::bf16_split3x2(x0, x1, w[0], w[1], w[2]);
-      } else {
-        uint16_t a[3], b[3];
-        bf16_terms_of_large(x0, a);
-        bf16_terms_of_large(x1, b);
+    for (int c = c0 + 2 * (threadIdx.x & 31); c < c1; c += 256) {   // ld and kSpan are even
+      float v[4][2];   // all loads before the first store
 #pragma unroll
-        for (int k = 0; k < 3; ++k) w[k] = (uint32_t)a[k] | (uint32_t)b[k] << 16;
+      for (int u = 0; u < 4; ++u) {
+        v[u][0] = c + 64 * u < c1 ? p[c + 64 * u] : 0.0f;
+        v[u][1] = c + 64 * u + 1 < c1 ? p[c + 64 * u + 1] : 0.0f;
       }
 #pragma unroll
-      for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(o + k * plane + c) = w[k];
+      for (int u = 0; u < 4; ++u) {
+        if (c + 64 * u >= c1) break;
+        uint32_t w[3];
+        const float x0 = v[u][0], x1 = v[u][1];
+        if (max(abs_bits(x0), abs_bits(x1)) < 0x7F7F8000u) {
+          tc::bf16_split3x2(x0, x1, w[0], w[1], w[2]);
+        } else {
+          uint16_t a[3], b[3];
+          bf16_terms_of_large(x0, a);
+          bf16_terms_of_large(x1, b);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) w[k] = (uint32_t)a[k] | (uint32_t)b[k] << 16;
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(o + k * plane + c + 64 * u) = w[k];
+      }
     }
   }
 }
 
-// Rows of `bytes` bytes at any alignment -> rows of ld (a multiple of 16) bytes; a warp per span, 16 bytes
-// per lane from the two aligned blocks that hold them.  Past a row's end nothing is read again (the
-// tensor map's width).
+// 16 bytes that start `off` bytes into a, of the 32 in a and b
+__device__ __forceinline__ uint4 shifted(uint4 a, uint4 b, int off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (off & 8) {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  }
+  const int sh = 8 * (off & 3);
+  return make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
+                    __funnelshift_r(w[3], w[4], sh));
+}
+// the 16-byte block at p, zeros outside [lo, hi)
 __device__ __forceinline__ uint4 aligned_block(uintptr_t p, uintptr_t lo, uintptr_t hi) {
   if (p >= lo && p + 16 <= hi) return *reinterpret_cast<const uint4 *>(p);
   uint32_t w[4] = {0u, 0u, 0u, 0u};   // the ends of the matrix
@@ -69,6 +91,9 @@ __device__ __forceinline__ uint4 aligned_block(uintptr_t p, uintptr_t lo, uintpt
     if (p + b >= lo && p + b < hi) w[b / 4] |= (uint32_t)*reinterpret_cast<const uint8_t *>(p + b) << (8 * (b % 4));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// Rows of `bytes` bytes at any alignment -> rows of ld (a multiple of 16) bytes; a warp per span, 16 bytes
+// per lane from the two aligned blocks that hold them.  Past a row's end nothing is read again (the
+// tensor map's width).
 __device__ __forceinline__ void repitch(const uint8_t *src, int T, size_t bytes, size_t ld, uint8_t *dst, int cta,
                                         int ctas) {
   constexpr size_t span = 2 * kSpan;
@@ -77,23 +102,27 @@ __device__ __forceinline__ void repitch(const uint8_t *src, int T, size_t bytes,
   for (size_t i = (size_t)cta * 8 + (threadIdx.x >> 5); i < all; i += (size_t)ctas * 8) {
     const size_t t = i / per, c0 = (i - t * per) * span, c1 = min(bytes, c0 + span);
     const uintptr_t row = lo + t * bytes;
-    const int off = (int)(row & 15), sh = 8 * (off & 3);
-#pragma unroll 4
-    for (size_t c = c0 + 16 * (threadIdx.x & 31); c < c1; c += 512) {
-      const uintptr_t at = row + c - off;
-      const uint4 a = aligned_block(at, lo, hi), b = off ? aligned_block(at + 16, lo, hi) : a;
-      uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-      if (off & 8) {   // the same for the whole row
+    const int off = (int)(row & 15);
+    // Away from the matrix's ends every block is whole: all loads before the first store
+    const bool inside = row + c0 - off >= lo && row + c1 + 32 <= hi;
+    const size_t c = c0 + 16 * (threadIdx.x & 31);
+    uint4 a[4], b[4];
 #pragma unroll
-        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+    for (int u = 0; u < 4; ++u) {
+      const uintptr_t at = row + c + 512 * u - off;
+      if (c + 512 * u >= c1) break;
+      if (inside) {
+        a[u] = *reinterpret_cast<const uint4 *>(at);
+        b[u] = *reinterpret_cast<const uint4 *>(at + (off ? 16 : 0));
+      } else {
+        a[u] = aligned_block(at, lo, hi);
+        b[u] = off ? aligned_block(at + 16, lo, hi) : a[u];
       }
-      if (off & 4) {
+    }
 #pragma unroll
-        for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
-      }
-      *reinterpret_cast<uint4 *>(dst + t * ld + c) =
-          make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
-                     __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
+    for (int u = 0; u < 4; ++u) {
+      if (c + 512 * u >= c1) break;
+      *reinterpret_cast<uint4 *>(dst + t * ld + c + 512 * u) = shifted(a[u], b[u], off);
     }
   }
 }

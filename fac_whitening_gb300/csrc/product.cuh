@@ -258,27 +258,31 @@ __device__ __forceinline__ void load_any(uint32_t buf, const void *base, int T, 
   const uintptr_t lo = (uintptr_t)base, hi = lo + (size_t)T * N * sizeof(E);
   const size_t step = (size_t)4 * N * sizeof(E);
   uintptr_t at = lo + ((size_t)(row0 + (lane >> 3)) * N + col) * sizeof(E) + 16 * j;
-#pragma unroll 4
+  const uintptr_t from = lo + ((size_t)row0 * N + col) * sizeof(E);
+  if (rows >= 32 && from >= lo + 16 && from + 31 * (step / 4) + 160 <= hi) {   // every block is whole
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 a[4], b[4];   // 16 rows' loads before the first store
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uintptr_t p = at + u * step, block = p & ~(uintptr_t)15;
+        a[u] = *reinterpret_cast<const uint4 *>(block);
+        b[u] = *reinterpret_cast<const uint4 *>(block + (p != block ? 16 : 0));
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        write_piece(piece_at(buf, 16 * h + 4 * u + (lane >> 3), j), shifted(a[u], b[u], (int)((at + u * step) & 15)));
+      at += 4 * step;
+    }
+    return;
+  }
+#pragma unroll 1
   for (int r = lane >> 3; r < 32; r += 4, at += step) {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (r < rows && at < hi) {   // past the row's end: what lies there, never stored
       const int off = (int)(at & 15);
       v = aligned_block(at - off, lo, hi);
-      if (off) {
-        const uint4 n = aligned_block(at - off + 16, lo, hi);
-        uint32_t w[8] = {v.x, v.y, v.z, v.w, n.x, n.y, n.z, n.w};
-        if (off & 8) {
-#pragma unroll
-          for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
-        }
-        if (off & 4) {
-#pragma unroll
-          for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
-        }
-        const int sh = 8 * (off & 3);
-        v = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
-                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
-      }
+      if (off) v = shifted(v, aligned_block(at - off + 16, lo, hi), off);
     }
     write_piece(piece_at(buf, r, j), v);
   }
@@ -307,32 +311,18 @@ __device__ __forceinline__ void store_any(uint32_t buf, void *base, int N, int r
   constexpr int size = sizeof(E);
   const int lane = threadIdx.x & 31, j = lane & 7, len = min(n, COLS) * size;
   E *p = static_cast<E *>(base) + (size_t)(row0 + (lane >> 3)) * N + col;
-#pragma unroll 2
+  constexpr int kRest = (2 * (16 / size - 1) + 7) / 8;   // elements before and after the blocks, by lane
+#pragma unroll 4
   for (int r = lane >> 3; r < min(rows, 32); r += 4, p += (size_t)4 * N) {
     const int head = min(len, (int)((0 - (uintptr_t)p) & 15)), blocks = (len - head) >> 4;
-    if (j < blocks) {
-      uint4 v = read_piece(piece_at(buf, r, j));
-      if (head) {
-        const uint4 m = read_piece(piece_at(buf, r, j + 1));
-        uint32_t w[8] = {v.x, v.y, v.z, v.w, m.x, m.y, m.z, m.w};
-        if (head & 8) {
-#pragma unroll
-          for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
-        }
-        if (head & 4) {
-#pragma unroll
-          for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
-        }
-        const int sh = 8 * (head & 3);
-        v = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh),
-                       __funnelshift_r(w[2], w[3], sh), __funnelshift_r(w[3], w[4], sh));
-      }
-      *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p) + head + 16 * j) = v;
-    }
+    if (j < blocks)
+      *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(p) + head + 16 * j) =
+          shifted(read_piece(piece_at(buf, r, j)), read_piece(piece_at(buf, r, head ? j + 1 : j)), head);
     const int rest = (len - 16 * blocks) / size, before = head / size;
-    for (int i = j; i < rest; i += 8) {
-      const int c = i < before ? i : i + 16 * blocks / size;
-      store_element(p + c, buf, r, c * size);
+#pragma unroll
+    for (int u = 0; u < kRest; ++u) {
+      const int i = j + 8 * u, c = i < before ? i : i + 16 * blocks / size;
+      if (i < rest) store_element(p + c, buf, r, c * size);
     }
   }
 }
