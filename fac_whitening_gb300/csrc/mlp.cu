@@ -38,35 +38,44 @@ __global__ void __launch_bounds__(256) k_operands(const __grid_constant__ Operan
   }
 }
 
-// ---- sums of slices of k -> the linear forward product's epilogue ----------------------------------------
-// A thread has eight columns of one row (one draw of dropout's bits); slices are added in order.
+// ---- sums of slices of k -> the linear product's epilogue ------------------------------------------------
+// A thread has eight columns of one row of a tile (one draw of dropout's bits); slices are added in order.
 template <typename E>
-__global__ void __launch_bounds__(256) k_join_linear(const float *__restrict__ part, int slices, int ld, int T, int N,
-                                                     const float *__restrict__ bias, const Dropout drop,
-                                                     const E *residual, E *y) {
-  const int groups = (N + 7) / 8;
-  const size_t all = (size_t)T * groups, plane = (size_t)T * ld;
+__global__ void __launch_bounds__(256) k_join_linear(const __grid_constant__ Params P) {
+  const int groups = P.bn / 8, tiles = P.mt * P.nt - P.whole;
+  const size_t all = (size_t)tiles * product::kTileRows * groups, plane = (size_t)product::kTileRows * P.bn;
   grid_wait();
-  const Draw draw(drop);
+  const Draw draw(P.drop);
+  const E *residual = static_cast<const E *>(P.in0);
+  E *y = static_cast<E *>(P.out0);
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
-    const size_t t = i / groups;
-    const int g = (int)(i - t * groups), n = N - 8 * g;
-    const float4 *p = reinterpret_cast<const float4 *>(part + t * ld + 8 * g);
-    float4 a = p[0], b = p[1];
-    for (int s = 1; s < slices; ++s) {
-      const float4 *q = reinterpret_cast<const float4 *>(part + s * plane + t * ld + 8 * g);
-      const float4 x = q[0], z = q[1];
+    const int tile = (int)(i / ((size_t)product::kTileRows * groups)), in = (int)(i - (size_t)tile * product::kTileRows * groups);
+    const int r = in / groups, g = in - r * groups;
+    int m, n;
+    product::tile_place(P.whole + tile, P.mt, P.nt, m, n);
+    const int row = m * product::kTileRows + r, col = n * P.bn + 8 * g, left = P.N - col;
+    if (row >= P.T || left <= 0) continue;
+    const float *p = P.part + (size_t)tile * P.slices * plane + (size_t)r * P.bn + 8 * g;
+    float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+#pragma unroll 4
+    for (int s = 1; s < P.slices; ++s) {
+      const float4 x = *reinterpret_cast<const float4 *>(p + s * plane), z = *reinterpret_cast<const float4 *>(p + s * plane + 4);
       a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
       b = make_float4(b.x + z.x, b.y + z.y, b.z + z.z, b.w + z.w);
     }
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const uint32_t keep = draw.below ? draw.keep8((uint32_t)t, g) : 0xFFu;
-    const size_t at = t * N + 8 * (size_t)g;
+    float2 v[4] = {{a.x, a.y}, {a.z, a.w}, {b.x, b.y}, {b.z, b.w}};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (P.bias0) {
+        if (2 * k < left) v[k].x += P.bias0[col + 2 * k];
+        if (2 * k + 1 < left) v[k].y += P.bias0[col + 2 * k + 1];
+      }
+    if (draw.below) draw.apply8(v, row, col / 8);
+    const size_t at = (size_t)row * P.N + col;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      if (e >= n) break;
-      float x = bias ? v[e] + bias[8 * g + e] : v[e];
-      if (draw.below) x = keep >> e & 1u ? x * draw.scale : 0.0f;
+      if (e >= left) break;
+      float x = e & 1 ? v[e / 2].y : v[e / 2].x;
       if (residual) x += ld1(residual + at + e);
       st1(y + at + e, x);
     }
@@ -157,29 +166,32 @@ cudaError_t operands(const Launch &L, bool bf16, const Source *src, int n, uint8
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// A launch's tiles: 256 rows x bn columns, k in `slices`.
+// A launch's tiles: 256 rows x bn columns; the first `whole` are an item each, the others are cut into slices of k.
 struct Plan {
-  int bn, slices;
+  int bn, whole, slices;
+  double cost;
 };
 
-// The width with the least waves x (an item's stages + its start and end); k cut into slices, joined by a kernel
-// of their own, where the tiles leave pairs of SMs idle.  In microseconds.
-Plan plan_linear(int sms, bool bf16, int T, int N, int kb) {
+// What a tile of bn columns costs: its stages, and its start and end (microseconds).
+double tile_cost(bool bf16, int bn, int blocks) {
+  return blocks * (bf16 ? 1 : 6) * (bn == 256 ? 0.285 : bn == 192 ? 0.25 : 0.2) + 0.5 + 2.0 * bn / 256;
+}
+
+// The width with the least time.  The tiles after the last full wave of pairs are cut into slices of k where that wave
+// and the kernel that joins the slices (its launch and 4 TB/s) end sooner than a wave of whole tiles would:
+// 16384 x 6144 x 1536 has 384 tiles of 256 on 76 pairs.
+Plan plan_linear(int sms, bool bf16, int T, int N, int kb, bool cut = true) {
   const int pairs = sms / 2 > 1 ? sms / 2 : 1;
-  const long long mt = ceil_div(T, product::kTileRows);
-  Plan best{256, 1};
-  double least = 1e300;
+  const int mt = ceil_div(T, product::kTileRows);
+  Plan best{256, 0, 1, 1e300};
   for (int bn = 256; bn >= 128; bn -= 64) {
-    const double stage = bn == 256 ? 0.28 : bn == 192 ? 0.23 : 0.18;
-    const long long tiles = mt * ceil_div(N, bn);
-    for (int s = 1; s <= 32 && s <= kb; ++s) {
-      const long long waves = (tiles * s + pairs - 1) / pairs;
-      const double cost = (double)waves * (ceil_div(kb, s) * (bf16 ? 1 : 6) * stage + 1.0) +
-                          (s > 1 ? 3.0 + s * 8.0 * T * N / 4.0e6 : 0.0);
-      if (cost < least) {
-        least = cost;
-        best = Plan{bn, s};
-      }
+    const int tiles = mt * ceil_div(N, bn), full = tiles / pairs, rest = tiles - full * pairs;
+    const double wave = tile_cost(bf16, bn, kb);
+    if ((full + (rest > 0)) * wave < best.cost) best = Plan{bn, tiles, 1, (full + (rest > 0)) * wave};
+    for (int s = 2; cut && s <= 32 && s <= kb && rest; ++s) {
+      const double cost = full * wave + ceil_div(rest * s, pairs) * tile_cost(bf16, bn, ceil_div(kb, s)) + 3.5 +
+                          2.0 * rest * s * product::kTileRows * bn * 4 / 4.0e6;
+      if (cost < best.cost) best = Plan{bn, tiles - rest, s, cost};
     }
   }
   return best;
@@ -188,18 +200,17 @@ Plan plan_linear(int sms, bool bf16, int T, int N, int kb) {
 int pairs_of(const Launch &L) { return L.sms / 2 > 1 ? L.sms / 2 : 1; }
 
 Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, bool b_mn, int kb,
-                 int slices = 1, int segment = kSegment) {
+                 int segment = kSegment) {
   Params P{};
   P.T = T;
   P.N = N;
   P.mt = ceil_div(T, product::kTileRows);
   P.nt = ceil_div(N, columns);
-  P.slices = slices;
-  P.items = P.mt * P.nt * slices;
+  P.slices = 1;
+  P.whole = P.items = P.mt * P.nt;
   P.kb = P.kb1 = kb;
   // segments of equal length, so that none ends long before the next is folded
-  const int most = ceil_div(kb, slices);
-  P.seg = bf16 ? ceil_div(most, ceil_div(most, segment)) : kSegment6;
+  P.seg = bf16 ? ceil_div(kb, ceil_div(kb, segment)) : kSegment6;
   P.bn = bn;
   P.idesc = tc::idesc_bf16(256, bn) | (b_mn ? 1u << 16 : 0u);
   P.budget = L.barrier_wait;
@@ -224,7 +235,7 @@ cudaError_t launch_gated_forward(const Launch &L, bool bf16, const GatedForward 
   maps[0] = maps[1] = made_maps[0];
   maps[2] = made_maps[1];
   maps[3] = made_maps[2];
-  Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK), 1, kSegmentForward);
+  Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK), kSegmentForward);
   P.fn = a.fn;
   P.fmt = a.fmt;
   P.groups = ceil_div(a.f, kActGroup);
@@ -255,7 +266,7 @@ cudaError_t launch_gated_backward(const Launch &L, bool bf16, const GatedBackwar
   if (e != cudaSuccess) return e;
   const CUtensorMap maps[4] = {made_maps[0], made_maps[0], made_maps[1], made_maps[1]};
   const int kb = ceil_div(a.d_out, product::kK);
-  const int bn = plan_linear(L.sms, bf16, a.T, a.f, kb).bn;
+  const int bn = plan_linear(L.sms, bf16, a.T, a.f, kb, false).bn;
   Params P = params_of(L, bf16, a.T, a.f, bn, bn, true, kb);
   P.fn = a.fn;
   P.in0 = a.gate;
@@ -270,32 +281,28 @@ cudaError_t launch_gated_backward(const Launch &L, bool bf16, const GatedBackwar
 
 namespace {
 
-// A product with the linear epilogue, whole or in slices.
+// A product with the linear epilogue, its last tiles in slices.
 cudaError_t linear(const Launch &L, bool bf16, bool mn, const Plan &p, Params P, const CUtensorMap *maps, bool made,
                    float *part) {
-  P.drop.scale = P.drop.below ? P.drop.scale : 1.0f;
-  if (p.slices == 1) {
-    product::IoMaps io{};
-    bool vec;
-    if (!unit_maps(io, bf16, P.T, P.N, P.in0, nullptr, P.out0, nullptr, nullptr, vec)) return cudaErrorInvalidValue;
-    return product::launch_linear(L, bf16, vec, mn, P, maps, io, pairs_of(L), made);
-  }
+  P.whole = p.whole;
+  P.slices = p.slices;
+  const int cut = P.mt * P.nt - p.whole;
+  P.items = p.whole + cut * p.slices;
   P.part = part;
-  P.part_ld = ceil_div(P.N, 16) * 16;
-  const cudaError_t e = product::launch_slices(L, bf16, mn, P, maps, product::IoMaps{}, pairs_of(L), made);
-  if (e != cudaSuccess) return e;
-  const size_t ctas = ((size_t)P.T * ceil_div(P.N, 8) + 255) / 256, most = (size_t)L.sms * 8;
+  product::IoMaps io{};
+  bool vec;
+  if (!unit_maps(io, bf16, P.T, P.N, P.in0, nullptr, P.out0, nullptr, nullptr, vec)) return cudaErrorInvalidValue;
+  const cudaError_t e = product::launch_linear(L, bf16, vec, mn, P, maps, io, pairs_of(L), made);
+  if (e != cudaSuccess || !cut) return e;
+  const size_t ctas = (size_t)cut * P.bn / 8, most = (size_t)L.sms * 8;   // 256 rows of bn / 8 groups a tile
   const dim3 grid((unsigned)(ctas < most ? ctas : most));
-  if (bf16)
-    return launch_after(L.stream, k_join_linear<__nv_bfloat16>, grid, 256, part, p.slices, P.part_ld, P.T, P.N,
-                        P.bias0, P.drop, static_cast<const __nv_bfloat16 *>(P.in0),
-                        static_cast<__nv_bfloat16 *>(P.out0));
-  return launch_after(L.stream, k_join_linear<float>, grid, 256, part, p.slices, P.part_ld, P.T, P.N, P.bias0, P.drop,
-                      static_cast<const float *>(P.in0), static_cast<float *>(P.out0));
+  return bf16 ? launch_after(L.stream, k_join_linear<__nv_bfloat16>, grid, 256, P)
+              : launch_after(L.stream, k_join_linear<float>, grid, 256, P);
 }
 
 size_t part_floats(const Plan &p, int T, int N) {
-  return p.slices > 1 ? (size_t)p.slices * T * (ceil_div(N, 16) * 16) : 0;
+  const size_t tiles = (size_t)ceil_div(T, product::kTileRows) * ceil_div(N, p.bn);
+  return (tiles - p.whole) * p.slices * product::kTileRows * p.bn;
 }
 
 }  // namespace
@@ -316,7 +323,7 @@ cudaError_t launch_linear_forward(const Launch &L, bool bf16, const LinearForwar
   const cudaError_t e = operands(L, bf16, src, 2, a.ws, made_maps, made);
   if (e != cudaSuccess) return e;
   const CUtensorMap maps[4] = {made_maps[0], made_maps[0], made_maps[1], made_maps[1]};
-  Params P = params_of(L, bf16, a.T, a.d_out, p.bn, p.bn, false, kb, p.slices);
+  Params P = params_of(L, bf16, a.T, a.d_out, p.bn, p.bn, false, kb);
   P.bias0 = a.bias;
   P.in0 = a.residual;
   P.out0 = a.y;
@@ -349,7 +356,7 @@ cudaError_t launch_input_grad(const Launch &L, bool bf16, const InputGrad &a) {
   const cudaError_t e = operands(L, bf16, src, 2 * n, a.ws, m, made);
   if (e != cudaSuccess) return e;
   const CUtensorMap maps[4] = {m[0], m[n == 2 ? 2 : 0], m[1], m[n == 2 ? 3 : 1]};
-  Params P = params_of(L, bf16, a.T, a.d_in, p.bn, p.bn, true, n * kb, p.slices);
+  Params P = params_of(L, bf16, a.T, a.d_in, p.bn, p.bn, true, n * kb);
   P.kb1 = kb;
   P.out0 = a.dx;
   return linear(L, bf16, true, p, P, maps, made, a.part);

@@ -43,7 +43,7 @@ constexpr int kEpiWarp = 4, kEpiWarps = 8;
 constexpr int kTileRows = 256;
 constexpr int kUnit = 32 * 128;             // bytes of an epilogue buffer: 32 rows of 64 BF16 or 32 FP32 columns
 
-enum Op { GATED_FORWARD, GATED_BACKWARD, LINEAR, SLICE };
+enum Op { GATED_FORWARD, GATED_BACKWARD, LINEAR };
 
 // Shared memory: a ring of stages, and epilogue buffers for each of its warps (backward: the gate's and the other
 // projection's unit side by side, the gradients in their place).
@@ -59,7 +59,9 @@ struct IoMaps {
 
 struct Params {
   int T, N;               // rows and columns of the output
-  int mt, nt, slices, items;
+  int mt, nt;             // tiles
+  int whole, slices;      // the first `whole` tiles are an item each, the others (linear only) `slices` each
+  int items;
   int kb, kb1;            // blocks of 64 k, and those of the first pair of operands
   int seg;                // stages of a segment
   int bn;                 // columns of a tile, a multiple of 64
@@ -72,23 +74,35 @@ struct Params {
   void *out0, *out1, *out2;     // forward: h, gate, up (nullable both); backward: dgate, dup; linear: y
   uint8_t *codes, *scales;      // nullable: h's 8-bit checkpoint
   Dropout drop;
-  float *part;                  // slices: [slices][T][part_ld]
-  int part_ld;
+  float *part;                  // slices: [tile - whole][slice][256][bn]
 };
 
+// Row m and column n of tiles of a tile.  Tiles are in groups of eight rows of tiles, column by column within a group: the
+// pairs that run at the same time share both operands in L2.
+__host__ __device__ inline void tile_place(int tile, int mt, int nt, int &m, int &n) {
+  const int per = 8 * nt, g = tile / per, rem = tile - g * per, rows = mt - 8 * g < 8 ? mt - 8 * g : 8;
+  n = rem / rows;
+  m = 8 * g + rem - n * rows;
+}
+
 struct Item {
-  int m, n, slice, k0, k1;   // tile, blocks of 64 k
-  // Tiles in groups of eight rows of tiles, column by column within a group: the pairs that run at the same time
-  // share both operands in L2.
+  int m, n, slice, k0, k1;   // tile, its slice (-1: all of it), blocks of 64 k
   __device__ __forceinline__ Item(const Params &P, int item) {
-    const int tiles = P.mt * P.nt, tile = item % tiles;
-    slice = item / tiles;
-    const int per = 8 * P.nt, g = tile / per, rem = tile - g * per, rows = min(8, P.mt - 8 * g);
-    n = rem / rows;
-    m = 8 * g + rem - n * rows;
-    k0 = (int)((long long)P.kb * slice / P.slices);
-    k1 = (int)((long long)P.kb * (slice + 1) / P.slices);
+    int tile = item;
+    slice = -1;
+    k0 = 0;
+    k1 = P.kb;
+    if (item >= P.whole) {
+      const int cut = P.mt * P.nt - P.whole, i = item - P.whole;
+      slice = i / cut;
+      tile = P.whole + i - slice * cut;
+      k0 = (int)((long long)P.kb * slice / P.slices);
+      k1 = (int)((long long)P.kb * (slice + 1) / P.slices);
+    }
+    tile_place(tile, P.mt, P.nt, m, n);
+    at = tile - P.whole;
   }
+  int at;   // the tile's place among the cut ones
 };
 
 constexpr int kMostStages = 6;
@@ -120,7 +134,7 @@ __device__ __forceinline__ void mma_pair_ss(uint32_t d, uint32_t a_lo, uint32_t 
       : "memory");
 }
 
-// Barriers and copies by shared-memory address, for the loops of one thread
+// Barriers and copies by shared-memory address
 __device__ __forceinline__ bool try_wait_at(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -416,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  if (OP == SLICE) grid_release();   // the kernel that joins the slices
+  if (OP == LINEAR && P.slices > 1) grid_release();   // the kernel that joins the slices
 
   if (warp == 0) alloc_pair(&sh.tmem);
   if (tid == 32) {
@@ -441,46 +455,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem;
 
   // Called by whole warps: the lanes go on together, or none does.
-  auto wait = [&](uint64_t *bar, uint32_t parity) {
-    bool done = tc::mbar_try_wait(bar, parity);
-    if (!done) {
-      const long long t0 = clock64();
-      do {
-        if (sh.failed || clock64() - t0 > P.budget) {
-          sh.failed = 1;
-          set_status(status, GIFT_ERR_TIMEOUT);
-          break;
-        }
-        done = tc::mbar_try_wait(bar, parity);
-      } while (!done);
-    }
-    return __all_sync(0xFFFFFFFFu, done) != 0;
-  };
-
-  // The same for one thread by itself.
   auto hold = [&](uint32_t bar, uint32_t parity) {
-    if (try_wait_at(bar, parity)) return true;
+    if (__all_sync(0xFFFFFFFFu, try_wait_at(bar, parity))) return true;
     const long long t0 = clock64();
-    do {
-      if (sh.failed || clock64() - t0 > P.budget) {
+    while (!__all_sync(0xFFFFFFFFu, try_wait_at(bar, parity))) {
+      if (__any_sync(0xFFFFFFFFu, sh.failed || clock64() - t0 > P.budget)) {
         sh.failed = 1;
         set_status(status, GIFT_ERR_TIMEOUT);
         return false;
       }
-    } while (!try_wait_at(bar, parity));
+    }
     return true;
   };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return hold(tc::smem_u32(bar), parity); };
 
   // registers: 168 per thread at launch (504 over the three groups of four warps), redistributed as 2 x 208 + 88
   if (warp < kEpiWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-    // One thread each.  A stage's 512 clocks are few for what a single thread does between two of them, so these loops keep
-    // their addresses running, and A and B have a thread each (one for both, its slot and terms computed per stage, took
-    // 550 clocks a stage).
+    // Each of these warps walks its loop whole and converged, so that what TMA and the MMAs take stays in uniform
+    // registers; one elected thread issues.  A stage's 512 clocks are few for what a warp does between two of them: the
+    // loops keep their addresses running, and A and B have a warp each (one for both, its slot and terms computed
+    // per stage, took 550 clocks a stage).
+    const bool one = elect_one();
     const uint32_t full = of_cta(tc::smem_u32(sh.full), 0), empty = tc::smem_u32(sh.empty);
     const uint32_t ring = tc::smem_u32(sm);
-    if (!elect_one()) {
-    } else if (warp == 0 || warp == 2) {
+    if (warp == 0 || warp == 2) {
       // ---------------- TMA ----------------
       const bool is_a = warp == 0;
       const int half = P.bn / 2, boxes = half > 64 ? 2 : 1;
@@ -492,13 +491,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto stage = [&](const CUtensorMap *map, int k, int y, int term) {
         const uint32_t bar = full + 8 * at, dst = base + at * kStage;
         if (!(ok = hold(empty + 8 * at, parity))) return;
-        expect_in_cluster(bar, bytes);
-        if (MN && !is_a) {
-          load_in_cluster(dst, map, y, k, term, bar);
-          if (boxes == 2) load_in_cluster(dst + kBox, map, y + 64, k, term, bar);
-        } else {
-          load_in_cluster(dst, map, k, y, term, bar);
+        if (one) {
+          expect_in_cluster(bar, bytes);
+          if (MN && !is_a) {
+            load_in_cluster(dst, map, y, k, term, bar);
+            if (boxes == 2) load_in_cluster(dst + kBox, map, y + 64, k, term, bar);
+          } else {
+            load_in_cluster(dst, map, k, y, term, bar);
+          }
         }
+        __syncwarp();
         advance<kStages>(at, parity);
         ++g;
       };
@@ -531,8 +533,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // the pair's first CTA may have a wait of its own to end before its last commit
       tc::mbar_wait_bounded(&sh.drained, 0, P.budget + kDrain);
+      __syncwarp();
       const uint32_t at_issued = tc::smem_u32(&sh.issued[2 * rank + (is_a ? 0 : 1)]);
-      for (uint32_t r = 0; r < 2; ++r) write_in_cluster(of_cta(at_issued, r), g | (ok ? 0u : kGaveUp));
+      if (one)
+        for (uint32_t r = 0; r < 2; ++r) write_in_cluster(of_cta(at_issued, r), g | (ok ? 0u : kGaveUp));
     } else if (warp == 1 && rank == 0) {
       // ---------------- MMA ----------------
       const uint32_t b_lead = MN ? (uint32_t)(kBox >> 4) << 16 : 1u << 16, b_step = MN ? 128u : 2u;
@@ -552,19 +556,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint32_t a = (ring + at * kStage) >> 4, b = a + (kABytes >> 4);
             uint64_t *const done = &sh.empty[at];
             advance<kStages>(at, parity);
-            there = test_wait_at(loaded + 8 * at, parity);
+            there = __all_sync(0xFFFFFFFFu, test_wait_at(loaded + 8 * at, parity)) != 0;
             tc::fence_after_sync();
+            if (one) {
 #pragma unroll
-            for (int k = 0; k < kK / 16; ++k) {
-              mma_pair_ss(d, (a + 2 * k) | 1u << 16, (b + b_step * k) | b_lead, idesc, accumulate);
-              accumulate = 1;
+              for (int k = 0; k < kK / 16; ++k)
+                mma_pair_ss(d, (a + 2 * k) | 1u << 16, (b + b_step * k) | b_lead, idesc, k ? 1u : accumulate);
+              commit_pair(done);
             }
-            commit_pair(done);
+            __syncwarp();
+            accumulate = 1;
           }
-          if (ok) commit_pair(&sh.dfull[n & 1]);
+          if (ok && one) commit_pair(&sh.dfull[n & 1]);
+          __syncwarp();
         }
       }
-      commit_pair(&sh.drained);
+      if (one) commit_pair(&sh.drained);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
@@ -601,11 +608,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           load_unit(buf, &io.m[0], col, row0, tc::smem_u32(&sh.in[e]));
         }
       };
-      const bool inputs = OP == GATED_BACKWARD || (OP == LINEAR && P.in0);
+      const bool inputs = OP == GATED_BACKWARD || (OP == LINEAR && P.in0 && w.slice < 0);
       if (inputs) load_inputs(0);
       // dropout's bits are drawn while the tile is multiplied: 16 columns each
       uint32_t keep[8];
-      if (OP == LINEAR && draw.below) {
+      if (OP == LINEAR && draw.below && w.slice < 0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (16 * i < own) keep[i] = draw.keep16(row0 + lane, (col0 + 16 * i) / 8);
@@ -618,6 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int left = (w.k1 - w.k0) * kTerms; left > 0; left -= P.seg, ++n) {
         if (!(ok = wait(&sh.dfull[n & 1], n >> 1 & 1u))) break;
+        __syncwarp();
         tc::fence_after_sync();
         const uint32_t from = lanes + 256 * (n & 1);
 #pragma unroll
@@ -751,7 +759,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (P.fn == GATE_SILU) walk(std::integral_constant<int, GATE_SILU>());
         else if (P.fn == GATE_GELU) walk(std::integral_constant<int, GATE_GELU>());
         else walk(std::integral_constant<int, GATE_GELU_TANH>());
-      } else if constexpr (OP == LINEAR) {
+      } else if (w.slice >= 0) {
+        const int at = 128 * rank + 32 * q + lane;   // row of the tile
+        float *p = P.part + (((size_t)w.at * P.slices + w.slice) * kTileRows + at) * P.bn + col0 - w.n * P.bn;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (16 * i < own && lane < rows) store_own(p + 16 * i, acc[i]);
+      } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (16 * i >= own) break;
@@ -780,15 +794,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           put(acc, &io.m[2], P.out0, v);
           if (inputs && kCols * (v + 1) < own) load_inputs(v + 1);
         }
-      } else {
-        float *p = P.part + ((size_t)w.slice * P.T + row0 + lane) * P.part_ld + col0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (16 * i >= own) break;
-          if (lane < rows && col0 + 16 * i < P.part_ld) store_own(p + 16 * i, acc[i]);
-        }
       }
     }
+    if (bad) set_status(status, GIFT_ERR_NONFINITE);
     // nothing of this warp's is in flight when the CTA leaves: its stores, and loads whose wait did not end
     if (one) {
       stores_done();
@@ -859,8 +867,6 @@ cudaError_t launch_linear(const Launch &L, bool bf16, bool vec, bool mn, const P
                           const IoMaps &io, int pairs, bool after);
 cudaError_t launch_linear_mn(const Launch &L, bool bf16, bool vec, const Params &P, const CUtensorMap *maps, const IoMaps &io, int pairs,
                              bool after);
-cudaError_t launch_slices(const Launch &L, bool bf16, bool mn, const Params &P, const CUtensorMap *maps, const IoMaps &io, int pairs,
-                          bool after);
 
 }  // namespace product
 
