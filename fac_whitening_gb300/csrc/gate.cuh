@@ -10,14 +10,14 @@ namespace gift {
 
 enum GateFn { GATE_SILU = 0, GATE_GELU = 1, GATE_GELU_TANH = 2 };
 
-// FP32 results take the library's expf and division (a few units in the last place).  Results that are rounded to
-// BF16 take the hardware's exponential and reciprocal (about 2^-21 off, 2^-13 of BF16's rounding; results below 2^-126
-// are 0, where s is 1 to the last place): with expf and a rounded division the gate's arithmetic took half as long again.
+// FP32 results take the library's expf; results that are rounded to BF16 the hardware's exponential (about 2^-21 off,
+// 2^-13 of BF16's rounding; results below 2^-126 are 0, where s is 1 to the last place).  Both take the hardware's
+// reciprocal, a unit in the last place off.
 template <bool ACCURATE>
 __device__ __forceinline__ float sigmoid(float z) {
-  if (ACCURATE) return 1.0f / (1.0f + expf(-z));
   float e, s;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  if (ACCURATE) e = expf(-z);
+  else asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));   // 0 where e is infinite
   return s;
 }

@@ -40,16 +40,19 @@ __global__ void __launch_bounds__(256) k_operands(const __grid_constant__ Operan
 
 // ---- sums of slices of k -> the linear product's epilogue ------------------------------------------------
 // A thread has eight columns of one row of a tile (one draw of dropout's bits); slices are added in order.
+constexpr int kJoinThreads = 128;
 template <typename E>
-__global__ void __launch_bounds__(256) k_join_linear(const __grid_constant__ Params P) {
+__global__ void __launch_bounds__(kJoinThreads) k_join_linear(const __grid_constant__ Params P, bool vec) {
   const int groups = P.bn / 8, tiles = P.mt * P.nt - P.whole;
   const size_t all = (size_t)tiles * product::kTileRows * groups, plane = (size_t)product::kTileRows * P.bn;
   grid_wait();
   const Draw draw(P.drop);
   const E *residual = static_cast<const E *>(P.in0);
   E *y = static_cast<E *>(P.out0);
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (size_t)gridDim.x * 256) {
-    const int tile = (int)(i / ((size_t)product::kTileRows * groups)), in = (int)(i - (size_t)tile * product::kTileRows * groups);
+  for (size_t i = (size_t)blockIdx.x * kJoinThreads + threadIdx.x; i < all;
+       i += (size_t)gridDim.x * kJoinThreads) {
+    const int tile = (int)(i / ((size_t)product::kTileRows * groups));
+    const int in = (int)(i - (size_t)tile * product::kTileRows * groups);
     const int r = in / groups, g = in - r * groups;
     int m, n;
     product::tile_place(P.whole + tile, P.mt, P.nt, m, n);
@@ -57,9 +60,10 @@ __global__ void __launch_bounds__(256) k_join_linear(const __grid_constant__ Par
     if (row >= P.T || left <= 0) continue;
     const float *p = P.part + (size_t)tile * P.slices * plane + (size_t)r * P.bn + 8 * g;
     float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 1; s < P.slices; ++s) {
-      const float4 x = *reinterpret_cast<const float4 *>(p + s * plane), z = *reinterpret_cast<const float4 *>(p + s * plane + 4);
+      const float4 x = *reinterpret_cast<const float4 *>(p + s * plane);
+      const float4 z = *reinterpret_cast<const float4 *>(p + s * plane + 4);
       a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
       b = make_float4(b.x + z.x, b.y + z.y, b.z + z.z, b.w + z.w);
     }
@@ -72,6 +76,18 @@ __global__ void __launch_bounds__(256) k_join_linear(const __grid_constant__ Par
       }
     if (draw.below) draw.apply8(v, row, col / 8);
     const size_t at = (size_t)row * P.N + col;
+    if (sizeof(E) == 2 && vec) {   // eight columns are 16 bytes
+      if (residual) {
+        const uint4 r = *reinterpret_cast<const uint4 *>(residual + at);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[k] = add2(v[k], make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
+      }
+      *reinterpret_cast<uint4 *>(y + at) = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
+                                                      pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
+      continue;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (e >= left) break;
@@ -172,29 +188,45 @@ struct Plan {
   double cost;
 };
 
-// What a tile of bn columns costs: its stages, and its start and end (microseconds).
-double tile_cost(bool bf16, int bn, int blocks) {
-  return blocks * (bf16 ? 1 : 6) * (bn == 256 ? 0.285 : bn == 192 ? 0.25 : 0.2) + 0.5 + 2.0 * bn / 256;
-}
+// Microseconds of a stage, and of a tile's epilogue: what it computes and stores after its last MMA.  A stage of fewer
+// columns is bound by its loads: 0.285, 0.25, 0.2 and 0.19 us at 256, 192, 128 and 64 columns (9728 x 4096 x 1536).  An
+// epilogue of 256 columns takes 2 us (linear), 5 (gated backward) and 4 to 8 with FP32's twice as many bytes; it
+// runs beside the next tile's product, so the last one counts.
+struct TileCost {
+  bool bf16;
+  double epilogue;   // of 256 columns
+  double stages(int bn, int blocks) const {
+    return blocks * (bf16 ? 1 : 6) * (bn == 256 ? 0.285 : bn == 192 ? 0.25 : bn == 128 ? 0.2 : 0.19) + 0.5;
+  }
+  double end(int bn) const { return epilogue * (bf16 ? 1.0 : 1.6) * bn / 256; }
+  double waves(int n, int bn, int blocks) const {
+    const double a = stages(bn, blocks), b = end(bn);
+    return n * (a > b ? a : b);
+  }
+};
+constexpr double kLinearEnd = 2.5, kGatedEnd = 5.0;
 
-// The width with the least time.  The tiles after the last full wave of pairs are cut into slices of k where that wave
-// and the kernel that joins the slices (its launch and 4 TB/s) end sooner than a wave of whole tiles would:
-// 16384 x 6144 x 1536 has 384 tiles of 256 on 76 pairs.
-Plan plan_linear(int sms, bool bf16, int T, int N, int kb, bool cut = true) {
+// The width with the least time.  With `cut`, the tiles after the last full wave of pairs are cut into slices of k where
+// that wave and the kernel that joins the slices (its launch and 6 TB/s) end sooner than a wave of whole tiles would:
+// 16384 x 6144 x 1536 has 384 tiles of 256 on 76 pairs, 187 us with six waves, 174 with five and slices.
+Plan plan_of(int sms, const TileCost &c, int T, int N, int kb, bool cut) {
   const int pairs = sms / 2 > 1 ? sms / 2 : 1;
   const int mt = ceil_div(T, product::kTileRows);
   Plan best{256, 0, 1, 1e300};
-  for (int bn = 256; bn >= 128; bn -= 64) {
+  for (int bn = 256; bn >= 64; bn -= 64) {
     const int tiles = mt * ceil_div(N, bn), full = tiles / pairs, rest = tiles - full * pairs;
-    const double wave = tile_cost(bf16, bn, kb);
-    if ((full + (rest > 0)) * wave < best.cost) best = Plan{bn, tiles, 1, (full + (rest > 0)) * wave};
+    const double whole = c.waves(full + (rest > 0), bn, kb) + c.end(bn);
+    if (whole < best.cost) best = Plan{bn, tiles, 1, whole};
     for (int s = 2; cut && s <= 32 && s <= kb && rest; ++s) {
-      const double cost = full * wave + ceil_div(rest * s, pairs) * tile_cost(bf16, bn, ceil_div(kb, s)) + 3.5 +
-                          2.0 * rest * s * product::kTileRows * bn * 4 / 4.0e6;
+      const double cost = c.waves(full, bn, kb) + c.waves(ceil_div(rest * s, pairs), bn, ceil_div(kb, s)) + c.end(bn) +
+                          3.0 + 2.0 * rest * s * (T < product::kTileRows ? T : product::kTileRows) * bn * 4 / 6.0e6;
       if (cost < best.cost) best = Plan{bn, tiles - rest, s, cost};
     }
   }
   return best;
+}
+Plan plan_linear(int sms, bool bf16, int T, int N, int kb) {
+  return plan_of(sms, TileCost{bf16, kLinearEnd}, T, N, kb, true);
 }
 
 int pairs_of(const Launch &L) { return L.sms / 2 > 1 ? L.sms / 2 : 1; }
@@ -266,7 +298,7 @@ cudaError_t launch_gated_backward(const Launch &L, bool bf16, const GatedBackwar
   if (e != cudaSuccess) return e;
   const CUtensorMap maps[4] = {made_maps[0], made_maps[0], made_maps[1], made_maps[1]};
   const int kb = ceil_div(a.d_out, product::kK);
-  const int bn = plan_linear(L.sms, bf16, a.T, a.f, kb, false).bn;
+  const int bn = plan_of(L.sms, TileCost{bf16, kGatedEnd}, a.T, a.f, kb, false).bn;
   Params P = params_of(L, bf16, a.T, a.f, bn, bn, true, kb);
   P.fn = a.fn;
   P.in0 = a.gate;
@@ -294,10 +326,10 @@ cudaError_t linear(const Launch &L, bool bf16, bool mn, const Plan &p, Params P,
   if (!unit_maps(io, bf16, P.T, P.N, P.in0, nullptr, P.out0, nullptr, nullptr, vec)) return cudaErrorInvalidValue;
   const cudaError_t e = product::launch_linear(L, bf16, vec, mn, P, maps, io, pairs_of(L), made);
   if (e != cudaSuccess || !cut) return e;
-  const size_t ctas = (size_t)cut * P.bn / 8, most = (size_t)L.sms * 8;   // 256 rows of bn / 8 groups a tile
+  const size_t ctas = (size_t)cut * product::kTileRows * (P.bn / 8) / kJoinThreads, most = (size_t)L.sms * 16;
   const dim3 grid((unsigned)(ctas < most ? ctas : most));
-  return bf16 ? launch_after(L.stream, k_join_linear<__nv_bfloat16>, grid, 256, P)
-              : launch_after(L.stream, k_join_linear<float>, grid, 256, P);
+  return bf16 ? launch_after(L.stream, k_join_linear<__nv_bfloat16>, grid, kJoinThreads, P, vec)
+              : launch_after(L.stream, k_join_linear<float>, grid, kJoinThreads, P, vec);
 }
 
 size_t part_floats(const Plan &p, int T, int N) {

@@ -575,8 +575,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-    // ---------------- fold and epilogue: 32 rows, and a part of the columns in whole units (128 and 64 of 192,
-    // otherwise half) ----------------
+    // ---------------- fold and epilogue: 32 rows, and a part of the columns in whole units of 64 (128 and 64 of
+    // 192, half of 256 and 128, all or none of 64) ----------------
     const int e = warp - kEpiWarp, q = warp & 3, c = e >> 2;
     const int first = (P.bn + 127) / 128 * 64, own = c ? P.bn - first : first;   // columns of the two parts, of this warp
     uint8_t *const mine = sm + kStages * kStage + e * kBufs * kUnit;
@@ -594,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // the inputs of unit v into the warp's buffers, whose last contents have been stored
       auto load_inputs = [&](int v) {
         const int col = col0 + kCols * v;
-        if (rows <= 0 || col >= P.N) return;
+        if (rows <= 0 || kCols * v >= own || col >= P.N) return;
         if (VEC && one) stores_read();
         __syncwarp();
         if constexpr (!VEC) {
@@ -753,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             store(buf, &io.m[2], P.out0, col);
             store(buf + kUnit, &io.m[3], P.out1, col);
-            if (kCols * (v + 1) < own) load_inputs(v + 1);
+            load_inputs(v + 1);
           }
         };
         if (P.fn == GATE_SILU) walk(std::integral_constant<int, GATE_SILU>());
@@ -792,7 +792,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           put(acc, &io.m[2], P.out0, v);
-          if (inputs && kCols * (v + 1) < own) load_inputs(v + 1);
+          if (inputs) load_inputs(v + 1);
         }
       }
     }
