@@ -365,22 +365,25 @@ __device__ __forceinline__ uint4 pack_codes(const float2 *v, float inv) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// bias of 16 columns (the same for every lane), n of them in the matrix; nullable
-__device__ __forceinline__ void add_bias(float2 *v, const float *bias, int n) {
-  if (!bias) return;
-  if (n >= 16 && aligned16(bias)) {
+// The bias of a warp's up to 32 J columns, n of them in the matrix, a column of each 32 per lane: loaded while the tile is
+// multiplied, handed round by shuffles in straight code (loads beside their use, by alignment, took 4300 clocks of a
+// small product's only epilogue, most of them for the instructions).
+template <int J>
+struct Bias {
+  float v[J];
+  __device__ __forceinline__ void load(const float *bias, int n) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 b = *reinterpret_cast<const float4 *>(bias + 4 * k);
-      v[2 * k] = add2(v[2 * k], make_float2(b.x, b.y));
-      v[2 * k + 1] = add2(v[2 * k + 1], make_float2(b.z, b.w));
-    }
-    return;
+    for (int j = 0; j < J; ++j) v[j] = bias && 32 * j + lane < n ? bias[32 * j + lane] : 0.0f;
   }
+  // to 16 columns, the i-th such group
+  __device__ __forceinline__ void add(float2 *to, int i) const {
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    v[k] = add2(v[k], make_float2(2 * k < n ? bias[2 * k] : 0.0f, 2 * k + 1 < n ? bias[2 * k + 1] : 0.0f));
-}
+    for (int k = 0; k < 8; ++k)
+      to[k] = add2(to[k], make_float2(__shfl_sync(0xFFFFFFFFu, v[i / 2], (16 * i + 2 * k) % 32),
+                                      __shfl_sync(0xFFFFFFFFu, v[i / 2], (16 * i + 2 * k + 1) % 32)));
+  }
+};
 
 // acc[0..3] the gate's 64 columns, acc[4..7] the other projection's: a(g) u in their place
 template <int FN, bool ACCURATE>
@@ -433,6 +436,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (OP == LINEAR && P.slices > 1) grid_release();   // the kernel that joins the slices
 
   if (warp == 0) alloc_pair(&sh.tmem);
+  if (tid == 96) {   // the maps on their way while the rest is set up
+    tc::prefetch_tensormap(&tm_a0);
+    tc::prefetch_tensormap(rank && kGated ? &tm_b1 : &tm_b0);
+  }
   if (tid == 32) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&sh.full[s], 4);
@@ -610,6 +617,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       const bool inputs = OP == GATED_BACKWARD || (OP == LINEAR && P.in0 && w.slice < 0);
       if (inputs) load_inputs(0);
+      Bias<4> bias;   // forward: the gate's two and the other projection's two
+      if (OP == LINEAR) {
+        bias.load(P.bias0 ? P.bias0 + col0 : nullptr, min(own, P.N - col0));
+      } else if (OP == GATED_FORWARD) {
+        Bias<2> b0, b1;
+        b0.load(P.bias0 ? P.bias0 + col0 : nullptr, P.N - col0);
+        b1.load(P.bias1 ? P.bias1 + col0 : nullptr, P.N - col0);
+        bias.v[0] = b0.v[0];
+        bias.v[1] = b0.v[1];
+        bias.v[2] = b1.v[0];
+        bias.v[3] = b1.v[1];
+      }
       // dropout's bits are drawn while the tile is multiplied: 16 columns each
       uint32_t keep[8];
       if (OP == LINEAR && draw.below && w.slice < 0) {
@@ -671,11 +690,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
 
       if constexpr (OP == GATED_FORWARD) {
+        if (P.bias0 || P.bias1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = col0 + 16 * i, left = P.N - col;
-          add_bias(acc[i], P.bias0 ? P.bias0 + col : nullptr, left);
-          add_bias(acc[4 + i], P.bias1 ? P.bias1 + col : nullptr, left);
+          for (int i = 0; i < 8; ++i) bias.add(acc[i], i);
         }
         // With one buffer, a store's read of it is covered by arithmetic: g, a(g) u in g's place, u.
         if (P.out1) {
@@ -766,12 +783,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 8; ++i)
           if (16 * i < own && lane < rows) store_own(p + 16 * i, acc[i]);
       } else {
+        if (P.bias0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (16 * i >= own) break;
-          const int col = col0 + 16 * i;
-          add_bias(acc[i], P.bias0 ? P.bias0 + col : nullptr, P.N - col);
-          if (draw.below) drop16(draw, acc[i], keep[i]);
+          for (int i = 0; i < 8; ++i)
+            if (16 * i < own) bias.add(acc[i], i);
+        }
+        if (draw.below) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (16 * i < own) drop16(draw, acc[i], keep[i]);
         }
 #pragma unroll
         for (int v = 0; v < 128 / kCols; ++v) {
