@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_linear(const __grid_const
     const int in = (int)(i - (size_t)tile * product::kTileRows * groups);
     const int r = in / groups, g = in - r * groups;
     int m, n;
-    product::tile_place(P.whole + tile, P.mt, P.nt, m, n);
+    product::tile_place(P, P.whole + tile, m, n);
     const int row = m * product::kTileRows + r, col = n * P.bn + 8 * g, left = P.N - col;
     if (row >= P.T || left <= 0) continue;
     const float *p = P.part + (size_t)tile * P.slices * plane + (size_t)r * P.bn + 8 * g;
@@ -238,6 +238,7 @@ Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, 
   P.N = N;
   P.mt = ceil_div(T, product::kTileRows);
   P.nt = ceil_div(N, columns);
+  P.group = 8;
   P.slices = 1;
   P.whole = P.items = P.mt * P.nt;
   P.kb = P.kb1 = kb;
@@ -268,6 +269,7 @@ cudaError_t launch_gated_forward(const Launch &L, bool bf16, const GatedForward 
   maps[2] = made_maps[1];
   maps[3] = made_maps[2];
   Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK), kSegmentForward);
+  P.group = 16;
   P.fn = a.fn;
   P.fmt = a.fmt;
   P.groups = ceil_div(a.f, kActGroup);
