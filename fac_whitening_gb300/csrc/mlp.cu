@@ -1,5 +1,7 @@
 // The feed-forward block's products, host side: operands as the tensor-core kernel reads them (product.cuh), its
 // tiles and slices, and the kernels before and after it.
+#include <cmath>
+
 #include "operand.cuh"
 #include "product.cuh"
 
@@ -99,8 +101,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_linear(const __grid_const
 }
 
 // ---- host ---------------------------------------------------------------------------------------------
-// Most stages of a segment: 1024 k, 768 for the forward product, or one block of 64 k of FP32's terms
-constexpr int kSegment = 16, kSegmentForward = 12, kSegment6 = 6;
+constexpr int kSegment = 16, kSegment6 = 6;   // most stages of a segment: 1024 k, or one block of 64 k of FP32's terms
 
 // `planes` matrices of rows x cols BF16, rows `pitch` bytes apart, read in boxes of 64 columns x `box` rows
 bool boxes(CUtensorMap *m, const void *base, int rows, int cols, size_t pitch, int planes, int box) {
@@ -231,8 +232,7 @@ Plan plan_linear(int sms, bool bf16, int T, int N, int kb) {
 
 int pairs_of(const Launch &L) { return L.sms / 2 > 1 ? L.sms / 2 : 1; }
 
-Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, bool b_mn, int kb,
-                 int segment = kSegment) {
+Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, bool b_mn, int kb) {
   Params P{};
   P.T = T;
   P.N = N;
@@ -243,7 +243,7 @@ Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, 
   P.whole = P.items = P.mt * P.nt;
   P.kb = P.kb1 = kb;
   // segments of equal length, so that none ends long before the next is folded
-  P.seg = bf16 ? ceil_div(kb, ceil_div(kb, segment)) : kSegment6;
+  P.head = P.seg = bf16 ? ceil_div(kb, ceil_div(kb, kSegment)) : kSegment6;
   P.bn = bn;
   P.idesc = tc::idesc_bf16(256, bn) | (b_mn ? 1u << 16 : 0u);
   P.budget = L.barrier_wait;
@@ -268,7 +268,14 @@ cudaError_t launch_gated_forward(const Launch &L, bool bf16, const GatedForward 
   maps[0] = maps[1] = made_maps[0];
   maps[2] = made_maps[1];
   maps[3] = made_maps[2];
-  Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK), kSegmentForward);
+  Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK));
+  if (bf16 && a.codes) {
+    // What truncation moves grows with a segment's length, what a plain FP32 sum's roundings move with the square root
+    // of k: 192 k of 1536, 320 of 4096.
+    P.seg = (int)(0.61 * std::sqrt((double)P.kb) + 0.5);
+    if (P.seg < 3) P.seg = 3;
+    P.head = P.kb > 8 ? 2 * P.seg : P.seg;
+  }
   P.group = 16;
   P.fn = a.fn;
   P.fmt = a.fmt;

@@ -7,10 +7,13 @@
 //   warps 0, 2   TMA: stages of 64 k, A's 128 x 64 and B's up to 128 x 64 elements;
 //   warp 1       the pair's first CTA issues 256 x N x 16 MMAs (both CTAs' copies complete on its barriers);
 //   warps 4-11   fold and epilogue: a thread has one token and half of the tile's columns.
-// The tensor core truncates its sums, so a segment of at most 1024 k (768 for the forward product, whose 8-bit checkpoint
-// tells FP32's last bits) goes into one of two accumulators in tensor memory and is added to FP32 registers to
-// nearest while the other is filled.  The epilogue runs from those registers while the next tile's first two
-// segments are multiplied: 1536 k are two segments, and the epilogue has a tile's whole time.
+// The tensor core truncates its sums, so a segment of at most 1024 k goes into one of two accumulators in tensor memory
+// and is added to FP32 registers to nearest while the other is filled.  The epilogue runs from those registers while
+// the next tile's first two segments are multiplied: 1536 k are two segments, and the epilogue has a tile's whole time.
+// An 8-bit checkpoint of h tells FP32's last bits (the codes of values next to a border), so a forward product that
+// makes one has shorter segments, the first two, which the epilogue needs, twice as long as the others: 1536 k in 384, 384
+// and 192s change as many codes as a plain FP32 product does (394 us for 16384 x 1536 x 6144, in 768s 345 us and 2.5 times as
+// many).
 // The gated forward product takes its two projections as one product of 128 + 128 columns: the first CTA loads
 // the gate's rows, the second the other projection's, and both halves of a row meet in one thread.
 // FP32 operands are three BF16 terms each (operand.cuh); a block of 64 k then takes six stages, the products i + j <= 2
@@ -63,7 +66,7 @@ struct Params {
   int whole, slices;      // the first `whole` tiles are an item each, the others (linear only) `slices` each
   int items;
   int kb, kb1;            // blocks of 64 k, and those of the first pair of operands
-  int seg;                // stages of a segment
+  int head, seg;          // stages of an item's first two segments, and of the others
   int bn;                 // columns of a tile, a multiple of 64
   uint32_t idesc;
   long long budget;       // clocks of a wait
@@ -550,17 +553,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---------------- MMA ----------------
       const uint32_t b_lead = MN ? (uint32_t)(kBox >> 4) << 16 : 1u << 16, b_step = MN ? 128u : 2u;
       const uint32_t loaded = tc::smem_u32(sh.full), dempty = tc::smem_u32(sh.dempty), idesc = P.idesc;
-      const int seg = P.seg;
+      const int head = P.head, seg = P.seg;
       uint32_t at = 0, parity = 0, n = 0;   // slot, segments
       bool ok = true, there = false;        // there: the stage was seen to be loaded
       for (int it = pair; it < P.items && ok; it += pairs) {
         const Item w(P, it);
-        for (int left = (w.k1 - w.k0) * kTerms; left > 0 && ok; left -= seg, ++n) {
+        for (int left = (w.k1 - w.k0) * kTerms, i = 0, len; left > 0 && ok; left -= len, ++i, ++n) {
+          len = i < 2 ? head : seg;
           const uint32_t d = tmem + 256 * (n & 1);
           if (!(ok = hold(dempty + 8 * (n & 1), (n >> 1 & 1u) ^ 1u))) break;
           tc::fence_after_sync();
           uint32_t accumulate = 0;
-          for (int j = min(seg, left); j > 0; --j) {
+          for (int j = min(len, left); j > 0; --j) {
             if (!there && !(ok = hold(loaded + 8 * at, parity))) break;
             const uint32_t a = (ring + at * kStage) >> 4, b = a + (kABytes >> 4);
             uint64_t *const done = &sh.empty[at];
@@ -644,7 +648,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[i][k] = both(0.0f);
 #pragma unroll 1
-      for (int left = (w.k1 - w.k0) * kTerms; left > 0; left -= P.seg, ++n) {
+      for (int left = (w.k1 - w.k0) * kTerms, i = 0; left > 0; left -= i < 2 ? P.head : P.seg, ++i, ++n) {
         if (!(ok = wait(&sh.dfull[n & 1], n >> 1 & 1u))) break;
         __syncwarp();
         tc::fence_after_sync();

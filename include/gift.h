@@ -603,7 +603,7 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
  *   dx = dg Wg + du Wu                                  gift_input_grad
  *
  * and gift_weight_grad makes dW from h's checkpoint and dz, dWg and dWu from the norm's checkpoint and dg, du.
- * Products are summed in FP32, rounded to nearest at least every 512 terms (the tensor core truncates in
+ * Products are summed in FP32, rounded to nearest at least every 1024 terms (the tensor core truncates in
  * between), and each output is rounded once, to its type.  FP32 operands enter as three BF16 terms each with the
  * six products i + j <= 4 of terms i and j (what is dropped is below 2^-23 of |x_k W_k|); operands below 2^-110 may lose
  * up to 2^-134.  Orders of summation are fixed by the shape, the buffers' alignment and the context: equal calls
