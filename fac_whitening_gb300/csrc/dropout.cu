@@ -1,7 +1,9 @@
 // Dropout by itself: y = residual + drop(x + bias), and its backward pass dx = drop(dy), dbias = sum_t dx.
 //
 // HBM bounds it.  A warp keeps one piece of 256 columns (8 a lane: one counter) and walks down the rows of its CTA's
-// slice, two at a time so that their loads are in flight together; the bits are drawn where they are used.
+// slice, two at a time so that their loads are in flight together; the bits are drawn where they are used.  32768 x 4096
+// BF16 130 us forward with bias and residual (6.2 TB/s), 105 backward with dbias (5.1); 16384 x 1536 31 and 29.  With pieces
+// of 512 columns, 16 a lane, 173 and 122: half the warps fit.
 #include "act.cuh"
 #include "dropout.cuh"
 #include "kernels.cuh"
@@ -25,7 +27,8 @@ __device__ __forceinline__ void drop(const Draw &d, float2 *v, uint32_t row, uin
   const uint32_t m = d.keep8(row, c0 / 8 + lane);
 #pragma unroll
   for (int k = 0; k < kC / 2; ++k) {
-    const uint32_t a = __shfl_sync(0xFFFFFFFFu, m, 8 * k + (lane >> 3)), b = __shfl_sync(0xFFFFFFFFu, m, 8 * k + 4 + (lane >> 3));
+    const uint32_t a = __shfl_sync(0xFFFFFFFFu, m, 8 * k + (lane >> 3));
+    const uint32_t b = __shfl_sync(0xFFFFFFFFu, m, 8 * k + 4 + (lane >> 3));
     v[k].x = a >> (lane & 7) & 1u ? v[k].x * d.scale : 0.0f;
     v[k].y = b >> (lane & 7) & 1u ? v[k].y * d.scale : 0.0f;
   }

@@ -169,12 +169,13 @@ typedef enum {
                                   gift_workspace_bytes: the two need different workspaces. */
   GIFT_OPT_BARRIER_WAIT = 1,   /* SM clock cycles a CTA of the shared-scale encode waits at its
                                   grid-wide barrier, and a warp of gift_weight_grad's tensor-core
-                                  kernel at a barrier of its pipeline, before it gives up and writes
-                                  GIFT_ERR_TIMEOUT to d_status (the encode then stores no codes,
-                                  the weight gradient leaves its outputs undefined; default 2e9,
-                                  about a second; 0..2e10).  A small value makes the wait run out
-                                  on purpose (the weight gradient's after a few microseconds): the
-                                  kernel still ends and the context stays usable. */
+                                  kernel and of the feed-forward products' at a barrier of its
+                                  pipeline, before it gives up and writes GIFT_ERR_TIMEOUT to
+                                  d_status (the encode then stores no codes, the others leave
+                                  their outputs undefined; default 2e9, about a second; 0..2e10).
+                                  A small value makes the wait run out on purpose (the pipelines'
+                                  after a few microseconds): the kernel still ends and the context
+                                  stays usable. */
   GIFT_OPT_SMS = 3             /* SMs the context's launches size their grids for (default and
                                   maximum: the device's SM count).  With a fraction of the SMs per
                                   context, calls on several streams run side by side on disjoint
