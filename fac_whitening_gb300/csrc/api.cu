@@ -1474,9 +1474,9 @@ namespace {
 
 bool valid_gate(gift_gate g) { return g == GIFT_GATE_SILU || g == GIFT_GATE_GELU || g == GIFT_GATE_GELU_TANH; }
 
-// Whether an output of T x N has a countable number of tiles (256 x 128 at the least).
+// Whether an output of T x N has a countable number of tiles (256 x 64 at the least).
 bool valid_tiles(int T, int N) {
-  return ((long long)T + 255) / 256 * (((long long)N + 127) / 128) <= 0x7FFFFFFFll;
+  return ((long long)T + 255) / 256 * (((long long)N + 63) / 64) <= 0x7FFFFFFFll;
 }
 
 // P = round(65536 p), the share of 16-bit numbers that drop an element; false: p is not a probability below 1 that

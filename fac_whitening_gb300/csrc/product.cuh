@@ -827,7 +827,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (bad) set_status(status, GIFT_ERR_NONFINITE);
     // nothing of this warp's is in flight when the CTA leaves: its stores, and loads whose wait did not end
     if (one) {
       stores_done();

@@ -610,7 +610,7 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
  * up to 2^-134.  Orders of summation are fixed by the shape, the buffers' alignment and the context: equal calls
  * give equal bits.  An infinity or NaN in a BF16 operand reaches the outputs as the formula has it; in an FP32
  * operand it makes NaN or Inf of every output that the formula makes not finite, without telling which.
- * T, d, f, d_in and d_out are at most 2^30 and an output has at most 2^31 - 1 tiles of 256 x 128 (INVALID_ARG above).
+ * T, d, f, d_in and d_out are at most 2^30 and an output has at most 2^31 - 1 tiles of 256 x 64 (INVALID_ARG above).
  * Alignment: any to the element.  BF16 operands of the products are read in place where their rows and pointers are
  * 16-byte aligned, copied into the workspace else; the products' other tensors are moved by TMA where all their rows
  * and pointers are 16-byte aligned, by shifted 16-byte accesses else; gift_dropout_forward and
