@@ -135,9 +135,10 @@ def whole(rng, dt, rows, k, top=None):
 
 
 # One token to more than a tile, odd and even, k of one block and of several segments, columns of one group and of several
-# tiles.
+# tiles, and of tiles of each width (64, 128, 192, 256).
 SHAPES = [(1, 1, 1), (1, 8, 16), (2, 64, 128), (3, 129, 257), (33, 72, 144), (130, 513, 96), (257, 40, 136),
-          (300, 1100, 528), (5, 2500, 300), (1, 1536, 1024)]
+          (300, 1100, 528), (5, 2500, 300), (1, 1536, 1024), (300, 72, 64), (300, 100, 192), (600, 130, 384),
+          (700, 257, 250)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -209,6 +210,29 @@ def test_gated_forward(shape, fmt, bias, dt, off, fn):
     steps = 2.0 ** np.repeat(s, 128, axis=1)[:, :f] * A.magnitudes(fmt)[1]
     half = {"e4m3": 2.0 ** -4, "e5m2": 2.0 ** -3}[fmt]
     assert (np.abs(v - h) <= 1.01 * eh + np.maximum(1.01 * half * np.abs(h), steps / 2)).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("off", [False, True], ids=["aligned", "unaligned"])
+def test_gated_forward_without_what_is_optional(dt, off):
+    rng = np.random.default_rng(8)
+    x, Wg, Wu = normal(rng, 140, 200, dt=dt), normal(rng, 272, 200, dt=dt) / 8, normal(rng, 272, 200, dt=dt) / 8
+    full = gated_forward(x, Wg, Wu, "silu", dt, fmt="e4m3", off=off)
+    kept = gated_forward(x, Wg, Wu, "silu", dt, fmt="e4m3", kept=False, off=off)
+    for k in ("h", "codes", "scales"):
+        assert np.array_equal(full[k], kept[k]), k
+    # without the checkpoint BF16 sums are folded less often: h within its rounding and that of the sums
+    plain = gated_forward(x, Wg, Wu, "silu", dt, kept=False, off=off)
+    (g, eg), (u, eu) = R.product(x, Wg.T, dt), R.product(x, Wu.T, dt)
+    a, _ = R.gate(g, "silu")
+    e = 1.13 * eg * (np.abs(u) + eu) + np.abs(a) * eu + (R.gate_error(g, "silu") + 2 * R.U32) * np.abs(a * u)
+    assert (np.abs(plain["h"] - full["h"]) <= 2 * e + 2.02 * R.half_step(full["h"], dt)).all()
+    # one bias alone
+    b = rounded(rng.standard_normal(272), "f32")
+    only = gated_forward(x, Wg, Wu, "silu", dt, bg=b, off=off)
+    both = gated_forward(x, Wg, Wu, "silu", dt, bg=b, bu=np.zeros(272), off=off)
+    for k in ("h", "gate", "up"):
+        assert np.array_equal(only[k], both[k]), k
 
 
 @pytest.mark.parametrize("fn", FNS)
@@ -306,4 +330,7 @@ def test_dropout(shape, p, off, dt):
     G.gift_dropout_backward(ctx(), dx2.t, dx2.t, p, r, site)
     want = R.drop(x, p, seed, step, site)
     assert (np.abs(host(y2.checked()) - want) <= R.U32 * np.abs(want) + 1.01 * R.half_step(want, dt)).all()
+    y2.t.copy_(put(res, dt))   # in the residual's place
+    G.gift_dropout_forward(ctx(), put(x, dt, off), y2.t, p, r, site, put(bias), y2.t)
+    assert torch.equal(y2.checked(), y.t)
     assert torch.equal(dx2.checked(), dx.t)

@@ -169,6 +169,18 @@ def test_equal_calls_give_equal_bits_and_graphs_read_new_steps(shape, dt):
     assert int(b.st.item()) == 0
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_a_workspace_may_start_anywhere(dt):
+    b = Block(67, 129, 257, dt)
+    b.step()
+    want = [t.clone() for t in b.results()]
+    flat = torch.full((b.ws.numel() + 8,), 0xFF, dtype=torch.uint8, device=DEV)
+    b.ws = flat[3:3 + b.ws.numel()]
+    b.step()
+    assert all(torch.equal(x, y) for x, y in zip(want, b.results()))
+    assert (flat[:3] == 0xFF).all() and (flat[3 + b.ws.numel():] == 0xFF).all()
+
+
 def test_two_graphs_share_a_workspace_one_after_the_other():
     a, b = Block(130, 96, 272, "f32", seed=1), Block(67, 129, 257, "f32", seed=2)
     want = []
