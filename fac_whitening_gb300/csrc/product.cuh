@@ -12,7 +12,7 @@
 // the next tile's first two segments are multiplied: 1536 k are two segments, and the epilogue has a tile's whole time.
 // An 8-bit checkpoint of h tells FP32's last bits (the codes of values next to a border), so a forward product that
 // makes one has shorter segments, the first two, which the epilogue needs, twice as long as the others: 1536 k in 384,
-// 384 and 192s change 1.1 times as many codes as a plain FP32 product does (394 us for 16384 x 1536 x 6144; in 768s 345
+// 384 and 192s change 1.1 times as many codes as a plain FP32 product does (385 us for 16384 x 1536 x 6144; in 768s 353
 // us and 2.5 times as many).
 // The gated forward product takes its two projections as one product of 128 + 128 columns: the first CTA loads
 // the gate's rows, the second the other projection's, and both halves of a row meet in one thread.
@@ -22,8 +22,8 @@
 // off instead of 2e-7 at 256 k).
 // What bounds it.  A stage's MMAs of 256 columns take 512 clocks, its 32 KB cross from L2 at up to 64 bytes a clock: 540 to
 // 560 clocks a stage.  16384 x 12288 x 1536 input gradient 330 us, 1.87 PFLOP/s; 16384 x 6144 x 1536 linear with dropout
-// and residual 180 us; 16384 x 1536 x 6144 gated forward 394 us with the checkpoint, backward 230 us (g, u and their
-// gradients are 805 MB: 157 us without them); 32768 x 4096 x 16384 gated forward 4.6 ms, 1.91 PFLOP/s.  Small ones: a start
+// and residual 180 us; 16384 x 1536 x 6144 gated forward 385 us with the checkpoint, backward 230 us (g, u and their
+// gradients are 805 MB: 157 us without them); 32768 x 4096 x 16384 gated forward 4.5 ms, 1.96 PFLOP/s.  Small ones: a start
 // of 1 us, 1 us to the first stage, 3 us for a BF16 epilogue.
 // Every mbarrier wait is bounded by the context's GIFT_OPT_BARRIER_WAIT and reports GIFT_ERR_TIMEOUT; a warp
 // leaves as one, and the copies and MMAs in flight are waited for before the CTA leaves.
@@ -53,12 +53,13 @@ constexpr int kUnit = 32 * 128;             // bytes of an epilogue buffer: 32 r
 
 enum Op { GATED_FORWARD, GATED_BACKWARD, LINEAR };
 
-// Shared memory: a ring of stages, and epilogue buffers for each of its warps (backward: the gate's and the other
-// projection's unit side by side, the gradients in their place).
+// Shared memory: a ring of stages, and epilogue buffers for each of its warps (forward: used in turn, so that a store is
+// read while the next buffer is written, 394 -> 385 us for 16384 x 1536 x 6144 although a stage had to go; backward: the
+// gate's and the other projection's unit side by side, the gradients in their place).
 template <int OP>
 struct Cfg {
-  static constexpr int stages = OP == GATED_BACKWARD ? 5 : 6;
-  static constexpr int bufs = OP == GATED_BACKWARD ? 2 : 1;
+  static constexpr int stages = OP == LINEAR ? 6 : 5;
+  static constexpr int bufs = OP == LINEAR ? 1 : 2;
   static constexpr int smem = stages * kStage + kEpiWarps * bufs * kUnit + 1024;
 };
 struct IoMaps {
@@ -269,7 +270,11 @@ __device__ __forceinline__ void load_rows(uint32_t buf, const void *base, size_t
   }
 }
 __device__ __forceinline__ void loads_done() { asm volatile("cp.async.wait_all;\n" ::: "memory"); }
-__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+// a thread's stores have been read, but for the last N
+template <int N = 0>
+__device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;\n" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
 // ---- units of rows of any alignment, 8 lanes to a row ------------------------------------------------------
@@ -604,6 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool one = elect_one();
     const Draw draw(P.drop);
     uint32_t n = 0, tile = 0, loads = 0, issued = 0;   // loads: buffers filled and read
+    uint32_t next = buf;                               // forward: the buffer that is written next
     bool ok = true, bad = false;
     for (int it = pair; it < P.items && ok; it += pairs, ++tile) {
       const Item w(P, it);
@@ -688,16 +694,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       };
-      // Unit v of 16-column groups `from` to a tensor: the buffer is written when its last contents have been stored.
+      // A buffer to write, whose last contents have been stored.
+      auto buffer = [&]() {
+        if (VEC && one) stores_read<kGated ? 1 : 0>();
+        __syncwarp();
+        const uint32_t b = next;
+        if (kGated) next = 2 * buf + kUnit - next;
+        return b;
+      };
+      // Unit v of 16-column groups `from` to a tensor.
       auto put = [&](const float2 (*from)[8], const CUtensorMap *map, void *to, int v) {
         const int col = col0 + kCols * v;
         if (rows <= 0 || col >= P.N) return;
-        if (VEC && one) stores_read();
-        __syncwarp();
+        const uint32_t b = buffer();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          write_piece(piece_at(buf, lane, j), pack_piece<E>(&from[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8]));
-        store(buf, map, to, col);
+          write_piece(piece_at(b, lane, j), pack_piece<E>(&from[kCols * v / 16 + j * kPairs / 8][j * kPairs % 8]));
+        store(b, map, to, col);
       };
 
       if constexpr (OP == GATED_FORWARD) {
@@ -705,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) bias.add(acc[i], i);
         }
-        // With one buffer, a store's read of it is covered by arithmetic: g, a(g) u in g's place, u.
+        // g, a(g) u in g's place, u: arithmetic between the stores
         if (P.out1) {
 #pragma unroll
           for (int v = 0; v < 64 / kCols; ++v) put(acc, &io.m[1], P.out1, v);
@@ -743,21 +756,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (c == 0) P.scales[(size_t)(row0 + lane) * P.groups + w.n] = (uint8_t)sb;
           }
           if (rows <= 0 || col0 >= P.N) continue;
-          if (VEC && one) stores_read();
-          __syncwarp();
+          const uint32_t b = buffer();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint4 w4 = P.fmt == FMT_E4M3 ? pack_codes<FMT_E4M3>(acc[i], inv) : pack_codes<FMT_E5M2>(acc[i], inv);
             // by TMA: rows of 64 bytes in the 64-byte swizzle
-            write_piece(VEC ? buf + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4) : piece_at(buf, lane, i), w4);
+            write_piece(VEC ? b + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4) : piece_at(b, lane, i), w4);
           }
           if constexpr (VEC) {
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (one) store_unit(buf, &io.m[3], col0, row0);
+            if (one) store_unit(b, &io.m[3], col0, row0);
           } else {
             __syncwarp();
-            store_any<uint8_t, 64>(buf, P.codes, P.N, row0, rows, col0, P.N - col0);
+            store_any<uint8_t, 64>(b, P.codes, P.N, row0, rows, col0, P.N - col0);
             __syncwarp();
           }
         }
