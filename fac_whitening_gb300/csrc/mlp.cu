@@ -250,6 +250,27 @@ Params params_of(const Launch &L, bool bf16, int T, int N, int columns, int bn, 
   return P;
 }
 
+// Stages of the segments of a BF16 product whose results are also kept in 8 bits: of the first two, which the epilogue needs
+// long, and of the others.  Error of the values that the codes stand for, and changed codes, over those of a plain FP32
+// product, and the product's time, 16384 tokens x 6144 (32768 x 16384 at 4096 k); right, longer ones of 0.61 sqrt(k / 64)
+// stages, at least 3, the first two twice as long:
+//      k   stages  error  codes      us     error  codes     us
+//    256     2, 2   1.10   1.11   162.5      1.19   1.45   162.5
+//    512     2, 2   1.14   0.87     253      1.33   1.12     237
+//    768     2, 2   1.09   0.75     300      1.88   1.82     226
+//   1024     3, 2   0.88   0.77     328      1.46   1.52     289
+//   1536     4, 2   0.97   0.70     410      1.23   1.08     381
+//   2048     5, 2   0.89   0.71     498      0.99   0.86     484
+//   4096     8, 3   0.80   0.67    4710      1.00   0.90    4570
+// Truncation moves a sum towards zero, the large ones most, in proportion to a segment's length; a plain sum's roundings
+// grow with the square root of k.  One stage a segment: 0.94 at 256 k, but 39 % more time.
+void checkpoint_segments(int kb, int &head, int &seg) {
+  const int root = (int)(std::sqrt((double)kb) + 0.5), line = 1 + kb / 8;
+  head = line < root ? line : root;
+  if (head < 2) head = 2;
+  seg = (head + 1) / 3 > 2 ? (head + 1) / 3 : 2;
+}
+
 }  // namespace
 
 MlpWs gated_forward_layout(bool bf16, int T, int f, int d) {
@@ -269,13 +290,7 @@ cudaError_t launch_gated_forward(const Launch &L, bool bf16, const GatedForward 
   maps[2] = made_maps[1];
   maps[3] = made_maps[2];
   Params P = params_of(L, bf16, a.T, a.f, 128, 256, false, ceil_div(a.d, product::kK));
-  if (bf16 && a.codes) {
-    // What truncation moves grows with a segment's length, what a plain FP32 sum's roundings move with the square root
-    // of k: 192 k of 1536, 320 of 4096.
-    P.seg = (int)(0.61 * std::sqrt((double)P.kb) + 0.5);
-    if (P.seg < 3) P.seg = 3;
-    P.head = P.kb > 8 ? 2 * P.seg : P.seg;
-  }
+  if (bf16 && a.codes) checkpoint_segments(P.kb, P.head, P.seg);
   P.group = 16;
   P.fn = a.fn;
   P.fmt = a.fmt;

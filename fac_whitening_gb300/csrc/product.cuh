@@ -11,9 +11,8 @@
 // and is added to FP32 registers to nearest while the other is filled.  The epilogue runs from those registers while
 // the next tile's first two segments are multiplied: 1536 k are two segments, and the epilogue has a tile's whole time.
 // An 8-bit checkpoint of h tells FP32's last bits (the codes of values next to a border), so a forward product that
-// makes one has shorter segments, the first two, which the epilogue needs, twice as long as the others: 1536 k in 384,
-// 384 and 192s change 1.1 times as many codes as a plain FP32 product does (385 us for 16384 x 1536 x 6144; in 768s 353
-// us and 2.5 times as many).
+// makes one has shorter segments (checkpoint_segments): 128 k of 512, 256 of 1536, 512 of 4096 in the first two, which
+// the epilogue needs, fewer in the others.
 // The gated forward product takes its two projections as one product of 128 + 128 columns: the first CTA loads
 // the gate's rows, the second the other projection's, and both halves of a row meet in one thread.
 // FP32 operands are three BF16 terms each (operand.cuh); a block of 64 k then takes six stages, the products i + j <= 2
@@ -22,7 +21,7 @@
 // off instead of 2e-7 at 256 k).
 // What bounds it.  A stage's MMAs of 256 columns take 512 clocks, its 32 KB cross from L2 at up to 64 bytes a clock: 540 to
 // 560 clocks a stage.  16384 x 12288 x 1536 input gradient 330 us, 1.87 PFLOP/s; 16384 x 6144 x 1536 linear with dropout
-// and residual 180 us; 16384 x 1536 x 6144 gated forward 385 us with the checkpoint, backward 230 us (g, u and their
+// and residual 180 us; 16384 x 1536 x 6144 gated forward 410 us with the checkpoint, backward 230 us (g, u and their
 // gradients are 805 MB: 157 us without them); 32768 x 4096 x 16384 gated forward 4.5 ms, 1.96 PFLOP/s.  Small ones: a start
 // of 1 us, 1 us to the first stage, 3 us for a BF16 epilogue.
 // Every mbarrier wait is bounded by the context's GIFT_OPT_BARRIER_WAIT and reports GIFT_ERR_TIMEOUT; a warp
