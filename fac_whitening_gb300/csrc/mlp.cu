@@ -268,6 +268,7 @@ void checkpoint_segments(int kb, int &head, int &seg) {
   const int root = (int)(std::sqrt((double)kb) + 0.5), line = 1 + kb / 8;
   head = line < root ? line : root;
   if (head < 2) head = 2;
+  if (head > kSegment) head = kSegment;
   seg = (head + 1) / 3 > 2 ? (head + 1) / 3 : 2;
 }
 

@@ -606,8 +606,8 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
  * and gift_weight_grad makes dW from h's checkpoint and dz, dWg and dWu from the norm's checkpoint and dg, du.
  * Products are summed in FP32, rounded to nearest at least every 1024 terms (the tensor core truncates in
  * between), and each output is rounded once, to its type.  BF16 sums of k terms whose results are also kept in 8
- * bits are rounded at least every 64 n, n = max(2, min(1 + b / 8 rounded down, the root of b to the nearest)), b = k / 64
- * rounded up: every 256 terms of 1536, every 512 of 4096.  FP32 operands enter as three BF16 terms each with the
+ * bits are rounded at least every 64 n, n = max(2, min(16, 1 + b / 8 rounded down, the root of b to the nearest)), b = k /
+ * 64 rounded up: every 256 terms of 1536, every 512 of 4096.  FP32 operands enter as three BF16 terms each with the
  * six products i + j <= 4 of terms i and j (what is dropped is below 2^-23 of |x_k W_k|); operands below 2^-110 may lose
  * up to 2^-134.  Orders of summation are fixed by the shape, the buffers' alignment and the context: equal calls
  * give equal bits.  An infinity or NaN in a BF16 operand reaches the outputs as the formula has it; in an FP32
