@@ -469,6 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::fence_mbar_init();
     sh.failed = 0;
   }
+  __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
   cluster_sync();
@@ -861,6 +862,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (uint32_t u = sh.issued[i] & ~kGaveUp; u < g; ++u) tc::mbar_arrive(&sh.full[u % kStages]);
       landed<kStages>(sh.full, g);
     }
+    __syncwarp();   // the cluster barrier and the dealloc below are for converged warps
     cluster_sync();
   }
   if (warp == 0) {
