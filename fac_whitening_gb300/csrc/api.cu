@@ -1309,6 +1309,11 @@ bool valid_act_fmt(gift_format f) { return f == GIFT_FMT_E4M3 || f == GIFT_FMT_E
 int fmt8(gift_format f) { return f == GIFT_FMT_E4M3 ? FMT_E4M3 : FMT_E5M2; }
 bool valid_extent(int n) { return n >= 1 && n <= kMaxExtent; }
 
+// Whether an output of T x N has a countable number of tiles (256 x 64 at the least).
+bool valid_tiles(int T, int N) {
+  return ((long long)T + 255) / 256 * (((long long)N + 63) / 64) <= 0x7FFFFFFFll;
+}
+
 // The workspace of one call, carved from the first 256-byte boundary (the size has room for it).
 struct ActWs {
   float *part = nullptr;    // slice partials of the sums over tokens
@@ -1363,6 +1368,8 @@ size_t gift_act_workspace_bytes(const gift_ctx *ctx, gift_op op, gift_dtype dt, 
   if (op < GIFT_OP_LAYERNORM_BACKWARD || op > GIFT_OP_DROPOUT_BACKWARD) return (size_t)-1;
   const bool rows_only = op == GIFT_OP_LAYERNORM_BACKWARD || op == GIFT_OP_DROPOUT_BACKWARD;
   if (!rows_only && !valid_extent(d_out)) return (size_t)-1;
+  if ((op == GIFT_OP_GATED_FORWARD || op == GIFT_OP_LINEAR_FORWARD) && !valid_tiles(T, d_out)) return (size_t)-1;
+  if ((op == GIFT_OP_GATED_BACKWARD || op == GIFT_OP_INPUT_GRAD) && !valid_tiles(T, d_in)) return (size_t)-1;
   return act_layout(nullptr, ctx, op, dt, T, d_out, d_in).bytes;
 }
 
@@ -1473,11 +1480,6 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
 namespace {
 
 bool valid_gate(gift_gate g) { return g == GIFT_GATE_SILU || g == GIFT_GATE_GELU || g == GIFT_GATE_GELU_TANH; }
-
-// Whether an output of T x N has a countable number of tiles (256 x 64 at the least).
-bool valid_tiles(int T, int N) {
-  return ((long long)T + 255) / 256 * (((long long)N + 63) / 64) <= 0x7FFFFFFFll;
-}
 
 // P = round(65536 p), the share of 16-bit numbers that drop an element; false: p is not a probability below 1 that
 // leaves one.
