@@ -10,16 +10,27 @@ namespace gift {
 
 enum GateFn { GATE_SILU = 0, GATE_GELU = 1, GATE_GELU_TANH = 2 };
 
-// FP32 results take the library's expf; results that are rounded to BF16 the hardware's exponential (about 2^-21 off,
-// 2^-13 of BF16's rounding; results below 2^-126 are 0, where s is 1 to the last place).  Both take the hardware's
-// reciprocal, a unit in the last place off.
+// The hardware's exponential, denormal results kept.
+__device__ __forceinline__ float exp_hw(float x) {
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+  return e;
+}
+
+// s, and 1 - s in `other`: with e = exp(-|z|), 1 / (1 + e) and e / (1 + e), so that neither is a difference and the smaller
+// one keeps what FP32 has below 2^-126 (g s is a normal number down to g = -91).  FP32 results take the library's
+// expf; those of BF16 calls the hardware's exponential, about 2^-21 off, 2^-13 of BF16's rounding.  Codes of h are made from
+// those too: with expf as many change (1.08 times a plain FP32 product's), 6 us more.  Both take the hardware's reciprocal,
+// of 1 to 2, a unit in the last place off.
 template <bool ACCURATE>
-__device__ __forceinline__ float sigmoid(float z) {
-  float e, s;
-  if (ACCURATE) e = expf(-z);
-  else asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));   // 0 where e is infinite
-  return s;
+__device__ __forceinline__ float sigmoid(float z, float &other) {
+  float e, r;
+  if (ACCURATE) e = expf(-fabsf(z));
+  else e = exp_hw(-fabsf(z));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  const float t = e * r;
+  other = z >= 0.0f ? t : r;
+  return z >= 0.0f ? r : t;
 }
 
 constexpr float kTanhScale = 1.5957691216057308f;   // 2 sqrt(2 / pi)
@@ -28,7 +39,8 @@ __device__ __forceinline__ float tanh_inner(float g) { return kTanhScale * fmaf(
 template <int FN, bool ACCURATE>
 __device__ __forceinline__ float gate_value(float g) {
   if (FN == GATE_GELU) return g * (0.5f * erfcf(g * -0.70710678118654752f));
-  return g * sigmoid<ACCURATE>(FN == GATE_SILU ? g : tanh_inner(g));
+  float other;
+  return g * sigmoid<ACCURATE>(FN == GATE_SILU ? g : tanh_inner(g), other);
 }
 
 // a(g), and a'(g) in `slope`
@@ -36,14 +48,15 @@ template <int FN, bool ACCURATE>
 __device__ __forceinline__ float gate_slope(float g, float &slope) {
   if (FN == GATE_GELU) {
     const float phi = 0.5f * erfcf(g * -0.70710678118654752f), e = -0.5f * g * g;
-    slope = fmaf(g * 0.3989422804014327f, ACCURATE ? expf(e) : __expf(e), phi);
+    slope = fmaf(g * 0.3989422804014327f, ACCURATE ? expf(e) : exp_hw(e), phi);
     return g * phi;
   }
-  const float s = sigmoid<ACCURATE>(FN == GATE_SILU ? g : tanh_inner(g)), a = g * s;
+  float other;
+  const float s = sigmoid<ACCURATE>(FN == GATE_SILU ? g : tanh_inner(g), other), a = g * s;
   if (FN == GATE_SILU) {
-    slope = fmaf(a, 1.0f - s, s);
+    slope = fmaf(a, other, s);
   } else {   // z' may overflow where s is 0 or 1 already
-    const float t = s * (1.0f - s);
+    const float t = s * other;
     slope = t == 0.0f ? s : fmaf(g * (kTanhScale * fmaf(3.0f * 0.044715f * g, g, 1.0f)), t, s);
   }
   return a;
