@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 import torch
 
+import act_ref as A
 from fac_whitening_gb300 import gift as G
-from test_gpu_mlp import gated_backward, gated_forward, input_grad, linear
+from test_gpu_mlp import gated_backward, gated_forward, input_grad, linear, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +80,29 @@ def test_products_round_their_sums_often_enough(k):
     assert np.array_equal(input_grad(X, V, "bf16", X, V), 2 * want)
     dg, _ = gated_backward(X, V, np.zeros((T, n)), np.full((T, n), 2.0), "silu", "bf16")   # a'(0) = 1/2
     assert np.array_equal(dg, want)
+
+
+# k of the first segment only, of a last one of one stage or of a part of it, and of many; one tile, and nine
+@pytest.mark.parametrize("sms", [None, 2], ids=["", "one-pair"])
+@pytest.mark.parametrize("off", [False, True], ids=["aligned", "unaligned"])
+@pytest.mark.parametrize("T,n", [(40, 48), (600, 272)], ids=str)
+@pytest.mark.parametrize("k", [100, 256, 320, 769, 1536, 2000, 4096])
+def test_segments_of_a_kept_forward_product(k, T, n, off, sms):
+    """gate, up, h, codes and scales from whole numbers.  The gates are at least 20, where a(g) = g in FP32."""
+    c = None
+    if sms:
+        c = G.Context(torch.cuda.current_device())
+        G.gift_set_option(c, G.OPT_SMS, sms)
+    rng = np.random.default_rng(k + T)
+    x, W, W2 = (rng.integers(-m, m + 1, s).astype(float) for m, s in ((8, (T, k)), (1, (n, k)), (1, (n, k))))
+    bias = rng.integers(2000, 2101, n).astype(float)
+    g, u = x @ W.T + bias, x @ W2.T
+    h = g * u
+    assert g.min() >= 20 and np.abs(h).max() < 2 ** 24
+    for fmt in ("e4m3", "e5m2"):
+        out = gated_forward(x, W, W2, "silu", "bf16", bg=bias, fmt=fmt, off=off, c=c)
+        assert out["status"] == 0
+        for key, want in (("gate", g), ("up", u), ("h", h)):
+            assert np.array_equal(out[key], rounded(want, "bf16")), key
+        codes, scales = A.encode(h, fmt)
+        assert np.array_equal(out["scales"], scales) and np.array_equal(out["codes"], codes)
