@@ -1552,6 +1552,7 @@ gift_status gift_linear_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int
   if (!ctx || !x || !W || !y || !ws || !valid_extent(T) || !valid_extent(d_in) || !valid_extent(d_out) ||
       !valid_tiles(T, d_out) || !valid_dt(dt) || !drop_below(p, rng, &a.below))
     return GIFT_ERR_INVALID_ARG;
+  if (y == x || y == W) return GIFT_ERR_INVALID_ARG;   // tiles are stored while others still read their operands
   if (ws_bytes < act_layout(nullptr, ctx, GIFT_OP_LINEAR_FORWARD, dt, T, d_out, d_in).bytes)
     return GIFT_ERR_INVALID_ARG;
   const ActWs w = act_layout(ws, ctx, GIFT_OP_LINEAR_FORWARD, dt, T, d_out, d_in);

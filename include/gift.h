@@ -654,9 +654,9 @@ gift_status gift_gated_backward(gift_ctx *ctx, const void *dy, gift_dtype dt, in
  *  x      : device, T x d_in of type dt.     W : device, d_out x d_in of type dt.
  *  bias   : device, d_out FP32, nullable.    residual : device, T x d_out of type dt, nullable.
  *  p, rng, site : as gift_dropout_forward.
- *  y      : device, T x d_out of type dt; may be residual.
+ *  y      : device, T x d_out of type dt; may be residual, but not x, even where residual is x.
  *  ws     : gift_act_workspace_bytes(GIFT_OP_LINEAR_FORWARD, dt, T, d_out, d_in) bytes.
- * INVALID_ARG: a null x, W, y or ws, T, d_in or d_out < 1, a bad type, p or rng, a workspace too small.  d_status:
+ * INVALID_ARG: a null x, W, y or ws, y equal to x or W, T, d_in or d_out < 1, a bad type, p or rng, a workspace too small.  d_status:
  * TIMEOUT. */
 gift_status gift_linear_forward(gift_ctx *ctx, const void *x, gift_dtype dt, int T, int d_in, const void *W, int d_out,
                                 const float *bias, const void *residual, float p, const unsigned long long *rng,

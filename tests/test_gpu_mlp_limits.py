@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from fac_whitening_gb300 import gift as G
-from gpu_util import ctx
+from gpu_util import DEV, ctx
 
 pytestmark = pytest.mark.gpu
 MOST = 1 << 30
@@ -25,3 +25,22 @@ def test_no_workspace_for_an_output_of_too_many_tiles(op, n_is_out, dt):
         assert size(T, n, 16) >= 0
     # terms of FP32, or copies of BF16 rows that TMA cannot read: the token and a row of the weights, 2 bytes a number
     assert size(1, 1, MOST) >= 4 * MOST
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_the_residual_stream_may_be_the_input_but_not_the_output_too(dt):
+    """y = x + x W^T: y in a buffer of its own is right, in x's place it is refused (other tiles still read x)."""
+    T, d = 300, 64
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randint(-8, 9, (T, d), device=DEV, generator=g).to(dt)
+    W = torch.randint(-1, 2, (d, d), device=DEV, generator=g).to(dt)
+    ws = torch.empty(G.gift_act_workspace_bytes(ctx(), "linear_forward", dt, T, d, d), dtype=torch.uint8, device=DEV)
+    y, want = torch.empty_like(x), (x.double() + x.double() @ W.double().t()).to(dt)
+    G.gift_linear_forward(ctx(), x, W, y, residual=x, ws=ws)
+    assert torch.equal(y, want)
+    kept = x.clone()
+    with pytest.raises(G.GiftError):
+        G.gift_linear_forward(ctx(), x, W, x, residual=x, ws=ws)
+    with pytest.raises(G.GiftError):
+        G.gift_linear_forward(ctx(), x[:d], W, W, residual=x[:d], ws=ws)
+    assert torch.equal(x, kept)
