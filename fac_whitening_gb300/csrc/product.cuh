@@ -476,11 +476,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem;
 
-  // Called by whole warps: the lanes go on together, or none does.
-  auto hold = [&](uint32_t bar, uint32_t parity) {
-    if (__all_sync(0xFFFFFFFFu, try_wait_at(bar, parity))) return true;
+  // Called by whole warps: the lanes go on together, or none does.  Not patient: gives up where a phase is not over when it is
+  // looked at.
+  auto hold = [&](uint32_t bar, uint32_t parity, bool patient) {
+    if (patient && __all_sync(0xFFFFFFFFu, try_wait_at(bar, parity))) return true;
     const long long t0 = clock64();
-    while (!__all_sync(0xFFFFFFFFu, try_wait_at(bar, parity))) {
+    while (!__all_sync(0xFFFFFFFFu, patient ? try_wait_at(bar, parity) : test_wait_at(bar, parity))) {
       if (__any_sync(0xFFFFFFFFu, sh.failed || clock64() - t0 > P.budget)) {
         sh.failed = 1;
         set_status(status, GIFT_ERR_TIMEOUT);
@@ -489,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     return true;
   };
-  auto wait = [&](uint64_t *bar, uint32_t parity) { return hold(tc::smem_u32(bar), parity); };
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return hold(tc::smem_u32(bar), parity, true); };
 
   // registers: 168 per thread at launch (504 over the three groups of four warps), redistributed as 2 x 208 + 88
   if (warp < kEpiWarp) {
@@ -498,7 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // registers; one elected thread issues.  A stage's 512 clocks are few for what a warp does between two of them: the
     // loops keep their addresses running, and A and B have a warp each (one for both, its slot and terms computed
     // per stage, took 550 clocks a stage).
-    const bool one = elect_one();
+    const bool one = elect_one(), patient = P.budget > 0;
     const uint32_t full = of_cta(tc::smem_u32(sh.full), 0), empty = tc::smem_u32(sh.empty);
     const uint32_t ring = tc::smem_u32(sm);
     if (warp == 0 || warp == 2) {
@@ -512,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       grid_wait();   // the operands that the launch before this one made
       auto stage = [&](const CUtensorMap *map, int k, int y, int term) {
         const uint32_t bar = full + 8 * at, dst = base + at * kStage;
-        if (!(ok = hold(empty + 8 * at, parity))) return;
+        if (!(ok = hold(empty + 8 * at, parity, patient))) return;
         if (one) {
           expect_in_cluster(bar, bytes);
           if (MN && !is_a) {
@@ -551,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // The last stages' MMAs are done (and leave no arrival of their commits behind): all copies have landed.
       for (uint32_t r = 1; ok && r <= kStages && r <= g; ++r) {
         const Slot<kStages> s(g - r);
-        ok = hold(empty + 8 * s.at, s.parity);
+        ok = hold(empty + 8 * s.at, s.parity, patient);
       }
       // the pair's first CTA may have a wait of its own to end before its last commit
       tc::mbar_wait_bounded(&sh.drained, 0, P.budget + kDrain);
@@ -566,16 +567,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int head = P.head, seg = P.seg;
       uint32_t at = 0, parity = 0, n = 0;   // slot, segments
       bool ok = true, there = false;        // there: the stage was seen to be loaded
+      grid_wait();   // no wait's budget is spent on the launch that makes the operands
       for (int it = pair; it < P.items && ok; it += pairs) {
         const Item w(P, it);
         for (int left = (w.k1 - w.k0) * kTerms, i = 0, len; left > 0 && ok; left -= len, ++i, ++n) {
           len = i < 2 ? head : seg;
           const uint32_t d = tmem + 256 * (n & 1);
-          if (!(ok = hold(dempty + 8 * (n & 1), (n >> 1 & 1u) ^ 1u))) break;
+          if (!(ok = hold(dempty + 8 * (n & 1), (n >> 1 & 1u) ^ 1u, patient))) break;
           tc::fence_after_sync();
           uint32_t accumulate = 0;
           for (int j = min(len, left); j > 0; --j) {
-            if (!there && !(ok = hold(loaded + 8 * at, parity))) break;
+            if (!there && !(ok = hold(loaded + 8 * at, parity, patient))) break;
             const uint32_t a = (ring + at * kStage) >> 4, b = a + (kABytes >> 4);
             uint64_t *const done = &sh.empty[at];
             advance<kStages>(at, parity);
@@ -611,6 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t n = 0, tile = 0, loads = 0, issued = 0;   // loads: buffers filled and read
     uint32_t next = buf;                               // forward: the buffer that is written next
     bool ok = true, bad = false;
+    grid_wait();   // as the MMA warp
     for (int it = pair; it < P.items && ok; it += pairs, ++tile) {
       const Item w(P, it);
       const int row0 = w.m * kTileRows + 128 * rank + 32 * q, rows = P.T - row0;   // may be <= 0

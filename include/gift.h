@@ -173,9 +173,13 @@ typedef enum {
                                   pipeline, before it gives up and writes GIFT_ERR_TIMEOUT to
                                   d_status (the encode then stores no codes, the others leave
                                   their outputs undefined; default 2e9, about a second; 0..2e10).
-                                  A small value makes the wait run out on purpose (the pipelines'
-                                  after a few microseconds): the kernel still ends and the context
-                                  stays usable. */
+                                  A small value makes the wait run out on purpose (the weight
+                                  gradient's after a few microseconds, the feed-forward products' at
+                                  0 where it is not over at once): the kernel still ends and the
+                                  context stays usable.  The feed-forward products' waits begin when
+                                  their operands are there; the weight gradient's first ones count the
+                                  launch that prepares its scales and operands too, beside which it
+                                  starts. */
   GIFT_OPT_SMS = 3             /* SMs the context's launches size their grids for (default and
                                   maximum: the device's SM count).  With a fraction of the SMs per
                                   context, calls on several streams run side by side on disjoint
