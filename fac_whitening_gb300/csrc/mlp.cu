@@ -191,8 +191,8 @@ struct Plan {
 
 // Microseconds of a stage, and of a tile's epilogue: what it computes and stores after its last MMA.  A stage of fewer
 // columns is bound by its loads: 0.285, 0.25, 0.2 and 0.19 us at 256, 192, 128 and 64 columns (9728 x 4096 x 1536).  An
-// epilogue of 256 columns takes 2 us (linear), 5 (gated backward) and 4 to 8 with FP32's twice as many bytes; it
-// runs beside the next tile's product, so the last one counts.
+// epilogue of 256 columns takes 2 us (linear; counted as 2.5, and 1.5 to 3.5 give the same times on 14 of 15 shapes), 5 (gated
+// backward) and 4 to 8 with FP32's twice as many bytes; it runs beside the next tile's product, so the last one counts.
 struct TileCost {
   bool bf16;
   double epilogue;   // of 256 columns
@@ -209,7 +209,8 @@ constexpr double kLinearEnd = 2.5, kGatedEnd = 5.0;
 
 // The width with the least time.  With `cut`, the tiles after the last full wave of pairs are cut into slices of k where
 // that wave and the kernel that joins the slices (its launch and 6 TB/s) end sooner than a wave of whole tiles would:
-// 16384 x 6144 x 1536 has 384 tiles of 256 on 76 pairs, 187 us with six waves, 174 with five and slices.
+// 16384 x 6144 x 1536 has 384 tiles of 256 on 76 pairs, 195 us with six waves, 182 with five and slices; 16384 x 12288 x 1536
+// 368 and 334.
 Plan plan_of(int sms, const TileCost &c, int T, int N, int kb, bool cut) {
   const int pairs = sms / 2 > 1 ? sms / 2 : 1;
   const int mt = ceil_div(T, product::kTileRows);

@@ -17,13 +17,14 @@
 // the gate's rows, the second the other projection's, and both halves of a row meet in one thread.
 // FP32 operands are three BF16 terms each (operand.cuh); a block of 64 k then takes six stages, the products i + j <= 2
 // of terms i and j; what is dropped is below 2^-23 of |A_k B_k|.  A block is a segment and the small products come
-// first, so that only the last stage's four steps truncate at the sum's size (segments of two blocks: outputs 6e-7
-// off instead of 2e-7 at 256 k).
+// first, so that only the last stage's four steps truncate at the sum's size: outputs are 0.9e-7 off at 256 k, 1.1e-7 at
+// 1021 and 4096 (relative Frobenius; a plain FP32 product 2.9e-7, 5.7e-7 and 1.1e-6; segments of two blocks 6e-7).
 // What bounds it.  A stage's MMAs of 256 columns take 512 clocks, its 32 KB cross from L2 at up to 64 bytes a clock: 540 to
 // 560 clocks a stage.  16384 x 12288 x 1536 input gradient 330 us, 1.87 PFLOP/s; 16384 x 6144 x 1536 linear with dropout
-// and residual 180 us; 16384 x 1536 x 6144 gated forward 410 us with the checkpoint, backward 230 us (g, u and their
-// gradients are 805 MB: 157 us without them); 32768 x 4096 x 16384 gated forward 4.5 ms, 1.96 PFLOP/s.  Small ones: a start
-// of 1 us, 1 us to the first stage, 3 us for a BF16 epilogue.
+// and residual 180 us; 16384 x 1536 x 6144 gated forward 414 us with the checkpoint, 345 without, backward 232 us (g, u and
+// their gradients are 805 MB: 157 us without them); 32768 x 4096 x 16384 gated forward with it 4.8 ms, 1.83 PFLOP/s.  A
+// library's BF16 product by itself takes 335, 171, 308 (both projections in one), 156 and 4660 us.  Small ones: a start of
+// 1 us, 1 us to the first stage, 3 us for a BF16 epilogue.
 // Every mbarrier wait is bounded by the context's GIFT_OPT_BARRIER_WAIT and reports GIFT_ERR_TIMEOUT; a warp
 // leaves as one, and the copies and MMAs in flight are waited for before the CTA leaves.
 #pragma once
@@ -86,8 +87,9 @@ struct Params {
 };
 
 // Row m and column n of tiles of a tile.  Tiles are in groups of rows of tiles, column by column within a group: the
-// pairs that run at the same time share both operands in L2.  Groups of 4, 8, 16 and 32 rows: 16384 x 1536 x 6144 gated
-// forward 361, 353, 347, 355 us; 16384 x 6144 x 1536 linear 178, 181, 184, 191 us.
+// pairs that run at the same time share both operands in L2.  Groups of 2, 4, 8, 16 and 32 rows: 16384 x 1536 x 6144 gated
+// forward 365, 367, 353, 345, 355 us, 32768 x 4096 x 16384 with the checkpoint 5510, 5340, 5330, 5280, 5380 (16 there);
+// 16384 x 6144 x 1536 linear 181, 183, 183, 187, 197, 32768 x 4096 x 16384 gated backward 2950, 2840, 2800, 2800, 2840 (8).
 __host__ __device__ inline void tile_place(const Params &P, int tile, int &m, int &n) {
   const int per = P.group * P.nt, g = tile / per, rem = tile - g * per;
   const int rows = P.mt - P.group * g < P.group ? P.mt - P.group * g : P.group;

@@ -613,9 +613,10 @@ gift_status gift_weight_grad(gift_ctx *ctx, const void *delta, gift_dtype delta_
  * bits are rounded at least every 64 n, n = max(2, min(16, 1 + b / 8 rounded down, the root of b to the nearest)), b = k /
  * 64 rounded up: every 256 terms of 1536, every 512 of 4096.  FP32 operands enter as three BF16 terms each with the
  * six products i + j <= 4 of terms i and j (what is dropped is below 2^-23 of |x_k W_k|); operands below 2^-110 may lose
- * up to 2^-134.  Orders of summation are fixed by the shape, the buffers' alignment and the context: equal calls
- * give equal bits.  An infinity or NaN in a BF16 operand reaches the outputs as the formula has it; in an FP32
- * operand it makes NaN or Inf of every output that the formula makes not finite, without telling which.
+ * up to 2^-134.  Orders of summation are fixed by the shape, the buffers' alignment, the context and, in a BF16 gated
+ * forward product, by whether h is also kept in 8 bits (g, u and h made again without codes may differ in their last
+ * place): equal calls give equal bits.  An infinity or NaN in a BF16 operand reaches the outputs as the formula has it; in
+ * an FP32 operand it makes NaN or Inf of every output that the formula makes not finite, without telling which.
  * T, d, f, d_in and d_out are at most 2^30 and an output has at most 2^31 - 1 tiles of 256 x 64 (INVALID_ARG above).
  * Alignment: any to the element.  BF16 operands of the products are read in place where their rows and pointers are
  * 16-byte aligned, copied into the workspace else; the products' other tensors are moved by TMA where all their rows
