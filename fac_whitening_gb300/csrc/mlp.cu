@@ -80,14 +80,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_linear(const __grid_const
     const size_t at = (size_t)row * P.N + col;
     if (sizeof(E) == 2 && vec) {   // eight columns are 16 bytes
       if (residual) {
-        const uint4 r = *reinterpret_cast<const uint4 *>(residual + at);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        const product::Piece<__nv_bfloat16> r(*reinterpret_cast<const uint4 *>(residual + at));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          v[k] = add2(v[k], make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)));
+        for (int k = 0; k < 4; ++k) v[k] = add2(v[k], r.v[k]);
       }
-      *reinterpret_cast<uint4 *>(y + at) = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
-                                                      pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
+      *reinterpret_cast<uint4 *>(y + at) = product::pack_piece<__nv_bfloat16>(v);
       continue;
     }
 #pragma unroll
@@ -102,18 +99,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_join_linear(const __grid_const
 
 // ---- host ---------------------------------------------------------------------------------------------
 constexpr int kSegment = 16, kSegment6 = 6;   // most stages of a segment: 1024 k, or one block of 64 k of FP32's terms
-
-// `planes` matrices of rows x cols BF16, rows `pitch` bytes apart, read in boxes of 64 columns x `box` rows
-bool boxes(CUtensorMap *m, const void *base, int rows, int cols, size_t pitch, int planes, int box) {
-  const auto enc = encoder();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-  const cuuint64_t strides[2] = {pitch, pitch * (cuuint64_t)rows};
-  const cuuint32_t size[3] = {64, (cuuint32_t)box, 1}, one[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, size, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 struct Source {
   const void *p;
@@ -174,7 +159,7 @@ cudaError_t operands(const Launch &L, bool bf16, const Source *src, int n, uint8
       at = ws;
     }
     ws += operand_bytes(bf16, s.rows, s.cols);
-    if (!boxes(&maps[i], at, s.rows, s.cols, pitch, bf16 ? 1 : 3, s.box)) return cudaErrorInvalidValue;
+    if (!boxes(&maps[i], true, at, s.rows, s.cols, pitch, bf16 ? 1 : 3, s.box)) return cudaErrorInvalidValue;
   }
   made = grid > 0;
   if (made) k_operands<<<grid, 256, 0, L.stream>>>(O, bf16);

@@ -94,4 +94,19 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
+// `planes` matrices of rows x cols elements (one of bytes; BF16 any number), rows `pitch` bytes apart, read in boxes of
+// 128 bytes x box_rows
+inline bool boxes(CUtensorMap *m, bool bf16, const void *base, int rows, int cols, size_t pitch, int planes,
+                  int box_rows) {
+  const auto enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {pitch, pitch * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {bf16 ? 64u : 128u, (cuuint32_t)box_rows, 1}, one[3] = {1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, bf16 ? 3 : 2,
+             const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace gift

@@ -835,21 +835,6 @@ __global__ void __launch_bounds__(256) k_prepare(const __grid_constant__ Prepare
 }
 
 // ---- host ---------------------------------------------------------------------------------------
-// `planes` matrices of rows x cols elements, rows `pitch` bytes apart, read in 128-byte x 64-row boxes
-bool boxes(CUtensorMap *m, bool bf16, const void *base, int rows, int cols, size_t pitch, int planes) {
-  const auto enc = encoder();
-  if (!enc) return false;
-  const int rank = bf16 ? 3 : 2;
-  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-  const cuuint64_t strides[2] = {pitch, pitch * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {bf16 ? 64u : 128u, (cuuint32_t)kK, 1};
-  const cuuint32_t one[3] = {1, 1, 1};
-  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank,
-             const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct Plan {
   int nh, mt, nt, ng, slices, pairs;
   bool ones;
@@ -1033,8 +1018,8 @@ cudaError_t launch_weight_grad(const Launch &L, int fmt, bool bf16, const Weight
   if (q.nsums && (e = launch_sum_parts(L, a.part, q.sum_slices, a.d_out, db)) != cudaSuccess) return e;
 
   CUtensorMap tm_codes, tm_delta;
-  if (!boxes(&tm_codes, false, codes, a.T, a.d_in, cpitch, 1) ||
-      !boxes(&tm_delta, true, delta, a.T, a.d_out, dpitch, bf16 ? 1 : 3))
+  if (!boxes(&tm_codes, false, codes, a.T, a.d_in, cpitch, 1, kK) ||
+      !boxes(&tm_delta, true, delta, a.T, a.d_out, dpitch, bf16 ? 1 : 3, kK))
     return cudaErrorInvalidValue;
   Params P;
   P.T = a.T;
