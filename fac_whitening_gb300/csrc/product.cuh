@@ -22,8 +22,8 @@
 // What bounds it.  A stage's MMAs of 256 columns take 512 clocks, its 32 KB cross from L2 at up to 64 bytes a clock: 540 to
 // 560 clocks a stage.  16384 x 12288 x 1536 input gradient 330 us, 1.87 PFLOP/s; 16384 x 6144 x 1536 linear with dropout
 // and residual 180 us; 16384 x 1536 x 6144 gated forward 414 us with the checkpoint, 345 without, backward 232 us (g, u and
-// their gradients are 805 MB: 157 us without them); 32768 x 4096 x 16384 gated forward with it 4.8 ms, 1.83 PFLOP/s.  A
-// library's BF16 product by itself takes 335, 171, 308 (both projections in one), 156 and 4660 us.  Small ones: a start of
+// their gradients are 805 MB: 157 us without them); 32768 x 4096 x 16384 gated forward with it 4.6 to 5.3 ms.  A
+// library's BF16 product by itself takes 335, 171, 308 (both projections in one), 156 us and, where that took 5.3 ms, 4.7.  Small ones: a start of
 // 1 us, 1 us to the first stage, 3 us for a BF16 epilogue.
 // Every mbarrier wait is bounded by the context's GIFT_OPT_BARRIER_WAIT and reports GIFT_ERR_TIMEOUT; a warp
 // leaves as one, and the copies and MMAs in flight are waited for before the CTA leaves.
